@@ -23,8 +23,11 @@ DSA_ERR_BOUNDS, DSA_ERR_RAW_RANGE = -9, -10
 
 EXPORTS = ("dsa_pool_append", "dsa_score_scratch_bytes", "dsa_index_score_topk",
            "dsa_window_sparse_attn", "dsa_prefill_chunk", "dsa_strerror",
-           "dsa_index_score_topk_noalloc", "dsa_bounded_wait_selftest", "dsa_prefill_chunk_host")
+           "dsa_index_score_topk_noalloc", "dsa_bounded_wait_selftest", "dsa_prefill_chunk_host",
+           "dsa_paged_append", "dsa_paged_attn")
 DSA_STATIC_SCRATCH_BYTES = 16 << 20
+DSA_PAGED_WORKSPACE_BYTES = 40 << 20
+ROPE_DIM, MAX_PAGE_SIZE, MAX_PAGED_HEADS = 64, 1024, 128
 
 
 class DsaError(RuntimeError):
@@ -74,11 +77,14 @@ def load(path: str | None = None):
     lib.dsa_prefill_chunk_host.argtypes = [S, ctypes.POINTER(dsa_prefill_workspace), P, i64, i64,
                                            P, P, P, P, i64, i64, i32, i32, ctypes.c_float, i64,
                                            P, P, P, P, P]
+    lib.dsa_paged_append.argtypes = [P, i64, P, P, i32, P, i32, P, i64, i64, i32, P, i64, P, P]
+    lib.dsa_paged_attn.argtypes = [P, i32, i64, P, P, i32, P, i32, P, i64, i64, i32, P, i64, i32,
+                                   ctypes.c_float, P, sz, P, P, P]
     lib.dsa_strerror.argtypes = [ctypes.c_int]
     lib.dsa_strerror.restype = ctypes.c_char_p
     for f in ("dsa_pool_append", "dsa_index_score_topk", "dsa_window_sparse_attn",
               "dsa_prefill_chunk", "dsa_index_score_topk_noalloc", "dsa_bounded_wait_selftest",
-              "dsa_prefill_chunk_host"):
+              "dsa_prefill_chunk_host", "dsa_paged_append", "dsa_paged_attn"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -258,3 +264,67 @@ def dsa_prefill_chunk_host(state: "PoolState", ws: PrefillWorkspace, raw_kv_h, r
         tile_rows, _p(sel_h), _p(out_h), _p(dev_status), _s(stream),
         _s(copy_stream) if copy_stream is not None else _s(stream))
     _check(rc, "dsa_prefill_chunk_host")
+
+
+def _take(where: str, name: str, t, dtype, shape, device) -> int:
+    """The address of a packed device tensor of this dtype and shape (-1: any size)."""
+    if (t.dtype is not dtype or t.device.index != device or t.dim() != len(shape)
+            or not t.is_contiguous()
+            or any(n >= 0 and m != n for m, n in zip(t.shape, shape))):
+        want = ", ".join("*" if n < 0 else str(n) for n in shape)
+        raise DsaError(DSA_ERR_ARG, f"{where}: {name} has to be a packed {dtype} tensor [{want}] "
+                                    f"on cuda:{device}")
+    return t.data_ptr()
+
+
+def _paged(where: str, new_start, seq_len, page_table, pages, cos_sin, device):
+    """The arguments both paged calls share, in the ABI's order."""
+    n_seqs, max_pages = page_table.shape if page_table.dim() == 2 else (0, 0)
+    if (pages.dtype is not torch.bfloat16 or pages.device.index != device or pages.dim() != 3
+            or pages.shape[2] != DIM or pages.stride(2) != 1 or pages.stride(1) != DIM):
+        raise DsaError(DSA_ERR_ARG, f"{where}: pages has to be a torch.bfloat16 tensor "
+                                    f"[*, *, {DIM}] on cuda:{device} with packed pages")
+    n_pages, page_size = pages.shape[0], pages.shape[1]
+    stride = pages.stride(0) if n_pages > 1 else max(pages.stride(0), page_size * DIM)
+    return (_take(where, "new_start", new_start, torch.int32, (n_seqs + 1,), device),
+            _take(where, "seq_len", seq_len, torch.int32, (n_seqs,), device), n_seqs,
+            _take(where, "page_table", page_table, torch.int32, (-1, -1), device), max_pages,
+            pages.data_ptr(), n_pages, stride, page_size,
+            None if cos_sin is None else _take(where, "cos_sin", cos_sin, torch.float32,
+                                               (-1, ROPE_DIM // 2, 2), device),
+            0 if cos_sin is None else cos_sin.shape[0])
+
+
+def _status(where: str, dev_status, device):
+    return None if dev_status is None else _take(where, "dev_status", dev_status, torch.int32,
+                                                 (1,), device)
+
+
+def dsa_paged_append(kv, new_start, seq_len, page_table, pages, cos_sin=None, dev_status=None,
+                     stream=None) -> None:
+    """Rotate the new tokens' rows kv [n_new, 512] by their positions into their pages
+    [n_pages, page_size, 512]. Tensors are on the current device; see include/dsa.h."""
+    where = "dsa_paged_append"
+    dev = torch.cuda.current_device()
+    rc = load().dsa_paged_append(
+        _take(where, "kv", kv, torch.bfloat16, (-1, DIM), dev), kv.shape[0],
+        *_paged(where, new_start, seq_len, page_table, pages, cos_sin, dev),
+        _status(where, dev_status, dev), _s(stream))
+    _check(rc, where)
+
+
+def dsa_paged_attn(q, new_start, seq_len, page_table, pages, window: int, scale: float, workspace,
+                   out, cos_sin=None, dev_status=None, stream=None) -> None:
+    """Attention of the new tokens q [n_new, heads, 512] over their sequences' paged rows
+    (window 0: all of them) into out. `workspace` is any packed tensor of at least
+    DSA_PAGED_WORKSPACE_BYTES. Tensors are on the current device; see include/dsa.h."""
+    where = "dsa_paged_attn"
+    dev = torch.cuda.current_device()
+    qp = _take(where, "q", q, torch.bfloat16, (-1, -1, DIM), dev)
+    op = _take(where, "out", out, torch.bfloat16, q.shape, dev)
+    rc = load().dsa_paged_attn(
+        qp, q.shape[1], q.shape[0],
+        *_paged(where, new_start, seq_len, page_table, pages, cos_sin, dev), window, scale,
+        _take(where, "workspace", workspace, workspace.dtype, (-1,) * workspace.dim(), dev),
+        _nbytes(workspace), op, _status(where, dev_status, dev), _s(stream))
+    _check(rc, where)

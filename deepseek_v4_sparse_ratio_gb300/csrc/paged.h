@@ -1,0 +1,49 @@
+// The paged KV cache of a ragged batch, as the append and the attention over it see it:
+// the arguments both calls share, their checks, and the rule that says which sequences of
+// the batch take part.
+#pragma once
+
+#include <cuda.h>
+#include <stdint.h>
+
+#include "internal.h"
+
+namespace dsa {
+
+constexpr int kRope = DSA_ROPE_DIM;           // rotated elements at the end of a row
+constexpr int kRopePairs = DSA_ROPE_DIM / 2;
+
+struct PagedBatch {
+    const int32_t *new_start;   // [n_seqs + 1] first row of each sequence's new tokens
+    const int32_t *seq_len;     // [n_seqs] tokens of each sequence, the new ones included
+    const int32_t *page_table;  // [n_seqs, max_pages]
+    const float *cos_sin;       // [n_pos, 32, 2] or null
+    int64_t n_new;              // rows of the new tokens' arrays
+    int64_t page_stride;        // elements
+    int32_t n_seqs, max_pages;
+    int32_t n_pages;
+    int32_t page_shift;         // log2(rows of a page)
+    int32_t len_limit;          // longest sequence the table (and cos_sin) can hold
+};
+
+// Checks every argument the two calls share and fills `b`; DSA_OK or a DSA_ERR_* code.
+int check_paged_batch(int64_t n_new, const int32_t *new_start, const int32_t *seq_len,
+                      int32_t n_seqs, const int32_t *page_table, int32_t max_pages,
+                      const void *pages, int64_t n_pages, int64_t page_stride, int32_t page_size,
+                      const float *cos_sin, int64_t n_pos, PagedBatch *b);
+
+// One sequence of the batch: rows [row0, row0 + n) are its new tokens, the last n of its len.
+struct PagedSeq {
+    int32_t row0, n, len;
+};
+
+// Sequence s of the batch. A sequence whose numbers contradict each other or the arrays'
+// sizes gets n = 0, so nothing of it is read or written; `bad` tells it from an idle one.
+__device__ __forceinline__ PagedSeq paged_seq(const PagedBatch &b, int s, bool &bad) {
+    const int32_t r0 = __ldg(b.new_start + s), r1 = __ldg(b.new_start + s + 1);
+    const int32_t len = __ldg(b.seq_len + s);
+    bad = r0 < 0 || r1 < r0 || r1 > b.n_new || len < r1 - r0 || len > b.len_limit;
+    return PagedSeq{r0, bad ? 0 : r1 - r0, len};
+}
+
+}  // namespace dsa

@@ -13,6 +13,11 @@
  *   dsa_prefill_chunk          the four steps for one chunk, in order;
  *   dsa_prefill_chunk_host     the same from host buffers, copies overlapped.
  *
+ * Beside it, for a ragged batch of sequences whose KV rows live in pages:
+ *   dsa_paged_append           the new tokens' rows, rotated by position, into the pages;
+ *   dsa_paged_attn             attention of the new tokens over their sequences' rows
+ *                              (prompt chunks, short bands, single tokens).
+ *
  * Shapes are fixed by the model: indexer heads H_I=64 of dim d_I=128, query
  * heads H=64, one shared KV row of dim D=512 (key and value for every head),
  * B=1, bf16 storage, fp32 accumulation. The pooling ratio is a power of two
@@ -63,6 +68,9 @@ extern "C" {
 #define DSA_INDEX_DIM 128
 #define DSA_HEADS 64
 #define DSA_DIM 512
+#define DSA_ROPE_DIM 64         /* rotated elements at the end of a paged KV row */
+#define DSA_MAX_PAGE_SIZE 1024  /* rows of a page: a power of two from 16 to this */
+#define DSA_MAX_PAGED_HEADS 128
 
 enum dsa_status {
     DSA_OK = 0,
@@ -325,6 +333,80 @@ int dsa_index_score_topk_noalloc(const void *q_idx, const float *w, const void *
                                  int64_t n_pooled, int64_t chunk, int64_t offset, int32_t ratio,
                                  int32_t index_topk, int64_t tile_rows, int32_t *sel,
                                  int32_t *dev_status, void *stream);
+
+/*
+ * The paged cache of a ragged batch, as dsa_paged_append and dsa_paged_attn take it. The
+ * pages have no counterpart to these two calls: they are additions of this library, for the
+ * layers of the same model that attend densely (their whole context, or the local window
+ * alone) when many sequences are served at once.
+ *
+ *   pages [n_pages] of [page_size, 512] bf16, page_stride elements from one page to the next
+ *     (>= page_size*512, a multiple of 8; larger where other data lies between). page_size is
+ *     a power of two from 16 to DSA_MAX_PAGE_SIZE. A row is key and value of every head.
+ *   page_table [n_seqs, max_pages] int32: entry [s][j] is the page of positions
+ *     j*page_size .. of sequence s. Entries that hold no position a call needs are not read.
+ *   seq_len [n_seqs] int32: tokens of each sequence, its new ones included.
+ *   new_start [n_seqs+1] int32: rows new_start[s] .. new_start[s+1]-1 of the new tokens'
+ *     arrays belong to sequence s; they are its last n_s = new_start[s+1]-new_start[s] tokens,
+ *     so row new_start[s]+i has position seq_len[s]-n_s+i. n_s may be 0.
+ *   n_new: rows of the new tokens' arrays, > 0. Rows from new_start[n_seqs] on belong to no
+ *     sequence (a batch padded to a captured size): they are not written.
+ *   cos_sin [n_pos, 32, 2] fp32 or NULL: (cos, sin) of every position and pair. A row's last
+ *     64 elements are 32 adjacent pairs (x, y); position p turns them by its angles,
+ *     R(p): (x, y) -> (x cos - y sin, x sin + y cos).
+ *
+ * These arrays (all but the sizes) are read on the device when the kernels run, so a captured
+ * graph replays with the lengths they hold then. A sequence whose numbers cannot be
+ * (new_start decreasing, negative or beyond n_new; seq_len < n_s, > max_pages*page_size or
+ * > n_pos) is skipped whole: its rows are not written, and DSA_ERR_BOUNDS goes to dev_status.
+ * A needed page_table entry outside [0, n_pages) is reported the same way and its rows are
+ * left out (not written by the append, not seen by the attention).
+ */
+
+/*
+ * Append the new tokens' rows: row p mod page_size of page page_table[s][p / page_size] :=
+ * R(p) kv[r] for every row r of a sequence, p its position (a plain copy when cos_sin is
+ * NULL). The rotation is taken in fp32 and rounded to bf16 once.
+ *   kv [n_new, 512] bf16. Two rows for one place (a page that two sequences of the batch
+ *   write) are the caller's mistake: either may end up there.
+ * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE, DSA_ERR_CUDA.
+ */
+int dsa_paged_append(const void *kv, int64_t n_new, const int32_t *new_start,
+                     const int32_t *seq_len, int32_t n_seqs, const int32_t *page_table,
+                     int32_t max_pages, void *pages, int64_t n_pages, int64_t page_stride,
+                     int32_t page_size, const float *cos_sin, int64_t n_pos, int32_t *dev_status,
+                     void *stream);
+
+/* Workspace bytes of dsa_paged_attn (partial results of keys split over SMs). */
+#define DSA_PAGED_WORKSPACE_BYTES ((size_t)40 << 20)
+
+/*
+ * Attention of the new tokens over their sequences' rows. For the token of position t and
+ * head h the keys are the cached rows u of its sequence with t-window < u <= t (window > 0)
+ * or 0 <= u <= t (window = 0):
+ *   logit_u = scale * (R(t) q[r,h]) . row_u,   p = softmax(logit),
+ *   out[r,h] = R(-t) sum_u p_u row_u,
+ * without R when cos_sin is NULL. The value is a rotated row, so turning the sum back by t
+ * leaves it a function of the distances t - u. The rows of the new tokens themselves are
+ * read from the pages: append them first. Accumulated in fp32; the probabilities and the
+ * rotated queries are rounded to bf16 for the matrix products, the output once to bf16.
+ *
+ *   q [n_new, heads, 512] bf16; out the same, not overlapping q; heads from 1 to
+ *   DSA_MAX_PAGED_HEADS (64 for the whole model, fewer on a shard of it); scale > 0;
+ *   workspace: device buffer of workspace_bytes >= DSA_PAGED_WORKSPACE_BYTES; nothing in it
+ *   needs to start at zero and nothing is kept in it. Calls (and captured graphs) that may
+ *   run at the same time need one each.
+ * A token that sees no row (every page of its keys left out) gets zeros. Rows of a page that
+ * a token does not see (past seq_len, later tokens, before the window) do not touch its
+ * output, whatever they hold, infinities and NaN among it.
+ * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE, DSA_ERR_SCRATCH, DSA_ERR_CUDA.
+ */
+int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new, const int32_t *new_start,
+                   const int32_t *seq_len, int32_t n_seqs, const int32_t *page_table,
+                   int32_t max_pages, const void *pages, int64_t n_pages, int64_t page_stride,
+                   int32_t page_size, const float *cos_sin, int64_t n_pos, int32_t window,
+                   float scale, void *workspace, size_t workspace_bytes, void *out,
+                   int32_t *dev_status, void *stream);
 
 /*
  * Self-check of the error path behind DSA_ERR_TIMEOUT, for failure detection.
