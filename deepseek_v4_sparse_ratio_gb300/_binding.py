@@ -285,7 +285,7 @@ def _paged(where: str, new_start, seq_len, page_table, pages, cos_sin, device):
         raise DsaError(DSA_ERR_ARG, f"{where}: pages has to be a torch.bfloat16 tensor "
                                     f"[*, *, {DIM}] on cuda:{device} with packed pages")
     n_pages, page_size = pages.shape[0], pages.shape[1]
-    stride = pages.stride(0) if n_pages > 1 else max(pages.stride(0), page_size * DIM)
+    stride = pages.stride(0) if n_pages > 1 else page_size * DIM
     return (_take(where, "new_start", new_start, torch.int32, (n_seqs + 1,), device),
             _take(where, "seq_len", seq_len, torch.int32, (n_seqs,), device), n_seqs,
             _take(where, "page_table", page_table, torch.int32, (-1, -1), device), max_pages,

@@ -32,6 +32,8 @@ int check_paged_batch(int64_t n_new, const int32_t *new_start, const int32_t *se
                       const void *pages, int64_t n_pages, int64_t page_stride, int32_t page_size,
                       const float *cos_sin, int64_t n_pos, PagedBatch *b);
 
+bool make_tmap_pages(CUtensorMap *map, const void *pages, const PagedBatch &b);
+
 // One sequence of the batch: rows [row0, row0 + n) are its new tokens, the last n of its len.
 struct PagedSeq {
     int32_t row0, n, len;

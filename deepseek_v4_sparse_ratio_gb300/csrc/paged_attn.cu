@@ -1,11 +1,37 @@
 // dsa_paged_attn: attention of a ragged batch's new tokens over their sequences' rows in a
 // paged cache.
 //
-// Simplest form: one warp per (token, head) walks the token's keys in order with an online
-// softmax in fp32; lane l holds elements 16 l .. 16 l + 15 of the query, the row and the sum.
+//   out[r,h] = R(-t) sum_u p_u row_u,   p = softmax_u(scale * (R(t) q[r,h]) . row_u)
+//
+// over the rows u of the token's sequence with t - window < u <= t. One 512-wide row is key
+// and value of every head, so the (token, head) rows of q that share keys can be stacked into
+// one matrix product whatever token or head they come from.
+//
+// Work. A unit is up to 64 rows of q: floor(64 / heads) whole tokens of a sequence, or half
+// of one token's heads when there are more than 64. Its keys are blocks of 128 positions
+// (aligned, so pages never straddle two blocks). All units' blocks form one sequence that is
+// cut into equal runs, one per CTA (one CTA per SM): a run takes whole units where they fit
+// and parts of a unit at its ends, so a single long sequence and a batch of thousands of short
+// ones both fill the machine, and causal triangles and ragged lengths balance by themselves.
+// A part leaves its (unnormalised sum, running maximum, sum of weights) in the workspace, and
+// a second kernel joins the parts. Every CTA finds its run from the lengths on the device:
+// the blocks of a sequence's first units are a sum of floors in closed form.
+//
+// A block (the layout that the window + selected attention of this library uses, with the
+// rows loaded by TMA, page by page): everything is transposed so that the 128 keys sit on the
+// MMA's M:
+//   S^T[key, row]  = K_blk[128 x 512] . Q^T        (M=128, N=64, K=512)
+//   O^T[d, row]   += V_blk^T[512 x 128] . P^T       (4 x (M=128, N=64, K=128))
+// K_blk and V_blk are one shared-memory tile of eight chunks [128 keys x 64 dims], filled and
+// released in pairs (one 128-dim tile of the second product each); a ninth chunk slot lets
+// one chunk of the next block land early. Chunk c holds dims 64 ((c + 2) mod 8) ..: the
+// rotated dims (448..511) are chunk 5, which the first product reaches in the middle of a
+// unit's first block, after other warps have turned that chunk of the queries in place.
+#include <cudaTypedefs.h>
 #include <math.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "common.cuh"
 #include "paged.h"
@@ -14,88 +40,1066 @@ namespace dsa {
 
 namespace {
 
-__device__ __forceinline__ void unpack16(const uint4 a, const uint4 b, float (&x)[16]) {
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+// Warpgroups 0-1 (80 registers a thread): the loader warp 0, warps 1-4 that turn the queries,
+// the QK-issuing warp 6 and the PV-issuing warp 7 (two issuing warps: a thread that waits
+// between MMAs stalls its own issue, not the other's). Warpgroups 2-3 (176): softmax.
+// 256*80 + 256*176 = 512*128, the launch allocation (checked before the first launch).
+constexpr int kTurnWarp0 = 1;
+constexpr int kTurnThreads = 128;
+constexpr int kQkWarp = 6;
+constexpr int kPvWarp = 7;
+constexpr int kSoftWarp0 = 8;
+constexpr int kThreads = 512;
+constexpr int kRegsLaunch = 128;
+constexpr int kRegsLow = 80;
+constexpr int kRegsSoft = 176;
+constexpr int kSoftThreads = 256;
+
+constexpr int kRows = 64;     // rows of q in a unit (MMA N)
+constexpr int kBlock = 128;   // keys in a block (MMA M)
+constexpr int kTurnChunk = 5; // the chunk that holds dims 448..511
+
+__host__ __device__ constexpr int chunk_dim(int c) { return ((c + 2) & 7) * 64; }
+
+// shared memory
+constexpr uint32_t kOffQ = 0;                // 8 chunks x [64 rows x 128 B]
+constexpr uint32_t kOffKV = 65536;           // 8 chunks x [128 keys x 128 B]
+constexpr uint32_t kOffP = 65536 + 131072;   // P^T [128 keys x 64 rows] bf16
+constexpr uint32_t kOffX = kOffP + 16384;    // chunk 7 of odd blocks
+constexpr uint32_t kOffRed = kOffX + 16384;  // [4][64] block maxima | partial sums
+constexpr uint32_t kOffLinv = kOffRed + 1024;// [64] rescale factors | 1/sum
+constexpr uint32_t kOffM = kOffLinv + 256;   // [2][64] running maximum, double-buffered
+constexpr uint32_t kOffBar = kOffM + 512;
+constexpr uint32_t kSmem = kOffBar + 256 + 1024;  // + slack for 1024-B alignment
+static_assert(kSmem <= 232448, "over the shared memory of one CTA");
+constexpr uint32_t kLbo7Spare = kOffX - (kOffKV + 6 * 16384);  // chunk 6 -> spare chunk 7
+
+// TMEM columns
+constexpr uint32_t kSCol = 0;    // S^T, 2 x 64, by block parity
+constexpr uint32_t kMCol = 128;  // the running maximum of each row, the same in all lanes
+constexpr uint32_t kOCol = 256;  // O^T: 4 d-tiles x 64
+
+constexpr float kRescale = 8.0f;      // log2 units the running maximum may lag behind
+constexpr float kNoMax = -1.0e30f;    // running maximum of a row that has seen no key: finite,
+                                      // so that (masked) -inf minus it stays -inf
+
+// workspace: descriptors, (maximum, sum) of every part, the parts' O
+constexpr int kMaxCtas = 152;
+constexpr size_t kWsDesc = 0;
+constexpr size_t kWsMl = 8192;
+constexpr size_t kWsO = kWsMl + size_t{2 * kMaxCtas} * kRows * 2 * sizeof(float);
+static_assert(kWsO + size_t{2 * kMaxCtas} * kRows * kD * sizeof(float) <= DSA_PAGED_WORKSPACE_BYTES,
+              "over the workspace");
+
+// A unit that begins in a CTA's run and ends in a later one, for the join.
+struct JoinDesc {
+    int64_t row;      // first row of q / out
+    int32_t nrows;
+    int32_t parts;    // 0: none
+    int32_t slot0;    // slot of the first part (the others are slot 0 of the next CTAs)
+    int32_t pos;      // position of the unit's first token
+    int32_t pad[2];
+};
+static_assert(sizeof(JoinDesc) == 32 && kMaxCtas * sizeof(JoinDesc) <= kWsMl, "descriptors");
+
+struct Params {
+    PagedBatch b;
+    __nv_bfloat16 *out;
+    uint8_t *ws;
+    int32_t heads;
+    int32_t tpu;      // tokens of a unit
+    int32_t upt;      // units of a token
+    int32_t rpt;      // rows of a token in a unit
+    int32_t window;   // 0: the whole context
+    float c;          // scale * log2(e)
+    int32_t *status;
+};
+
+// ------------------------------------------------------------------ the list of units
+
+// sum_{i < n} floor((a + d i) / 128) for a, d >= 0 (the Euclid-like reduction of such sums).
+__device__ int64_t floor_sum(int64_t n, int64_t a, int64_t d) {
+    int64_t m = kBlock, ans = 0;
+    while (n > 0) {
+        if (d >= m) {
+            ans += (n - 1) * n / 2 * (d / m);
+            d %= m;
+        }
+        if (a >= m) {
+            ans += n * (a / m);
+            a %= m;
+        }
+        const int64_t y = d * n + a;
+        if (y < m) break;
+        n = y / m;
+        a = y % m;
+        const int64_t t = m;
+        m = d;
+        d = t;
+    }
+    return ans;
+}
+
+// Keys of the tokens [t0, t1) of a sequence: positions lo .. hi, blocks lo / 128 .. hi / 128.
+__device__ __forceinline__ void key_range(const Params &p, const PagedSeq &q, int t0, int &lo,
+                                          int &hi) {
+    const int first = q.len - q.n + t0;
+    lo = p.window > 0 ? max(0, first - p.window + 1) : 0;
+    hi = q.len - q.n + min(t0 + p.tpu, q.n) - 1;
+}
+
+__device__ __forceinline__ int group_blocks(const Params &p, const PagedSeq &q, int g) {
+    int lo, hi;
+    key_range(p, q, g * p.tpu, lo, hi);
+    return (hi >> 7) - (lo >> 7) + 1;
+}
+
+// Blocks of the first G token groups of a sequence (G = all of them: the last one may be short).
+__device__ int64_t blocks_before(const Params &p, const PagedSeq &q, int64_t G) {
+    if (G <= 0) return 0;
+    if (G == 1) return group_blocks(p, q, 0);
+    const int64_t base = q.len - q.n, d = p.tpu;
+    int64_t sum = floor_sum(G, base + d - 1, d) + G;
+    if (G * d > q.n) sum += ((int64_t{q.len} - 1) >> 7) - ((base + G * d - 1) >> 7);
+    if (p.window > 0) {
+        const int64_t a = base - p.window + 1;
+        const int64_t g0 = a >= 0 ? 0 : (-a + d - 1) / d;
+        sum -= floor_sum(G - g0, a + g0 * d, d);
+    }
+    return sum;
+}
+
+__device__ __forceinline__ int groups_of(const Params &p, const PagedSeq &q) {
+    return (q.n + p.tpu - 1) / p.tpu;
+}
+
+struct Place {
+    int s, g, part, off;  // sequence, token group, unit of the group, block of the unit
+};
+
+// The place of block r of sequence s's blocks.
+__device__ Place find_block(const Params &p, const PagedSeq &q, int s, int64_t r) {
+    int lo = 0, hi = groups_of(p, q);  // upt * blocks_before(lo) <= r < upt * blocks_before(hi)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.upt * blocks_before(p, q, mid) <= r) lo = mid;
+        else hi = mid;
+    }
+    r -= p.upt * blocks_before(p, q, lo);
+    const int nb = group_blocks(p, q, lo);
+    return Place{s, lo, static_cast<int>(r) / nb, static_cast<int>(r) % nb};
+}
+
+// A run of blocks of one unit.
+struct Segment {
+    int64_t row;       // first row of q / out
+    int nrows;         // rows of the unit, <= 64
+    int s;             // sequence
+    int blk;           // first block (positions 128 blk ..)
+    int nb;            // blocks
+    int posf, posl;    // positions of the unit's first and last token
+    int lo;            // lowest position any of its tokens sees
+    bool whole;        // all of the unit's blocks
+};
+
+// Walks the segments of a CTA's run. Every role walks on its own.
+struct Walk {
+    Place at;
+    PagedSeq q;
+    int left;
+
+    __device__ __forceinline__ Walk(const Params &p, const int *start) {
+        at = Place{start[0], start[1], start[2], start[3]};
+        left = start[4];
+        q.n = 0;
+        if (left > 0) {
+            bool bad;
+            q = paged_seq(p.b, at.s, bad);
+        }
+    }
+
+    __device__ __forceinline__ bool next(const Params &p, Segment &x) {
+        if (left <= 0) return false;
+        while (at.g * p.tpu >= q.n) {
+            if (++at.s >= p.b.n_seqs) return false;
+            at.g = 0;
+            bool bad;
+            q = paged_seq(p.b, at.s, bad);
+        }
+        const int t0 = at.g * p.tpu, t1 = min(t0 + p.tpu, q.n);
+        int hi;
+        key_range(p, q, t0, x.lo, hi);
+        const int blo = x.lo >> 7, nblk = (hi >> 7) - blo + 1;
+        x.s = at.s;
+        x.posf = q.len - q.n + t0;
+        x.posl = hi;
+        x.row = (int64_t{q.row0} + t0) * p.heads + at.part * kRows;
+        x.nrows = p.upt > 1 ? min(kRows, p.heads - at.part * kRows) : (t1 - t0) * p.heads;
+        x.blk = blo + at.off;
+        x.nb = min(nblk - at.off, left);
+        x.whole = x.nb == nblk;
+        left -= x.nb;
+        at.off = 0;
+        if (++at.part == p.upt) {
+            at.part = 0;
+            ++at.g;
+        }
+        return true;
+    }
+};
+
+// Position of row r of a unit.
+__device__ __forceinline__ int row_pos(const Params &p, int posf, int r) {
+    return p.upt > 1 ? posf : posf + r / p.rpt;
+}
+
+// ------------------------------------------------------------------ small helpers
+
+__device__ __forceinline__ float redux_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The softmax warps form two groups of four, one per half of the rows (named barriers 1 and
+// 2, 128 threads each).
+__device__ __forceinline__ bool vote_any_group(bool pred, int hh) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, %2, 128, p;\n"
+        " selp.b32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(pred)), "r"(1 + hh)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void bar_group(int hh) {
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + hh) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, uint64_t *bar, int x,
+                                            int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(tm), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// tcgen05.mma / tcgen05.commit run by every lane of a converged warp but issued only where
+// `issue` is non-zero: the warp stays converged and the descriptors in uniform registers.
+__device__ __forceinline__ void mma_bf16_if(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate, uint32_t issue) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit_if(uint64_t *bar, uint32_t issue) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+            smem_u32(bar)),
+        "r"(issue)
+        : "memory");
+}
+
+__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
+    const uint32_t b = smem_u32(bar);
+    const long long t0 = clock64();
+    while (!mbar_test(b, parity))
+        if (clock64() - t0 > kWaitBudget) break;
+}
+
+// Both bf16 values of a word with infinities and NaN replaced by zero.
+__device__ __forceinline__ uint32_t finite2(uint32_t v) {
+    if ((v & 0x7F800000u) == 0x7F800000u) v &= 0x0000FFFFu;
+    if ((v & 0x00007F80u) == 0x00007F80u) v &= 0xFFFF0000u;
+    return v;
+}
+
+__device__ __forceinline__ uint32_t turn_pair(uint32_t v, float c, float s) {
+    const float x = bf16lo(v), y = bf16hi(v);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(x * c - y * s, x * s + y * c);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// ------------------------------------------------------------------ the kernel
+
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
+                      const __grid_constant__ CUtensorMap tm_kv,
+                      const __grid_constant__ Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *sQ = smem + kOffQ;
+    uint8_t *sKV = smem + kOffKV;
+    uint8_t *sP = smem + kOffP;
+    uint8_t *sX = smem + kOffX;
+    float *sRed = reinterpret_cast<float *>(smem + kOffRed);
+    float *sL = sRed;
+    float *sLinv = reinterpret_cast<float *>(smem + kOffLinv);
+    float *sAlpha = sLinv;
+    float *sM = reinterpret_cast<float *>(smem + kOffM);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBar);
+    uint64_t *q_full = bars + 0;
+    uint64_t *q_free = bars + 1;
+    uint64_t *kv_full = bars + 2;   // [4] chunk pairs 0-2, then chunk 6, landed
+    uint64_t *x_full = bars + 6;    // [2] chunk 7 landed, by block parity (usual / spare slot)
+    uint64_t *s_free = bars + 8;    // [2] S^T buffer read by the softmax, by block parity
+    uint64_t *kv_free = bars + 10;  // [4] chunk pairs 0-2, then chunk 6 (and 7), used by PV
+    uint64_t *s_full = bars + 14;
+    uint64_t *p_full = bars + 15;
+    uint64_t *o_full = bars + 16;
+    uint64_t *o_free = bars + 17;
+    uint64_t *drain = bars + 18;    // [2] one per issuing warp
+    uint64_t *q_turned = bars + 20;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 21);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    volatile uint32_t *sPages = tmem_holder + 2;  // [2] pages of a block that were loaded
+    int *sStart = reinterpret_cast<int *>(tmem_holder + 4);  // [5] start of this CTA's run
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_free, 1);
+        mbar_init(q_turned, kTurnThreads);
+        for (int m = 0; m < 4; ++m) {
+            mbar_init(&kv_full[m], 1);
+            mbar_init(&kv_free[m], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&x_full[i], 1);
+            mbar_init(&s_free[i], 8);  // one arrival per softmax warp
+            mbar_init(&drain[i], 1);
+        }
+        // S^T of a block is ready once its QK is done (QK warp) and the previous block's PV no
+        // longer reads P or writes O^T (PV warp)
+        mbar_init(s_full, 2);
+        mbar_init(p_full, kSoftThreads);
+        mbar_init(o_full, 1);
+        mbar_init(o_free, 8);
+        *abort_flag = 0;
+        sStart[4] = 0;
+        fence_barrier_init();
+    }
+    if (warp == kPvWarp) tmem_alloc(tmem_holder, 512);
+
+    // ---------------- this CTA's run: blocks [T0, T1) of all blocks
+    const int cta = static_cast<int>(blockIdx.x);
+    JoinDesc *desc = reinterpret_cast<JoinDesc *>(p.ws + kWsDesc) + cta;
+    {
+        int64_t *part = reinterpret_cast<int64_t *>(sKV);  // free until the first load
+        const int per = (p.b.n_seqs + kThreads - 1) / kThreads;
+        const int s0 = min(tid * per, p.b.n_seqs), s1 = min(s0 + per, p.b.n_seqs);
+        int64_t mine = 0;
+        for (int s = s0; s < s1; ++s) {
+            bool bad;
+            const PagedSeq q = paged_seq(p.b, s, bad);
+            if (bad && cta == 0) report(p.status, DSA_ERR_BOUNDS);
+            mine += p.upt * blocks_before(p, q, groups_of(p, q));
+        }
+        int64_t incl = mine;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[2 * i] = bf16lo(w[i]);
-        x[2 * i + 1] = bf16hi(w[i]);
+        for (int w = 1; w < 32; w <<= 1) {
+            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, w);
+            if (lane >= w) incl += v;
+        }
+        if (lane == 31) part[warp] = incl;
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        int64_t total = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) incl += part[w];
+            total += part[w];
+        }
+        const int64_t run = (total + gridDim.x - 1) / gridDim.x;
+        const int64_t T0 = run * cta, T1 = min(T0 + run, total);
+        if (T0 < T1) {
+            const int64_t excl = incl - mine;
+            for (int which = 0; which < 2; ++which) {
+                const int64_t at = which ? T1 - 1 : T0;
+                if (at < excl || at >= incl) continue;
+                int64_t acc = excl;
+                for (int s = s0; s < s1; ++s) {
+                    bool bad;
+                    const PagedSeq q = paged_seq(p.b, s, bad);
+                    const int64_t nb = p.upt * blocks_before(p, q, groups_of(p, q));
+                    if (at >= acc + nb) {
+                        acc += nb;
+                        continue;
+                    }
+                    const Place x = find_block(p, q, s, at - acc);
+                    if (which == 0) {
+                        sStart[0] = x.s;
+                        sStart[1] = x.g;
+                        sStart[2] = x.part;
+                        sStart[3] = x.off;
+                        sStart[4] = static_cast<int>(T1 - T0);
+                    } else {
+                        // a unit that begins in this run and ends in a later one
+                        const int64_t u0 = at - x.off, u1 = u0 + group_blocks(p, q, x.g);
+                        JoinDesc d = {};
+                        if (u0 >= T0 && u1 > T1) {
+                            const int t0 = x.g * p.tpu, t1 = min(t0 + p.tpu, q.n);
+                            d.row = (int64_t{q.row0} + t0) * p.heads + x.part * kRows;
+                            d.nrows = p.upt > 1 ? min(kRows, p.heads - x.part * kRows)
+                                                : (t1 - t0) * p.heads;
+                            d.parts = static_cast<int>((u1 - 1) / run) - cta + 1;
+                            d.slot0 = u0 == T0 ? 0 : 1;
+                            d.pos = q.len - q.n + t0;
+                        }
+                        *desc = d;
+                    }
+                    break;
+                }
+            }
+        } else if (tid == 0) {
+            *desc = JoinDesc{};
+        }
+        fence_proxy_async_smem();  // the scratch's tile is next written by TMA
+        __syncthreads();
+    }
+    const uint32_t tmem = *tmem_holder;
+
+    if (warp < kSoftWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
+        if (warp == 0) {
+            // ---------------- loader: the pages of each block, chunk by chunk. Lane i < np
+            // loads page i of the block; its table entry is read one block ahead.
+            const int prows = min(1 << p.b.page_shift, kBlock), np = kBlock / prows;
+            Walk walk(p, sStart);
+            Segment x;
+            int g = 0, m_at = 0;
+            bool ok = true;
+            // table entry of this lane's page in block `blk` of x: -1 when no token needs it
+            auto entry = [&](const Segment &y, int blk) -> int32_t {
+                const int pos = blk * kBlock + lane * prows;
+                if (lane >= np || pos > y.posl || pos <= y.lo - prows) return -1;
+                const int32_t e =
+                    __ldg(p.b.page_table + int64_t{y.s} * p.b.max_pages + (pos >> p.b.page_shift));
+                if (e < 0 || e >= p.b.n_pages) {
+                    report(p.status, DSA_ERR_BOUNDS);
+                    return -1;
+                }
+                return e;
+            };
+            bool have = walk.next(p, x);
+            int32_t e_next = have ? entry(x, x.blk) : -1;
+            while (have && ok) {
+                Segment y;
+                const bool more = walk.next(p, y);
+                for (int b = 0; b < x.nb && ok; ++b, ++g) {
+                    const int32_t e = e_next;
+                    const int par = g & 1;
+                    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, e >= 0);
+                    const uint32_t bytes = static_cast<uint32_t>(__popc(mask)) * prows * 128;
+                    const int y0 =
+                        ((x.blk + b) * kBlock + lane * prows) & ((1 << p.b.page_shift) - 1);
+                    const uint32_t off = lane * prows * 128;
+                    // chunk 7 first, into the slot that the block two back released
+                    if (lane == 0) {
+                        sPages[par] = mask;
+                        mbar_expect_tx(&x_full[par], bytes);
+                    }
+                    __syncwarp();
+                    if (e >= 0)
+                        tma_load_3d((par ? sX : sKV + 7 * 16384) + off, &tm_kv, &x_full[par],
+                                    chunk_dim(7), y0, e);
+                    if (b + 1 < x.nb) e_next = entry(x, x.blk + b + 1);
+                    else e_next = more ? entry(y, y.blk) : -1;
+                    for (int m = 0; m < 4; ++m) {
+                        if (lane == 0)
+                            ok = mbar_wait(&kv_free[m], (g & 1) ^ 1, abort_flag, p.status);
+                        ok = (__ballot_sync(0xFFFFFFFFu, ok) & 1u) != 0;
+                        m_at = m;
+                        if (!ok) break;
+                        if (lane == 0) mbar_expect_tx(&kv_full[m], m < 3 ? 2 * bytes : bytes);
+                        __syncwarp();
+                        if (e >= 0) {
+                            uint8_t *dst = sKV + 2 * m * 16384 + off;
+                            tma_load_3d(dst, &tm_kv, &kv_full[m], chunk_dim(2 * m), y0, e);
+                            if (m < 3)
+                                tma_load_3d(dst + 16384, &tm_kv, &kv_full[m],
+                                            chunk_dim(2 * m + 1), y0, e);
+                        }
+                    }
+                    if (!ok) break;
+                }
+                x = y;
+                have = more;
+            }
+            if (!ok && lane == 0) {
+                // gave up in block g before its chunk group m_at: no copy into this CTA's
+                // shared memory may still be in flight at exit
+                for (int m = 0; m < 4; ++m) {
+                    const int last = m < m_at ? g : g - 1;
+                    if (last >= 0) drain_wait(&kv_full[m], last & 1);
+                }
+                for (int last = g; last >= 0 && last >= g - 1; --last)
+                    drain_wait(&x_full[last & 1], (last >> 1) & 1);
+            }
+            __syncwarp();
+        } else if (warp >= kTurnWarp0 && warp < kTurnWarp0 + kTurnThreads / 32) {
+            // ---------------- the queries' rotation, in place: two threads per row, four
+            // 16-byte pieces (16 pairs) each; the angles are read before the queries land
+            if (p.b.cos_sin) {
+                const int t = tid - 32 * kTurnWarp0, r = t >> 1, half = t & 1;
+                uint8_t *row = sQ + kTurnChunk * 8192 + r * 128;
+                Walk walk(p, sStart);
+                Segment x;
+                for (int i = 0; walk.next(p, x); ++i) {
+                    float4 cs[8];
+                    const bool mine = r < x.nrows;
+                    if (mine) {
+                        const float4 *src =
+                            reinterpret_cast<const float4 *>(
+                                p.b.cos_sin + int64_t{row_pos(p, x.posf, r)} * kRope) +
+                            8 * half;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) cs[k] = __ldg(src + k);
+                    }
+                    if (!mbar_wait(q_full, i & 1, abort_flag, p.status)) break;
+                    if (mine) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint4 *at =
+                                reinterpret_cast<uint4 *>(row + (((4 * half + k) ^ (r & 7)) << 4));
+                            uint4 v = *at;
+                            v.x = turn_pair(v.x, cs[2 * k].x, cs[2 * k].y);
+                            v.y = turn_pair(v.y, cs[2 * k].z, cs[2 * k].w);
+                            v.z = turn_pair(v.z, cs[2 * k + 1].x, cs[2 * k + 1].y);
+                            v.w = turn_pair(v.w, cs[2 * k + 1].z, cs[2 * k + 1].w);
+                            *at = v;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(q_turned);
+                }
+            }
+        } else if (warp == kQkWarp) {
+            // ---------------- QK issuer: S^T = K_blk . Q^T, chunk pair by chunk pair as the
+            // rows land. It loads the unit's queries itself as soon as its own MMAs have read
+            // the previous ones.
+            const uint32_t leader = lane == 0;
+            constexpr uint32_t idesc_qk = idesc_bf16(kBlock, kRows, false, false);
+            const uint64_t ad0 = desc_sw128(smem_u32(sKV), 16, 1024);
+            const uint64_t adx = desc_sw128(smem_u32(sX), 16, 1024);
+            const uint64_t bd0 = desc_sw128(smem_u32(sQ), 16, 1024);
+            const uint64_t pol_stream = policy_evict_first();
+            Walk walk(p, sStart);
+            Segment x;
+            int i = 0, g = 0, last_q = -1;
+            bool ok = true;
+            for (; ok && walk.next(p, x); ++i) {
+                if (!(ok = mbar_wait(q_free, (i & 1) ^ 1, abort_flag, p.status))) break;
+                if (leader) {
+                    mbar_expect_tx(q_full, 65536);
+                    for (int c = 0; c < 8; ++c)
+                        tma_load_2d(sQ + c * 8192, &tm_q, q_full, chunk_dim(c),
+                                    static_cast<int>(x.row), pol_stream);
+                }
+                last_q = i;
+                if (!(ok = mbar_wait(q_full, i & 1, abort_flag, p.status))) break;
+                tc_fence_after();
+                for (int b = 0; b < x.nb && ok; ++b, ++g) {
+                    // S^T is double-buffered: QK of a block may run while the softmax of the
+                    // block before it does
+                    const int par = g & 1;
+                    if (!(ok = mbar_wait(&s_free[par], ((g >> 1) & 1) ^ 1, abort_flag, p.status)))
+                        break;
+                    const uint32_t s_col = tmem + kSCol + 64 * par;
+                    if (!(ok = mbar_wait(&x_full[par], (g >> 1) & 1, abort_flag, p.status))) break;
+                    tc_fence_after();
+                    {
+                        const uint64_t ad = par ? adx : ad0 + ((7 * 16384) >> 4);
+                        const uint64_t bd = bd0 + ((7 * 8192) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_bf16_if(s_col, ad + 2 * kk, bd + 2 * kk, idesc_qk, kk != 0,
+                                        leader);
+                    }
+#pragma unroll 1
+                    for (int m = 0; m < 4; ++m) {
+                        if (!(ok = mbar_wait(&kv_full[m], g & 1, abort_flag, p.status))) break;
+                        if (m == 2 && b == 0 && p.b.cos_sin &&
+                            !(ok = mbar_wait(q_turned, i & 1, abort_flag, p.status)))
+                            break;
+                        tc_fence_after();
+                        const uint64_t ad = ad0 + ((2 * m * 16384) >> 4);
+                        const uint64_t bd = bd0 + ((2 * m * 8192) >> 4);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                if (m < 3 || h == 0)
+                                    mma_bf16_if(s_col, ad + ((h * 16384) >> 4) + 2 * kk,
+                                                bd + ((h * 8192) >> 4) + 2 * kk, idesc_qk, 1u,
+                                                leader);
+                    }
+                    if (!ok) break;
+                    mma_commit_if(s_full, leader);
+                    if (b == x.nb - 1) mma_commit_if(q_free, leader);
+                }
+            }
+            mma_commit_if(&drain[0], leader);
+            if (leader) drain_wait(&drain[0], 0);
+            // no copy into this CTA's shared memory may still be in flight at exit
+            if (leader && last_q >= 0) drain_wait(q_full, last_q & 1);
+            __syncwarp();
+        } else if (warp == kPvWarp) {
+            // ---------------- PV issuer: O^T += V_blk^T . P^T, one d-tile at a time
+            const uint32_t leader = lane == 0;
+            constexpr uint32_t idesc_pv = idesc_bf16(128, kRows, true, true);
+            Walk walk(p, sStart);
+            Segment x;
+            int i = 0, g = 0;
+            bool ok = true;
+            if (leader) mbar_arrive(s_full);  // no PV precedes the first block
+            __syncwarp();
+            for (; ok && walk.next(p, x); ++i) {
+                for (int b = 0; b < x.nb && ok; ++b, ++g) {
+                    if (!(ok = mbar_wait(p_full, g & 1, abort_flag, p.status))) break;
+                    tc_fence_after();
+                    if (b == 0 && i > 0) {
+                        // the epilogue of the previous unit must have read O^T
+                        if (!(ok = mbar_wait(o_free, (i - 1) & 1, abort_flag, p.status))) break;
+                        tc_fence_after();
+                    }
+                    const uint32_t acc0 = b > 0;
+                    const uint32_t lbo3 = (g & 1) ? kLbo7Spare : 16384u;
+                    if (leader) {
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                mma_bf16(tmem + kOCol + 64 * m,
+                                         desc_sw128(smem_u32(sKV + 2 * m * 16384 + kk * 2048),
+                                                    m < 3 ? 16384u : lbo3, 1024),
+                                         desc_sw128(smem_u32(sP + kk * 2048), 8192, 1024),
+                                         idesc_pv, kk > 0 ? 1u : acc0);
+                            mma_commit(&kv_free[m]);
+                        }
+                    }
+                    __syncwarp();
+                    mma_commit_if(s_full, leader);
+                    if (b == x.nb - 1) mma_commit_if(o_full, leader);
+                }
+            }
+            mma_commit_if(&drain[1], leader);
+            if (leader) drain_wait(&drain[1], 0);
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        // ---------------- softmax + epilogue, 8 warps: TMEM lanes of sub-partition sp (keys,
+        // later dims) x rows [32 hh, 32 hh + 32)
+        const int sp = warp & 3;
+        const int hh = (warp - kSoftWarp0) >> 2;
+        const int hb = 32 * hh;
+        const int kl = sp * 32 + lane;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(sp * 32) << 16);
+        const int page_shift = min(p.b.page_shift, 7);
+        const uint32_t all_pages = (1u << (kBlock >> page_shift)) - 1u;
+        Walk walk(p, sStart);
+        Segment x;
+        int i = 0, g = 0, cur = 0;
+        for (; walk.next(p, x); ++i) {
+            float l[32];
+#pragma unroll
+            for (int h = 0; h < 32; ++h) l[h] = 0.0f;
+            if (sp == 0) sM[cur * 64 + hb + lane] = kNoMax;
+            {
+                uint32_t none[32];
+#pragma unroll
+                for (int h = 0; h < 32; ++h) none[h] = __float_as_uint(kNoMax);
+                tmem_st32(lane_base + kMCol + hb, none);
+                tmem_wait_st();
+            }
+            bar_group(hh);
+            for (int b = 0; b < x.nb; ++b, ++g) {
+                const int par = g & 1;
+                const int k0 = (x.blk + b) * kBlock;
+                // S^T of this block is ready and the previous block's PV is done with P and O^T
+                const bool live = mbar_wait(s_full, g & 1, abort_flag, p.status);
+                // (complete since QK of this block waited for it: orders sPages before here)
+                mbar_wait(&x_full[par], (g >> 1) & 1, abort_flag, p.status);
+                tc_fence_after();
+                uint32_t sa[32], mv[32];
+                tmem_ld32(lane_base + kMCol + hb, mv);
+                if (live) tmem_ld32(lane_base + kSCol + 64 * par + hb, sa);
+                const uint32_t pages = sPages[par];
+                tmem_wait_ld();
+                // this S^T buffer may take the QK of the block after next
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_free[par]);
+                // every row sees every key of the block, unless ...
+                if (k0 + kBlock - 1 > x.posf || (p.window > 0 && k0 <= x.posl - p.window) ||
+                    pages != all_pages || !live) {
+                    // rows [ra, rb) of the unit see key k0 + kl: their token is not before it
+                    // and less than `window` after it
+                    const int64_t ahead = int64_t{k0} + kl - x.posf;
+                    const int ta = static_cast<int>(max(int64_t{0}, min(ahead, int64_t{64})));
+                    const int64_t gone = p.window > 0 ? ahead + p.window : 64;
+                    const int tb = static_cast<int>(max(int64_t{0}, min(gone, int64_t{64})));
+                    const int ra = min(64, ta * p.rpt);
+                    int rb = min(64, tb * p.rpt);
+                    if (!((pages >> (kl >> page_shift)) & 1u) || !live) rb = 0;
+                    // A key's S is finite in no row exactly when its row holds an infinity or
+                    // NaN. Where some row must not see the key, such elements become zero in
+                    // the tile, as 0 * inf in PV would reach every row; the rows that see the
+                    // key have a NaN probability already.
+                    bool odd = false;
+                    const int a = max(0, min(32, ra - hb)), e = max(0, min(32, rb - hb));
+                    const uint32_t below_e = e == 32 ? 0xFFFFFFFFu : (1u << e) - 1u;
+                    const uint32_t below_a = a == 32 ? 0xFFFFFFFFu : (1u << a) - 1u;
+                    const uint32_t vis = below_e & ~below_a;
+#pragma unroll
+                    for (int h = 0; h < 32; ++h) {
+                        odd = odd || !(fabsf(__uint_as_float(sa[h])) <= 3.4028234e38f);
+                        if (!((vis >> h) & 1u)) sa[h] = __float_as_uint(-INFINITY);
+                    }
+                    if (odd && live && (ra > 0 || rb < x.nrows)) {
+                        for (int m = 0; m < 4; ++m)
+                            mbar_wait(&kv_full[m], g & 1, abort_flag, p.status);
+                        // four chunks by each of the key's two threads
+#pragma unroll 1
+                        for (int c = 4 * hh; c < 4 * hh + 4; ++c) {
+                            uint4 *at = reinterpret_cast<uint4 *>(
+                                (c == 7 && par ? sX : sKV + c * 16384) + kl * 128);
+#pragma unroll 1
+                            for (int k = 0; k < 8; ++k) {
+                                uint4 v = at[k];
+                                v.x = finite2(v.x);
+                                v.y = finite2(v.y);
+                                v.z = finite2(v.z);
+                                v.w = finite2(v.w);
+                                at[k] = v;
+                            }
+                        }
+                    }
+                }
+                // xv = scale * log2e * logit - running maximum: decides the rescale, feeds exp2
+                float xv[32];
+                float xmax;
+                {
+#pragma unroll
+                    for (int h = 0; h < 32; ++h)
+                        xv[h] = fmaf(__uint_as_float(sa[h]), p.c, -__uint_as_float(mv[h]));
+                    float t16[16];
+#pragma unroll
+                    for (int h = 0; h < 16; ++h) t16[h] = fmaxf(xv[h], xv[h + 16]);
+#pragma unroll
+                    for (int w = 8; w >= 1; w >>= 1)
+#pragma unroll
+                        for (int h = 0; h < w; ++h) t16[h] = fmaxf(t16[h], t16[h + w]);
+                    xmax = t16[0];
+                }
+                if (vote_any_group(xmax > kRescale, hh)) {
+                    // exact block maxima -> new running maximum; sums and O^T rescaled
+#pragma unroll
+                    for (int h = 0; h < 32; ++h) {
+                        const float wm = redux_max(__uint_as_float(sa[h]) * p.c);
+                        if (lane == h) sRed[sp * 64 + hb + h] = wm;
+                    }
+                    bar_group(hh);
+                    if (sp == 0) {
+                        const int r = hb + lane;
+                        const float bm = fmaxf(fmaxf(sRed[r], sRed[64 + r]),
+                                               fmaxf(sRed[128 + r], sRed[192 + r]));
+                        const float m_old = sM[cur * 64 + r];
+                        const float m_new = fmaxf(m_old, bm);
+                        sM[(cur ^ 1) * 64 + r] = m_new;
+                        sAlpha[r] = ex2(m_old - m_new);
+                    }
+                    bar_group(hh);
+                    cur ^= 1;
+                    const float *m_now = sM + cur * 64 + hb;
+#pragma unroll
+                    for (int h = 0; h < 32; ++h) {
+                        mv[h] = __float_as_uint(m_now[h]);
+                        l[h] *= sAlpha[hb + h];
+                        xv[h] = fmaf(__uint_as_float(sa[h]), p.c, -m_now[h]);
+                    }
+                    tmem_st32(lane_base + kMCol + hb, mv);
+                    tmem_wait_st();
+                    if (b > 0 && live) {
+#pragma unroll 1
+                        for (int m = 0; m < 4; ++m) {
+                            uint32_t oa[32];
+                            const uint32_t col = lane_base + kOCol + 64 * m + hb;
+                            tmem_ld32(col, oa);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int h = 0; h < 32; ++h)
+                                oa[h] = __float_as_uint(__uint_as_float(oa[h]) * sAlpha[hb + h]);
+                            tmem_st32(col, oa);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                // this thread's 32 rows of P^T for key kl: four swizzled 16-byte pieces. The
+                // sums take P as rounded to bf16, the values that PV multiplies.
+                {
+                    uint8_t *prow = sP + kl * 128;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(
+                                ex2(xv[8 * q + 2 * e]), ex2(xv[8 * q + 2 * e + 1]));
+                            pk[e] = *reinterpret_cast<const uint32_t *>(&v);
+                            l[8 * q + 2 * e] += bf16lo(pk[e]);
+                            l[8 * q + 2 * e + 1] += bf16hi(pk[e]);
+                        }
+                        *reinterpret_cast<uint4 *>(prow + (((4 * hh + q) ^ (kl & 7)) << 4)) =
+                            make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                mbar_arrive(p_full);
+            }
+            // ---- end of the segment: sums over the keys. Transpose-reduce the 32 partial
+            // sums across the warp: lane ends with the warp's total for row hb + lane
+#pragma unroll
+            for (int w = 16; w >= 1; w >>= 1) {
+                const bool up = (lane & w) != 0;
+#pragma unroll
+                for (int h = 0; h < w; ++h) {
+                    const float send = up ? l[h] : l[h + w];
+                    const float keep = up ? l[h + w] : l[h];
+                    l[h] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, w);
+                }
+            }
+            sL[sp * 64 + hb + lane] = l[0];
+            bar_group(hh);
+            const int slot = 2 * cta + (i > 0);
+            if (sp == 0) {
+                // (each half's own warp: `cur` goes by the half)
+                const int r = hb + lane;
+                const float tot = sL[r] + sL[64 + r] + sL[128 + r] + sL[192 + r];
+                // a row that saw no key has sum 0 and O 0
+                sLinv[r] = tot == 0.0f ? 0.0f : 1.0f / tot;
+                if (!x.whole)
+                    reinterpret_cast<float2 *>(p.ws + kWsMl)[slot * kRows + r] =
+                        make_float2(sM[cur * 64 + r], tot);
+            }
+            bar_group(hh);
+            // O^T into registers one d-tile at a time: lane holds dim 128 m' + 32 sp + lane of
+            // rows hb .. hb + 31, so a warp writes 32 consecutive dims of each row
+            const bool live = mbar_wait(o_full, i & 1, abort_flag, p.status);
+            tc_fence_after();
+            const int rows = min(32, x.nrows - hb);
+            if (x.whole) {
+                __nv_bfloat16 *orow = p.out + (x.row + hb) * kD + 32 * sp + lane;
+                float linv[32];
+#pragma unroll
+                for (int h = 0; h < 32; h += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(&sLinv[hb + h]);
+                    linv[h] = v.x;
+                    linv[h + 1] = v.y;
+                    linv[h + 2] = v.z;
+                    linv[h + 3] = v.w;
+                }
+#pragma unroll 1
+                for (int m = 0; m < 4; ++m) {
+                    uint32_t oa[32];
+                    if (!live) break;
+                    tmem_ld32(lane_base + kOCol + 64 * m + hb, oa);
+                    tmem_wait_ld();
+                    __nv_bfloat16 *o = orow + chunk_dim(2 * m);
+                    if (p.b.cos_sin && m == kTurnChunk / 2 && sp >= 2) {
+                        // turned back by the token's position; a pair is in two adjacent lanes
+                        const float2 *cs = reinterpret_cast<const float2 *>(p.b.cos_sin) +
+                                           ((sp - 2) * 16 + (lane >> 1));
+                        float2 a = make_float2(1.0f, 0.0f);
+                        int at = -1;
+#pragma unroll
+                        for (int h = 0; h < 32; ++h) {
+                            const float v = __uint_as_float(oa[h]) * linv[h];
+                            const float w = __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+                            if (h < rows) {
+                                const int pos = row_pos(p, x.posf, hb + h);
+                                if (pos != at) {
+                                    a = __ldg(cs + int64_t{pos} * kRopePairs);
+                                    at = pos;
+                                }
+                                o[h * kD] = __float2bfloat16_rn(v * a.x + (lane & 1 ? -w : w) * a.y);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 32; ++h)
+                            if (h < rows)
+                                o[h * kD] =
+                                    __float2bfloat16_rn(__uint_as_float(oa[h]) * linv[h]);
+                    }
+                }
+            } else {
+                float *orow = reinterpret_cast<float *>(p.ws + kWsO) +
+                              (int64_t{slot} * kRows + hb) * kD + 32 * sp + lane;
+#pragma unroll 1
+                for (int m = 0; m < 4; ++m) {
+                    uint32_t oa[32];
+                    if (!live) break;
+                    tmem_ld32(lane_base + kOCol + 64 * m + hb, oa);
+                    tmem_wait_ld();
+                    float *o = orow + chunk_dim(2 * m);
+#pragma unroll
+                    for (int h = 0; h < 32; ++h)
+                        if (h < rows) o[h * kD] = __uint_as_float(oa[h]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free);
+        }
+    }
+    __syncthreads();
+    if (warp == kPvWarp) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
     }
 }
 
-// grid.x: sequences, grid.y: token stride; the warps of a block share a token's heads.
-__global__ void __launch_bounds__(256)
-    paged_attn_kernel(const PagedBatch b, const uint4 *__restrict__ q, const uint4 *pages,
-                      int heads, int window, float c, uint4 *out, int32_t *status) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int s = blockIdx.x;
-    bool bad;
-    const PagedSeq sq = paged_seq(b, s, bad);
-    if (bad && blockIdx.y == 0 && threadIdx.x == 0) report(status, DSA_ERR_BOUNDS);
-    const int32_t *table = b.page_table + int64_t{s} * b.max_pages;
-    const int64_t units = int64_t{sq.n} * heads;
-    for (int64_t u = int64_t{blockIdx.y} * 8 + warp; u < units; u += int64_t{gridDim.y} * 8) {
-        const int i = static_cast<int>(u / heads);
-        const int32_t t = sq.len - sq.n + i;
-        const int64_t row = int64_t{sq.row0} * heads + u;
-        float x[16], o[16];
-        unpack16(q[row * 64 + 2 * lane], q[row * 64 + 2 * lane + 1], x);
-        const float *cs = b.cos_sin ? b.cos_sin + int64_t{t} * kRope + (lane - 28) * 16 : nullptr;
-        const bool turn = cs && lane >= 28;
-        if (turn) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float a = x[2 * e], d = x[2 * e + 1];
-                x[2 * e] = a * cs[2 * e] - d * cs[2 * e + 1];
-                x[2 * e + 1] = a * cs[2 * e + 1] + d * cs[2 * e];
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = 0.0f;
-        float m = -INFINITY, l = 0.0f;
-        for (int32_t k = window > 0 ? max(0, t - window + 1) : 0; k <= t; ++k) {
-            const int32_t page = __ldg(table + (k >> b.page_shift));
-            if (page < 0 || page >= b.n_pages) {
-                if (lane == 0) report(status, DSA_ERR_BOUNDS);
-                continue;
-            }
-            const uint4 *src = pages + page * (b.page_stride / 8) +
-                               int64_t{k & ((1 << b.page_shift) - 1)} * 64 + 2 * lane;
-            float v[16];
-            unpack16(src[0], src[1], v);
-            float dot = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) dot = fmaf(x[e], v[e], dot);
-#pragma unroll
-            for (int w = 16; w >= 1; w >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, w);
-            dot *= c;
-            const float mn = fmaxf(m, dot);
-            const float a = m == mn ? 1.0f : exp2f(m - mn), p = exp2f(dot - mn);
-            m = mn;
-            l = l * a + p;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = fmaf(p, v[e], o[e] * a);
-        }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] *= inv;
-        if (turn) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float a = o[2 * e], d = o[2 * e + 1];
-                o[2 * e] = a * cs[2 * e] + d * cs[2 * e + 1];
-                o[2 * e + 1] = d * cs[2 * e] - a * cs[2 * e + 1];
-            }
-        }
-        uint32_t w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const __nv_bfloat162 r = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
-            w[e] = *reinterpret_cast<const uint32_t *>(&r);
-        }
-        out[row * 64 + 2 * lane] = make_uint4(w[0], w[1], w[2], w[3]);
-        out[row * 64 + 2 * lane + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+// ------------------------------------------------------------------ the join
+
+// out[row] = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M), M = max_p m_p, over the parts of a
+// unit: one row at a time per CTA, its parts shared by four groups of 128 threads (four dims
+// each). The parts are added in the same order every time.
+constexpr int kJoinThreads = 512;
+
+__global__ void __launch_bounds__(kJoinThreads)
+    paged_join_kernel(const Params p, int ctas) {
+    __shared__ int active[kMaxCtas];
+    __shared__ int count[kJoinThreads / 32];
+    __shared__ float weight[kMaxCtas];
+    __shared__ float red[2][kJoinThreads / 32];
+    __shared__ float4 sum[3][128];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const JoinDesc *desc = reinterpret_cast<const JoinDesc *>(p.ws + kWsDesc);
+    const bool has = tid < ctas && desc[tid].parts > 0;
+    const uint32_t vote = __ballot_sync(0xFFFFFFFFu, has);
+    if (lane == 0) count[warp] = __popc(vote);
+    __syncthreads();
+    int before = 0, n = 0;
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+        if (w < warp) before += count[w];
+        n += count[w];
     }
+    if (has) active[before + __popc(vote & ((1u << lane) - 1u))] = tid;
+    __syncthreads();
+    for (int it = blockIdx.x; it < n * kRows; it += gridDim.x) {
+        const int cta = active[it / kRows], r = it % kRows;
+        const JoinDesc d = desc[cta];
+        if (r >= d.nrows) continue;
+        auto slot_of = [&](int k) { return k == 0 ? 2 * cta + d.slot0 : 2 * (cta + k); };
+        float2 ml = make_float2(kNoMax, 0.0f);
+        if (tid < d.parts)
+            ml = reinterpret_cast<const float2 *>(p.ws + kWsMl)[slot_of(tid) * kRows + r];
+        const float wm = redux_max(ml.x);
+        if (lane == 0) red[0][warp] = wm;
+        __syncthreads();
+        float M = red[0][0];
+        for (int w = 1; w < kJoinThreads / 32; ++w) M = fmaxf(M, red[0][w]);
+        const float wt = tid < d.parts ? ex2(ml.x - M) : 0.0f;
+        if (tid < d.parts) weight[tid] = wt;
+        float ls = tid < d.parts ? ml.y * wt : 0.0f;
+#pragma unroll
+        for (int w = 16; w >= 1; w >>= 1) ls += __shfl_xor_sync(0xFFFFFFFFu, ls, w);
+        if (lane == 0) red[1][warp] = ls;
+        __syncthreads();
+        const int grp = tid >> 7, t = tid & 127;
+        const float4 *src = reinterpret_cast<const float4 *>(p.ws + kWsO) + r * (kD / 4) + t;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int k = grp; k < d.parts; k += 4) {
+            const float4 v = src[int64_t{slot_of(k)} * kRows * (kD / 4)];
+            const float w = weight[k];
+            acc.x = fmaf(v.x, w, acc.x);
+            acc.y = fmaf(v.y, w, acc.y);
+            acc.z = fmaf(v.z, w, acc.z);
+            acc.w = fmaf(v.w, w, acc.w);
+        }
+        if (grp > 0) sum[grp - 1][t] = acc;
+        __syncthreads();
+        if (grp == 0) {
+            for (int k = 0; k < 3; ++k) {
+                const float4 v = sum[k][t];
+                acc.x += v.x;
+                acc.y += v.y;
+                acc.z += v.z;
+                acc.w += v.w;
+            }
+            float tot = 0.0f;
+            for (int w = 0; w < kJoinThreads / 32; ++w) tot += red[1][w];
+            const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
+            acc.x *= inv;
+            acc.y *= inv;
+            acc.z *= inv;
+            acc.w *= inv;
+            if (p.b.cos_sin && t >= (kD - kRope) / 4) {
+                const float4 a = __ldg(reinterpret_cast<const float4 *>(
+                                           p.b.cos_sin + int64_t{row_pos(p, d.pos, r)} * kRope) +
+                                       (t - (kD - kRope) / 4));
+                acc = make_float4(acc.x * a.x + acc.y * a.y, acc.y * a.x - acc.x * a.y,
+                                  acc.z * a.z + acc.w * a.w, acc.w * a.z - acc.z * a.w);
+            }
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z, acc.w);
+            *reinterpret_cast<uint2 *>(p.out + (d.row + r) * kD + 4 * t) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                           *reinterpret_cast<const uint32_t *>(&hi));
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+struct Setup {
+    bool done = false;
+    int rc = DSA_OK;
+    int sms = 0;
+};
+std::mutex g_mu;
+Setup g_setup[kMaxDevices];
+
+// Per-device one-time set-up: the raised shared-memory limit and the register split's check.
+int setup(int *sms) {
+    const int dev = current_device();
+    if (dev < 0) return DSA_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_mu);
+    Setup &st = g_setup[dev];
+    if (!st.done) {
+        cudaFuncAttributes fa;
+        st.sms = sm_count();
+        st.rc = st.sms > 0 && cudaFuncGetAttributes(&fa, paged_attn_kernel) == cudaSuccess &&
+                        fa.numRegs == kRegsLaunch &&
+                        cudaFuncSetAttribute(paged_attn_kernel,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kSmem) == cudaSuccess
+                    ? DSA_OK
+                    : DSA_ERR_CUDA;
+        st.done = true;
+    }
+    *sms = st.sms;
+    return st.rc;
 }
 
 }  // namespace
@@ -112,9 +1116,9 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
     if (!q || !out || !aligned16(q) || !aligned16(out) ||
         (reinterpret_cast<uintptr_t>(dev_status) & 3u) != 0)
         return DSA_ERR_ARG;
-    PagedBatch b;
+    Params p;
     int rc = check_paged_batch(n_new, new_start, seq_len, n_seqs, page_table, max_pages, pages,
-                               n_pages, page_stride, page_size, cos_sin, n_pos, &b);
+                               n_pages, page_stride, page_size, cos_sin, n_pos, &p.b);
     if (rc != DSA_OK) return rc;
     if (heads < 1 || heads > DSA_MAX_PAGED_HEADS || window < 0 || !(scale > 0.0f) ||
         isinf(scale) || n_new * heads > (int64_t{1} << 31) - 1)
@@ -124,10 +1128,27 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
     if (qa < oa + bytes && oa < qa + bytes) return DSA_ERR_ARG;
     if (!workspace || !aligned16(workspace) || workspace_bytes < DSA_PAGED_WORKSPACE_BYTES)
         return DSA_ERR_SCRATCH;
-    const unsigned gy = static_cast<unsigned>(
-        std::min<int64_t>((n_new * heads + 7) / 8, std::max(1, 4864 / n_seqs)));
-    paged_attn_kernel<<<dim3(n_seqs, gy), 256, 0, static_cast<cudaStream_t>(stream)>>>(
-        b, static_cast<const uint4 *>(q), static_cast<const uint4 *>(pages), heads, window,
-        scale * 1.4426950408889634f, static_cast<uint4 *>(out), dev_status);
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.ws = static_cast<uint8_t *>(workspace);
+    p.heads = heads;
+    p.tpu = heads <= kRows ? kRows / heads : 1;
+    p.upt = (heads + kRows - 1) / kRows;
+    p.rpt = std::min<int32_t>(heads, kRows);
+    // a window no shorter than any sequence is no window
+    p.window = window >= p.b.len_limit ? 0 : window;
+    p.c = scale * 1.4426950408889634f;
+    p.status = dev_status;
+    int sms = 0;
+    rc = setup(&sms);
+    if (rc != DSA_OK) return rc;
+    CUtensorMap tm_q, tm_kv;
+    if (!make_tmap_bf16(&tm_q, q, kD, static_cast<uint64_t>(n_new) * heads, kD * 2, 64, kRows) ||
+        !make_tmap_pages(&tm_kv, pages, p.b))
+        return DSA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int ctas = std::min(sms, kMaxCtas);
+    paged_attn_kernel<<<ctas, kThreads, kSmem, s>>>(tm_q, tm_kv, p);
+    if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
+    paged_join_kernel<<<2 * ctas, kJoinThreads, 0, s>>>(p, ctas);
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }

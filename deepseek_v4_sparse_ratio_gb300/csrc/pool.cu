@@ -24,6 +24,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "paged.h"
 
 namespace dsa {
 
@@ -289,8 +290,7 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 }  // namespace
 
-bool make_tmap_bf16(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,
-                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, bool swizzle128) {
+static PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
     std::call_once(g_encode_once, [] {
         void *fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -299,7 +299,12 @@ bool make_tmap_bf16(CUtensorMap *map, const void *base, uint64_t inner, uint64_t
             q == cudaDriverEntryPointSuccess)
             g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     });
-    if (!g_encode) return false;
+    return g_encode;
+}
+
+bool make_tmap_bf16(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,
+                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, bool swizzle128) {
+    if (!tmap_encoder()) return false;
     cuuint64_t dims[2] = {inner, rows};
     cuuint64_t strides[1] = {row_bytes};
     cuuint32_t box[2] = {box_inner, box_rows};
@@ -308,6 +313,22 @@ bool make_tmap_bf16(CUtensorMap *map, const void *base, uint64_t inner, uint64_t
                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+// The pages as [n_pages][page_size][512]; a box is 64 dims of one page, or of 128 rows of a
+// longer one, with the 128-byte swizzle.
+bool make_tmap_pages(CUtensorMap *map, const void *pages, const PagedBatch &b) {
+    if (!tmap_encoder()) return false;
+    const cuuint64_t rows = cuuint64_t{1} << b.page_shift;
+    cuuint64_t dims[3] = {kD, rows, static_cast<cuuint64_t>(b.n_pages)};
+    cuuint64_t strides[2] = {kD * 2, static_cast<cuuint64_t>(b.page_stride) * 2};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows < 128 ? rows : 128), 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(pages),
+                          dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }

@@ -145,6 +145,10 @@ ATTN = [  # (sequences (new, total), heads, page, window, rope, padded rows)
     ([(64, 64), (1, 4096)], 7, 128, 5000, True, 0),
     ([(1, 30 + 7 * i) for i in range(200)], 4, 16, 0, True, 3),
     ([(150, 700)], 64, 64, 0, True, 0),
+    # many short units per SM, cut where a run ends
+    ([(700, 900), (1, 33), (350, 350)], 16, 32, 100, True, 1),
+    ([(600, 2000)], 64, 64, 128, True, 0),
+    ([(900, 1200)], 8, 16, 0, True, 0),
 ]
 
 
@@ -178,6 +182,23 @@ def test_attention_rising_logits_rescale_every_block(dsa, workspace):
             batch["pages"][e, r] = (d * (0.2 + p / 400.0)
                                     + 0.1 * batch["pages"][e, r].float()).bfloat16()
     q = (d[None, None] + 0.1 * queries(batch, 64, 3).float()).bfloat16()
+    out = run_attn(batch, q, 0, workspace)
+    check_attn(out, batch, q, 0)
+
+
+@pytest.mark.parametrize("half", [0, 1])
+def test_one_half_of_the_rows_rescales_alone(dsa, workspace, half):
+    """Logits rise block by block for half of the heads only, in a unit cut into parts of
+    several blocks: each half keeps its own running maximum."""
+    batch = R.make([(1, 40000)], 64, rope=False, seed=19)
+    d = torch.randn(512, generator=torch.Generator().manual_seed(2))
+    at = torch.tensor([R.place(batch, 0, p) for p in range(40000)])
+    rise = torch.arange(40000)[:, None] / 10000.0
+    rows = batch["pages"][at[:, 0], at[:, 1]].float() * 0.2 + d * rise
+    batch["pages"][at[:, 0], at[:, 1]] = rows.bfloat16()
+    q = queries(batch, 64, 16).float() * 0.05
+    q[:, 32 * half:32 * half + 32] += d
+    q = q.bfloat16()
     out = run_attn(batch, q, 0, workspace)
     check_attn(out, batch, q, 0)
 
