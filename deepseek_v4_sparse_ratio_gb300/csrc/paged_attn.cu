@@ -34,11 +34,13 @@
 #include <mutex>
 
 #include "common.cuh"
-#include "paged.h"
+#include "paged_walk.cuh"
 
 namespace dsa {
 
 namespace {
+
+using namespace paged;
 
 // Warpgroups 0-1 (80 registers a thread): the loader warp 0, warps 1-4 that turn the queries,
 // the QK-issuing warp 6 and the PV-issuing warp 7 (two issuing warps: a thread that waits
@@ -49,14 +51,12 @@ constexpr int kTurnThreads = 128;
 constexpr int kQkWarp = 6;
 constexpr int kPvWarp = 7;
 constexpr int kSoftWarp0 = 8;
-constexpr int kThreads = 512;
 constexpr int kRegsLaunch = 128;
 constexpr int kRegsLow = 80;
 constexpr int kRegsSoft = 176;
 constexpr int kSoftThreads = 256;
 
 constexpr int kRows = 64;     // rows of q in a unit (MMA N)
-constexpr int kBlock = 128;   // keys in a block (MMA M)
 constexpr int kTurnChunk = 5; // the chunk that holds dims 448..511
 
 __host__ __device__ constexpr int chunk_dim(int c) { return ((c + 2) & 7) * 64; }
@@ -79,194 +79,6 @@ constexpr uint32_t kSCol = 0;    // S^T, 2 x 64, by block parity
 constexpr uint32_t kMCol = 128;  // the running maximum of each row, the same in all lanes
 constexpr uint32_t kOCol = 256;  // O^T: 4 d-tiles x 64
 
-constexpr float kRescale = 8.0f;      // log2 units the running maximum may lag behind
-constexpr float kNoMax = -1.0e30f;    // running maximum of a row that has seen no key: finite,
-                                      // so that (masked) -inf minus it stays -inf
-
-// workspace: descriptors, (maximum, sum) of every part, the parts' O
-constexpr int kMaxCtas = 152;
-constexpr size_t kWsDesc = 0;
-constexpr size_t kWsMl = 8192;
-constexpr size_t kWsO = kWsMl + size_t{2 * kMaxCtas} * kRows * 2 * sizeof(float);
-static_assert(kWsO + size_t{2 * kMaxCtas} * kRows * kD * sizeof(float) <= DSA_PAGED_WORKSPACE_BYTES,
-              "over the workspace");
-
-// A unit that begins in a CTA's run and ends in a later one, for the join.
-struct JoinDesc {
-    int64_t row;      // first row of q / out
-    int32_t nrows;
-    int32_t parts;    // 0: none
-    int32_t slot0;    // slot of the first part (the others are slot 0 of the next CTAs)
-    int32_t pos;      // position of the unit's first token
-    int32_t pad[2];
-};
-static_assert(sizeof(JoinDesc) == 32 && kMaxCtas * sizeof(JoinDesc) <= kWsMl, "descriptors");
-
-struct Params {
-    PagedBatch b;
-    __nv_bfloat16 *out;
-    uint8_t *ws;
-    int32_t heads;
-    int32_t tpu;      // tokens of a unit
-    int32_t upt;      // units of a token
-    int32_t rpt;      // rows of a token in a unit
-    int32_t window;   // 0: the whole context
-    float c;          // scale * log2(e)
-    int32_t *status;
-};
-
-// ------------------------------------------------------------------ the list of units
-
-// sum_{i < n} floor((a + d i) / 128) for a, d >= 0 (the Euclid-like reduction of such sums).
-__device__ int64_t floor_sum(int64_t n, int64_t a, int64_t d) {
-    int64_t m = kBlock, ans = 0;
-    while (n > 0) {
-        if (d >= m) {
-            ans += (n - 1) * n / 2 * (d / m);
-            d %= m;
-        }
-        if (a >= m) {
-            ans += n * (a / m);
-            a %= m;
-        }
-        const int64_t y = d * n + a;
-        if (y < m) break;
-        n = y / m;
-        a = y % m;
-        const int64_t t = m;
-        m = d;
-        d = t;
-    }
-    return ans;
-}
-
-// Keys of the tokens [t0, t1) of a sequence: positions lo .. hi, blocks lo / 128 .. hi / 128.
-__device__ __forceinline__ void key_range(const Params &p, const PagedSeq &q, int t0, int &lo,
-                                          int &hi) {
-    const int first = q.len - q.n + t0;
-    lo = p.window > 0 ? max(0, first - p.window + 1) : 0;
-    hi = q.len - q.n + min(t0 + p.tpu, q.n) - 1;
-}
-
-__device__ __forceinline__ int group_blocks(const Params &p, const PagedSeq &q, int g) {
-    int lo, hi;
-    key_range(p, q, g * p.tpu, lo, hi);
-    return (hi >> 7) - (lo >> 7) + 1;
-}
-
-// Blocks of the first G token groups of a sequence (G = all of them: the last one may be short).
-__device__ int64_t blocks_before(const Params &p, const PagedSeq &q, int64_t G) {
-    if (G <= 0) return 0;
-    if (G == 1) return group_blocks(p, q, 0);
-    const int64_t base = q.len - q.n, d = p.tpu;
-    int64_t sum = floor_sum(G, base + d - 1, d) + G;
-    if (G * d > q.n) sum += ((int64_t{q.len} - 1) >> 7) - ((base + G * d - 1) >> 7);
-    if (p.window > 0) {
-        const int64_t a = base - p.window + 1;
-        const int64_t g0 = a >= 0 ? 0 : (-a + d - 1) / d;
-        sum -= floor_sum(G - g0, a + g0 * d, d);
-    }
-    return sum;
-}
-
-__device__ __forceinline__ int groups_of(const Params &p, const PagedSeq &q) {
-    return (q.n + p.tpu - 1) / p.tpu;
-}
-
-struct Place {
-    int s, g, part, off;  // sequence, token group, unit of the group, block of the unit
-};
-
-// The place of block r of sequence s's blocks.
-__device__ Place find_block(const Params &p, const PagedSeq &q, int s, int64_t r) {
-    int lo = 0, hi = groups_of(p, q);  // upt * blocks_before(lo) <= r < upt * blocks_before(hi)
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.upt * blocks_before(p, q, mid) <= r) lo = mid;
-        else hi = mid;
-    }
-    r -= p.upt * blocks_before(p, q, lo);
-    const int nb = group_blocks(p, q, lo);
-    return Place{s, lo, static_cast<int>(r) / nb, static_cast<int>(r) % nb};
-}
-
-// A run of blocks of one unit.
-struct Segment {
-    int64_t row;       // first row of q / out
-    int nrows;         // rows of the unit, <= 64
-    int s;             // sequence
-    int blk;           // first block (positions 128 blk ..)
-    int nb;            // blocks
-    int posf, posl;    // positions of the unit's first and last token
-    int lo;            // lowest position any of its tokens sees
-    bool whole;        // all of the unit's blocks
-};
-
-// Walks the segments of a CTA's run. Every role walks on its own.
-struct Walk {
-    Place at;
-    PagedSeq q;
-    int left;
-
-    __device__ __forceinline__ Walk(const Params &p, const int *start) {
-        at = Place{start[0], start[1], start[2], start[3]};
-        left = start[4];
-        q.n = 0;
-        if (left > 0) {
-            bool bad;
-            q = paged_seq(p.b, at.s, bad);
-        }
-    }
-
-    __device__ __forceinline__ bool next(const Params &p, Segment &x) {
-        if (left <= 0) return false;
-        while (at.g * p.tpu >= q.n) {
-            if (++at.s >= p.b.n_seqs) return false;
-            at.g = 0;
-            bool bad;
-            q = paged_seq(p.b, at.s, bad);
-        }
-        const int t0 = at.g * p.tpu, t1 = min(t0 + p.tpu, q.n);
-        int hi;
-        key_range(p, q, t0, x.lo, hi);
-        const int blo = x.lo >> 7, nblk = (hi >> 7) - blo + 1;
-        x.s = at.s;
-        x.posf = q.len - q.n + t0;
-        x.posl = hi;
-        x.row = (int64_t{q.row0} + t0) * p.heads + at.part * kRows;
-        x.nrows = p.upt > 1 ? min(kRows, p.heads - at.part * kRows) : (t1 - t0) * p.heads;
-        x.blk = blo + at.off;
-        x.nb = min(nblk - at.off, left);
-        x.whole = x.nb == nblk;
-        left -= x.nb;
-        at.off = 0;
-        if (++at.part == p.upt) {
-            at.part = 0;
-            ++at.g;
-        }
-        return true;
-    }
-};
-
-// Position of row r of a unit.
-__device__ __forceinline__ int row_pos(const Params &p, int posf, int r) {
-    return p.upt > 1 ? posf : posf + r / p.rpt;
-}
-
-// ------------------------------------------------------------------ small helpers
-
-__device__ __forceinline__ float redux_max(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // The softmax warps form two groups of four, one per half of the rows (named barriers 1 and
 // 2, 128 threads each).
 __device__ __forceinline__ bool vote_any_group(bool pred, int hh) {
@@ -282,55 +94,6 @@ __device__ __forceinline__ bool vote_any_group(bool pred, int hh) {
 
 __device__ __forceinline__ void bar_group(int hh) {
     asm volatile("bar.sync %0, 128;" ::"r"(1 + hh) : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, uint64_t *bar, int x,
-                                            int y, int z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-        "l"(tm), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-
-// tcgen05.mma / tcgen05.commit run by every lane of a converged warp but issued only where
-// `issue` is non-zero: the warp stays converged and the descriptors in uniform registers.
-__device__ __forceinline__ void mma_bf16_if(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate, uint32_t issue) {
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
-        : "memory");
-}
-
-__device__ __forceinline__ void mma_commit_if(uint64_t *bar, uint32_t issue) {
-    asm volatile(
-        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
-            smem_u32(bar)),
-        "r"(issue)
-        : "memory");
-}
-
-__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
-    const uint32_t b = smem_u32(bar);
-    const long long t0 = clock64();
-    while (!mbar_test(b, parity))
-        if (clock64() - t0 > kWaitBudget) break;
-}
-
-// Both bf16 values of a word with infinities and NaN replaced by zero.
-__device__ __forceinline__ uint32_t finite2(uint32_t v) {
-    if ((v & 0x7F800000u) == 0x7F800000u) v &= 0x0000FFFFu;
-    if ((v & 0x00007F80u) == 0x00007F80u) v &= 0xFFFF0000u;
-    return v;
-}
-
-__device__ __forceinline__ uint32_t turn_pair(uint32_t v, float c, float s) {
-    const float x = bf16lo(v), y = bf16hi(v);
-    const __nv_bfloat162 r = __floats2bfloat162_rn(x * c - y * s, x * s + y * c);
-    return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -395,82 +158,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == kPvWarp) tmem_alloc(tmem_holder, 512);
 
-    // ---------------- this CTA's run: blocks [T0, T1) of all blocks
     const int cta = static_cast<int>(blockIdx.x);
-    JoinDesc *desc = reinterpret_cast<JoinDesc *>(p.ws + kWsDesc) + cta;
-    {
-        int64_t *part = reinterpret_cast<int64_t *>(sKV);  // free until the first load
-        const int per = (p.b.n_seqs + kThreads - 1) / kThreads;
-        const int s0 = min(tid * per, p.b.n_seqs), s1 = min(s0 + per, p.b.n_seqs);
-        int64_t mine = 0;
-        for (int s = s0; s < s1; ++s) {
-            bool bad;
-            const PagedSeq q = paged_seq(p.b, s, bad);
-            if (bad && cta == 0) report(p.status, DSA_ERR_BOUNDS);
-            mine += p.upt * blocks_before(p, q, groups_of(p, q));
-        }
-        int64_t incl = mine;
-#pragma unroll
-        for (int w = 1; w < 32; w <<= 1) {
-            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, w);
-            if (lane >= w) incl += v;
-        }
-        if (lane == 31) part[warp] = incl;
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        int64_t total = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) incl += part[w];
-            total += part[w];
-        }
-        const int64_t run = (total + gridDim.x - 1) / gridDim.x;
-        const int64_t T0 = run * cta, T1 = min(T0 + run, total);
-        if (T0 < T1) {
-            const int64_t excl = incl - mine;
-            for (int which = 0; which < 2; ++which) {
-                const int64_t at = which ? T1 - 1 : T0;
-                if (at < excl || at >= incl) continue;
-                int64_t acc = excl;
-                for (int s = s0; s < s1; ++s) {
-                    bool bad;
-                    const PagedSeq q = paged_seq(p.b, s, bad);
-                    const int64_t nb = p.upt * blocks_before(p, q, groups_of(p, q));
-                    if (at >= acc + nb) {
-                        acc += nb;
-                        continue;
-                    }
-                    const Place x = find_block(p, q, s, at - acc);
-                    if (which == 0) {
-                        sStart[0] = x.s;
-                        sStart[1] = x.g;
-                        sStart[2] = x.part;
-                        sStart[3] = x.off;
-                        sStart[4] = static_cast<int>(T1 - T0);
-                    } else {
-                        // a unit that begins in this run and ends in a later one
-                        const int64_t u0 = at - x.off, u1 = u0 + group_blocks(p, q, x.g);
-                        JoinDesc d = {};
-                        if (u0 >= T0 && u1 > T1) {
-                            const int t0 = x.g * p.tpu, t1 = min(t0 + p.tpu, q.n);
-                            d.row = (int64_t{q.row0} + t0) * p.heads + x.part * kRows;
-                            d.nrows = p.upt > 1 ? min(kRows, p.heads - x.part * kRows)
-                                                : (t1 - t0) * p.heads;
-                            d.parts = static_cast<int>((u1 - 1) / run) - cta + 1;
-                            d.slot0 = u0 == T0 ? 0 : 1;
-                            d.pos = q.len - q.n + t0;
-                        }
-                        *desc = d;
-                    }
-                    break;
-                }
-            }
-        } else if (tid == 0) {
-            *desc = JoinDesc{};
-        }
-        fence_proxy_async_smem();  // the scratch's tile is next written by TMA
-        __syncthreads();
-    }
+    find_run(p, reinterpret_cast<int64_t *>(sKV), sStart);
     const uint32_t tmem = *tmem_holder;
 
     if (warp < kSoftWarp0) {
@@ -732,7 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int par = g & 1;
                 const int k0 = (x.blk + b) * kBlock;
                 // S^T of this block is ready and the previous block's PV is done with P and O^T
-                const bool live = mbar_wait(s_full, g & 1, abort_flag, p.status);
+                const bool live = __all_sync(
+                    0xFFFFFFFFu, mbar_wait(s_full, g & 1, abort_flag, p.status));
                 // (complete since QK of this block waited for it: orders sPages before here)
                 mbar_wait(&x_full[par], (g >> 1) & 1, abort_flag, p.status);
                 tc_fence_after();
@@ -757,10 +447,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int ra = min(64, ta * p.rpt);
                     int rb = min(64, tb * p.rpt);
                     if (!((pages >> (kl >> page_shift)) & 1u) || !live) rb = 0;
-                    // A key's S is finite in no row exactly when its row holds an infinity or
-                    // NaN. Where some row must not see the key, such elements become zero in
-                    // the tile, as 0 * inf in PV would reach every row; the rows that see the
-                    // key have a NaN probability already.
+                    // A row of the cache that holds an infinity or NaN makes its logit non-finite
+                    // in every row of q. Where a row of q must not see the key, those elements
+                    // become zero in the tile (0 * inf in PV would reach every row); rows that
+                    // do see the key have a NaN probability already. A key at a time: lane =
+                    // 16-byte piece of four of its chunks.
                     bool odd = false;
                     const int a = max(0, min(32, ra - hb)), e = max(0, min(32, rb - hb));
                     const uint32_t below_e = e == 32 ? 0xFFFFFFFFu : (1u << e) - 1u;
@@ -771,23 +462,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         odd = odd || !(fabsf(__uint_as_float(sa[h])) <= 3.4028234e38f);
                         if (!((vis >> h) & 1u)) sa[h] = __float_as_uint(-INFINITY);
                     }
-                    if (odd && live && (ra > 0 || rb < x.nrows)) {
+                    uint32_t keys =
+                        __ballot_sync(0xFFFFFFFFu, odd && live && (ra > 0 || rb < x.nrows));
+                    if (keys) {
                         for (int m = 0; m < 4; ++m)
                             mbar_wait(&kv_full[m], g & 1, abort_flag, p.status);
-                        // four chunks by each of the key's two threads
-#pragma unroll 1
-                        for (int c = 4 * hh; c < 4 * hh + 4; ++c) {
-                            uint4 *at = reinterpret_cast<uint4 *>(
-                                (c == 7 && par ? sX : sKV + c * 16384) + kl * 128);
-#pragma unroll 1
-                            for (int k = 0; k < 8; ++k) {
-                                uint4 v = at[k];
-                                v.x = finite2(v.x);
-                                v.y = finite2(v.y);
-                                v.z = finite2(v.z);
-                                v.w = finite2(v.w);
-                                at[k] = v;
-                            }
+                        const int c = 4 * hh + (lane >> 3);
+                        uint8_t *tile =
+                            (c == 7 && par ? sX : sKV + c * 16384) + sp * 4096 + (lane & 7) * 16;
+                        for (; keys; keys &= keys - 1) {
+                            uint4 *at = reinterpret_cast<uint4 *>(tile + (__ffs(keys) - 1) * 128);
+                            uint4 v = *at;
+                            v.x = finite2(v.x);
+                            v.y = finite2(v.y);
+                            v.z = finite2(v.z);
+                            v.w = finite2(v.w);
+                            *at = v;
                         }
                     }
                 }
@@ -895,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // a row that saw no key has sum 0 and O 0
                 sLinv[r] = tot == 0.0f ? 0.0f : 1.0f / tot;
                 if (!x.whole)
-                    reinterpret_cast<float2 *>(p.ws + kWsMl)[slot * kRows + r] =
+                    reinterpret_cast<float2 *>(p.ws + kWsMl)[slot * kMaxRows + r] =
                         make_float2(sM[cur * 64 + r], tot);
             }
             bar_group(hh);
@@ -980,17 +670,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ the join
 
 // out[row] = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M), M = max_p m_p, over the parts of a
-// unit: one row at a time per CTA, its parts shared by four groups of 128 threads (four dims
-// each). The parts are added in the same order every time.
+// unit: one row (kDims of its dims) at a time per CTA, its parts shared by groups of kDims / 4
+// threads (four dims each). The parts are added in the same order every time.
 constexpr int kJoinThreads = 512;
 
-__global__ void __launch_bounds__(kJoinThreads)
-    paged_join_kernel(const Params p, int ctas) {
+template <int kDims>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const Params p, int ctas) {
+    constexpr int kT = kDims / 4, kGroups = kJoinThreads / kT;
     __shared__ int active[kMaxCtas];
     __shared__ int count[kJoinThreads / 32];
     __shared__ float weight[kMaxCtas];
     __shared__ float red[2][kJoinThreads / 32];
-    __shared__ float4 sum[3][128];
+    __shared__ float4 sum[kGroups][kT];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const JoinDesc *desc = reinterpret_cast<const JoinDesc *>(p.ws + kWsDesc);
     const bool has = tid < ctas && desc[tid].parts > 0;
@@ -1004,14 +695,14 @@ __global__ void __launch_bounds__(kJoinThreads)
     }
     if (has) active[before + __popc(vote & ((1u << lane) - 1u))] = tid;
     __syncthreads();
-    for (int it = blockIdx.x; it < n * kRows; it += gridDim.x) {
-        const int cta = active[it / kRows], r = it % kRows;
+    for (int it = blockIdx.x; it < n * p.rows; it += gridDim.x) {
+        const int cta = active[it / p.rows], r = it % p.rows;
         const JoinDesc d = desc[cta];
         if (r >= d.nrows) continue;
         auto slot_of = [&](int k) { return k == 0 ? 2 * cta + d.slot0 : 2 * (cta + k); };
         float2 ml = make_float2(kNoMax, 0.0f);
         if (tid < d.parts)
-            ml = reinterpret_cast<const float2 *>(p.ws + kWsMl)[slot_of(tid) * kRows + r];
+            ml = reinterpret_cast<const float2 *>(p.ws + kWsMl)[slot_of(tid) * kMaxRows + r];
         const float wm = redux_max(ml.x);
         if (lane == 0) red[0][warp] = wm;
         __syncthreads();
@@ -1024,22 +715,22 @@ __global__ void __launch_bounds__(kJoinThreads)
         for (int w = 16; w >= 1; w >>= 1) ls += __shfl_xor_sync(0xFFFFFFFFu, ls, w);
         if (lane == 0) red[1][warp] = ls;
         __syncthreads();
-        const int grp = tid >> 7, t = tid & 127;
-        const float4 *src = reinterpret_cast<const float4 *>(p.ws + kWsO) + r * (kD / 4) + t;
+        const int grp = tid / kT, t = tid % kT;
+        const float4 *src = reinterpret_cast<const float4 *>(p.ws + kWsO) + r * kT + t;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-        for (int k = grp; k < d.parts; k += 4) {
-            const float4 v = src[int64_t{slot_of(k)} * kRows * (kD / 4)];
+        for (int k = grp; k < d.parts; k += kGroups) {
+            const float4 v = src[int64_t{slot_of(k)} * (kSlotFloats / 4)];
             const float w = weight[k];
             acc.x = fmaf(v.x, w, acc.x);
             acc.y = fmaf(v.y, w, acc.y);
             acc.z = fmaf(v.z, w, acc.z);
             acc.w = fmaf(v.w, w, acc.w);
         }
-        if (grp > 0) sum[grp - 1][t] = acc;
+        sum[grp][t] = acc;
         __syncthreads();
         if (grp == 0) {
-            for (int k = 0; k < 3; ++k) {
+            for (int k = 1; k < kGroups; ++k) {
                 const float4 v = sum[k][t];
                 acc.x += v.x;
                 acc.y += v.y;
@@ -1053,16 +744,16 @@ __global__ void __launch_bounds__(kJoinThreads)
             acc.y *= inv;
             acc.z *= inv;
             acc.w *= inv;
-            if (p.b.cos_sin && t >= (kD - kRope) / 4) {
+            const int dim = (kDims < kD ? d.part * kDims : 0) + 4 * t;
+            if (p.b.cos_sin && dim >= kD - kRope) {
                 const float4 a = __ldg(reinterpret_cast<const float4 *>(
-                                           p.b.cos_sin + int64_t{row_pos(p, d.pos, r)} * kRope) +
-                                       (t - (kD - kRope) / 4));
+                    p.b.cos_sin + int64_t{row_pos(p, d.pos, r)} * kRope + (dim - (kD - kRope))));
                 acc = make_float4(acc.x * a.x + acc.y * a.y, acc.y * a.x - acc.x * a.y,
                                   acc.z * a.z + acc.w * a.w, acc.w * a.z - acc.z * a.w);
             }
             const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y);
             const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z, acc.w);
-            *reinterpret_cast<uint2 *>(p.out + (d.row + r) * kD + 4 * t) =
+            *reinterpret_cast<uint2 *>(p.out + (d.row + r) * kD + dim) =
                 make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
                            *reinterpret_cast<const uint32_t *>(&hi));
         }
@@ -1131,24 +822,42 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.ws = static_cast<uint8_t *>(workspace);
     p.heads = heads;
-    p.tpu = heads <= kRows ? kRows / heads : 1;
-    p.upt = (heads + kRows - 1) / kRows;
-    p.rpt = std::min<int32_t>(heads, kRows);
+    const bool chunk = n_new * heads > int64_t{n_seqs} * kRows;
+    if (chunk) {
+        p.rows = kChunkRows;
+        p.tpu = kChunkRows / heads;
+        p.upt = 2;
+        p.row_step = 0;
+    } else {
+        p.rows = kRows;
+        p.tpu = heads <= kRows ? kRows / heads : 1;
+        p.upt = (heads + kRows - 1) / kRows;
+        p.row_step = kRows;
+    }
+    p.rpt = std::min(heads, p.rows);
     // a window no shorter than any sequence is no window
     p.window = window >= p.b.len_limit ? 0 : window;
     p.c = scale * 1.4426950408889634f;
     p.status = dev_status;
     int sms = 0;
     rc = setup(&sms);
+    if (rc == DSA_OK && chunk) rc = prepare_paged_chunk();
     if (rc != DSA_OK) return rc;
     CUtensorMap tm_q, tm_kv;
-    if (!make_tmap_bf16(&tm_q, q, kD, static_cast<uint64_t>(n_new) * heads, kD * 2, 64, kRows) ||
+    if (!make_tmap_bf16(&tm_q, q, kD, static_cast<uint64_t>(n_new) * heads, kD * 2, 64,
+                        p.rows) ||
         !make_tmap_pages(&tm_kv, pages, p.b))
         return DSA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int ctas = std::min(sms, kMaxCtas);
-    paged_attn_kernel<<<ctas, kThreads, kSmem, s>>>(tm_q, tm_kv, p);
-    if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
-    paged_join_kernel<<<2 * ctas, kJoinThreads, 0, s>>>(p, ctas);
+    if (chunk) {
+        rc = enqueue_paged_chunk(tm_q, tm_kv, p, q, ctas, s);
+        if (rc != DSA_OK) return rc;
+        paged_join_kernel<kD / 2><<<2 * ctas, kJoinThreads, 0, s>>>(p, ctas);
+    } else {
+        paged_attn_kernel<<<ctas, kThreads, kSmem, s>>>(tm_q, tm_kv, p);
+        if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
+        paged_join_kernel<kD><<<2 * ctas, kJoinThreads, 0, s>>>(p, ctas);
+    }
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }

@@ -1,0 +1,659 @@
+// dsa_paged_attn for chunks: units of up to 128 rows of q (whole tokens of one sequence) and half
+// of the output dims.
+//
+// The kernel for single tokens (paged_attn.cu) keeps one 128-key tile of all 512 dims beside 64
+// rows of q; its block is one serial chain (load, QK, softmax, PV), and its N=64 products read
+// 6 KB of shared memory for 131,072 multiply-adds. With 128 rows the products run at full rate
+// (8 KB for 262,144), but the sums of 128 rows x 512 dims would fill TMEM alone. So a unit takes
+// 256 of the output dims and the logits are computed twice, once for each half (3 units of work
+// where 2 would do), which leaves room to have two blocks in flight:
+//   S[row, key]   = Q[128 x 512] . K_blk^T           (M=128, N=128, K=512)
+//   O[row, d]    += P[128 x 128] . V_blk[128 x 256]   (2 x (M=128, N=128, K=128), P from TMEM)
+//
+// Shared memory (227 KB): six 64-dim chunks of q (96 KB; the last two, dims 384..511, live in TMEM
+// as MMA operand, which is also where the rotation is applied on the way) and eight 16 KB slabs
+// [128 keys x 64 dims] of K, in two groups of four by block parity. A block first streams the
+// four foreign slabs (dims of the other half, used by QK alone) through its group and then its
+// own four into the same slots, where PV finds them; meanwhile the other group holds the block
+// before for its PV. TMEM: O 256 columns, S 128, P 64, q 64: all 512.
+//
+// Roles: warps 0-3 bring q's last chunks to TMEM and store finished units (so the softmax of the
+// next unit need not wait for the stores), warp 4 loads, warp 5 issues QK, warp 6 PV, warps
+// 8-15 the softmax: TMEM lane = row, two warps per 32 rows, 64 keys each.
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "paged_walk.cuh"
+
+namespace dsa {
+
+namespace {
+
+using namespace paged;
+
+constexpr int kRows = 128;      // rows of q in a unit (MMA M)
+constexpr int kHalf = kD / 2;   // output dims of a unit
+constexpr int kOutWarps = 4;
+constexpr int kLoadWarp = 4;
+constexpr int kQkWarp = 5;
+constexpr int kPvWarp = 6;
+constexpr int kSoftWarp0 = 8;
+constexpr int kRegsLaunch = 128;
+constexpr int kRegsLow = 80;
+constexpr int kRegsSoft = 176;   // 256*80 + 256*176 = 512*128, the launch allocation
+constexpr int kQSmem = 6;        // chunks of q in shared memory; the last two are in TMEM
+
+// shared memory (the base is 1024-byte aligned: nothing static precedes it)
+constexpr uint32_t kSlab = 16384;               // [128 rows x 128 B]
+constexpr uint32_t kOffQ = 0;
+constexpr uint32_t kOffKV = kQSmem * kSlab;
+constexpr uint32_t kOffMx = kOffKV + 8 * kSlab;  // [2][128] block maxima of a row's two halves
+constexpr uint32_t kOffL1 = kOffMx + 1024;       // [128] sum of the second half
+constexpr uint32_t kOffLinv = kOffL1 + 512;      // [2][128] 1/sum, by unit parity
+constexpr uint32_t kOffBar = kOffLinv + 1024;
+constexpr uint32_t kSmem = kOffBar + 384;
+static_assert(kSmem <= 232448, "over the shared memory of one CTA");
+
+// TMEM columns
+constexpr uint32_t kOCol = 0;
+constexpr uint32_t kSCol = 256;
+constexpr uint32_t kPCol = 384;
+constexpr uint32_t kQCol = 448;
+
+// D[tmem] (+)= A[tmem] * B[smem]^T; A: lane = row, a column holds two bf16 along K.
+__device__ __forceinline__ void mma_bf16_ta_if(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate,
+                                               uint32_t issue) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+        : "memory");
+}
+
+// The two softmax warps of a sub-partition (same 32 rows): named barrier 1 + sp, 64 threads.
+__device__ __forceinline__ bool vote_any_pair(bool pred, int sp) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, %2, 64, p;\n"
+        " selp.b32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(pred)), "r"(1 + sp)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void bar_pair(int sp) {
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + sp) : "memory");
+}
+
+// Bits [a, b) of a 32-bit word, a and b clamped to 0..32.
+__device__ __forceinline__ uint32_t bits_between(int a, int b) {
+    a = max(0, min(32, a));
+    b = max(0, min(32, b));
+    const uint32_t below_b = b == 32 ? 0xFFFFFFFFu : (1u << b) - 1u;
+    const uint32_t below_a = a == 32 ? 0xFFFFFFFFu : (1u << a) - 1u;
+    return below_b & ~below_a;
+}
+
+// Masks 32 logits by `vis`; returns the bits of the masked ones that are not finite.
+__device__ __forceinline__ uint32_t mask32(uint32_t (&s)[32], uint32_t vis) {
+    uint32_t odd = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        if (!((vis >> j) & 1u)) {
+            if (!(fabsf(__uint_as_float(s[j])) <= 3.4028234e38f)) odd |= 1u << j;
+            s[j] = __float_as_uint(-INFINITY);
+        }
+    }
+    return odd;
+}
+
+__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
+    float t[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        t[j] = fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 16]));
+#pragma unroll
+    for (int w = 8; w >= 1; w >>= 1)
+#pragma unroll
+        for (int j = 0; j < w; ++j) t[j] = fmaxf(t[j], t[j + w]);
+    return t[0];
+}
+
+// exp2(s c - m) of 32 logits as 16 bf16 pairs; adds the rounded values to l.
+__device__ __forceinline__ void exp32(const uint32_t (&s)[32], float c, float m, uint32_t *out,
+                                      float (&l)[4]) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const float a = ex2(fmaf(__uint_as_float(s[2 * j]), c, -m));
+        const float b = ex2(fmaf(__uint_as_float(s[2 * j + 1]), c, -m));
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        out[j] = *reinterpret_cast<const uint32_t *>(&v);
+        l[(2 * j) & 3] += bf16lo(out[j]);
+        l[(2 * j + 1) & 3] += bf16hi(out[j]);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
+                       const __grid_constant__ CUtensorMap tm_kv,
+                       const __grid_constant__ Params p, const __nv_bfloat16 *__restrict__ q) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *sQ = smem + kOffQ;
+    uint8_t *sKV = smem + kOffKV;
+    float *sMx = reinterpret_cast<float *>(smem + kOffMx);
+    float *sL1 = reinterpret_cast<float *>(smem + kOffL1);
+    float *sLinv = reinterpret_cast<float *>(smem + kOffLinv);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBar);
+    uint64_t *full = bars + 0;      // [8] slab landed: its foreign content, then its own
+    uint64_t *f_free = bars + 8;    // [8] foreign content used by QK
+    uint64_t *v_free = bars + 16;   // [2][2] pair of own slabs used by PV, by block parity
+    uint64_t *pg_full = bars + 20;  // [2] sPages written, by block parity
+    uint64_t *q_full = bars + 22;   // q's chunks in shared memory landed
+    uint64_t *q_tm = bars + 23;     // q's chunks in TMEM written
+    uint64_t *q_free = bars + 24;   // the unit's last QK done
+    uint64_t *s_full = bars + 25;
+    uint64_t *s_free = bars + 26;
+    uint64_t *p_full = bars + 27;
+    uint64_t *pv_done = bars + 28;  // PV of a block done: P may be written, O rescaled
+    uint64_t *o_full = bars + 29;
+    uint64_t *o_free = bars + 30;
+    uint64_t *stat_full = bars + 31;
+    uint64_t *drain = bars + 32;    // [2] one per issuing warp
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 34);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    volatile uint32_t *sPages = tmem_holder + 2;             // [2]
+    int *sStart = reinterpret_cast<int *>(tmem_holder + 4);  // [5]
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (smem_u32(smem) & 1023u) {  // the tiles' swizzle counts on it
+        if (tid == 0) {
+            report(p.status, DSA_ERR_CUDA);
+            reinterpret_cast<JoinDesc *>(p.ws + kWsDesc)[blockIdx.x] = JoinDesc{};
+        }
+        return;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&f_free[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(&v_free[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&pg_full[i], 1);
+            mbar_init(&drain[i], 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_tm, kRows);
+        mbar_init(q_free, 1);
+        mbar_init(s_full, 1);
+        mbar_init(s_free, 8);
+        mbar_init(p_full, 256);
+        mbar_init(pv_done, 1);
+        mbar_init(o_full, 1);
+        mbar_init(o_free, kRows);
+        mbar_init(stat_full, kRows);
+        *abort_flag = 0;
+        sStart[4] = 0;
+        fence_barrier_init();
+    }
+    if (warp == kPvWarp) tmem_alloc(tmem_holder, 512);
+    const int cta = static_cast<int>(blockIdx.x);
+    find_run(p, reinterpret_cast<int64_t *>(sKV), sStart);
+    const uint32_t tmem = *tmem_holder;
+
+    if (warp < kSoftWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
+        if (warp < kOutWarps) {
+            // ---------------- q's last two chunks to TMEM (the rotation on the way), and the
+            // finished units to memory. Thread = row.
+            const int r = tid;
+            const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+            Walk ahead(p, sStart), walk(p, sStart);
+            Segment x, y;
+            auto stage = [&](const Segment &u, int i) -> bool {
+                const bool mine = r < u.nrows;
+                const uint4 *src = reinterpret_cast<const uint4 *>(q + (u.row + r) * kD + 384);
+                uint32_t v[32];
+                // dims 448..511 first: they take longest
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint4 w = mine ? __ldg(src + 8 + k) : make_uint4(0, 0, 0, 0);
+                    v[4 * k] = w.x;
+                    v[4 * k + 1] = w.y;
+                    v[4 * k + 2] = w.z;
+                    v[4 * k + 3] = w.w;
+                }
+                if (p.b.cos_sin && mine) {
+                    const float4 *cs = reinterpret_cast<const float4 *>(
+                        p.b.cos_sin + int64_t{row_pos(p, u.posf, r)} * kRope);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float4 a = __ldg(cs + k);
+                        v[2 * k] = turn_pair(v[2 * k], a.x, a.y);
+                        v[2 * k + 1] = turn_pair(v[2 * k + 1], a.z, a.w);
+                    }
+                }
+                const bool ok = mbar_wait(q_free, (i & 1) ^ 1, abort_flag, p.status);
+                tc_fence_after();
+                tmem_st32(lane_base + kQCol + 32, v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint4 w = mine ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+                    v[4 * k] = w.x;
+                    v[4 * k + 1] = w.y;
+                    v[4 * k + 2] = w.z;
+                    v[4 * k + 3] = w.w;
+                }
+                tmem_st32(lane_base + kQCol, v);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(q_tm);
+                return ok;
+            };
+            bool have = ahead.next(p, y);
+            if (have) stage(y, 0);
+            for (int i = 0; walk.next(p, x); ++i) {
+                have = ahead.next(p, y);
+                if (have) stage(y, i + 1);
+                mbar_wait(stat_full, i & 1, abort_flag, p.status);
+                const bool live = mbar_wait(o_full, i & 1, abort_flag, p.status);
+                tc_fence_after();
+                const float linv = sLinv[(i & 1) * kRows + r];
+                const bool mine = r < x.nrows && live;
+                const int slot = 2 * cta + (i > 0);
+                const float4 *cs =
+                    p.b.cos_sin && x.part == 1 && r < x.nrows
+                        ? reinterpret_cast<const float4 *>(
+                              p.b.cos_sin + int64_t{row_pos(p, x.posf, r)} * kRope)
+                        : nullptr;
+                uint4 *orow = reinterpret_cast<uint4 *>(p.out + (x.row + r) * kD + x.part * kHalf);
+                float4 *prow = reinterpret_cast<float4 *>(p.ws + kWsO) +
+                               (int64_t{slot} * kSlotFloats + r * kHalf) / 4;
+#pragma unroll 1
+                for (int k = 0; k < kHalf / 32; ++k) {
+                    uint32_t o[32];
+                    tmem_ld32(lane_base + kOCol + 32 * k, o);
+                    tmem_wait_ld();
+                    if (x.whole) {
+                        float v[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * linv;
+                        if (cs && k >= 6) {
+                            // dims 448..511 turned back by the token's position
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float4 a = __ldg(cs + 8 * (k - 6) + j);
+                                const float v0 = v[4 * j], v1 = v[4 * j + 1];
+                                const float v2 = v[4 * j + 2], v3 = v[4 * j + 3];
+                                v[4 * j] = v0 * a.x + v1 * a.y;
+                                v[4 * j + 1] = v1 * a.x - v0 * a.y;
+                                v[4 * j + 2] = v2 * a.z + v3 * a.w;
+                                v[4 * j + 3] = v3 * a.z - v2 * a.w;
+                            }
+                        }
+                        if (mine) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const __nv_bfloat162 t = __floats2bfloat162_rn(
+                                        v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
+                                    w[e] = *reinterpret_cast<const uint32_t *>(&t);
+                                }
+                                orow[4 * k + j] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        }
+                    } else if (mine) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            prow[8 * k + j] = make_float4(
+                                __uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                                __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(o_free);
+            }
+        } else if (warp == kLoadWarp) {
+            // ---------------- loader: lane i < np loads page i of a block, slab by slab; its
+            // table entry is read one block ahead
+            const int prows = min(1 << p.b.page_shift, kBlock), np = kBlock / prows;
+            Walk walk(p, sStart);
+            Segment x;
+            int g = 0;
+            int64_t issued = 0;  // loads so far: eight per block
+            bool ok = true;
+            auto entry = [&](const Segment &y, int blk) -> int32_t {
+                const int pos = blk * kBlock + lane * prows;
+                if (lane >= np || pos > y.posl || pos <= y.lo - prows) return -1;
+                const int32_t e =
+                    __ldg(p.b.page_table + int64_t{y.s} * p.b.max_pages + (pos >> p.b.page_shift));
+                if (e < 0 || e >= p.b.n_pages) {
+                    report(p.status, DSA_ERR_BOUNDS);
+                    return -1;
+                }
+                return e;
+            };
+            bool have = walk.next(p, x);
+            int32_t e_next = have ? entry(x, x.blk) : -1;
+            while (have && ok) {
+                Segment y;
+                const bool more = walk.next(p, y);
+                for (int b = 0; b < x.nb && ok; ++b, ++g) {
+                    const int32_t e = e_next;
+                    const int par = g & 1;
+                    const uint32_t use = (g >> 1) & 1;
+                    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, e >= 0);
+                    const uint32_t bytes = static_cast<uint32_t>(__popc(mask)) * prows * 128;
+                    const int y0 =
+                        ((x.blk + b) * kBlock + lane * prows) & ((1 << p.b.page_shift) - 1);
+                    uint8_t *dst = sKV + par * 4 * kSlab + lane * prows * 128;
+#pragma unroll 1
+                    for (int j = 0; j < 8; ++j) {
+                        // slots of the group: own slabs of the block two back used by PV (in
+                        // pairs), then this block's foreign slabs used by QK
+                        const int slot = j & 3;
+                        if (lane == 0) {
+                            if (j == 0 || j == 2)
+                                ok = mbar_wait(&v_free[2 * par + (j >> 1)], use ^ 1, abort_flag,
+                                               p.status);
+                            else if (j >= 4)
+                                ok = mbar_wait(&f_free[4 * par + slot], use, abort_flag, p.status);
+                            if (ok && j == 0) {
+                                sPages[par] = mask;
+                                mbar_arrive(&pg_full[par]);
+                            }
+                            if (ok) mbar_expect_tx(&full[4 * par + slot], bytes);
+                        }
+                        ok = (__ballot_sync(0xFFFFFFFFu, ok) & 1u) != 0;
+                        if (!ok) break;
+                        ++issued;
+                        const int half = (j >> 2) ^ 1 ^ x.part;  // of the dims: foreign, own
+                        if (e >= 0)
+                            tma_load_3d(dst + slot * kSlab, &tm_kv, &full[4 * par + slot],
+                                        (4 * half + slot) * 64, y0, e);
+                    }
+                    if (b + 1 < x.nb) e_next = entry(x, x.blk + b + 1);
+                    else e_next = more ? entry(y, y.blk) : -1;
+                }
+                x = y;
+                have = more;
+            }
+            if (!ok && lane == 0) {
+                // gave up: no copy into this CTA's shared memory may still be in flight at exit
+                uint32_t seen = 0;
+                for (int64_t n = issued - 1; n >= 0 && seen != 0xFFu; --n) {
+                    const int slot = 4 * static_cast<int>((n >> 3) & 1) + static_cast<int>(n & 3);
+                    if ((seen >> slot) & 1u) continue;
+                    seen |= 1u << slot;
+                    drain_wait(&full[slot], static_cast<uint32_t>((n >> 2) & 1));
+                }
+            }
+            __syncwarp();
+        } else if (warp == kQkWarp) {
+            // ---------------- QK issuer: S = Q . K_blk^T, slab by slab
+            const uint32_t leader = lane == 0;
+            constexpr uint32_t idesc_qk = idesc_bf16(kRows, kBlock, false, false);
+            const uint64_t qd0 = desc_sw128(smem_u32(sQ), 16, 1024);
+            const uint64_t kd0 = desc_sw128(smem_u32(sKV), 16, 1024);
+            const uint64_t pol_stream = policy_evict_first();
+            Walk walk(p, sStart);
+            Segment x;
+            int i = 0, g = 0, last_q = -1;
+            bool ok = true;
+            for (; ok && walk.next(p, x); ++i) {
+                if (!(ok = mbar_wait(q_free, (i & 1) ^ 1, abort_flag, p.status))) break;
+                if (leader) {
+                    mbar_expect_tx(q_full, kQSmem * kSlab);
+                    for (int c = 0; c < kQSmem; ++c)
+                        tma_load_2d(sQ + c * kSlab, &tm_q, q_full, c * 64,
+                                    static_cast<int>(x.row), pol_stream);
+                }
+                last_q = i;
+                if (!(ok = mbar_wait(q_full, i & 1, abort_flag, p.status))) break;
+                if (!(ok = mbar_wait(q_tm, i & 1, abort_flag, p.status))) break;
+                tc_fence_after();
+                for (int b = 0; b < x.nb && ok; ++b, ++g) {
+                    const int par = g & 1;
+                    // the softmax must have read the block before's S
+                    if (!(ok = mbar_wait(s_free, par ^ 1, abort_flag, p.status))) break;
+#pragma unroll 1
+                    for (int j = 0; j < 8; ++j) {
+                        const int slot = 4 * par + (j & 3);
+                        if (!(ok = mbar_wait(&full[slot], j >> 2, abort_flag, p.status))) break;
+                        tc_fence_after();
+                        const int c = 4 * ((j >> 2) ^ 1 ^ x.part) + (j & 3);  // chunk of dims
+                        const uint64_t kd = kd0 + ((slot * kSlab) >> 4);
+                        if (c < kQSmem) {
+                            const uint64_t qd = qd0 + ((c * kSlab) >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_bf16_if(tmem + kSCol, qd + 2 * kk, kd + 2 * kk, idesc_qk,
+                                            j > 0 || kk > 0, leader);
+                        } else {
+                            const uint32_t qt = tmem + kQCol + 32 * (c - kQSmem);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_bf16_ta_if(tmem + kSCol, qt + 8 * kk, kd + 2 * kk, idesc_qk,
+                                               j > 0 || kk > 0, leader);
+                        }
+                        if (j < 4) mma_commit_if(&f_free[slot], leader);
+                    }
+                    if (!ok) break;
+                    mma_commit_if(s_full, leader);
+                    if (b == x.nb - 1) mma_commit_if(q_free, leader);
+                }
+            }
+            mma_commit_if(&drain[0], leader);
+            if (leader) drain_wait(&drain[0], 0);
+            if (leader && last_q >= 0) drain_wait(q_full, last_q & 1);
+            __syncwarp();
+        } else if (warp == kPvWarp) {
+            // ---------------- PV issuer: O += P . V_blk, two slabs (128 dims) at a time
+            const uint32_t leader = lane == 0;
+            constexpr uint32_t idesc_pv = idesc_bf16(kRows, 128, false, true);
+            const uint64_t vd0 = desc_sw128(smem_u32(sKV), kSlab, 1024);
+            Walk walk(p, sStart);
+            Segment x;
+            int i = 0, g = 0;
+            bool ok = true;
+            for (; ok && walk.next(p, x); ++i) {
+                for (int b = 0; b < x.nb && ok; ++b, ++g) {
+                    const int par = g & 1;
+                    if (!(ok = mbar_wait(p_full, par, abort_flag, p.status))) break;
+                    if (b == 0 && i > 0 &&
+                        !(ok = mbar_wait(o_free, (i - 1) & 1, abort_flag, p.status)))
+                        break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const uint64_t vd = vd0 + (((4 * par + 2 * n) * kSlab) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_bf16_ta_if(tmem + kOCol + 128 * n, tmem + kPCol + 8 * kk,
+                                           vd + ((kk * 2048) >> 4), idesc_pv, b > 0 || kk > 0,
+                                           leader);
+                        mma_commit_if(&v_free[2 * par + n], leader);
+                    }
+                    mma_commit_if(pv_done, leader);
+                    if (b == x.nb - 1) mma_commit_if(o_full, leader);
+                }
+            }
+            mma_commit_if(&drain[1], leader);
+            if (leader) drain_wait(&drain[1], 0);
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        // ---------------- softmax, 8 warps: rows of sub-partition sp x keys [64 hh, 64 hh + 64)
+        const int sp = warp & 3;
+        const int hh = (warp - kSoftWarp0) >> 2;
+        const int r = 32 * sp + lane;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(sp * 32) << 16);
+        const int page_shift = min(p.b.page_shift, 7);
+        const uint32_t all_pages = (1u << (kBlock >> page_shift)) - 1u;
+        Walk walk(p, sStart);
+        Segment x;
+        int i = 0, g = 0;
+        for (; walk.next(p, x); ++i) {
+            float l[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            float m = kNoMax;
+            const int pos = r < x.nrows ? row_pos(p, x.posf, r) : x.posl;
+            for (int b = 0; b < x.nb; ++b, ++g) {
+                const int par = g & 1;
+                const int k0 = (x.blk + b) * kBlock;
+                const bool live = __all_sync(
+                    0xFFFFFFFFu, mbar_wait(s_full, par, abort_flag, p.status));
+                mbar_wait(&pg_full[par], (g >> 1) & 1, abort_flag, p.status);
+                tc_fence_after();
+                uint32_t s0[32], s1[32];
+                tmem_ld32(lane_base + kSCol + 64 * hh, s0);
+                tmem_ld32(lane_base + kSCol + 64 * hh + 32, s1);
+                const uint32_t pages = sPages[par];
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free);
+                // every row sees every key of the block, unless ...
+                if (k0 + kBlock - 1 > x.posf || (p.window > 0 && k0 <= x.posl - p.window) ||
+                    pages != all_pages || !live) {
+                    const int end = pos - k0 - 64 * hh + 1;   // keys [from, end) of this thread's
+                    const int from = p.window > 0 ? end - p.window : 0;
+                    uint32_t v0 = bits_between(from, end), v1 = bits_between(from - 32, end - 32);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const bool in = live && ((pages >> ((64 * hh + 16 * k) >> page_shift)) & 1u);
+                        const uint32_t half = (k & 1) ? 0xFFFF0000u : 0x0000FFFFu;
+                        if (!in && k < 2) v0 &= ~half;
+                        if (!in && k >= 2) v1 &= ~half;
+                    }
+                    // A row of the cache that holds an infinity or NaN makes its logit non-finite
+                    // in every row of q. Where a row of q must not see the key, those elements
+                    // become zero in the own slabs (0 * inf in PV would reach every row); rows
+                    // that do see the key have a NaN probability already. A key at a time: lane
+                    // = 16-byte piece of its four slabs.
+                    uint32_t odd0 = __reduce_or_sync(0xFFFFFFFFu, mask32(s0, v0));
+                    uint32_t odd1 = __reduce_or_sync(0xFFFFFFFFu, mask32(s1, v1));
+                    if ((odd0 | odd1) && live) {
+                        for (int j = 0; j < 4; ++j)
+                            mbar_wait(&full[4 * par + j], 1, abort_flag, p.status);
+                        uint8_t *tile = sKV + (4 * par + (lane >> 3)) * kSlab + (lane & 7) * 16;
+                        while (odd0 | odd1) {
+                            int key;
+                            if (odd0) {
+                                key = __ffs(odd0) - 1;
+                                odd0 &= odd0 - 1;
+                            } else {
+                                key = 32 + __ffs(odd1) - 1;
+                                odd1 &= odd1 - 1;
+                            }
+                            uint4 *at = reinterpret_cast<uint4 *>(tile + (64 * hh + key) * 128);
+                            uint4 v = *at;
+                            v.x = finite2(v.x);
+                            v.y = finite2(v.y);
+                            v.z = finite2(v.z);
+                            v.w = finite2(v.w);
+                            *at = v;
+                        }
+                        fence_proxy_async_smem();
+                    }
+                }
+                const float mx = fmaxf(max32(s0), max32(s1));
+                if (vote_any_pair(fmaf(mx, p.c, -m) > kRescale, sp)) {
+                    // the row's block maximum from both halves; sums and O rescaled
+                    sMx[hh * kRows + r] = mx;
+                    bar_pair(sp);
+                    const float m_new =
+                        fmaxf(m, fmaxf(mx, sMx[(hh ^ 1) * kRows + r]) * p.c);
+                    const float alpha = ex2(m - m_new);
+                    m = m_new;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) l[k] *= alpha;
+                    if (b > 0) {
+                        mbar_wait(pv_done, par ^ 1, abort_flag, p.status);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t o[32];
+                            const uint32_t col = lane_base + kOCol + 128 * hh + 32 * k;
+                            tmem_ld32(col, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                            tmem_st32(col, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                // P rounded to bf16; the sums take the rounded values, which PV multiplies
+                uint32_t pk[32];
+                exp32(s0, p.c, m, pk, l);
+                exp32(s1, p.c, m, pk + 16, l);
+                mbar_wait(pv_done, par ^ 1, abort_flag, p.status);  // P of the block before is used
+                tc_fence_after();
+                tmem_st32(lane_base + kPCol + 32 * hh, pk);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(p_full);
+            }
+            const float sum = (l[0] + l[1]) + (l[2] + l[3]);
+            if (hh == 1) sL1[r] = sum;
+            bar_pair(sp);
+            if (hh == 0) {
+                const float tot = sum + sL1[r];
+                // a row that saw no key has sum 0 and O 0
+                sLinv[(i & 1) * kRows + r] = tot == 0.0f ? 0.0f : 1.0f / tot;
+                if (!x.whole)
+                    reinterpret_cast<float2 *>(p.ws + kWsMl)[(2 * cta + (i > 0)) * kMaxRows + r] =
+                        make_float2(m, tot);
+                mbar_arrive(stat_full);
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == kPvWarp) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+std::mutex g_mu;
+int g_rc[kMaxDevices];
+bool g_done[kMaxDevices];
+
+}  // namespace
+
+int prepare_paged_chunk() {
+    const int dev = current_device();
+    if (dev < 0) return DSA_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (!g_done[dev]) {
+        cudaFuncAttributes fa;
+        g_rc[dev] = cudaFuncGetAttributes(&fa, paged_chunk_kernel) == cudaSuccess &&
+                            fa.numRegs == kRegsLaunch &&
+                            cudaFuncSetAttribute(paged_chunk_kernel,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 kSmem) == cudaSuccess
+                        ? DSA_OK
+                        : DSA_ERR_CUDA;
+        g_done[dev] = true;
+    }
+    return g_rc[dev];
+}
+
+int enqueue_paged_chunk(const CUtensorMap &tm_q, const CUtensorMap &tm_kv,
+                        const paged::Params &p, const void *q, int ctas, cudaStream_t s) {
+    paged_chunk_kernel<<<ctas, kThreads, kSmem, s>>>(tm_q, tm_kv, p,
+                                                     static_cast<const __nv_bfloat16 *>(q));
+    return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+}  // namespace dsa

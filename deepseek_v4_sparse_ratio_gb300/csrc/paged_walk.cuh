@@ -1,0 +1,366 @@
+// What the two kernels of dsa_paged_attn share: the list of units and key blocks that is cut
+// evenly over the CTAs, the workspace in which the parts of a cut unit meet, and small helpers.
+//
+// Work. A unit is a few whole tokens of one sequence (or part of one token's heads): rows of q
+// that attend over the same rows of the cache, each up to its own position. Its keys are blocks
+// of 128 positions (aligned, so a page never straddles two blocks). All units' blocks form one
+// sequence that is cut into equal runs, one per CTA (one CTA per SM): a run takes whole units
+// where they fit and parts of a unit at its ends, so a single long sequence and a batch of
+// thousands of short ones both fill the machine, and causal triangles and ragged lengths balance
+// by themselves. A part leaves its unnormalised sum, running maximum and sum of weights in the
+// workspace, and a second kernel joins the parts. Every CTA finds its run from the lengths on
+// the device: the blocks of a sequence's first units are sums of floors, known in closed form.
+#pragma once
+
+#include "common.cuh"
+#include "paged.h"
+
+namespace dsa {
+namespace paged {
+
+constexpr int kBlock = 128;        // keys in a block
+constexpr int kThreads = 512;      // of both kernels
+constexpr int kMaxCtas = 152;
+
+constexpr float kRescale = 8.0f;      // log2 units the running maximum may lag behind
+constexpr float kNoMax = -1.0e30f;    // running maximum of a row that has seen no key: finite,
+                                      // so that (masked) -inf minus it stays -inf
+
+// Workspace: descriptors, (maximum, sum) of every part's rows, the parts' O. A CTA has two
+// slots, as only the first and the last segment of a run can be parts. A slot holds 64 rows of
+// 512 dims or 128 rows of 256.
+constexpr int kMaxRows = 128;
+constexpr size_t kSlotFloats = 64 * kD;
+constexpr size_t kWsDesc = 0;
+constexpr size_t kWsMl = 8192;
+constexpr size_t kWsO = kWsMl + size_t{2 * kMaxCtas} * kMaxRows * 2 * sizeof(float);
+static_assert(kWsO + size_t{2 * kMaxCtas} * kSlotFloats * sizeof(float) <= DSA_PAGED_WORKSPACE_BYTES,
+              "over the workspace");
+
+// A unit that begins in a CTA's run and ends in a later one, for the join.
+struct JoinDesc {
+    int64_t row;      // first row of q / out
+    int32_t nrows;
+    int32_t parts;    // 0: none
+    int32_t slot0;    // slot of the first part (the others are slot 0 of the next CTAs)
+    int32_t pos;      // position of the unit's first token
+    int32_t part;     // which of the group's units
+    int32_t pad;
+};
+static_assert(sizeof(JoinDesc) == 32 && kMaxCtas * sizeof(JoinDesc) <= kWsMl, "descriptors");
+
+struct Params {
+    PagedBatch b;
+    __nv_bfloat16 *out;
+    uint8_t *ws;
+    int32_t heads;
+    int32_t tpu;       // tokens of a unit
+    int32_t upt;       // units of a token group: parts of its heads, or of its output dims
+    int32_t rows;      // rows of a unit at most
+    int32_t row_step;  // rows from one part's first row to the next part's (0: same rows)
+    int32_t rpt;       // rows of a token in a unit
+    int32_t window;    // 0: the whole context
+    float c;           // scale * log2(e)
+    int32_t *status;
+};
+
+// ------------------------------------------------------------------ the list of units
+
+// sum_{i < n} floor((a + d i) / 128) for a, d >= 0 (the Euclid-like reduction of such sums).
+__device__ inline int64_t floor_sum(int64_t n, int64_t a, int64_t d) {
+    int64_t m = kBlock, ans = 0;
+    while (n > 0) {
+        if (d >= m) {
+            ans += (n - 1) * n / 2 * (d / m);
+            d %= m;
+        }
+        if (a >= m) {
+            ans += n * (a / m);
+            a %= m;
+        }
+        const int64_t y = d * n + a;
+        if (y < m) break;
+        n = y / m;
+        a = y % m;
+        const int64_t t = m;
+        m = d;
+        d = t;
+    }
+    return ans;
+}
+
+// Keys of the tokens [t0, t1) of a sequence: positions lo .. hi, blocks lo / 128 .. hi / 128.
+__device__ __forceinline__ void key_range(const Params &p, const PagedSeq &q, int t0, int &lo,
+                                          int &hi) {
+    const int first = q.len - q.n + t0;
+    lo = p.window > 0 ? max(0, first - p.window + 1) : 0;
+    hi = q.len - q.n + min(t0 + p.tpu, q.n) - 1;
+}
+
+__device__ __forceinline__ int group_blocks(const Params &p, const PagedSeq &q, int g) {
+    int lo, hi;
+    key_range(p, q, g * p.tpu, lo, hi);
+    return (hi >> 7) - (lo >> 7) + 1;
+}
+
+// Blocks of the first G token groups of a sequence (G = all of them: the last one may be short).
+__device__ inline int64_t blocks_before(const Params &p, const PagedSeq &q, int64_t G) {
+    if (G <= 0) return 0;
+    if (G == 1) return group_blocks(p, q, 0);
+    const int64_t base = q.len - q.n, d = p.tpu;
+    int64_t sum = floor_sum(G, base + d - 1, d) + G;
+    if (G * d > q.n) sum += ((int64_t{q.len} - 1) >> 7) - ((base + G * d - 1) >> 7);
+    if (p.window > 0) {
+        const int64_t a = base - p.window + 1;
+        const int64_t g0 = a >= 0 ? 0 : (-a + d - 1) / d;
+        sum -= floor_sum(G - g0, a + g0 * d, d);
+    }
+    return sum;
+}
+
+__device__ __forceinline__ int groups_of(const Params &p, const PagedSeq &q) {
+    return (q.n + p.tpu - 1) / p.tpu;
+}
+
+__device__ __forceinline__ int64_t unit_row(const Params &p, const PagedSeq &q, int t0, int part) {
+    return (int64_t{q.row0} + t0) * p.heads + part * p.row_step;
+}
+
+__device__ __forceinline__ int unit_rows(const Params &p, int tokens, int part) {
+    return min(p.rows, tokens * p.heads - part * p.row_step);
+}
+
+struct Place {
+    int s, g, part, off;  // sequence, token group, unit of the group, block of the unit
+};
+
+// The place of block r of sequence s's blocks.
+__device__ inline Place find_block(const Params &p, const PagedSeq &q, int s, int64_t r) {
+    int lo = 0, hi = groups_of(p, q);  // upt * blocks_before(lo) <= r < upt * blocks_before(hi)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.upt * blocks_before(p, q, mid) <= r) lo = mid;
+        else hi = mid;
+    }
+    r -= p.upt * blocks_before(p, q, lo);
+    const int nb = group_blocks(p, q, lo);
+    return Place{s, lo, static_cast<int>(r) / nb, static_cast<int>(r) % nb};
+}
+
+// A run of blocks of one unit.
+struct Segment {
+    int64_t row;       // first row of q / out
+    int nrows;         // rows of the unit
+    int part;          // which of the group's units
+    int s;             // sequence
+    int blk;           // first block (positions 128 blk ..)
+    int nb;            // blocks
+    int posf, posl;    // positions of the unit's first and last token
+    int lo;            // lowest position any of its tokens sees
+    bool whole;        // all of the unit's blocks
+};
+
+// Walks the segments of a CTA's run. Every role walks on its own.
+struct Walk {
+    Place at;
+    PagedSeq q;
+    int left;
+
+    __device__ __forceinline__ Walk(const Params &p, const int *start) {
+        at = Place{start[0], start[1], start[2], start[3]};
+        left = start[4];
+        q.n = 0;
+        if (left > 0) {
+            bool bad;
+            q = paged_seq(p.b, at.s, bad);
+        }
+    }
+
+    __device__ __forceinline__ bool next(const Params &p, Segment &x) {
+        if (left <= 0) return false;
+        while (at.g * p.tpu >= q.n) {
+            if (++at.s >= p.b.n_seqs) return false;
+            at.g = 0;
+            bool bad;
+            q = paged_seq(p.b, at.s, bad);
+        }
+        const int t0 = at.g * p.tpu, t1 = min(t0 + p.tpu, q.n);
+        int hi;
+        key_range(p, q, t0, x.lo, hi);
+        const int blo = x.lo >> 7, nblk = (hi >> 7) - blo + 1;
+        x.s = at.s;
+        x.posf = q.len - q.n + t0;
+        x.posl = hi;
+        x.row = unit_row(p, q, t0, at.part);
+        x.nrows = unit_rows(p, t1 - t0, at.part);
+        x.part = at.part;
+        x.blk = blo + at.off;
+        x.nb = min(nblk - at.off, left);
+        x.whole = x.nb == nblk;
+        left -= x.nb;
+        at.off = 0;
+        if (++at.part == p.upt) {
+            at.part = 0;
+            ++at.g;
+        }
+        return true;
+    }
+};
+
+// Position of row r of a unit.
+__device__ __forceinline__ int row_pos(const Params &p, int posf, int r) {
+    return p.tpu == 1 ? posf : posf + r / p.rpt;
+}
+
+// Finds this CTA's run, blocks [T0, T1) of all blocks: start[0..3] its first place, start[4] its
+// length (0 on entry); describes the unit that begins in it and ends beyond for the join. All
+// threads call it; `scratch` holds one value per warp. Ends with a barrier of the CTA, and one
+// inside it publishes what was set up before (TMEM, mbarriers).
+__device__ __forceinline__ void find_run(const Params &p, int64_t *scratch, int *start) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cta = static_cast<int>(blockIdx.x);
+    JoinDesc *desc = reinterpret_cast<JoinDesc *>(p.ws + kWsDesc) + cta;
+    const int per = (p.b.n_seqs + kThreads - 1) / kThreads;
+    const int s0 = min(tid * per, p.b.n_seqs), s1 = min(s0 + per, p.b.n_seqs);
+    int64_t mine = 0;
+    for (int s = s0; s < s1; ++s) {
+        bool bad;
+        const PagedSeq q = paged_seq(p.b, s, bad);
+        if (bad && cta == 0) report(p.status, DSA_ERR_BOUNDS);
+        mine += p.upt * blocks_before(p, q, groups_of(p, q));
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, w);
+        if (lane >= w) incl += v;
+    }
+    if (lane == 31) scratch[warp] = incl;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int64_t total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) incl += scratch[w];
+        total += scratch[w];
+    }
+    const int64_t run = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t T0 = run * cta, T1 = min(T0 + run, total);
+    if (T0 < T1) {
+        const int64_t excl = incl - mine;
+        for (int which = 0; which < 2; ++which) {
+            const int64_t at = which ? T1 - 1 : T0;
+            if (at < excl || at >= incl) continue;
+            int64_t acc = excl;
+            for (int s = s0; s < s1; ++s) {
+                bool bad;
+                const PagedSeq q = paged_seq(p.b, s, bad);
+                const int64_t nb = p.upt * blocks_before(p, q, groups_of(p, q));
+                if (at >= acc + nb) {
+                    acc += nb;
+                    continue;
+                }
+                const Place x = find_block(p, q, s, at - acc);
+                if (which == 0) {
+                    start[0] = x.s;
+                    start[1] = x.g;
+                    start[2] = x.part;
+                    start[3] = x.off;
+                    start[4] = static_cast<int>(T1 - T0);
+                } else {
+                    // a unit that begins in this run and ends in a later one
+                    const int64_t u0 = at - x.off, u1 = u0 + group_blocks(p, q, x.g);
+                    JoinDesc d = {};
+                    if (u0 >= T0 && u1 > T1) {
+                        const int t0 = x.g * p.tpu, t1 = min(t0 + p.tpu, q.n);
+                        d.row = unit_row(p, q, t0, x.part);
+                        d.nrows = unit_rows(p, t1 - t0, x.part);
+                        d.part = x.part;
+                        d.parts = static_cast<int>((u1 - 1) / run) - cta + 1;
+                        d.slot0 = u0 == T0 ? 0 : 1;
+                        d.pos = q.len - q.n + t0;
+                    }
+                    *desc = d;
+                }
+                break;
+            }
+        }
+    } else if (tid == 0) {
+        *desc = JoinDesc{};
+    }
+    fence_proxy_async_smem();  // the scratch's tile is next written by TMA
+    __syncthreads();
+}
+
+// ------------------------------------------------------------------ small helpers
+
+__device__ __forceinline__ float redux_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, uint64_t *bar, int x,
+                                            int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(tm), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// tcgen05.mma / tcgen05.commit run by every lane of a converged warp but issued only where
+// `issue` is non-zero: the warp stays converged and the descriptors in uniform registers.
+__device__ __forceinline__ void mma_bf16_if(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate, uint32_t issue) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit_if(uint64_t *bar, uint32_t issue) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+            smem_u32(bar)),
+        "r"(issue)
+        : "memory");
+}
+
+__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
+    const uint32_t b = smem_u32(bar);
+    const long long t0 = clock64();
+    while (!mbar_test(b, parity))
+        if (clock64() - t0 > kWaitBudget) break;
+}
+
+// Both bf16 values of a word with infinities and NaN replaced by zero.
+__device__ __forceinline__ uint32_t finite2(uint32_t v) {
+    if ((v & 0x7F800000u) == 0x7F800000u) v &= 0x0000FFFFu;
+    if ((v & 0x00007F80u) == 0x00007F80u) v &= 0xFFFF0000u;
+    return v;
+}
+
+__device__ __forceinline__ uint32_t turn_pair(uint32_t v, float c, float s) {
+    const float x = bf16lo(v), y = bf16hi(v);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(x * c - y * s, x * s + y * c);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+}  // namespace paged
+
+// The chunk kernel (paged_chunk.cu): one-time set-up, and its launch.
+constexpr int kChunkRows = 128;
+int prepare_paged_chunk();
+int enqueue_paged_chunk(const CUtensorMap &tm_q, const CUtensorMap &tm_kv,
+                        const paged::Params &p, const void *q, int ctas, cudaStream_t s);
+
+}  // namespace dsa
