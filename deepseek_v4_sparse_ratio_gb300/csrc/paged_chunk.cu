@@ -18,8 +18,8 @@
 // before for its PV. TMEM: O 256 columns, S 128, P 64, q 64: all 512.
 //
 // Roles: warps 0-3 bring q's last chunks to TMEM and store finished units (so the softmax of the
-// next unit need not wait for the stores), warp 4 loads, warp 5 issues QK, warp 6 PV, warps
-// 8-15 the softmax: TMEM lane = row, two warps per 32 rows, 64 keys each.
+// next unit need not wait for the stores), warp 4 loads K, warp 5 issues the products, warp 6
+// loads q, warps 8-15 the softmax: TMEM lane = row, two warps per 32 rows, 64 keys each.
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -38,8 +38,8 @@ constexpr int kRows = 128;      // rows of q in a unit (MMA M)
 constexpr int kHalf = kD / 2;   // output dims of a unit
 constexpr int kOutWarps = 4;
 constexpr int kLoadWarp = 4;
-constexpr int kQkWarp = 5;
-constexpr int kPvWarp = 6;
+constexpr int kMmaWarp = 5;
+constexpr int kQWarp = 6;
 constexpr int kSoftWarp0 = 8;
 constexpr int kRegsLaunch = 128;
 constexpr int kRegsLow = 80;
@@ -64,14 +64,49 @@ constexpr uint32_t kPCol = 384;
 constexpr uint32_t kQCol = 448;
 
 // D[tmem] (+)= A[tmem] * B[smem]^T; A: lane = row, a column holds two bf16 along K.
-__device__ __forceinline__ void mma_bf16_ta_if(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                               uint32_t idesc, uint32_t accumulate,
-                                               uint32_t issue) {
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// S (+)= Q . K^T over two slabs, dims 64 kChunk .. 64 kChunk + 127, in the group of block parity
+// par (slots kChunk mod 4 and the next). The descriptors are built anew at every call: kept
+// across calls they would be more than the warp's registers hold.
+template <int kChunk>
+__device__ __forceinline__ void issue_qk(const uint8_t *smem, uint32_t tmem, int par,
+                                         uint32_t acc0) {
+    constexpr uint32_t idesc = idesc_bf16(kRows, kBlock, false, false);
+    uint64_t qd = desc_sw128(smem_u32(smem + kOffQ) + (kChunk < kQSmem ? kChunk : 0) * kSlab, 16, 1024);
+    uint64_t kd = desc_sw128(smem_u32(smem + kOffKV) + (4 * par + kChunk % 4) * kSlab, 16, 1024);
+    asm volatile("" : "+l"(qd), "+l"(kd), "+r"(tmem));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t acc = j > 0 || kk > 0 ? 1u : acc0;
+            const uint32_t step = ((j * kSlab) >> 4) + 2 * kk;
+            if (kChunk < kQSmem)
+                mma_bf16(tmem + kSCol, qd + step, kd + step, idesc, acc);
+            else
+                mma_bf16_ta(tmem + kSCol, tmem + kQCol + 32 * j + 8 * kk, kd + step, idesc, acc);
+        }
+    }
+}
+
+// O (+)= P . V over the block's keys and 128 of the unit's dims (own slabs 2 half, 2 half + 1).
+__device__ __forceinline__ void issue_pv(const uint8_t *smem, uint32_t tmem, int par, int half,
+                                         uint32_t acc0) {
+    constexpr uint32_t idesc = idesc_bf16(kRows, 128, false, true);
+    uint64_t vd = desc_sw128(smem_u32(smem + kOffKV) + (4 * par + 2 * half) * kSlab, kSlab, 1024);
+    asm volatile("" : "+l"(vd), "+r"(tmem));
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+        mma_bf16_ta(tmem + kOCol + 128 * half, tmem + kPCol + 8 * kk, vd + ((kk * 2048) >> 4),
+                    idesc, kk > 0 ? 1u : acc0);
 }
 
 // The two softmax warps of a sub-partition (same 32 rows): named barrier 1 + sp, 64 threads.
@@ -149,22 +184,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     float *sL1 = reinterpret_cast<float *>(smem + kOffL1);
     float *sLinv = reinterpret_cast<float *>(smem + kOffLinv);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBar);
-    uint64_t *full = bars + 0;      // [8] slab landed: its foreign content, then its own
-    uint64_t *f_free = bars + 8;    // [8] foreign content used by QK
-    uint64_t *v_free = bars + 16;   // [2][2] pair of own slabs used by PV, by block parity
-    uint64_t *pg_full = bars + 20;  // [2] sPages written, by block parity
-    uint64_t *q_full = bars + 22;   // q's chunks in shared memory landed
-    uint64_t *q_tm = bars + 23;     // q's chunks in TMEM written
-    uint64_t *q_free = bars + 24;   // the unit's last QK done
-    uint64_t *s_full = bars + 25;
-    uint64_t *s_free = bars + 26;
-    uint64_t *p_full = bars + 27;
-    uint64_t *pv_done = bars + 28;  // PV of a block done: P may be written, O rescaled
-    uint64_t *o_full = bars + 29;
-    uint64_t *o_free = bars + 30;
-    uint64_t *stat_full = bars + 31;
-    uint64_t *drain = bars + 32;    // [2] one per issuing warp
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 34);
+    uint64_t *full = bars + 0;      // [2][2] pair of slabs landed, by block parity: the foreign
+                                    // ones, then the own ones
+    uint64_t *f_free = bars + 4;    // [2][2] pair of foreign slabs used by QK
+    uint64_t *v_free = bars + 8;    // [2][2] pair of own slabs used by PV
+    uint64_t *pg_full = bars + 12;  // [2] sPages written, by block parity
+    uint64_t *q_full = bars + 14;   // q's chunks in shared memory landed
+    uint64_t *q_tm = bars + 15;     // q's chunks in TMEM written
+    uint64_t *q_free = bars + 16;   // the unit's last QK done
+    uint64_t *s_full = bars + 17;
+    uint64_t *s_free = bars + 18;
+    uint64_t *p_full = bars + 19;
+    uint64_t *pv_done = bars + 20;  // PV of a block done: P may be written, O rescaled
+    uint64_t *o_full = bars + 21;
+    uint64_t *o_free = bars + 22;
+    uint64_t *stat_full = bars + 23;
+    uint64_t *drain = bars + 24;    // every product issued is done
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 25);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     volatile uint32_t *sPages = tmem_holder + 2;             // [2]
     int *sStart = reinterpret_cast<int *>(tmem_holder + 4);  // [5]
@@ -178,15 +214,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&f_free[i], 1);
+            mbar_init(&v_free[i], 1);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&v_free[i], 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&pg_full[i], 1);
-            mbar_init(&drain[i], 1);
-        }
+        for (int i = 0; i < 2; ++i) mbar_init(&pg_full[i], 1);
+        mbar_init(drain, 1);
         mbar_init(q_full, 1);
         mbar_init(q_tm, kRows);
         mbar_init(q_free, 1);
@@ -201,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sStart[4] = 0;
         fence_barrier_init();
     }
-    if (warp == kPvWarp) tmem_alloc(tmem_holder, 512);
+    if (warp == kMmaWarp) tmem_alloc(tmem_holder, 512);
     const int cta = static_cast<int>(blockIdx.x);
     find_run(p, reinterpret_cast<int64_t *>(sKV), sStart);
     const uint32_t tmem = *tmem_holder;
@@ -321,17 +355,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(o_free);
             }
         } else if (warp == kLoadWarp) {
-            // ---------------- loader: lane i < np loads page i of a block, slab by slab; its
-            // table entry is read one block ahead
+            // ---------------- loader: a block in four steps of two slabs, each one instruction:
+            // lane i < np loads page i of the first slab, lane np + i of the second. The block's
+            // table entries are read one block ahead.
             const int prows = min(1 << p.b.page_shift, kBlock), np = kBlock / prows;
+            const int second = lane >= np, page = second ? lane - np : lane;
+            uint8_t *const dst0 = sKV + second * kSlab + page * prows * 128;
             Walk walk(p, sStart);
             Segment x;
-            int g = 0;
-            int64_t issued = 0;  // loads so far: eight per block
+            int g = 0, at = 0;
             bool ok = true;
             auto entry = [&](const Segment &y, int blk) -> int32_t {
-                const int pos = blk * kBlock + lane * prows;
-                if (lane >= np || pos > y.posl || pos <= y.lo - prows) return -1;
+                const int pos = blk * kBlock + page * prows;
+                if (lane >= 2 * np || pos > y.posl || pos <= y.lo - prows) return -1;
                 const int32_t e =
                     __ldg(p.b.page_table + int64_t{y.s} * p.b.max_pages + (pos >> p.b.page_shift));
                 if (e < 0 || e >= p.b.n_pages) {
@@ -345,148 +381,151 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (have && ok) {
                 Segment y;
                 const bool more = walk.next(p, y);
-                for (int b = 0; b < x.nb && ok; ++b, ++g) {
+                for (int b = 0; b < x.nb; ++b, ++g) {
                     const int32_t e = e_next;
                     const int par = g & 1;
                     const uint32_t use = (g >> 1) & 1;
-                    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, e >= 0);
+                    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, e >= 0);  // both slabs' pages
                     const uint32_t bytes = static_cast<uint32_t>(__popc(mask)) * prows * 128;
                     const int y0 =
-                        ((x.blk + b) * kBlock + lane * prows) & ((1 << p.b.page_shift) - 1);
-                    uint8_t *dst = sKV + par * 4 * kSlab + lane * prows * 128;
+                        ((x.blk + b) * kBlock + page * prows) & ((1 << p.b.page_shift) - 1);
 #pragma unroll 1
-                    for (int j = 0; j < 8; ++j) {
-                        // slots of the group: own slabs of the block two back used by PV (in
-                        // pairs), then this block's foreign slabs used by QK
-                        const int slot = j & 3;
+                    for (at = 0; at < 4; ++at) {
+                        // the pair's own slabs of the block two back used by PV; then its
+                        // foreign slabs used by QK
+                        const int pair = 2 * par + (at & 1);
+                        ok = at < 2 ? mbar_wait(&v_free[pair], use ^ 1, abort_flag, p.status)
+                                    : mbar_wait(&f_free[pair], use, abort_flag, p.status);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) break;
                         if (lane == 0) {
-                            if (j == 0 || j == 2)
-                                ok = mbar_wait(&v_free[2 * par + (j >> 1)], use ^ 1, abort_flag,
-                                               p.status);
-                            else if (j >= 4)
-                                ok = mbar_wait(&f_free[4 * par + slot], use, abort_flag, p.status);
-                            if (ok && j == 0) {
-                                sPages[par] = mask;
+                            if (at == 0) {
+                                sPages[par] = mask & ((1u << np) - 1u);
                                 mbar_arrive(&pg_full[par]);
                             }
-                            if (ok) mbar_expect_tx(&full[4 * par + slot], bytes);
+                            mbar_expect_tx(&full[pair], bytes);
                         }
-                        ok = (__ballot_sync(0xFFFFFFFFu, ok) & 1u) != 0;
-                        if (!ok) break;
-                        ++issued;
-                        const int half = (j >> 2) ^ 1 ^ x.part;  // of the dims: foreign, own
+                        __syncwarp();
+                        const int half = (at >> 1) ^ 1 ^ x.part;  // of the dims: foreign, own
                         if (e >= 0)
-                            tma_load_3d(dst + slot * kSlab, &tm_kv, &full[4 * par + slot],
-                                        (4 * half + slot) * 64, y0, e);
+                            tma_load_3d(dst0 + 2 * pair * kSlab, &tm_kv, &full[pair],
+                                        (4 * half + 2 * (at & 1) + second) * 64, y0, e);
                     }
+                    if (!ok) break;
                     if (b + 1 < x.nb) e_next = entry(x, x.blk + b + 1);
                     else e_next = more ? entry(y, y.blk) : -1;
                 }
+                if (!ok) break;
                 x = y;
                 have = more;
             }
             if (!ok && lane == 0) {
-                // gave up: no copy into this CTA's shared memory may still be in flight at exit
-                uint32_t seen = 0;
-                for (int64_t n = issued - 1; n >= 0 && seen != 0xFFu; --n) {
-                    const int slot = 4 * static_cast<int>((n >> 3) & 1) + static_cast<int>(n & 3);
-                    if ((seen >> slot) & 1u) continue;
-                    seen |= 1u << slot;
-                    drain_wait(&full[slot], static_cast<uint32_t>((n >> 2) & 1));
+                // gave up in block g before its step `at`: no copy into this CTA's shared memory
+                // may still be in flight at exit
+                for (int h = 0; h < 2; ++h) {
+                    if (at > h || g > 1) drain_wait(&full[2 * (g & 1) + h], at <= h || at > 2 + h);
+                    if (g > 0) drain_wait(&full[2 * ((g - 1) & 1) + h], 1);
                 }
             }
             __syncwarp();
-        } else if (warp == kQkWarp) {
-            // ---------------- QK issuer: S = Q . K_blk^T, slab by slab
-            const uint32_t leader = lane == 0;
-            constexpr uint32_t idesc_qk = idesc_bf16(kRows, kBlock, false, false);
-            const uint64_t qd0 = desc_sw128(smem_u32(sQ), 16, 1024);
-            const uint64_t kd0 = desc_sw128(smem_u32(sKV), 16, 1024);
+        } else if (warp == kQWarp) {
+            // ---------------- q's chunks in shared memory, as soon as the last unit's are read
             const uint64_t pol_stream = policy_evict_first();
             Walk walk(p, sStart);
             Segment x;
-            int i = 0, g = 0, last_q = -1;
-            bool ok = true;
-            for (; ok && walk.next(p, x); ++i) {
-                if (!(ok = mbar_wait(q_free, (i & 1) ^ 1, abort_flag, p.status))) break;
-                if (leader) {
+            int i = 0;
+            for (; walk.next(p, x); ++i) {
+                if (!mbar_wait(q_free, (i & 1) ^ 1, abort_flag, p.status)) break;
+                if (lane == 0) {
                     mbar_expect_tx(q_full, kQSmem * kSlab);
                     for (int c = 0; c < kQSmem; ++c)
                         tma_load_2d(sQ + c * kSlab, &tm_q, q_full, c * 64,
                                     static_cast<int>(x.row), pol_stream);
                 }
-                last_q = i;
-                if (!(ok = mbar_wait(q_full, i & 1, abort_flag, p.status))) break;
-                if (!(ok = mbar_wait(q_tm, i & 1, abort_flag, p.status))) break;
-                tc_fence_after();
-                for (int b = 0; b < x.nb && ok; ++b, ++g) {
-                    const int par = g & 1;
-                    // the softmax must have read the block before's S
-                    if (!(ok = mbar_wait(s_free, par ^ 1, abort_flag, p.status))) break;
-#pragma unroll 1
-                    for (int j = 0; j < 8; ++j) {
-                        const int slot = 4 * par + (j & 3);
-                        if (!(ok = mbar_wait(&full[slot], j >> 2, abort_flag, p.status))) break;
-                        tc_fence_after();
-                        const int c = 4 * ((j >> 2) ^ 1 ^ x.part) + (j & 3);  // chunk of dims
-                        const uint64_t kd = kd0 + ((slot * kSlab) >> 4);
-                        if (c < kQSmem) {
-                            const uint64_t qd = qd0 + ((c * kSlab) >> 4);
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma_bf16_if(tmem + kSCol, qd + 2 * kk, kd + 2 * kk, idesc_qk,
-                                            j > 0 || kk > 0, leader);
-                        } else {
-                            const uint32_t qt = tmem + kQCol + 32 * (c - kQSmem);
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma_bf16_ta_if(tmem + kSCol, qt + 8 * kk, kd + 2 * kk, idesc_qk,
-                                               j > 0 || kk > 0, leader);
-                        }
-                        if (j < 4) mma_commit_if(&f_free[slot], leader);
-                    }
-                    if (!ok) break;
-                    mma_commit_if(s_full, leader);
-                    if (b == x.nb - 1) mma_commit_if(q_free, leader);
-                }
             }
-            mma_commit_if(&drain[0], leader);
-            if (leader) drain_wait(&drain[0], 0);
-            if (leader && last_q >= 0) drain_wait(q_full, last_q & 1);
+            // no copy into this CTA's shared memory may still be in flight at exit
+            if (lane == 0 && i > 0) drain_wait(q_full, (i - 1) & 1);
             __syncwarp();
-        } else if (warp == kPvWarp) {
-            // ---------------- PV issuer: O += P . V_blk, two slabs (128 dims) at a time
-            const uint32_t leader = lane == 0;
-            constexpr uint32_t idesc_pv = idesc_bf16(kRows, 128, false, true);
-            const uint64_t vd0 = desc_sw128(smem_u32(sKV), kSlab, 1024);
+        } else if (warp == kMmaWarp) {
+            // ---------------- the products, in the order QK foreign (b), PV first half (b - 1),
+            // QK own (b), PV second half (b - 1): PV runs where QK would wait, for the own slabs
+            // and for the softmax to read S, and the two never alternate MMA by MMA (which
+            // costs about 130 cycles a change)
+            const bool leader = lane == 0;
             Walk walk(p, sStart);
             Segment x;
-            int i = 0, g = 0;
+            int i = 0, g = 0;  // g: blocks begun
             bool ok = true;
             for (; ok && walk.next(p, x); ++i) {
-                for (int b = 0; b < x.nb && ok; ++b, ++g) {
+                if (!(ok = mbar_wait(q_full, i & 1, abort_flag, p.status))) break;
+                if (!(ok = mbar_wait(q_tm, i & 1, abort_flag, p.status))) break;
+                for (int b = 0; b <= x.nb; ++b) {
                     const int par = g & 1;
-                    if (!(ok = mbar_wait(p_full, par, abort_flag, p.status))) break;
-                    if (b == 0 && i > 0 &&
-                        !(ok = mbar_wait(o_free, (i - 1) & 1, abort_flag, p.status)))
-                        break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const uint64_t vd = vd0 + (((4 * par + 2 * n) * kSlab) >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            mma_bf16_ta_if(tmem + kOCol + 128 * n, tmem + kPCol + 8 * kk,
-                                           vd + ((kk * 2048) >> 4), idesc_pv, b > 0 || kk > 0,
-                                           leader);
-                        mma_commit_if(&v_free[2 * par + n], leader);
+                    if (b < x.nb) {
+                        // the softmax must have read the block before's S
+                        if (!(ok = mbar_wait(s_free, par ^ 1, abort_flag, p.status))) break;
+                        if (!(ok = mbar_wait(&full[2 * par], 0, abort_flag, p.status))) break;
+                        tc_fence_after();
+                        if (leader) {
+                            if (x.part) issue_qk<0>(smem, tmem, par, 0u);
+                            else issue_qk<4>(smem, tmem, par, 0u);
+                            mma_commit(&f_free[2 * par]);
+                        }
+                        __syncwarp();
+                        if (!(ok = mbar_wait(&full[2 * par + 1], 0, abort_flag, p.status))) break;
+                        if (leader) {
+                            if (x.part) issue_qk<2>(smem, tmem, par, 1u);
+                            else issue_qk<6>(smem, tmem, par, 1u);
+                            mma_commit(&f_free[2 * par + 1]);
+                        }
+                        __syncwarp();
                     }
-                    mma_commit_if(pv_done, leader);
-                    if (b == x.nb - 1) mma_commit_if(o_full, leader);
+                    if (b > 0) {
+                        if (!(ok = mbar_wait(p_full, par ^ 1, abort_flag, p.status))) break;
+                        if (b == 1 && i > 0 &&
+                            !(ok = mbar_wait(o_free, (i - 1) & 1, abort_flag, p.status)))
+                            break;
+                        tc_fence_after();
+                        if (leader) {
+                            issue_pv(smem, tmem, par ^ 1, 0, b > 1);
+                            mma_commit(&v_free[2 * (par ^ 1)]);
+                        }
+                        __syncwarp();
+                    }
+                    if (b < x.nb) {
+                        if (!(ok = mbar_wait(&full[2 * par], 1, abort_flag, p.status))) break;
+                        tc_fence_after();
+                        if (leader) {
+                            if (x.part) issue_qk<4>(smem, tmem, par, 1u);
+                            else issue_qk<0>(smem, tmem, par, 1u);
+                        }
+                        __syncwarp();
+                        if (!(ok = mbar_wait(&full[2 * par + 1], 1, abort_flag, p.status))) break;
+                        if (leader) {
+                            if (x.part) issue_qk<6>(smem, tmem, par, 1u);
+                            else issue_qk<2>(smem, tmem, par, 1u);
+                            mma_commit(s_full);
+                            if (b == x.nb - 1) mma_commit(q_free);
+                        }
+                        __syncwarp();
+                        ++g;
+                    }
+                    if (b > 0) {
+                        // (par is still that of the step's first product)
+                        if (leader) {
+                            issue_pv(smem, tmem, par ^ 1, 1, b > 1);
+                            mma_commit(&v_free[2 * (par ^ 1) + 1]);
+                            mma_commit(pv_done);
+                            if (b == x.nb) mma_commit(o_full);
+                        }
+                        __syncwarp();
+                    }
                 }
             }
-            mma_commit_if(&drain[1], leader);
-            if (leader) drain_wait(&drain[1], 0);
+            if (leader) {
+                mma_commit(drain);
+                drain_wait(drain, 0);
+            }
             __syncwarp();
         }
     } else {
@@ -541,8 +580,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t odd0 = __reduce_or_sync(0xFFFFFFFFu, mask32(s0, v0));
                     uint32_t odd1 = __reduce_or_sync(0xFFFFFFFFu, mask32(s1, v1));
                     if ((odd0 | odd1) && live) {
-                        for (int j = 0; j < 4; ++j)
-                            mbar_wait(&full[4 * par + j], 1, abort_flag, p.status);
+                        mbar_wait(&full[2 * par], 1, abort_flag, p.status);
+                        mbar_wait(&full[2 * par + 1], 1, abort_flag, p.status);
                         uint8_t *tile = sKV + (4 * par + (lane >> 3)) * kSlab + (lane & 7) * 16;
                         while (odd0 | odd1) {
                             int key;
@@ -618,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
-    if (warp == kPvWarp) {
+    if (warp == kMmaWarp) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
