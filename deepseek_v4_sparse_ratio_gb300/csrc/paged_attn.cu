@@ -281,7 +281,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---------------- QK issuer: S^T = K_blk . Q^T, chunk pair by chunk pair as the
             // rows land. It loads the unit's queries itself as soon as its own MMAs have read
             // the previous ones.
-            const uint32_t leader = lane == 0;
             constexpr uint32_t idesc_qk = idesc_bf16(kBlock, kRows, false, false);
             const uint64_t ad0 = desc_sw128(smem_u32(sKV), 16, 1024);
             const uint64_t adx = desc_sw128(smem_u32(sX), 16, 1024);
@@ -293,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (; ok && walk.next(p, x); ++i) {
                 if (!(ok = mbar_wait(q_free, (i & 1) ^ 1, abort_flag, p.status))) break;
-                if (leader) {
+                if (elect_one()) {
                     mbar_expect_tx(q_full, 65536);
                     for (int c = 0; c < 8; ++c)
                         tma_load_2d(sQ + c * 8192, &tm_q, q_full, chunk_dim(c),
@@ -311,14 +310,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t s_col = tmem + kSCol + 64 * par;
                     if (!(ok = mbar_wait(&x_full[par], (g >> 1) & 1, abort_flag, p.status))) break;
                     tc_fence_after();
-                    {
+                    if (elect_one()) {
                         const uint64_t ad = par ? adx : ad0 + ((7 * 16384) >> 4);
                         const uint64_t bd = bd0 + ((7 * 8192) >> 4);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_bf16_if(s_col, ad + 2 * kk, bd + 2 * kk, idesc_qk, kk != 0,
-                                        leader);
+                            mma_bf16(s_col, ad + 2 * kk, bd + 2 * kk, idesc_qk, kk != 0);
                     }
+                    __syncwarp();
 #pragma unroll 1
                     for (int m = 0; m < 4; ++m) {
                         if (!(ok = mbar_wait(&kv_full[m], g & 1, abort_flag, p.status))) break;
@@ -326,36 +325,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                             !(ok = mbar_wait(q_turned, i & 1, abort_flag, p.status)))
                             break;
                         tc_fence_after();
-                        const uint64_t ad = ad0 + ((2 * m * 16384) >> 4);
-                        const uint64_t bd = bd0 + ((2 * m * 8192) >> 4);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
+                        if (elect_one()) {
+                            const uint64_t ad = ad0 + ((2 * m * 16384) >> 4);
+                            const uint64_t bd = bd0 + ((2 * m * 8192) >> 4);
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                if (m < 3 || h == 0)
-                                    mma_bf16_if(s_col, ad + ((h * 16384) >> 4) + 2 * kk,
-                                                bd + ((h * 8192) >> 4) + 2 * kk, idesc_qk, 1u,
-                                                leader);
+                                mma_bf16(s_col, ad + 2 * kk, bd + 2 * kk, idesc_qk, 1u);
+                            if (m < 3) {
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    mma_bf16(s_col, ad + (16384 >> 4) + 2 * kk,
+                                             bd + (8192 >> 4) + 2 * kk, idesc_qk, 1u);
+                            } else {
+                                mma_commit(s_full);
+                                if (b == x.nb - 1) mma_commit(q_free);
+                            }
+                        }
+                        __syncwarp();
                     }
-                    if (!ok) break;
-                    mma_commit_if(s_full, leader);
-                    if (b == x.nb - 1) mma_commit_if(q_free, leader);
                 }
             }
-            mma_commit_if(&drain[0], leader);
-            if (leader) drain_wait(&drain[0], 0);
-            // no copy into this CTA's shared memory may still be in flight at exit
-            if (leader && last_q >= 0) drain_wait(q_full, last_q & 1);
+            if (elect_one()) {
+                mma_commit(&drain[0]);
+                drain_wait(&drain[0], 0);
+                // no copy into this CTA's shared memory may still be in flight at exit
+                if (last_q >= 0) drain_wait(q_full, last_q & 1);
+            }
             __syncwarp();
         } else if (warp == kPvWarp) {
             // ---------------- PV issuer: O^T += V_blk^T . P^T, one d-tile at a time
-            const uint32_t leader = lane == 0;
             constexpr uint32_t idesc_pv = idesc_bf16(128, kRows, true, true);
             Walk walk(p, sStart);
             Segment x;
             int i = 0, g = 0;
             bool ok = true;
-            if (leader) mbar_arrive(s_full);  // no PV precedes the first block
+            if (lane == 0) mbar_arrive(s_full);  // no PV precedes the first block
             __syncwarp();
             for (; ok && walk.next(p, x); ++i) {
                 for (int b = 0; b < x.nb && ok; ++b, ++g) {
@@ -368,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const uint32_t acc0 = b > 0;
                     const uint32_t lbo3 = (g & 1) ? kLbo7Spare : 16384u;
-                    if (leader) {
+                    if (elect_one()) {
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
 #pragma unroll
@@ -380,14 +384,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          idesc_pv, kk > 0 ? 1u : acc0);
                             mma_commit(&kv_free[m]);
                         }
+                        mma_commit(s_full);
+                        if (b == x.nb - 1) mma_commit(o_full);
                     }
                     __syncwarp();
-                    mma_commit_if(s_full, leader);
-                    if (b == x.nb - 1) mma_commit_if(o_full, leader);
                 }
             }
-            mma_commit_if(&drain[1], leader);
-            if (leader) drain_wait(&drain[1], 0);
+            if (elect_one()) {
+                mma_commit(&drain[1]);
+                drain_wait(&drain[1], 0);
+            }
             __syncwarp();
         }
     } else {

@@ -74,15 +74,13 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
 }
 
 // S (+)= Q . K^T over two slabs, dims 64 kChunk .. 64 kChunk + 127, in the group of block parity
-// par (slots kChunk mod 4 and the next). The descriptors are built anew at every call: kept
-// across calls they would be more than the warp's registers hold.
+// par (slots kChunk mod 4 and the next).
 template <int kChunk>
 __device__ __forceinline__ void issue_qk(const uint8_t *smem, uint32_t tmem, int par,
                                          uint32_t acc0) {
     constexpr uint32_t idesc = idesc_bf16(kRows, kBlock, false, false);
-    uint64_t qd = desc_sw128(smem_u32(smem + kOffQ) + (kChunk < kQSmem ? kChunk : 0) * kSlab, 16, 1024);
-    uint64_t kd = desc_sw128(smem_u32(smem + kOffKV) + (4 * par + kChunk % 4) * kSlab, 16, 1024);
-    asm volatile("" : "+l"(qd), "+l"(kd), "+r"(tmem));
+    const uint64_t qd = desc_sw128(smem_u32(smem + kOffQ) + (kChunk < kQSmem ? kChunk : 0) * kSlab, 16, 1024);
+    const uint64_t kd = desc_sw128(smem_u32(smem + kOffKV) + (4 * par + kChunk % 4) * kSlab, 16, 1024);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -101,8 +99,7 @@ __device__ __forceinline__ void issue_qk(const uint8_t *smem, uint32_t tmem, int
 __device__ __forceinline__ void issue_pv(const uint8_t *smem, uint32_t tmem, int par, int half,
                                          uint32_t acc0) {
     constexpr uint32_t idesc = idesc_bf16(kRows, 128, false, true);
-    uint64_t vd = desc_sw128(smem_u32(smem + kOffKV) + (4 * par + 2 * half) * kSlab, kSlab, 1024);
-    asm volatile("" : "+l"(vd), "+r"(tmem));
+    const uint64_t vd = desc_sw128(smem_u32(smem + kOffKV) + (4 * par + 2 * half) * kSlab, kSlab, 1024);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
         mma_bf16_ta(tmem + kOCol + 128 * half, tmem + kPCol + 8 * kk, vd + ((kk * 2048) >> 4),
@@ -451,7 +448,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             // QK own (b), PV second half (b - 1): PV runs where QK would wait, for the own slabs
             // and for the softmax to read S, and the two never alternate MMA by MMA (which
             // costs about 130 cycles a change)
-            const bool leader = lane == 0;
             Walk walk(p, sStart);
             Segment x;
             int i = 0, g = 0;  // g: blocks begun
@@ -466,14 +462,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!(ok = mbar_wait(s_free, par ^ 1, abort_flag, p.status))) break;
                         if (!(ok = mbar_wait(&full[2 * par], 0, abort_flag, p.status))) break;
                         tc_fence_after();
-                        if (leader) {
+                        if (elect_one()) {
                             if (x.part) issue_qk<0>(smem, tmem, par, 0u);
                             else issue_qk<4>(smem, tmem, par, 0u);
                             mma_commit(&f_free[2 * par]);
                         }
                         __syncwarp();
                         if (!(ok = mbar_wait(&full[2 * par + 1], 0, abort_flag, p.status))) break;
-                        if (leader) {
+                        if (elect_one()) {
                             if (x.part) issue_qk<2>(smem, tmem, par, 1u);
                             else issue_qk<6>(smem, tmem, par, 1u);
                             mma_commit(&f_free[2 * par + 1]);
@@ -486,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             !(ok = mbar_wait(o_free, (i - 1) & 1, abort_flag, p.status)))
                             break;
                         tc_fence_after();
-                        if (leader) {
+                        if (elect_one()) {
                             issue_pv(smem, tmem, par ^ 1, 0, b > 1);
                             mma_commit(&v_free[2 * (par ^ 1)]);
                         }
@@ -495,13 +491,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (b < x.nb) {
                         if (!(ok = mbar_wait(&full[2 * par], 1, abort_flag, p.status))) break;
                         tc_fence_after();
-                        if (leader) {
+                        if (elect_one()) {
                             if (x.part) issue_qk<4>(smem, tmem, par, 1u);
                             else issue_qk<0>(smem, tmem, par, 1u);
                         }
                         __syncwarp();
                         if (!(ok = mbar_wait(&full[2 * par + 1], 1, abort_flag, p.status))) break;
-                        if (leader) {
+                        if (elect_one()) {
                             if (x.part) issue_qk<6>(smem, tmem, par, 1u);
                             else issue_qk<2>(smem, tmem, par, 1u);
                             mma_commit(s_full);
@@ -512,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (b > 0) {
                         // (par is still that of the step's first product)
-                        if (leader) {
+                        if (elect_one()) {
                             issue_pv(smem, tmem, par ^ 1, 1, b > 1);
                             mma_commit(&v_free[2 * (par ^ 1) + 1]);
                             mma_commit(pv_done);
@@ -522,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (leader) {
+            if (elect_one()) {
                 mma_commit(drain);
                 drain_wait(drain, 0);
             }

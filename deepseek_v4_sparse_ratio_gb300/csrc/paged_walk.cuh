@@ -315,24 +315,16 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, ui
         : "memory");
 }
 
-// tcgen05.mma / tcgen05.commit run by every lane of a converged warp but issued only where
-// `issue` is non-zero: the warp stays converged and the descriptors in uniform registers.
-__device__ __forceinline__ void mma_bf16_if(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate, uint32_t issue) {
+// One lane of a converged warp, the same one every time. A branch on it (rather than on
+// lane == 0) lets the compiler keep what the tensor instructions take in uniform registers:
+// M=128 N=16 MMAs issue one per 39 cycles behind it, one per 59 behind lane == 0, one per 81
+// from a converged warp with a predicate (the products here need one per 48 to 64).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
-        : "memory");
-}
-
-__device__ __forceinline__ void mma_commit_if(uint64_t *bar, uint32_t issue) {
-    asm volatile(
-        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
-            smem_u32(bar)),
-        "r"(issue)
-        : "memory");
+        "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n"
+        : "=r"(r));
+    return r != 0;
 }
 
 __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
