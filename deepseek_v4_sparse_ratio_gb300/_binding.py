@@ -266,12 +266,18 @@ def dsa_prefill_chunk_host(state: "PoolState", ws: PrefillWorkspace, raw_kv_h, r
     _check(rc, "dsa_prefill_chunk_host")
 
 
-def _take(where: str, name: str, t, dtype, shape, device) -> int:
-    """The address of a packed device tensor of this dtype and shape (-1: any size)."""
-    if (t.dtype is not dtype or t.device.index != device or t.dim() != len(shape)
-            or not t.is_contiguous()
-            or any(n >= 0 and m != n for m, n in zip(t.shape, shape))):
-        want = ", ".join("*" if n < 0 else str(n) for n in shape)
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # absent from CPU builds
+
+
+def _stream_of(stream, device):
+    """As _s, by the shorter way to the current stream of `device`."""
+    return _raw_stream(device) if stream is None and _raw_stream is not None else _s(stream)
+
+
+def _take(where: str, name: str, t, dtype, device, want: str, fits: bool) -> int:
+    """The address of a packed tensor of this dtype on this device whose shape fits."""
+    if not (fits and t.dtype is dtype and t.get_device() == device and t.is_contiguous()):
         raise DsaError(DSA_ERR_ARG, f"{where}: {name} has to be a packed {dtype} tensor [{want}] "
                                     f"on cuda:{device}")
     return t.data_ptr()
@@ -279,25 +285,32 @@ def _take(where: str, name: str, t, dtype, shape, device) -> int:
 
 def _paged(where: str, new_start, seq_len, page_table, pages, cos_sin, device):
     """The arguments both paged calls share, in the ABI's order."""
-    n_seqs, max_pages = page_table.shape if page_table.dim() == 2 else (0, 0)
-    if (pages.dtype is not torch.bfloat16 or pages.device.index != device or pages.dim() != 3
-            or pages.shape[2] != DIM or pages.stride(2) != 1 or pages.stride(1) != DIM):
-        raise DsaError(DSA_ERR_ARG, f"{where}: pages has to be a torch.bfloat16 tensor "
+    table = tuple(page_table.shape)
+    n_seqs, max_pages = table if len(table) == 2 else (-1, -1)
+    shape, strides = tuple(pages.shape), pages.stride()
+    if not (pages.dtype is _BF16 and pages.get_device() == device and len(shape) == 3
+            and shape[2] == DIM and strides[2] == 1 and strides[1] == DIM):
+        raise DsaError(DSA_ERR_ARG, f"{where}: pages has to be a {_BF16} tensor "
                                     f"[*, *, {DIM}] on cuda:{device} with packed pages")
-    n_pages, page_size = pages.shape[0], pages.shape[1]
-    stride = pages.stride(0) if n_pages > 1 else page_size * DIM
-    return (_take(where, "new_start", new_start, torch.int32, (n_seqs + 1,), device),
-            _take(where, "seq_len", seq_len, torch.int32, (n_seqs,), device), n_seqs,
-            _take(where, "page_table", page_table, torch.int32, (-1, -1), device), max_pages,
-            pages.data_ptr(), n_pages, stride, page_size,
-            None if cos_sin is None else _take(where, "cos_sin", cos_sin, torch.float32,
-                                               (-1, ROPE_DIM // 2, 2), device),
-            0 if cos_sin is None else cos_sin.shape[0])
+    n_pages, page_size = shape[0], shape[1]
+    angles, n_pos = None, 0
+    if cos_sin is not None:
+        at = tuple(cos_sin.shape)
+        angles = _take(where, "cos_sin", cos_sin, _F32, device, f"*, {ROPE_DIM // 2}, 2",
+                       at[1:] == (ROPE_DIM // 2, 2))
+        n_pos = at[0]
+    return (_take(where, "new_start", new_start, _I32, device, str(n_seqs + 1),
+                  new_start.shape == (n_seqs + 1,)),
+            _take(where, "seq_len", seq_len, _I32, device, str(n_seqs),
+                  seq_len.shape == (n_seqs,)), n_seqs,
+            _take(where, "page_table", page_table, _I32, device, "*, *", n_seqs >= 0), max_pages,
+            pages.data_ptr(), n_pages, strides[0] if n_pages > 1 else page_size * DIM, page_size,
+            angles, n_pos)
 
 
 def _status(where: str, dev_status, device):
-    return None if dev_status is None else _take(where, "dev_status", dev_status, torch.int32,
-                                                 (1,), device)
+    return None if dev_status is None else _take(where, "dev_status", dev_status, _I32, device,
+                                                 "1", dev_status.shape == (1,))
 
 
 def dsa_paged_append(kv, new_start, seq_len, page_table, pages, cos_sin=None, dev_status=None,
@@ -306,10 +319,11 @@ def dsa_paged_append(kv, new_start, seq_len, page_table, pages, cos_sin=None, de
     [n_pages, page_size, 512]. Tensors are on the current device; see include/dsa.h."""
     where = "dsa_paged_append"
     dev = torch.cuda.current_device()
-    rc = load().dsa_paged_append(
-        _take(where, "kv", kv, torch.bfloat16, (-1, DIM), dev), kv.shape[0],
-        *_paged(where, new_start, seq_len, page_table, pages, cos_sin, dev),
-        _status(where, dev_status, dev), _s(stream))
+    rows = tuple(kv.shape)
+    rc = (_lib or load()).dsa_paged_append(
+        _take(where, "kv", kv, _BF16, dev, f"*, {DIM}", len(rows) == 2 and rows[1] == DIM),
+        rows[0], *_paged(where, new_start, seq_len, page_table, pages, cos_sin, dev),
+        _status(where, dev_status, dev), _stream_of(stream, dev))
     _check(rc, where)
 
 
@@ -320,11 +334,12 @@ def dsa_paged_attn(q, new_start, seq_len, page_table, pages, window: int, scale:
     DSA_PAGED_WORKSPACE_BYTES. Tensors are on the current device; see include/dsa.h."""
     where = "dsa_paged_attn"
     dev = torch.cuda.current_device()
-    qp = _take(where, "q", q, torch.bfloat16, (-1, -1, DIM), dev)
-    op = _take(where, "out", out, torch.bfloat16, q.shape, dev)
-    rc = load().dsa_paged_attn(
-        qp, q.shape[1], q.shape[0],
-        *_paged(where, new_start, seq_len, page_table, pages, cos_sin, dev), window, scale,
-        _take(where, "workspace", workspace, workspace.dtype, (-1,) * workspace.dim(), dev),
-        _nbytes(workspace), op, _status(where, dev_status, dev), _s(stream))
+    shape = tuple(q.shape)
+    rc = (_lib or load()).dsa_paged_attn(
+        _take(where, "q", q, _BF16, dev, f"*, *, {DIM}", len(shape) == 3 and shape[2] == DIM),
+        shape[1], shape[0], *_paged(where, new_start, seq_len, page_table, pages, cos_sin, dev),
+        window, scale, _take(where, "workspace", workspace, workspace.dtype, dev, "*", True),
+        _nbytes(workspace),
+        _take(where, "out", out, _BF16, dev, ", ".join(map(str, shape)), out.shape == shape),
+        _status(where, dev_status, dev), _stream_of(stream, dev))
     _check(rc, where)

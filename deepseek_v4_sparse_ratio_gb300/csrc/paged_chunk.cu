@@ -356,65 +356,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             // lane i < np loads page i of the first slab, lane np + i of the second. The block's
             // table entries are read one block ahead.
             const int prows = min(1 << p.b.page_shift, kBlock), np = kBlock / prows;
-            const int second = lane >= np, page = second ? lane - np : lane;
+            const int second = lane >= np, page = second ? lane - np : lane;  // (np: no page)
             uint8_t *const dst0 = sKV + second * kSlab + page * prows * 128;
-            Walk walk(p, sStart);
-            Segment x;
-            int g = 0, at = 0;
+            PageWalk walk(p, sStart);
+            const int blocks = sStart[4];
+            int row, row_next = 0, own, own_next = walk.x.part, g = 0, at = 0;
+            int32_t e, e_next = walk.next(p, page, prows, np, row_next);
             bool ok = true;
-            auto entry = [&](const Segment &y, int blk) -> int32_t {
-                const int pos = blk * kBlock + page * prows;
-                if (lane >= 2 * np || pos > y.posl || pos <= y.lo - prows) return -1;
-                const int32_t e =
-                    __ldg(p.b.page_table + int64_t{y.s} * p.b.max_pages + (pos >> p.b.page_shift));
-                if (e < 0 || e >= p.b.n_pages) {
-                    report(p.status, DSA_ERR_BOUNDS);
-                    return -1;
-                }
-                return e;
-            };
-            bool have = walk.next(p, x);
-            int32_t e_next = have ? entry(x, x.blk) : -1;
-            while (have && ok) {
-                Segment y;
-                const bool more = walk.next(p, y);
-                for (int b = 0; b < x.nb; ++b, ++g) {
-                    const int32_t e = e_next;
-                    const int par = g & 1;
-                    const uint32_t use = (g >> 1) & 1;
-                    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, e >= 0);  // both slabs' pages
-                    const uint32_t bytes = static_cast<uint32_t>(__popc(mask)) * prows * 128;
-                    const int y0 =
-                        ((x.blk + b) * kBlock + page * prows) & ((1 << p.b.page_shift) - 1);
+            for (; g < blocks; ++g) {
+                e = e_next;
+                row = row_next;
+                own = own_next;
+                own_next = walk.x.part;
+                e_next = walk.next(p, page, prows, np, row_next);
+                const int par = g & 1;
+                const uint32_t use = (g >> 1) & 1;
+                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, e >= 0);  // both slabs' pages
+                const uint32_t bytes = static_cast<uint32_t>(__popc(mask)) * prows * 128;
 #pragma unroll 1
-                    for (at = 0; at < 4; ++at) {
-                        // the pair's own slabs of the block two back used by PV; then its
-                        // foreign slabs used by QK
-                        const int pair = 2 * par + (at & 1);
-                        ok = at < 2 ? mbar_wait(&v_free[pair], use ^ 1, abort_flag, p.status)
-                                    : mbar_wait(&f_free[pair], use, abort_flag, p.status);
-                        ok = __all_sync(0xFFFFFFFFu, ok);
-                        if (!ok) break;
-                        if (lane == 0) {
-                            if (at == 0) {
-                                sPages[par] = mask & ((1u << np) - 1u);
-                                mbar_arrive(&pg_full[par]);
-                            }
-                            mbar_expect_tx(&full[pair], bytes);
-                        }
-                        __syncwarp();
-                        const int half = (at >> 1) ^ 1 ^ x.part;  // of the dims: foreign, own
-                        if (e >= 0)
-                            tma_load_3d(dst0 + 2 * pair * kSlab, &tm_kv, &full[pair],
-                                        (4 * half + 2 * (at & 1) + second) * 64, y0, e);
-                    }
+                for (at = 0; at < 4; ++at) {
+                    // the pair's own slabs of the block two back used by PV; then its foreign
+                    // slabs used by QK
+                    const int pair = 2 * par + (at & 1);
+                    ok = at < 2 ? mbar_wait(&v_free[pair], use ^ 1, abort_flag, p.status)
+                                : mbar_wait(&f_free[pair], use, abort_flag, p.status);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
-                    if (b + 1 < x.nb) e_next = entry(x, x.blk + b + 1);
-                    else e_next = more ? entry(y, y.blk) : -1;
+                    if (lane == 0) {
+                        if (at == 0) {
+                            sPages[par] = mask & ((1u << np) - 1u);
+                            mbar_arrive(&pg_full[par]);
+                        }
+                        mbar_expect_tx(&full[pair], bytes);
+                    }
+                    __syncwarp();
+                    const int half = at < 2 ? own ^ 1 : own;  // of the dims
+                    if (e >= 0)
+                        tma_load_3d(dst0 + 2 * pair * kSlab, &tm_kv, &full[pair],
+                                    (4 * half + 2 * (at & 1) + second) * 64, row, e);
                 }
                 if (!ok) break;
-                x = y;
-                have = more;
             }
             if (!ok && lane == 0) {
                 // gave up in block g before its step `at`: no copy into this CTA's shared memory

@@ -207,6 +207,41 @@ struct Walk {
     }
 };
 
+// Walks a run block by block for the loaders: the lane's page of each block, ahead of its load.
+struct PageWalk {
+    Walk walk;
+    Segment x;
+    int b;
+    bool have;
+
+    __device__ __forceinline__ PageWalk(const Params &p, const int *start) : walk(p, start), b(0) {
+        have = walk.next(p, x);
+    }
+
+    // The page that holds this lane's rows [pos, pos + prows) of the next block (-1: no token
+    // needs one, or a bad table entry), and the row of the page they begin at.
+    __device__ __forceinline__ int32_t next(const Params &p, int page, int prows, int pages,
+                                            int &row) {
+        int32_t e = -1;
+        if (have) {
+            const int pos = (x.blk + b) * kBlock + page * prows;
+            row = pos & ((1 << p.b.page_shift) - 1);
+            if (page < pages && pos <= x.posl && pos > x.lo - prows) {
+                e = __ldg(p.b.page_table + int64_t{x.s} * p.b.max_pages + (pos >> p.b.page_shift));
+                if (e < 0 || e >= p.b.n_pages) {
+                    report(p.status, DSA_ERR_BOUNDS);
+                    e = -1;
+                }
+            }
+            if (++b == x.nb) {
+                b = 0;
+                have = walk.next(p, x);
+            }
+        }
+        return e;
+    }
+};
+
 // Position of row r of a unit.
 __device__ __forceinline__ int row_pos(const Params &p, int posf, int r) {
     return p.tpu == 1 ? posf : posf + r / p.rpt;

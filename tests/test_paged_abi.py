@@ -92,7 +92,7 @@ def test_binding_refuses_tensors_of_another_kind(lib, monkeypatch):
         B.dsa_paged_attn(torch.zeros(3, 64, 512, dtype=torch.bfloat16), *common, 0, 0.1,
                          torch.zeros(8), torch.zeros(3, 64, 512, dtype=torch.bfloat16))
     # shapes and types are looked at the same way on the device the tensors are said to be on
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
     for bad in (kv.float(), kv[:, :256], torch.zeros(512, 3, dtype=torch.bfloat16).t()):
         with pytest.raises(B.DsaError, match="kv"):
             B.dsa_paged_append(bad, *common)
