@@ -44,8 +44,9 @@ __device__ __forceinline__ uint32_t rotate_pair(uint32_t v, float c, float s) {
 // One warp per row; lane l moves 16-byte pieces l and l + 32, and the last eight pieces
 // hold the rotated pairs.
 __global__ void __launch_bounds__(kAppendWarps * 32)
-    paged_append_kernel(const PagedBatch b, const uint4 *__restrict__ kv, __nv_bfloat16 *pages,
+    paged_append_kernel(const PagedBatch b, const uint4 *kv, __nv_bfloat16 *pages,
                         int32_t *status) {
+    wait_before();
     const int lane = threadIdx.x & 31;
     const int64_t r = int64_t{blockIdx.x} * kAppendWarps + (threadIdx.x >> 5);
     if (blockIdx.x == 0) {
@@ -138,7 +139,7 @@ extern "C" int dsa_paged_append(const void *kv, int64_t n_new, const int32_t *ne
                                n_pages, page_stride, page_size, cos_sin, n_pos, &b);
     if (rc != DSA_OK) return rc;
     const unsigned grid = static_cast<unsigned>((n_new + kAppendWarps - 1) / kAppendWarps);
-    paged_append_kernel<<<grid, kAppendWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(
-        b, static_cast<const uint4 *>(kv), static_cast<__nv_bfloat16 *>(pages), dev_status);
-    return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+    return launch_overlapped(paged_append_kernel, grid, kAppendWarps * 32, 0,
+                             static_cast<cudaStream_t>(stream), b, static_cast<const uint4 *>(kv),
+                             static_cast<__nv_bfloat16 *>(pages), dev_status);
 }

@@ -133,31 +133,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     int *sStart = reinterpret_cast<int *>(tmem_holder + 4);  // [5] start of this CTA's run
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) {
-        mbar_init(q_full, 1);
-        mbar_init(q_free, 1);
-        mbar_init(q_turned, kTurnThreads);
-        for (int m = 0; m < 4; ++m) {
-            mbar_init(&kv_full[m], 1);
-            mbar_init(&kv_free[m], 1);
+    if (warp == 0) {
+        // arrivals a phase takes: 128 turning threads on q_turned; 8 softmax warps on s_free
+        // and o_free, 256 softmax threads on p_full; on s_full (S^T of a block may be read) QK's
+        // commit for it and PV's for the block before; one on the others
+        int n = 1;
+        uint64_t *bar = bars + lane;
+        if (bar == q_turned) n = kTurnThreads;
+        if (bar == &s_free[0] || bar == &s_free[1] || bar == o_free) n = 8;
+        if (bar == p_full) n = kSoftThreads;
+        if (bar == s_full) n = 2;
+        if (bar <= q_turned) mbar_init(bar, n);
+        if (lane == 31) {
+            *abort_flag = 0;
+            sStart[4] = 0;
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&x_full[i], 1);
-            mbar_init(&s_free[i], 8);  // one arrival per softmax warp
-            mbar_init(&drain[i], 1);
-        }
-        // S^T of a block is ready once its QK is done (QK warp) and the previous block's PV no
-        // longer reads P or writes O^T (PV warp)
-        mbar_init(s_full, 2);
-        mbar_init(p_full, kSoftThreads);
-        mbar_init(o_full, 1);
-        mbar_init(o_free, 8);
-        *abort_flag = 0;
-        sStart[4] = 0;
         fence_barrier_init();
     }
     if (warp == kPvWarp) tmem_alloc(tmem_holder, 512);
-
+    if (tid == 32 * kQkWarp) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_kv);
+    }
+    wait_before();
     const int cta = static_cast<int>(blockIdx.x);
     find_run(p, reinterpret_cast<int64_t *>(sKV), sStart);
     const uint32_t tmem = *tmem_holder;
@@ -656,94 +654,160 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ the join
 
 // out[row] = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M), M = max_p m_p, over the parts of a
-// unit: one row (kDims of its dims) at a time per CTA, its parts shared by groups of kDims / 4
-// threads (four dims each). The parts are added in the same order every time.
-constexpr int kJoinThreads = 512;
+// unit, always added in the same order. A warp takes one row: up to kFew parts (what a run's
+// ends leave of most batches) with all their loads in flight at once, 128 dims a load. A row of
+// more parts is taken in pieces of 32 dims, one per warp: four groups of eight lanes share the
+// parts, eight loads in flight each, so that one unit of 147 parts (a single token at 128K)
+// takes a few microseconds too.
+constexpr int kJoinWarps = 8;
+constexpr int kFew = 4;
+
+__device__ __forceinline__ void store_joined(const Params &p, const JoinDesc &d, int r, int dim,
+                                             float4 acc, float inv) {
+    acc.x *= inv;
+    acc.y *= inv;
+    acc.z *= inv;
+    acc.w *= inv;
+    if (p.b.cos_sin && dim >= kD - kRope) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(
+            p.b.cos_sin + int64_t{row_pos(p, d.pos, r)} * kRope + (dim - (kD - kRope))));
+        acc = make_float4(acc.x * a.x + acc.y * a.y, acc.y * a.x - acc.x * a.y,
+                          acc.z * a.z + acc.w * a.w, acc.w * a.z - acc.z * a.w);
+    }
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z, acc.w);
+    *reinterpret_cast<uint2 *>(p.out + (d.row + r) * kD + dim) = make_uint2(
+        *reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+}
+
+__device__ __forceinline__ void add_scaled(float4 &acc, float4 o, float w) {
+    acc.x = fmaf(o.x, w, acc.x);
+    acc.y = fmaf(o.y, w, acc.y);
+    acc.z = fmaf(o.z, w, acc.z);
+    acc.w = fmaf(o.w, w, acc.w);
+}
 
 template <int kDims>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const Params p, int ctas) {
-    constexpr int kT = kDims / 4, kGroups = kJoinThreads / kT;
-    __shared__ int active[kMaxCtas];
-    __shared__ int count[kJoinThreads / 32];
-    __shared__ float weight[kMaxCtas];
-    __shared__ float red[2][kJoinThreads / 32];
-    __shared__ float4 sum[kGroups][kT];
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    paged_join_kernel(const __grid_constant__ Params p, int ctas) {
+    constexpr int kWords = (kMaxCtas + 31) / 32, kLoads = kDims / 128;
+    __shared__ JoinDesc descs[kMaxCtas];
+    __shared__ int owner[kMaxCtas];           // the CTA a descriptor is of
+    __shared__ int count[2][kWords];
+    __shared__ float weight[kJoinWarps][kWords * 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const JoinDesc *desc = reinterpret_cast<const JoinDesc *>(p.ws + kWsDesc);
-    const bool has = tid < ctas && desc[tid].parts > 0;
-    const uint32_t vote = __ballot_sync(0xFFFFFFFFu, has);
-    if (lane == 0) count[warp] = __popc(vote);
-    __syncthreads();
-    int before = 0, n = 0;
-    for (int w = 0; w < kJoinThreads / 32; ++w) {
-        if (w < warp) before += count[w];
-        n += count[w];
+    wait_before();
+    // the units of few parts first, then the others
+    JoinDesc d = {};
+    if (tid < ctas) d = reinterpret_cast<const JoinDesc *>(p.ws + kWsDesc)[tid];
+    const uint32_t few = __ballot_sync(0xFFFFFFFFu, d.parts > 0 && d.parts <= kFew);
+    const uint32_t many = __ballot_sync(0xFFFFFFFFu, d.parts > kFew);
+    if (lane == 0 && warp < kWords) {
+        count[0][warp] = __popc(few);
+        count[1][warp] = __popc(many);
     }
-    if (has) active[before + __popc(vote & ((1u << lane) - 1u))] = tid;
     __syncthreads();
-    for (int it = blockIdx.x; it < n * p.rows; it += gridDim.x) {
-        const int cta = active[it / p.rows], r = it % p.rows;
-        const JoinDesc d = desc[cta];
-        if (r >= d.nrows) continue;
-        auto slot_of = [&](int k) { return k == 0 ? 2 * cta + d.slot0 : 2 * (cta + k); };
-        float2 ml = make_float2(kNoMax, 0.0f);
-        if (tid < d.parts)
-            ml = reinterpret_cast<const float2 *>(p.ws + kWsMl)[slot_of(tid) * kMaxRows + r];
-        const float wm = redux_max(ml.x);
-        if (lane == 0) red[0][warp] = wm;
-        __syncthreads();
-        float M = red[0][0];
-        for (int w = 1; w < kJoinThreads / 32; ++w) M = fmaxf(M, red[0][w]);
-        const float wt = tid < d.parts ? ex2(ml.x - M) : 0.0f;
-        if (tid < d.parts) weight[tid] = wt;
-        float ls = tid < d.parts ? ml.y * wt : 0.0f;
+    int before[2] = {0, 0}, n[2] = {0, 0};
+    for (int k = 0; k < 2; ++k)
+        for (int w = 0; w < kWords; ++w) {
+            if (w < warp) before[k] += count[k][w];
+            n[k] += count[k][w];
+        }
+    if (d.parts > 0) {
+        const int k = d.parts > kFew;
+        const uint32_t below = (k ? many : few) & ((1u << lane) - 1u);
+        const int at = (k ? n[0] : 0) + before[k] + __popc(below);
+        descs[at] = d;
+        owner[at] = tid;
+    }
+    __syncthreads();
+    const float *const parts_o = reinterpret_cast<const float *>(p.ws + kWsO);
+    const float2 *const parts_ml = reinterpret_cast<const float2 *>(p.ws + kWsMl);
+    const int stride = static_cast<int>(gridDim.x) * kJoinWarps;
+    const int first = static_cast<int>(blockIdx.x) * kJoinWarps + warp;
+
+    for (int it = first; it < n[0] * p.rows; it += stride) {
+        const JoinDesc &u = descs[it / p.rows];
+        const int cta = owner[it / p.rows], r = it % p.rows;
+        if (r >= u.nrows) continue;
+        float4 o[kFew][kLoads];
+        float2 ml[kFew];
 #pragma unroll
-        for (int w = 16; w >= 1; w >>= 1) ls += __shfl_xor_sync(0xFFFFFFFFu, ls, w);
-        if (lane == 0) red[1][warp] = ls;
-        __syncthreads();
-        const int grp = tid / kT, t = tid % kT;
-        const float4 *src = reinterpret_cast<const float4 *>(p.ws + kWsO) + r * kT + t;
+        for (int k = 0; k < kFew; ++k) {
+            const int slot = k == 0 ? 2 * cta + u.slot0 : 2 * (cta + k);
+            ml[k] = make_float2(kNoMax, 0.0f);
+            if (k < u.parts) {
+                ml[k] = parts_ml[slot * kMaxRows + r];
+#pragma unroll
+                for (int j = 0; j < kLoads; ++j)
+                    o[k][j] = *reinterpret_cast<const float4 *>(
+                        parts_o + slot * kSlotFloats + r * kDims + 128 * j + 4 * lane);
+            }
+        }
+        float M = ml[0].x, sum = 0.0f;
+#pragma unroll
+        for (int k = 1; k < kFew; ++k) M = fmaxf(M, ml[k].x);
+        float4 acc[kLoads] = {};
+#pragma unroll
+        for (int k = 0; k < kFew; ++k) {
+            if (k < u.parts) {
+                const float w = ex2(ml[k].x - M);
+                sum += ml[k].y * w;
+#pragma unroll
+                for (int j = 0; j < kLoads; ++j) add_scaled(acc[j], o[k][j], w);
+            }
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            store_joined(p, u, r, (kDims < kD ? u.part * kDims : 0) + 128 * j + 4 * lane, acc[j],
+                         inv);
+    }
+
+    const int pieces = p.rows * (kDims / 32);  // of a unit
+    for (int it = first; it < n[1] * pieces; it += stride) {
+        const JoinDesc &u = descs[n[0] + it / pieces];
+        const int cta = owner[n[0] + it / pieces];
+        const int r = it % pieces / (kDims / 32), dim0 = it % (kDims / 32) * 32;
+        if (r >= u.nrows) continue;
+        auto slot_of = [&](int k) { return k == 0 ? 2 * cta + u.slot0 : 2 * (cta + k); };
+        float2 v[kWords];
+        float M = kNoMax;
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+            const int k = 32 * j + lane;
+            v[j] = k < u.parts ? parts_ml[slot_of(k) * kMaxRows + r] : make_float2(kNoMax, 0.0f);
+            M = fmaxf(M, v[j].x);
+        }
+        M = redux_max(M);
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+            const float w = ex2(v[j].x - M);
+            weight[warp][32 * j + lane] = w;
+            sum += v[j].y * w;
+        }
+#pragma unroll
+        for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, w);
+        __syncwarp();
+        const int grp = lane >> 3, dim = dim0 + 4 * (lane & 7);
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int k = grp; k < d.parts; k += kGroups) {
-            const float4 v = src[int64_t{slot_of(k)} * (kSlotFloats / 4)];
-            const float w = weight[k];
-            acc.x = fmaf(v.x, w, acc.x);
-            acc.y = fmaf(v.y, w, acc.y);
-            acc.z = fmaf(v.z, w, acc.z);
-            acc.w = fmaf(v.w, w, acc.w);
+#pragma unroll 8
+        for (int k = grp; k < u.parts; k += 4)
+            add_scaled(acc, *reinterpret_cast<const float4 *>(
+                                parts_o + slot_of(k) * kSlotFloats + r * kDims + dim),
+                       weight[warp][k]);
+        __syncwarp();  // the weights are read
+#pragma unroll
+        for (int w = 8; w <= 16; w <<= 1) {
+            acc.x += __shfl_xor_sync(0xFFFFFFFFu, acc.x, w);
+            acc.y += __shfl_xor_sync(0xFFFFFFFFu, acc.y, w);
+            acc.z += __shfl_xor_sync(0xFFFFFFFFu, acc.z, w);
+            acc.w += __shfl_xor_sync(0xFFFFFFFFu, acc.w, w);
         }
-        sum[grp][t] = acc;
-        __syncthreads();
-        if (grp == 0) {
-            for (int k = 1; k < kGroups; ++k) {
-                const float4 v = sum[k][t];
-                acc.x += v.x;
-                acc.y += v.y;
-                acc.z += v.z;
-                acc.w += v.w;
-            }
-            float tot = 0.0f;
-            for (int w = 0; w < kJoinThreads / 32; ++w) tot += red[1][w];
-            const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
-            acc.x *= inv;
-            acc.y *= inv;
-            acc.z *= inv;
-            acc.w *= inv;
-            const int dim = (kDims < kD ? d.part * kDims : 0) + 4 * t;
-            if (p.b.cos_sin && dim >= kD - kRope) {
-                const float4 a = __ldg(reinterpret_cast<const float4 *>(
-                    p.b.cos_sin + int64_t{row_pos(p, d.pos, r)} * kRope + (dim - (kD - kRope))));
-                acc = make_float4(acc.x * a.x + acc.y * a.y, acc.y * a.x - acc.x * a.y,
-                                  acc.z * a.z + acc.w * a.w, acc.w * a.z - acc.z * a.w);
-            }
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y);
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z, acc.w);
-            *reinterpret_cast<uint2 *>(p.out + (d.row + r) * kD + dim) =
-                make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
-                           *reinterpret_cast<const uint32_t *>(&hi));
-        }
-        __syncthreads();
+        if (grp == 0)
+            store_joined(p, u, r, (kDims < kD ? u.part * kDims : 0) + dim, acc,
+                         sum == 0.0f ? 0.0f : 1.0f / sum);
     }
 }
 
@@ -836,14 +900,11 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
         return DSA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int ctas = std::min(sms, kMaxCtas);
-    if (chunk) {
-        rc = enqueue_paged_chunk(tm_q, tm_kv, p, q, ctas, s);
-        if (rc != DSA_OK) return rc;
-        paged_join_kernel<kD / 2><<<2 * ctas, kJoinThreads, 0, s>>>(p, ctas);
-    } else {
-        paged_attn_kernel<<<ctas, kThreads, kSmem, s>>>(tm_q, tm_kv, p);
-        if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
-        paged_join_kernel<kD><<<2 * ctas, kJoinThreads, 0, s>>>(p, ctas);
-    }
-    return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+    rc = chunk ? enqueue_paged_chunk(tm_q, tm_kv, p, q, ctas, s)
+               : launch_overlapped(paged_attn_kernel, ctas, kThreads, kSmem, s, tm_q, tm_kv, p);
+    if (rc != DSA_OK) return rc;
+    return chunk ? launch_overlapped(paged_join_kernel<kD / 2>, 4 * ctas, kJoinWarps * 32, 0, s,
+                                     p, ctas)
+                 : launch_overlapped(paged_join_kernel<kD>, 4 * ctas, kJoinWarps * 32, 0, s, p,
+                                     ctas);
 }

@@ -204,35 +204,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (smem_u32(smem) & 1023u) {  // the tiles' swizzle counts on it
+        wait_before();
         if (tid == 0) {
             report(p.status, DSA_ERR_CUDA);
             reinterpret_cast<JoinDesc *>(p.ws + kWsDesc)[blockIdx.x] = JoinDesc{};
         }
         return;
     }
-    if (tid == 0) {
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&f_free[i], 1);
-            mbar_init(&v_free[i], 1);
+    if (warp == 0) {
+        // arrivals a phase takes: a thread per row on q_tm, o_free and stat_full, 8 softmax
+        // warps on s_free, 256 softmax threads on p_full, one on the others
+        int n = 1;
+        uint64_t *bar = bars + lane;
+        if (bar == q_tm || bar == o_free || bar == stat_full) n = kRows;
+        if (bar == s_free) n = 8;
+        if (bar == p_full) n = 256;
+        if (bar <= drain) mbar_init(bar, n);
+        if (lane == 31) {
+            *abort_flag = 0;
+            sStart[4] = 0;
         }
-        for (int i = 0; i < 2; ++i) mbar_init(&pg_full[i], 1);
-        mbar_init(drain, 1);
-        mbar_init(q_full, 1);
-        mbar_init(q_tm, kRows);
-        mbar_init(q_free, 1);
-        mbar_init(s_full, 1);
-        mbar_init(s_free, 8);
-        mbar_init(p_full, 256);
-        mbar_init(pv_done, 1);
-        mbar_init(o_full, 1);
-        mbar_init(o_free, kRows);
-        mbar_init(stat_full, kRows);
-        *abort_flag = 0;
-        sStart[4] = 0;
         fence_barrier_init();
     }
     if (warp == kMmaWarp) tmem_alloc(tmem_holder, 512);
+    if (tid == 32 * kQWarp) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_kv);
+    }
+    wait_before();
     const int cta = static_cast<int>(blockIdx.x);
     find_run(p, reinterpret_cast<int64_t *>(sKV), sStart);
     const uint32_t tmem = *tmem_holder;
@@ -667,9 +666,8 @@ int prepare_paged_chunk() {
 
 int enqueue_paged_chunk(const CUtensorMap &tm_q, const CUtensorMap &tm_kv,
                         const paged::Params &p, const void *q, int ctas, cudaStream_t s) {
-    paged_chunk_kernel<<<ctas, kThreads, kSmem, s>>>(tm_q, tm_kv, p,
-                                                     static_cast<const __nv_bfloat16 *>(q));
-    return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+    return launch_overlapped(paged_chunk_kernel, ctas, kThreads, kSmem, s, tm_q, tm_kv, p,
+                             static_cast<const __nv_bfloat16 *>(q));
 }
 
 }  // namespace dsa

@@ -142,9 +142,19 @@ __device__ inline Place find_block(const Params &p, const PagedSeq &q, int s, in
         if (p.upt * blocks_before(p, q, mid) <= r) lo = mid;
         else hi = mid;
     }
-    r -= p.upt * blocks_before(p, q, lo);
+    int in = static_cast<int>(r - p.upt * blocks_before(p, q, lo)), part = 0;
     const int nb = group_blocks(p, q, lo);
-    return Place{s, lo, static_cast<int>(r) / nb, static_cast<int>(r) % nb};
+    if (in >= nb) {  // (upt is 1 or 2)
+        in -= nb;
+        part = 1;
+    }
+    return Place{s, lo, part, in};
+}
+
+// a / b for a >= 0, b > 0: the 32-bit division where both fit, as they nearly always do.
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
+    if (((a | b) >> 31) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
 }
 
 // A run of blocks of one unit.
@@ -257,12 +267,14 @@ __device__ __forceinline__ void find_run(const Params &p, int64_t *scratch, int 
     JoinDesc *desc = reinterpret_cast<JoinDesc *>(p.ws + kWsDesc) + cta;
     const int per = (p.b.n_seqs + kThreads - 1) / kThreads;
     const int s0 = min(tid * per, p.b.n_seqs), s1 = min(s0 + per, p.b.n_seqs);
-    int64_t mine = 0;
+    int64_t mine = 0, nb = 0;
+    PagedSeq q = {};
     for (int s = s0; s < s1; ++s) {
         bool bad;
-        const PagedSeq q = paged_seq(p.b, s, bad);
+        q = paged_seq(p.b, s, bad);
         if (bad && cta == 0) report(p.status, DSA_ERR_BOUNDS);
-        mine += p.upt * blocks_before(p, q, groups_of(p, q));
+        nb = p.upt * blocks_before(p, q, groups_of(p, q));
+        mine += nb;
     }
     int64_t incl = mine;
 #pragma unroll
@@ -275,53 +287,51 @@ __device__ __forceinline__ void find_run(const Params &p, int64_t *scratch, int 
     __syncthreads();
     tc_fence_after();
     int64_t total = 0;
+#pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) incl += scratch[w];
-        total += scratch[w];
+        const int64_t v = scratch[w];
+        if (w < warp) incl += v;
+        total += v;
     }
-    const int64_t run = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t run = div_pos(total + gridDim.x - 1, gridDim.x);
     const int64_t T0 = run * cta, T1 = min(T0 + run, total);
-    if (T0 < T1) {
-        const int64_t excl = incl - mine;
-        for (int which = 0; which < 2; ++which) {
-            const int64_t at = which ? T1 - 1 : T0;
-            if (at < excl || at >= incl) continue;
-            int64_t acc = excl;
-            for (int s = s0; s < s1; ++s) {
+    if (T0 >= T1) {
+        if (tid == 0) *desc = JoinDesc{};
+    } else if (mine > 0 && T0 < incl && T1 > incl - mine) {
+        // one of this thread's sequences holds the run's first block, its last, or both
+        int64_t acc = incl - mine;
+        for (int s = s0; s < s1; ++s) {
+            if (s1 - s0 > 1) {
                 bool bad;
-                const PagedSeq q = paged_seq(p.b, s, bad);
-                const int64_t nb = p.upt * blocks_before(p, q, groups_of(p, q));
-                if (at >= acc + nb) {
-                    acc += nb;
-                    continue;
-                }
-                const Place x = find_block(p, q, s, at - acc);
-                if (which == 0) {
-                    start[0] = x.s;
-                    start[1] = x.g;
-                    start[2] = x.part;
-                    start[3] = x.off;
-                    start[4] = static_cast<int>(T1 - T0);
-                } else {
-                    // a unit that begins in this run and ends in a later one
-                    const int64_t u0 = at - x.off, u1 = u0 + group_blocks(p, q, x.g);
-                    JoinDesc d = {};
-                    if (u0 >= T0 && u1 > T1) {
-                        const int t0 = x.g * p.tpu, t1 = min(t0 + p.tpu, q.n);
-                        d.row = unit_row(p, q, t0, x.part);
-                        d.nrows = unit_rows(p, t1 - t0, x.part);
-                        d.part = x.part;
-                        d.parts = static_cast<int>((u1 - 1) / run) - cta + 1;
-                        d.slot0 = u0 == T0 ? 0 : 1;
-                        d.pos = q.len - q.n + t0;
-                    }
-                    *desc = d;
-                }
-                break;
+                q = paged_seq(p.b, s, bad);
+                nb = p.upt * blocks_before(p, q, groups_of(p, q));
             }
+            if (T0 >= acc && T0 < acc + nb) {
+                const Place x = find_block(p, q, s, T0 - acc);
+                start[0] = x.s;
+                start[1] = x.g;
+                start[2] = x.part;
+                start[3] = x.off;
+                start[4] = static_cast<int>(T1 - T0);
+            }
+            if (T1 > acc && T1 <= acc + nb) {
+                // the unit of the last block: does it begin in this run and end in a later one?
+                const Place x = find_block(p, q, s, T1 - 1 - acc);
+                const int64_t u0 = T1 - 1 - x.off, u1 = u0 + group_blocks(p, q, x.g);
+                JoinDesc d = {};
+                if (u0 >= T0 && u1 > T1) {
+                    const int t0 = x.g * p.tpu, t1 = min(t0 + p.tpu, q.n);
+                    d.row = unit_row(p, q, t0, x.part);
+                    d.nrows = unit_rows(p, t1 - t0, x.part);
+                    d.part = x.part;
+                    d.parts = static_cast<int>(div_pos(u1 - 1, run)) - cta + 1;
+                    d.slot0 = u0 == T0 ? 0 : 1;
+                    d.pos = q.len - q.n + t0;
+                }
+                *desc = d;
+            }
+            acc += nb;
         }
-    } else if (tid == 0) {
-        *desc = JoinDesc{};
     }
     fence_proxy_async_smem();  // the scratch's tile is next written by TMA
     __syncthreads();
@@ -348,6 +358,10 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, ui
         " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
         "l"(tm), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
+}
+
+__device__ __forceinline__ void prefetch_tmap(const CUtensorMap *tm) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(tm) : "memory");
 }
 
 // One lane of a converged warp, the same one every time. A branch on it (rather than on
@@ -387,6 +401,7 @@ __device__ __forceinline__ uint32_t turn_pair(uint32_t v, float c, float s) {
 // The chunk kernel (paged_chunk.cu): one-time set-up, and its launch.
 constexpr int kChunkRows = 128;
 int prepare_paged_chunk();
+
 int enqueue_paged_chunk(const CUtensorMap &tm_q, const CUtensorMap &tm_kv,
                         const paged::Params &p, const void *q, int ctas, cudaStream_t s);
 
