@@ -436,16 +436,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // become zero in the tile (0 * inf in PV would reach every row); rows that
                     // do see the key have a NaN probability already. A key at a time: lane =
                     // 16-byte piece of four of its chunks.
-                    bool odd = false;
                     const int a = max(0, min(32, ra - hb)), e = max(0, min(32, rb - hb));
                     const uint32_t below_e = e == 32 ? 0xFFFFFFFFu : (1u << e) - 1u;
                     const uint32_t below_a = a == 32 ? 0xFFFFFFFFu : (1u << a) - 1u;
                     const uint32_t vis = below_e & ~below_a;
+                    float t4[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // NaN if any is not finite
 #pragma unroll
-                    for (int h = 0; h < 32; ++h) {
-                        odd = odd || !(fabsf(__uint_as_float(sa[h])) <= 3.4028234e38f);
+                    for (int h = 0; h < 32; ++h)
+                        t4[h & 3] = fmaf(__uint_as_float(sa[h]), 0.0f, t4[h & 3]);
+                    const bool odd = !((t4[0] + t4[1]) + (t4[2] + t4[3]) == 0.0f);
+#pragma unroll
+                    for (int h = 0; h < 32; ++h)
                         if (!((vis >> h) & 1u)) sa[h] = __float_as_uint(-INFINITY);
-                    }
                     uint32_t keys =
                         __ballot_sync(0xFFFFFFFFu, odd && live && (ra > 0 || rb < x.nrows));
                     if (keys) {
@@ -654,9 +656,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ the join
 
 // out[row] = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M), M = max_p m_p, over the parts of a
-// unit, always added in the same order. A warp takes one row: up to kFew parts (what a run's
-// ends leave of most batches) with all their loads in flight at once, 128 dims a load. A row of
-// more parts is taken in pieces of 32 dims, one per warp: four groups of eight lanes share the
+// unit, always added in the same order. A warp takes one row (or 32 rows x 32 dims of the chunk
+// kernel's units): up to kFew parts, what a run's ends leave of most batches, with all their
+// loads in flight at once. A row of more parts is taken in pieces of 32 dims, one per warp: four groups of eight lanes share the
 // parts, eight loads in flight each, so that one unit of 147 parts (a single token at 128K)
 // takes a few microseconds too.
 constexpr int kJoinWarps = 8;
@@ -678,6 +680,11 @@ __device__ __forceinline__ void store_joined(const Params &p, const JoinDesc &d,
     const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z, acc.w);
     *reinterpret_cast<uint2 *>(p.out + (d.row + r) * kD + dim) = make_uint2(
         *reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+}
+
+// Where dim `dim` (a multiple of four) of row r is in a slot of 128 rows x 256 dims.
+__device__ __forceinline__ int slot_at(int r, int dim) {
+    return dim / 8 * 8 * kChunkRows + r * 8 + dim % 8;
 }
 
 __device__ __forceinline__ void add_scaled(float4 &acc, float4 o, float w) {
@@ -726,42 +733,83 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     const int stride = static_cast<int>(gridDim.x) * kJoinWarps;
     const int first = static_cast<int>(blockIdx.x) * kJoinWarps + warp;
 
-    for (int it = first; it < n[0] * p.rows; it += stride) {
-        const JoinDesc &u = descs[it / p.rows];
-        const int cta = owner[it / p.rows], r = it % p.rows;
-        if (r >= u.nrows) continue;
-        float4 o[kFew][kLoads];
-        float2 ml[kFew];
+    if constexpr (kDims == kD) {
+        for (int it = first; it < n[0] * p.rows; it += stride) {
+            const JoinDesc &u = descs[it / p.rows];
+            const int cta = owner[it / p.rows], r = it % p.rows;
+            if (r >= u.nrows) continue;
+            float4 o[kFew][kLoads];
+            float2 ml[kFew];
 #pragma unroll
-        for (int k = 0; k < kFew; ++k) {
-            const int slot = k == 0 ? 2 * cta + u.slot0 : 2 * (cta + k);
-            ml[k] = make_float2(kNoMax, 0.0f);
-            if (k < u.parts) {
-                ml[k] = parts_ml[slot * kMaxRows + r];
+            for (int k = 0; k < kFew; ++k) {
+                const int slot = k == 0 ? 2 * cta + u.slot0 : 2 * (cta + k);
+                ml[k] = make_float2(kNoMax, 0.0f);
+                if (k < u.parts) {
+                    ml[k] = parts_ml[slot * kMaxRows + r];
 #pragma unroll
-                for (int j = 0; j < kLoads; ++j)
-                    o[k][j] = *reinterpret_cast<const float4 *>(
-                        parts_o + slot * kSlotFloats + r * kDims + 128 * j + 4 * lane);
+                    for (int j = 0; j < kLoads; ++j)
+                        o[k][j] = *reinterpret_cast<const float4 *>(
+                            parts_o + slot * kSlotFloats + r * kDims + 128 * j + 4 * lane);
+                }
+            }
+            float M = ml[0].x, sum = 0.0f;
+#pragma unroll
+            for (int k = 1; k < kFew; ++k) M = fmaxf(M, ml[k].x);
+            float4 acc[kLoads] = {};
+#pragma unroll
+            for (int k = 0; k < kFew; ++k) {
+                if (k < u.parts) {
+                    const float w = ex2(ml[k].x - M);
+                    sum += ml[k].y * w;
+#pragma unroll
+                    for (int j = 0; j < kLoads; ++j) add_scaled(acc[j], o[k][j], w);
+                }
+            }
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j)
+                store_joined(p, u, r, (kDims < kD ? u.part * kDims : 0) + 128 * j + 4 * lane, acc[j],
+                             inv);
+        }
+    } else {
+        // 32 rows x 32 dims, lane = row: the slots' layout gives whole lines
+        const int pieces = (kChunkRows / 32) * (kDims / 32);  // of a unit
+        for (int it = first; it < n[0] * pieces; it += stride) {
+            const JoinDesc &u = descs[it / pieces];
+            const int cta = owner[it / pieces];
+            const int r = it % pieces / (kDims / 32) * 32 + lane, dim0 = it % (kDims / 32) * 32;
+            if (r - lane >= u.nrows) continue;
+            float2 ml[kFew];
+            float M = kNoMax, sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kFew; ++k) {
+                const int slot = k == 0 ? 2 * cta + u.slot0 : 2 * (cta + k);
+                ml[k] = k < u.parts ? parts_ml[slot * kMaxRows + r] : make_float2(kNoMax, 0.0f);
+                M = fmaxf(M, ml[k].x);
+            }
+            float4 acc[8] = {};
+#pragma unroll
+            for (int k = 0; k < kFew; ++k) {
+                if (k < u.parts) {
+                    const int slot = k == 0 ? 2 * cta + u.slot0 : 2 * (cta + k);
+                    const float w = ex2(ml[k].x - M);
+                    sum += ml[k].y * w;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        add_scaled(acc[j],
+                                   *reinterpret_cast<const float4 *>(
+                                       parts_o + slot * kSlotFloats +
+                                       slot_at(r, dim0 + 4 * j)),
+                                   w);
+                }
+            }
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            if (r < u.nrows) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    store_joined(p, u, r, u.part * kDims + dim0 + 4 * j, acc[j], inv);
             }
         }
-        float M = ml[0].x, sum = 0.0f;
-#pragma unroll
-        for (int k = 1; k < kFew; ++k) M = fmaxf(M, ml[k].x);
-        float4 acc[kLoads] = {};
-#pragma unroll
-        for (int k = 0; k < kFew; ++k) {
-            if (k < u.parts) {
-                const float w = ex2(ml[k].x - M);
-                sum += ml[k].y * w;
-#pragma unroll
-                for (int j = 0; j < kLoads; ++j) add_scaled(acc[j], o[k][j], w);
-            }
-        }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j)
-            store_joined(p, u, r, (kDims < kD ? u.part * kDims : 0) + 128 * j + 4 * lane, acc[j],
-                         inv);
     }
 
     const int pieces = p.rows * (kDims / 32);  // of a unit
@@ -794,8 +842,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
         for (int k = grp; k < u.parts; k += 4)
-            add_scaled(acc, *reinterpret_cast<const float4 *>(
-                                parts_o + slot_of(k) * kSlotFloats + r * kDims + dim),
+            add_scaled(acc,
+                       *reinterpret_cast<const float4 *>(
+                           parts_o + slot_of(k) * kSlotFloats +
+                           (kDims == kD ? r * kDims + dim : slot_at(r, dim))),
                        weight[warp][k]);
         __syncwarp();  // the weights are read
 #pragma unroll

@@ -42,8 +42,8 @@ constexpr int kMmaWarp = 5;
 constexpr int kQWarp = 6;
 constexpr int kSoftWarp0 = 8;
 constexpr int kRegsLaunch = 128;
-constexpr int kRegsLow = 80;
-constexpr int kRegsSoft = 176;   // 256*80 + 256*176 = 512*128, the launch allocation
+constexpr int kRegsLow = 104;
+constexpr int kRegsSoft = 152;   // 256*104 + 256*152 = 512*128, the launch allocation
 constexpr int kQSmem = 6;        // chunks of q in shared memory; the last two are in TMEM
 
 // shared memory (the base is 1024-byte aligned: nothing static precedes it)
@@ -122,6 +122,20 @@ __device__ __forceinline__ void bar_pair(int sp) {
     asm volatile("bar.sync %0, 64;" ::"r"(1 + sp) : "memory");
 }
 
+// 32 bytes to global memory: a whole sector per lane.
+__device__ __forceinline__ void store8(void *to, const uint32_t *v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// Whether segment i of a run needs other queries than the one before it: the second unit of a
+// token group follows the first with the same ones. And whether the segment after x does.
+__device__ __forceinline__ bool fresh_q(const Segment &x, int i) { return i == 0 || x.part == 0; }
+__device__ __forceinline__ bool last_of_q(const Segment &x, const Walk &w) {
+    return x.part == 1 || w.left <= 0;
+}
+
 // Bits [a, b) of a 32-bit word, a and b clamped to 0..32.
 __device__ __forceinline__ uint32_t bits_between(int a, int b) {
     a = max(0, min(32, a));
@@ -131,17 +145,27 @@ __device__ __forceinline__ uint32_t bits_between(int a, int b) {
     return below_b & ~below_a;
 }
 
-// Masks 32 logits by `vis`; returns the bits of the masked ones that are not finite.
-__device__ __forceinline__ uint32_t mask32(uint32_t (&s)[32], uint32_t vis) {
+__device__ __forceinline__ void mask32(uint32_t (&s)[32], uint32_t vis) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (!((vis >> j) & 1u)) s[j] = __float_as_uint(-INFINITY);
+}
+
+// 0 when all 32 logits are finite, else NaN.
+__device__ __forceinline__ float zero_if_finite32(const uint32_t (&s)[32]) {
+    float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 32; ++j) t[j & 3] = fmaf(__uint_as_float(s[j]), 0.0f, t[j & 3]);
+    return (t[0] + t[1]) + (t[2] + t[3]);
+}
+
+// Bits of the logits among `of` that are not finite.
+__device__ __forceinline__ uint32_t odd32(const uint32_t (&s)[32], uint32_t of) {
     uint32_t odd = 0;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        if (!((vis >> j) & 1u)) {
-            if (!(fabsf(__uint_as_float(s[j])) <= 3.4028234e38f)) odd |= 1u << j;
-            s[j] = __float_as_uint(-INFINITY);
-        }
-    }
-    return odd;
+    for (int j = 0; j < 32; ++j)
+        if (!(fabsf(__uint_as_float(s[j])) <= 3.4028234e38f)) odd |= 1u << j;
+    return odd & of;
 }
 
 __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
@@ -248,48 +272,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto stage = [&](const Segment &u, int i) -> bool {
                 const bool mine = r < u.nrows;
                 const uint4 *src = reinterpret_cast<const uint4 *>(q + (u.row + r) * kD + 384);
-                uint32_t v[32];
-                // dims 448..511 first: they take longest
+                const float4 *cs = reinterpret_cast<const float4 *>(
+                    p.b.cos_sin + (mine ? int64_t{row_pos(p, u.posf, r)} * kRope : 0));
+                // all of the row's loads before the wait for the previous unit's last QK
+                uint32_t v[64];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint4 w = mine ? __ldg(src + 8 + k) : make_uint4(0, 0, 0, 0);
-                    v[4 * k] = w.x;
-                    v[4 * k + 1] = w.y;
-                    v[4 * k + 2] = w.z;
-                    v[4 * k + 3] = w.w;
-                }
-                if (p.b.cos_sin && mine) {
-                    const float4 *cs = reinterpret_cast<const float4 *>(
-                        p.b.cos_sin + int64_t{row_pos(p, u.posf, r)} * kRope);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float4 a = __ldg(cs + k);
-                        v[2 * k] = turn_pair(v[2 * k], a.x, a.y);
-                        v[2 * k + 1] = turn_pair(v[2 * k + 1], a.z, a.w);
-                    }
-                }
-                const bool ok = mbar_wait(q_free, (i & 1) ^ 1, abort_flag, p.status);
-                tc_fence_after();
-                tmem_st32(lane_base + kQCol + 32, v);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 16; ++k) {
                     const uint4 w = mine ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
                     v[4 * k] = w.x;
                     v[4 * k + 1] = w.y;
                     v[4 * k + 2] = w.z;
                     v[4 * k + 3] = w.w;
                 }
-                tmem_st32(lane_base + kQCol, v);
+                if (p.b.cos_sin && mine) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float4 a = __ldg(cs + k);
+                        v[32 + 2 * k] = turn_pair(v[32 + 2 * k], a.x, a.y);
+                        v[33 + 2 * k] = turn_pair(v[33 + 2 * k], a.z, a.w);
+                    }
+                }
+                const bool ok = mbar_wait(q_free, (i & 1) ^ 1, abort_flag, p.status);
+                tc_fence_after();
+                tmem_st32(lane_base + kQCol, reinterpret_cast<const uint32_t(&)[32]>(v[0]));
+                tmem_st32(lane_base + kQCol + 32, reinterpret_cast<const uint32_t(&)[32]>(v[32]));
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(q_tm);
                 return ok;
             };
+            int loads = 0;
             bool have = ahead.next(p, y);
-            if (have) stage(y, 0);
+            if (have) stage(y, loads++);
             for (int i = 0; walk.next(p, x); ++i) {
                 have = ahead.next(p, y);
-                if (have) stage(y, i + 1);
+                if (have && fresh_q(y, i + 1)) stage(y, loads++);
                 mbar_wait(stat_full, i & 1, abort_flag, p.status);
                 const bool live = mbar_wait(o_full, i & 1, abort_flag, p.status);
                 tc_fence_after();
@@ -301,9 +318,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ? reinterpret_cast<const float4 *>(
                               p.b.cos_sin + int64_t{row_pos(p, x.posf, r)} * kRope)
                         : nullptr;
-                uint4 *orow = reinterpret_cast<uint4 *>(p.out + (x.row + r) * kD + x.part * kHalf);
-                float4 *prow = reinterpret_cast<float4 *>(p.ws + kWsO) +
-                               (int64_t{slot} * kSlotFloats + r * kHalf) / 4;
+                __nv_bfloat16 *orow = p.out + (x.row + r) * kD + x.part * kHalf;
+                // a part's slot: eight dims of a row are 32 bytes, then the next row's, so that a
+                // warp writes whole lines
+                float *prow = reinterpret_cast<float *>(p.ws + kWsO) + slot * kSlotFloats + r * 8;
 #pragma unroll 1
                 for (int k = 0; k < kHalf / 32; ++k) {
                     uint32_t o[32];
@@ -326,25 +344,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 v[4 * j + 3] = v3 * a.z - v2 * a.w;
                             }
                         }
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                            w[j] = *reinterpret_cast<const uint32_t *>(&t);
+                        }
                         if (mine) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const __nv_bfloat162 t = __floats2bfloat162_rn(
-                                        v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
-                                    w[e] = *reinterpret_cast<const uint32_t *>(&t);
-                                }
-                                orow[4 * k + j] = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
+                            store8(orow + 32 * k, w);
+                            store8(orow + 32 * k + 16, w + 8);
                         }
                     } else if (mine) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            prow[8 * k + j] = make_float4(
-                                __uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
-                                __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+                        for (int j = 0; j < 4; ++j)
+                            store8(prow + (4 * k + j) * 8 * kRows, o + 8 * j);
                     }
                 }
                 tc_fence_before();
@@ -406,22 +419,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         } else if (warp == kQWarp) {
-            // ---------------- q's chunks in shared memory, as soon as the last unit's are read
+            // ---------------- q's chunks in shared memory, as soon as the last ones are read;
+            // its rows are brought to L2 before that
             const uint64_t pol_stream = policy_evict_first();
             Walk walk(p, sStart);
             Segment x;
-            int i = 0;
-            for (; walk.next(p, x); ++i) {
-                if (!mbar_wait(q_free, (i & 1) ^ 1, abort_flag, p.status)) break;
+            int loads = 0;
+            for (int i = 0; walk.next(p, x); ++i) {
+                if (!fresh_q(x, i)) continue;
+                if (lane == 0) prefetch_l2(q + x.row * kD, static_cast<uint32_t>(x.nrows) * kD * 2);
+                if (!mbar_wait(q_free, (loads & 1) ^ 1, abort_flag, p.status)) break;
                 if (lane == 0) {
                     mbar_expect_tx(q_full, kQSmem * kSlab);
                     for (int c = 0; c < kQSmem; ++c)
                         tma_load_2d(sQ + c * kSlab, &tm_q, q_full, c * 64,
                                     static_cast<int>(x.row), pol_stream);
                 }
+                ++loads;
             }
             // no copy into this CTA's shared memory may still be in flight at exit
-            if (lane == 0 && i > 0) drain_wait(q_full, (i - 1) & 1);
+            if (lane == 0 && loads > 0) drain_wait(q_full, (loads - 1) & 1);
             __syncwarp();
         } else if (warp == kMmaWarp) {
             // ---------------- the products, in the order QK foreign (b), PV first half (b - 1),
@@ -430,74 +447,85 @@ __global__ void __launch_bounds__(kThreads, 1)
             // costs about 130 cycles a change)
             Walk walk(p, sStart);
             Segment x;
-            int i = 0, g = 0;  // g: blocks begun
-            bool ok = true;
-            for (; ok && walk.next(p, x); ++i) {
-                if (!(ok = mbar_wait(q_full, i & 1, abort_flag, p.status))) break;
-                if (!(ok = mbar_wait(q_tm, i & 1, abort_flag, p.status))) break;
-                for (int b = 0; b <= x.nb; ++b) {
-                    const int par = g & 1;
-                    if (b < x.nb) {
-                        // the softmax must have read the block before's S
-                        if (!(ok = mbar_wait(s_free, par ^ 1, abort_flag, p.status))) break;
-                        if (!(ok = mbar_wait(&full[2 * par], 0, abort_flag, p.status))) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-                            if (x.part) issue_qk<0>(smem, tmem, par, 0u);
-                            else issue_qk<4>(smem, tmem, par, 0u);
-                            mma_commit(&f_free[2 * par]);
-                        }
-                        __syncwarp();
-                        if (!(ok = mbar_wait(&full[2 * par + 1], 0, abort_flag, p.status))) break;
-                        if (elect_one()) {
-                            if (x.part) issue_qk<2>(smem, tmem, par, 1u);
-                            else issue_qk<6>(smem, tmem, par, 1u);
-                            mma_commit(&f_free[2 * par + 1]);
-                        }
-                        __syncwarp();
-                    }
-                    if (b > 0) {
-                        if (!(ok = mbar_wait(p_full, par ^ 1, abort_flag, p.status))) break;
-                        if (b == 1 && i > 0 &&
-                            !(ok = mbar_wait(o_free, (i - 1) & 1, abort_flag, p.status)))
-                            break;
-                        tc_fence_after();
-                        if (elect_one()) {
-                            issue_pv(smem, tmem, par ^ 1, 0, b > 1);
-                            mma_commit(&v_free[2 * (par ^ 1)]);
-                        }
-                        __syncwarp();
-                    }
-                    if (b < x.nb) {
-                        if (!(ok = mbar_wait(&full[2 * par], 1, abort_flag, p.status))) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-                            if (x.part) issue_qk<4>(smem, tmem, par, 1u);
-                            else issue_qk<0>(smem, tmem, par, 1u);
-                        }
-                        __syncwarp();
-                        if (!(ok = mbar_wait(&full[2 * par + 1], 1, abort_flag, p.status))) break;
-                        if (elect_one()) {
-                            if (x.part) issue_qk<6>(smem, tmem, par, 1u);
-                            else issue_qk<2>(smem, tmem, par, 1u);
-                            mma_commit(s_full);
-                            if (b == x.nb - 1) mma_commit(q_free);
-                        }
-                        __syncwarp();
-                        ++g;
-                    }
-                    if (b > 0) {
-                        // (par is still that of the step's first product)
-                        if (elect_one()) {
-                            issue_pv(smem, tmem, par ^ 1, 1, b > 1);
-                            mma_commit(&v_free[2 * (par ^ 1) + 1]);
-                            mma_commit(pv_done);
-                            if (b == x.nb) mma_commit(o_full);
-                        }
-                        __syncwarp();
+            int g = 0, loads = 0;              // blocks begun, queries begun
+            int ends = 0;                      // segments whose PV is all issued
+            bool ok = true, pend = false;      // a block whose PV is to come, ...
+            bool pend_first = false, pend_last = false;  // ... of its segment
+            // the first or second half of that PV
+            auto pv = [&](int half) -> bool {
+                const int par = (g - 1) & 1;
+                if (half == 0) {
+                    if (!mbar_wait(p_full, par, abort_flag, p.status)) return false;
+                    // the segment before must have left O
+                    if (pend_first && ends > 0 &&
+                        !mbar_wait(o_free, (ends - 1) & 1, abort_flag, p.status))
+                        return false;
+                    tc_fence_after();
+                }
+                if (elect_one()) {
+                    issue_pv(smem, tmem, par, half, !pend_first);
+                    mma_commit(&v_free[2 * par + half]);
+                    if (half == 1) {
+                        mma_commit(pv_done);
+                        if (pend_last) mma_commit(o_full);
                     }
                 }
+                __syncwarp();
+                if (half == 1 && pend_last) ++ends;
+                return true;
+            };
+            for (int i = 0; ok && walk.next(p, x); ++i) {
+                if (fresh_q(x, i)) {
+                    // (the queries are on their way: no QK to put between the halves)
+                    if (pend && !(ok = pv(0) && pv(1))) break;
+                    pend = false;
+                    if (!(ok = mbar_wait(q_full, loads & 1, abort_flag, p.status))) break;
+                    if (!(ok = mbar_wait(q_tm, loads & 1, abort_flag, p.status))) break;
+                    ++loads;
+                }
+                for (int b = 0; b < x.nb; ++b) {
+                    const int par = g & 1;
+                    // the softmax must have read the block before's S
+                    if (!(ok = mbar_wait(s_free, par ^ 1, abort_flag, p.status))) break;
+                    if (!(ok = mbar_wait(&full[2 * par], 0, abort_flag, p.status))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (x.part) issue_qk<0>(smem, tmem, par, 0u);
+                        else issue_qk<4>(smem, tmem, par, 0u);
+                        mma_commit(&f_free[2 * par]);
+                    }
+                    __syncwarp();
+                    if (!(ok = mbar_wait(&full[2 * par + 1], 0, abort_flag, p.status))) break;
+                    if (elect_one()) {
+                        if (x.part) issue_qk<2>(smem, tmem, par, 1u);
+                        else issue_qk<6>(smem, tmem, par, 1u);
+                        mma_commit(&f_free[2 * par + 1]);
+                    }
+                    __syncwarp();
+                    if (pend && !(ok = pv(0))) break;
+                    if (!(ok = mbar_wait(&full[2 * par], 1, abort_flag, p.status))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (x.part) issue_qk<4>(smem, tmem, par, 1u);
+                        else issue_qk<0>(smem, tmem, par, 1u);
+                    }
+                    __syncwarp();
+                    if (!(ok = mbar_wait(&full[2 * par + 1], 1, abort_flag, p.status))) break;
+                    if (elect_one()) {
+                        if (x.part) issue_qk<6>(smem, tmem, par, 1u);
+                        else issue_qk<2>(smem, tmem, par, 1u);
+                        mma_commit(s_full);
+                        if (b == x.nb - 1 && last_of_q(x, walk)) mma_commit(q_free);
+                    }
+                    __syncwarp();
+                    if (pend) pv(1);
+                    ++g;
+                    pend = true;
+                    pend_first = b == 0;
+                    pend_last = b == x.nb - 1;
+                }
             }
+            if (ok && pend) ok = pv(0) && pv(1);
             if (elect_one()) {
                 mma_commit(drain);
                 drain_wait(drain, 0);
@@ -553,9 +581,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // become zero in the own slabs (0 * inf in PV would reach every row); rows
                     // that do see the key have a NaN probability already. A key at a time: lane
                     // = 16-byte piece of its four slabs.
-                    uint32_t odd0 = __reduce_or_sync(0xFFFFFFFFu, mask32(s0, v0));
-                    uint32_t odd1 = __reduce_or_sync(0xFFFFFFFFu, mask32(s1, v1));
-                    if ((odd0 | odd1) && live) {
+                    if (__any_sync(0xFFFFFFFFu,
+                                   live && !(zero_if_finite32(s0) + zero_if_finite32(s1) == 0.0f))) {
+                        uint32_t odd0 = __reduce_or_sync(0xFFFFFFFFu, odd32(s0, ~v0));
+                        uint32_t odd1 = __reduce_or_sync(0xFFFFFFFFu, odd32(s1, ~v1));
                         mbar_wait(&full[2 * par], 1, abort_flag, p.status);
                         mbar_wait(&full[2 * par + 1], 1, abort_flag, p.status);
                         uint8_t *tile = sKV + (4 * par + (lane >> 3)) * kSlab + (lane & 7) * 16;
@@ -578,6 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         fence_proxy_async_smem();
                     }
+                    mask32(s0, v0);
+                    mask32(s1, v1);
                 }
                 const float mx = fmaxf(max32(s0), max32(s1));
                 if (vote_any_pair(fmaf(mx, p.c, -m) > kRescale, sp)) {

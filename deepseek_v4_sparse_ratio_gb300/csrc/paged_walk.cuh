@@ -28,7 +28,7 @@ constexpr float kNoMax = -1.0e30f;    // running maximum of a row that has seen 
 
 // Workspace: descriptors, (maximum, sum) of every part's rows, the parts' O. A CTA has two
 // slots, as only the first and the last segment of a run can be parts. A slot holds 64 rows of
-// 512 dims or 128 rows of 256.
+// 512 dims, or 128 rows of 256 (there eight dims of a row, then the next row's).
 constexpr int kMaxRows = 128;
 constexpr size_t kSlotFloats = 64 * kD;
 constexpr size_t kWsDesc = 0;
@@ -362,6 +362,11 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, ui
 
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap *tm) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(tm) : "memory");
+}
+
+// Brings `bytes` from `src` (both multiples of 16) into L2.
+__device__ __forceinline__ void prefetch_l2(const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
 // One lane of a converged warp, the same one every time. A branch on it (rather than on
