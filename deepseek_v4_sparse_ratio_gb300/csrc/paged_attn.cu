@@ -662,7 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // parts, eight loads in flight each, so that one unit of 147 parts (a single token at 128K)
 // takes a few microseconds too.
 constexpr int kJoinWarps = 8;
-constexpr int kFew = 4;
+constexpr int kFew = 4;        // of 512 dims: all loads in registers at once
+constexpr int kFewHalf = 16;   // of 256 dims
 
 __device__ __forceinline__ void store_joined(const Params &p, const JoinDesc &d, int r, int dim,
                                              float4 acc, float inv) {
@@ -682,11 +683,6 @@ __device__ __forceinline__ void store_joined(const Params &p, const JoinDesc &d,
         *reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
 }
 
-// Where dim `dim` (a multiple of four) of row r is in a slot of 128 rows x 256 dims.
-__device__ __forceinline__ int slot_at(int r, int dim) {
-    return dim / 8 * 8 * kChunkRows + r * 8 + dim % 8;
-}
-
 __device__ __forceinline__ void add_scaled(float4 &acc, float4 o, float w) {
     acc.x = fmaf(o.x, w, acc.x);
     acc.y = fmaf(o.y, w, acc.y);
@@ -698,6 +694,7 @@ template <int kDims>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     paged_join_kernel(const __grid_constant__ Params p, int ctas) {
     constexpr int kWords = (kMaxCtas + 31) / 32, kLoads = kDims / 128;
+    constexpr int kFewest = kDims == kD ? kFew : kFewHalf;
     __shared__ JoinDesc descs[kMaxCtas];
     __shared__ int owner[kMaxCtas];           // the CTA a descriptor is of
     __shared__ int count[2][kWords];
@@ -707,8 +704,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     // the units of few parts first, then the others
     JoinDesc d = {};
     if (tid < ctas) d = reinterpret_cast<const JoinDesc *>(p.ws + kWsDesc)[tid];
-    const uint32_t few = __ballot_sync(0xFFFFFFFFu, d.parts > 0 && d.parts <= kFew);
-    const uint32_t many = __ballot_sync(0xFFFFFFFFu, d.parts > kFew);
+    const uint32_t few = __ballot_sync(0xFFFFFFFFu, d.parts > 0 && d.parts <= kFewest);
+    const uint32_t many = __ballot_sync(0xFFFFFFFFu, d.parts > kFewest);
     if (lane == 0 && warp < kWords) {
         count[0][warp] = __popc(few);
         count[1][warp] = __popc(many);
@@ -721,7 +718,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             n[k] += count[k][w];
         }
     if (d.parts > 0) {
-        const int k = d.parts > kFew;
+        const int k = d.parts > kFewest;
         const uint32_t below = (k ? many : few) & ((1u << lane) - 1u);
         const int at = (k ? n[0] : 0) + before[k] + __popc(below);
         descs[at] = d;
@@ -779,29 +776,25 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             const int cta = owner[it / pieces];
             const int r = it % pieces / (kDims / 32) * 32 + lane, dim0 = it % (kDims / 32) * 32;
             if (r - lane >= u.nrows) continue;
-            float2 ml[kFew];
+            auto slot_of = [&](int k) { return k == 0 ? 2 * cta + u.slot0 : 2 * (cta + k); };
             float M = kNoMax, sum = 0.0f;
-#pragma unroll
-            for (int k = 0; k < kFew; ++k) {
-                const int slot = k == 0 ? 2 * cta + u.slot0 : 2 * (cta + k);
-                ml[k] = k < u.parts ? parts_ml[slot * kMaxRows + r] : make_float2(kNoMax, 0.0f);
-                M = fmaxf(M, ml[k].x);
-            }
+#pragma unroll 4
+            for (int k = 0; k < u.parts; ++k)
+                M = fmaxf(M, parts_ml[slot_of(k) * kMaxRows + r].x);
             float4 acc[8] = {};
+#pragma unroll 2
+            for (int k = 0; k < u.parts; ++k) {
+                const int slot = slot_of(k);
+                const float2 ml = parts_ml[slot * kMaxRows + r];
+                const float w = ex2(ml.x - M);
+                sum += ml.y * w;
 #pragma unroll
-            for (int k = 0; k < kFew; ++k) {
-                if (k < u.parts) {
-                    const int slot = k == 0 ? 2 * cta + u.slot0 : 2 * (cta + k);
-                    const float w = ex2(ml[k].x - M);
-                    sum += ml[k].y * w;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        add_scaled(acc[j],
-                                   *reinterpret_cast<const float4 *>(
-                                       parts_o + slot * kSlotFloats +
-                                       slot_at(r, dim0 + 4 * j)),
-                                   w);
-                }
+                for (int j = 0; j < 8; ++j)
+                    add_scaled(acc[j],
+                               *reinterpret_cast<const float4 *>(
+                                   parts_o + slot * kSlotFloats +
+                                   slot_at(kChunkRows, r, dim0 + 4 * j)),
+                               w);
             }
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             if (r < u.nrows) {
@@ -845,7 +838,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             add_scaled(acc,
                        *reinterpret_cast<const float4 *>(
                            parts_o + slot_of(k) * kSlotFloats +
-                           (kDims == kD ? r * kDims + dim : slot_at(r, dim))),
+                           (kDims == kD ? r * kDims + dim : slot_at(kChunkRows, r, dim))),
                        weight[warp][k]);
         __syncwarp();  // the weights are read
 #pragma unroll

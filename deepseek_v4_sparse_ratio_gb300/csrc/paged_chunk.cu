@@ -73,24 +73,23 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
-// S (+)= Q . K^T over two slabs, dims 64 kChunk .. 64 kChunk + 127, in the group of block parity
-// par (slots kChunk mod 4 and the next).
-template <int kChunk>
-__device__ __forceinline__ void issue_qk(const uint8_t *smem, uint32_t tmem, int par,
+// S (+)= Q . K^T over two slabs, dims 64 c .. 64 c + 127, in slots `slot` and the next.
+__device__ __forceinline__ void issue_qk(const uint8_t *smem, uint32_t tmem, int c, int slot,
                                          uint32_t acc0) {
     constexpr uint32_t idesc = idesc_bf16(kRows, kBlock, false, false);
-    const uint64_t qd = desc_sw128(smem_u32(smem + kOffQ) + (kChunk < kQSmem ? kChunk : 0) * kSlab, 16, 1024);
-    const uint64_t kd = desc_sw128(smem_u32(smem + kOffKV) + (4 * par + kChunk % 4) * kSlab, 16, 1024);
+    const uint64_t kd = desc_sw128(smem_u32(smem + kOffKV) + slot * kSlab, 16, 1024);
+    if (c < kQSmem) {
+        const uint64_t qd = desc_sw128(smem_u32(smem + kOffQ) + c * kSlab, 16, 1024);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t step = ((k / 4 * kSlab) >> 4) + 2 * (k % 4);
+            mma_bf16(tmem + kSCol, qd + step, kd + step, idesc, k > 0 ? 1u : acc0);
+        }
+    } else {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            const uint32_t acc = j > 0 || kk > 0 ? 1u : acc0;
-            const uint32_t step = ((j * kSlab) >> 4) + 2 * kk;
-            if (kChunk < kQSmem)
-                mma_bf16(tmem + kSCol, qd + step, kd + step, idesc, acc);
-            else
-                mma_bf16_ta(tmem + kSCol, tmem + kQCol + 32 * j + 8 * kk, kd + step, idesc, acc);
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t step = ((k / 4 * kSlab) >> 4) + 2 * (k % 4);
+            mma_bf16_ta(tmem + kSCol, tmem + kQCol + 8 * k, kd + step, idesc, k > 0 ? 1u : acc0);
         }
     }
 }
@@ -99,7 +98,8 @@ __device__ __forceinline__ void issue_qk(const uint8_t *smem, uint32_t tmem, int
 __device__ __forceinline__ void issue_pv(const uint8_t *smem, uint32_t tmem, int par, int half,
                                          uint32_t acc0) {
     constexpr uint32_t idesc = idesc_bf16(kRows, 128, false, true);
-    const uint64_t vd = desc_sw128(smem_u32(smem + kOffKV) + (4 * par + 2 * half) * kSlab, kSlab, 1024);
+    const uint64_t vd =
+        desc_sw128(smem_u32(smem + kOffKV) + (4 * par + 2 * half) * kSlab, kSlab, 1024);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
         mma_bf16_ta(tmem + kOCol + 128 * half, tmem + kPCol + 8 * kk, vd + ((kk * 2048) >> 4),
@@ -447,85 +447,84 @@ __global__ void __launch_bounds__(kThreads, 1)
             // costs about 130 cycles a change)
             Walk walk(p, sStart);
             Segment x;
-            int g = 0, loads = 0;              // blocks begun, queries begun
+            int g = 0, loads = 0;              // blocks and queries begun
             int ends = 0;                      // segments whose PV is all issued
-            bool ok = true, pend = false;      // a block whose PV is to come, ...
-            bool pend_first = false, pend_last = false;  // ... of its segment
-            // the first or second half of that PV
-            auto pv = [&](int half) -> bool {
-                const int par = (g - 1) & 1;
-                if (half == 0) {
-                    if (!mbar_wait(p_full, par, abort_flag, p.status)) return false;
-                    // the segment before must have left O
-                    if (pend_first && ends > 0 &&
-                        !mbar_wait(o_free, (ends - 1) & 1, abort_flag, p.status))
-                        return false;
-                    tc_fence_after();
-                }
-                if (elect_one()) {
-                    issue_pv(smem, tmem, par, half, !pend_first);
-                    mma_commit(&v_free[2 * par + half]);
-                    if (half == 1) {
-                        mma_commit(pv_done);
-                        if (pend_last) mma_commit(o_full);
+            bool ok = true, pend = false;      // a block whose PV is to come: is there one, and is
+            bool pend_first = false, pend_last = false;  // it its segment's first, last
+            // One pass per block, and one more where PV of the last one has no QK to hide behind:
+            // before new queries, and at the end.
+            bool have = walk.next(p, x), wait_q = have;
+            for (int b = 0; ok && (have || pend);) {
+                const bool qk = have && !(wait_q && pend);
+                const int par = g & 1;
+                if (qk) {
+                    if (wait_q) {
+                        if (!(ok = mbar_wait(q_full, loads & 1, abort_flag, p.status))) break;
+                        if (!(ok = mbar_wait(q_tm, loads & 1, abort_flag, p.status))) break;
+                        ++loads;
+                        wait_q = false;
                     }
-                }
-                __syncwarp();
-                if (half == 1 && pend_last) ++ends;
-                return true;
-            };
-            for (int i = 0; ok && walk.next(p, x); ++i) {
-                if (fresh_q(x, i)) {
-                    // (the queries are on their way: no QK to put between the halves)
-                    if (pend && !(ok = pv(0) && pv(1))) break;
-                    pend = false;
-                    if (!(ok = mbar_wait(q_full, loads & 1, abort_flag, p.status))) break;
-                    if (!(ok = mbar_wait(q_tm, loads & 1, abort_flag, p.status))) break;
-                    ++loads;
-                }
-                for (int b = 0; b < x.nb; ++b) {
-                    const int par = g & 1;
                     // the softmax must have read the block before's S
                     if (!(ok = mbar_wait(s_free, par ^ 1, abort_flag, p.status))) break;
-                    if (!(ok = mbar_wait(&full[2 * par], 0, abort_flag, p.status))) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        if (x.part) issue_qk<0>(smem, tmem, par, 0u);
-                        else issue_qk<4>(smem, tmem, par, 0u);
-                        mma_commit(&f_free[2 * par]);
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {   // of the block: foreign, own
+                    if (qk) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (!(ok = mbar_wait(&full[2 * par + h], half, abort_flag, p.status)))
+                                break;
+                            tc_fence_after();
+                            if (elect_one()) {
+                                if (half ^ x.part)
+                                    issue_qk(smem, tmem, 2 * h, 4 * par + 2 * h, half | h);
+                                else
+                                    issue_qk(smem, tmem, 4 + 2 * h, 4 * par + 2 * h, half | h);
+                                if (half == 0) mma_commit(&f_free[2 * par + h]);
+                            }
+                            __syncwarp();
+                        }
+                        if (!ok) break;
+                        if (half == 1 && elect_one()) {
+                            mma_commit(s_full);
+                            if (b == x.nb - 1 && last_of_q(x, walk)) mma_commit(q_free);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    if (!(ok = mbar_wait(&full[2 * par + 1], 0, abort_flag, p.status))) break;
-                    if (elect_one()) {
-                        if (x.part) issue_qk<2>(smem, tmem, par, 1u);
-                        else issue_qk<6>(smem, tmem, par, 1u);
-                        mma_commit(&f_free[2 * par + 1]);
+                    if (pend) {
+                        if (half == 0) {
+                            ok = mbar_wait(p_full, (g - 1) & 1, abort_flag, p.status);
+                            // the segment before must have left O
+                            if (ok && pend_first && ends > 0)
+                                ok = mbar_wait(o_free, (ends - 1) & 1, abort_flag, p.status);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        if (elect_one()) {
+                            issue_pv(smem, tmem, (g - 1) & 1, half, !pend_first);
+                            mma_commit(&v_free[2 * ((g - 1) & 1) + half]);
+                            if (half == 1) {
+                                mma_commit(pv_done);
+                                if (pend_last) mma_commit(o_full);
+                            }
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    if (pend && !(ok = pv(0))) break;
-                    if (!(ok = mbar_wait(&full[2 * par], 1, abort_flag, p.status))) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        if (x.part) issue_qk<4>(smem, tmem, par, 1u);
-                        else issue_qk<0>(smem, tmem, par, 1u);
-                    }
-                    __syncwarp();
-                    if (!(ok = mbar_wait(&full[2 * par + 1], 1, abort_flag, p.status))) break;
-                    if (elect_one()) {
-                        if (x.part) issue_qk<6>(smem, tmem, par, 1u);
-                        else issue_qk<2>(smem, tmem, par, 1u);
-                        mma_commit(s_full);
-                        if (b == x.nb - 1 && last_of_q(x, walk)) mma_commit(q_free);
-                    }
-                    __syncwarp();
-                    if (pend) pv(1);
+                }
+                if (!ok) break;
+                if (pend && pend_last) ++ends;
+                pend = qk;
+                if (qk) {
                     ++g;
-                    pend = true;
                     pend_first = b == 0;
                     pend_last = b == x.nb - 1;
+                    if (++b == x.nb) {
+                        b = 0;
+                        have = walk.next(p, x);
+                        wait_q = have && x.part == 0;
+                    }
                 }
             }
-            if (ok && pend) ok = pv(0) && pv(1);
             if (elect_one()) {
                 mma_commit(drain);
                 drain_wait(drain, 0);

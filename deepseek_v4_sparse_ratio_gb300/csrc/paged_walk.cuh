@@ -28,7 +28,7 @@ constexpr float kNoMax = -1.0e30f;    // running maximum of a row that has seen 
 
 // Workspace: descriptors, (maximum, sum) of every part's rows, the parts' O. A CTA has two
 // slots, as only the first and the last segment of a run can be parts. A slot holds 64 rows of
-// 512 dims, or 128 rows of 256 (there eight dims of a row, then the next row's).
+// 512 dims or 128 rows of 256: eight dims (a 32-byte sector) of a row, then the next row's.
 constexpr int kMaxRows = 128;
 constexpr size_t kSlotFloats = 64 * kD;
 constexpr size_t kWsDesc = 0;
@@ -36,6 +36,11 @@ constexpr size_t kWsMl = 8192;
 constexpr size_t kWsO = kWsMl + size_t{2 * kMaxCtas} * kMaxRows * 2 * sizeof(float);
 static_assert(kWsO + size_t{2 * kMaxCtas} * kSlotFloats * sizeof(float) <= DSA_PAGED_WORKSPACE_BYTES,
               "over the workspace");
+
+// Where dim `dim` of row r is in a slot of `rows` rows.
+__host__ __device__ constexpr int slot_at(int rows, int r, int dim) {
+    return dim / 8 * 8 * rows + r * 8 + dim % 8;
+}
 
 // A unit that begins in a CTA's run and ends in a later one, for the join.
 struct JoinDesc {
