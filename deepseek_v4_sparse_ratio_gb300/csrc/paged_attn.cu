@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 chunk_dim(7), row, e);
                 for (int m = 0; m < 4; ++m) {
                     m_at = m;
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&kv_free[m], (g & 1) ^ 1, abort_flag,
+                    ok = __all_sync(0xFFFFFFFFu, wait_bar(&kv_free[m], (g & 1) ^ 1, abort_flag,
                                                            p.status));
                     if (!ok) break;
                     if (lane == 0) mbar_expect_tx(&kv_full[m], m < 3 ? 2 * bytes : bytes);
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 8; ++k) cs[k] = __ldg(src + k);
                     }
-                    if (!mbar_wait(q_full, i & 1, abort_flag, p.status)) break;
+                    if (!wait_bar(q_full, i & 1, abort_flag, p.status)) break;
                     if (mine) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int i = 0, g = 0, last_q = -1;
             bool ok = true;
             for (; ok && walk.next(p, x); ++i) {
-                if (!(ok = mbar_wait(q_free, (i & 1) ^ 1, abort_flag, p.status))) break;
+                if (!(ok = wait_bar(q_free, (i & 1) ^ 1, abort_flag, p.status))) break;
                 if (elect_one()) {
                     mbar_expect_tx(q_full, 65536);
                     for (int c = 0; c < 8; ++c)
@@ -277,16 +277,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     static_cast<int>(x.row), pol_stream);
                 }
                 last_q = i;
-                if (!(ok = mbar_wait(q_full, i & 1, abort_flag, p.status))) break;
+                if (!(ok = wait_bar(q_full, i & 1, abort_flag, p.status))) break;
                 tc_fence_after();
                 for (int b = 0; b < x.nb && ok; ++b, ++g) {
                     // S^T is double-buffered: QK of a block may run while the softmax of the
                     // block before it does
                     const int par = g & 1;
-                    if (!(ok = mbar_wait(&s_free[par], ((g >> 1) & 1) ^ 1, abort_flag, p.status)))
+                    if (!(ok = wait_bar(&s_free[par], ((g >> 1) & 1) ^ 1, abort_flag, p.status)))
                         break;
                     const uint32_t s_col = tmem + kSCol + 64 * par;
-                    if (!(ok = mbar_wait(&x_full[par], (g >> 1) & 1, abort_flag, p.status))) break;
+                    if (!(ok = wait_bar(&x_full[par], (g >> 1) & 1, abort_flag, p.status))) break;
                     tc_fence_after();
                     if (elect_one()) {
                         const uint64_t ad = par ? adx : ad0 + ((7 * 16384) >> 4);
@@ -298,9 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
 #pragma unroll 1
                     for (int m = 0; m < 4; ++m) {
-                        if (!(ok = mbar_wait(&kv_full[m], g & 1, abort_flag, p.status))) break;
+                        if (!(ok = wait_bar(&kv_full[m], g & 1, abort_flag, p.status))) break;
                         if (m == 2 && b == 0 && p.b.cos_sin &&
-                            !(ok = mbar_wait(q_turned, i & 1, abort_flag, p.status)))
+                            !(ok = wait_bar(q_turned, i & 1, abort_flag, p.status)))
                             break;
                         tc_fence_after();
                         if (elect_one()) {
@@ -341,11 +341,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             for (; ok && walk.next(p, x); ++i) {
                 for (int b = 0; b < x.nb && ok; ++b, ++g) {
-                    if (!(ok = mbar_wait(p_full, g & 1, abort_flag, p.status))) break;
+                    if (!(ok = wait_bar(p_full, g & 1, abort_flag, p.status))) break;
                     tc_fence_after();
                     if (b == 0 && i > 0) {
                         // the epilogue of the previous unit must have read O^T
-                        if (!(ok = mbar_wait(o_free, (i - 1) & 1, abort_flag, p.status))) break;
+                        if (!(ok = wait_bar(o_free, (i - 1) & 1, abort_flag, p.status))) break;
                         tc_fence_after();
                     }
                     const uint32_t acc0 = b > 0;
@@ -602,18 +602,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // turned back by the token's position; a pair is in two adjacent lanes
                         const float2 *cs = reinterpret_cast<const float2 *>(p.b.cos_sin) +
                                            ((sp - 2) * 16 + (lane >> 1));
-                        float2 a = make_float2(1.0f, 0.0f);
-                        int at = -1;
+                        // (a unit of one token's heads has one position)
+                        int pos = p.tpu == 1 ? x.posf : x.posf + hb / p.rpt;
+                        int left = p.tpu == 1 ? 32 : p.rpt - hb % p.rpt;  // rows at pos
+                        float2 a = __ldg(cs + int64_t{pos <= x.posl ? pos : x.posl} * kRopePairs);
 #pragma unroll
                         for (int h = 0; h < 32; ++h) {
                             const float v = __uint_as_float(oa[h]) * linv[h];
                             const float w = __shfl_xor_sync(0xFFFFFFFFu, v, 1);
                             if (h < rows) {
-                                const int pos = row_pos(p, x.posf, hb + h);
-                                if (pos != at) {
+                                if (left == 0) {
+                                    ++pos;
+                                    left = p.rpt;
                                     a = __ldg(cs + int64_t{pos} * kRopePairs);
-                                    at = pos;
                                 }
+                                --left;
                                 o[h * kD] = __float2bfloat16_rn(v * a.x + (lane & 1 ? -w : w) * a.y);
                             }
                         }

@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         v[33 + 2 * k] = turn_pair(v[33 + 2 * k], a.z, a.w);
                     }
                 }
-                const bool ok = mbar_wait(q_free, (i & 1) ^ 1, abort_flag, p.status);
+                const bool ok = wait_bar(q_free, (i & 1) ^ 1, abort_flag, p.status);
                 tc_fence_after();
                 tmem_st32(lane_base + kQCol, reinterpret_cast<const uint32_t(&)[32]>(v[0]));
                 tmem_st32(lane_base + kQCol + 32, reinterpret_cast<const uint32_t(&)[32]>(v[32]));
@@ -307,8 +307,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; walk.next(p, x); ++i) {
                 have = ahead.next(p, y);
                 if (have && fresh_q(y, i + 1)) stage(y, loads++);
-                mbar_wait(stat_full, i & 1, abort_flag, p.status);
-                const bool live = mbar_wait(o_full, i & 1, abort_flag, p.status);
+                wait_bar(stat_full, i & 1, abort_flag, p.status);
+                const bool live = wait_bar(o_full, i & 1, abort_flag, p.status);
                 tc_fence_after();
                 const float linv = sLinv[(i & 1) * kRows + r];
                 const bool mine = r < x.nrows && live;
@@ -390,8 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // the pair's own slabs of the block two back used by PV; then its foreign
                     // slabs used by QK
                     const int pair = 2 * par + (at & 1);
-                    ok = at < 2 ? mbar_wait(&v_free[pair], use ^ 1, abort_flag, p.status)
-                                : mbar_wait(&f_free[pair], use, abort_flag, p.status);
+                    ok = at < 2 ? wait_bar(&v_free[pair], use ^ 1, abort_flag, p.status)
+                                : wait_bar(&f_free[pair], use, abort_flag, p.status);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     if (lane == 0) {
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; walk.next(p, x); ++i) {
                 if (!fresh_q(x, i)) continue;
                 if (lane == 0) prefetch_l2(q + x.row * kD, static_cast<uint32_t>(x.nrows) * kD * 2);
-                if (!mbar_wait(q_free, (loads & 1) ^ 1, abort_flag, p.status)) break;
+                if (!wait_bar(q_free, (loads & 1) ^ 1, abort_flag, p.status)) break;
                 if (lane == 0) {
                     mbar_expect_tx(q_full, kQSmem * kSlab);
                     for (int c = 0; c < kQSmem; ++c)

@@ -72,7 +72,7 @@ struct Params {
 // ------------------------------------------------------------------ the list of units
 
 // sum_{i < n} floor((a + d i) / 128) for a, d >= 0 (the Euclid-like reduction of such sums).
-__device__ inline int64_t floor_sum(int64_t n, int64_t a, int64_t d) {
+static __device__ __noinline__ int64_t floor_sum(int64_t n, int64_t a, int64_t d) {
     int64_t m = kBlock, ans = 0;
     while (n > 0) {
         if (d >= m) {
@@ -109,9 +109,7 @@ __device__ __forceinline__ int group_blocks(const Params &p, const PagedSeq &q, 
 }
 
 // Blocks of the first G token groups of a sequence (G = all of them: the last one may be short).
-__device__ inline int64_t blocks_before(const Params &p, const PagedSeq &q, int64_t G) {
-    if (G <= 0) return 0;
-    if (G == 1) return group_blocks(p, q, 0);
+static __device__ __noinline__ int64_t blocks_before_many(const Params &p, PagedSeq q, int64_t G) {
     const int64_t base = q.len - q.n, d = p.tpu;
     int64_t sum = floor_sum(G, base + d - 1, d) + G;
     if (G * d > q.n) sum += ((int64_t{q.len} - 1) >> 7) - ((base + G * d - 1) >> 7);
@@ -121,6 +119,10 @@ __device__ inline int64_t blocks_before(const Params &p, const PagedSeq &q, int6
         sum -= floor_sum(G - g0, a + g0 * d, d);
     }
     return sum;
+}
+
+__device__ __forceinline__ int64_t blocks_before(const Params &p, const PagedSeq &q, int G) {
+    return G <= 0 ? 0 : G == 1 ? group_blocks(p, q, 0) : blocks_before_many(p, q, G);
 }
 
 __device__ __forceinline__ int groups_of(const Params &p, const PagedSeq &q) {
@@ -140,7 +142,7 @@ struct Place {
 };
 
 // The place of block r of sequence s's blocks.
-__device__ inline Place find_block(const Params &p, const PagedSeq &q, int s, int64_t r) {
+static __device__ __noinline__ Place find_block(const Params &p, PagedSeq q, int s, int64_t r) {
     int lo = 0, hi = groups_of(p, q);  // upt * blocks_before(lo) <= r < upt * blocks_before(hi)
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -372,6 +374,18 @@ __device__ __forceinline__ void prefetch_tmap(const CUtensorMap *tm) {
 // Brings `bytes` from `src` (both multiples of 16) into L2.
 __device__ __forceinline__ void prefetch_l2(const void *src, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
+// mbar_wait with the loop out of line: its many copies would push the roles' code out of the
+// instruction caches.
+static __device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                       int32_t *status) {
+    return mbar_wait(bar, parity, abort, status);
+}
+
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                         int32_t *status) {
+    return mbar_test(smem_u32(bar), parity) || wait_long(bar, parity, abort, status);
 }
 
 // One lane of a converged warp, the same one every time. A branch on it (rather than on
