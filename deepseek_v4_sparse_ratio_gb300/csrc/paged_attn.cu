@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // parts, eight loads in flight each, so that one unit of 147 parts (a single token at 128K)
 // takes a few microseconds too.
 constexpr int kJoinWarps = 8;
-constexpr int kFew = 4;        // of 512 dims: all loads in registers at once
+constexpr int kFew = 32;       // of 512 dims
 constexpr int kFewHalf = 16;   // of 256 dims
 
 __device__ __forceinline__ void store_joined(const Params &p, const JoinDesc &d, int r, int dim,
@@ -738,32 +738,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             const JoinDesc &u = descs[it / p.rows];
             const int cta = owner[it / p.rows], r = it % p.rows;
             if (r >= u.nrows) continue;
-            float4 o[kFew][kLoads];
-            float2 ml[kFew];
+            auto slot_of = [&](int k) { return k == 0 ? 2 * cta + u.slot0 : 2 * (cta + k); };
+            // lane k holds part k's maximum and sum
+            const float2 ml = lane < u.parts ? parts_ml[slot_of(lane) * kMaxRows + r]
+                                             : make_float2(kNoMax, 0.0f);
+            const float wt = ex2(ml.x - redux_max(ml.x));
+            float sum = lane < u.parts ? ml.y * wt : 0.0f;
 #pragma unroll
-            for (int k = 0; k < kFew; ++k) {
-                const int slot = k == 0 ? 2 * cta + u.slot0 : 2 * (cta + k);
-                ml[k] = make_float2(kNoMax, 0.0f);
-                if (k < u.parts) {
-                    ml[k] = parts_ml[slot * kMaxRows + r];
-#pragma unroll
-                    for (int j = 0; j < kLoads; ++j)
-                        o[k][j] = *reinterpret_cast<const float4 *>(
-                            parts_o + slot * kSlotFloats + r * kDims + 128 * j + 4 * lane);
-                }
-            }
-            float M = ml[0].x, sum = 0.0f;
-#pragma unroll
-            for (int k = 1; k < kFew; ++k) M = fmaxf(M, ml[k].x);
+            for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, w);
             float4 acc[kLoads] = {};
+#pragma unroll 4
+            for (int k = 0; k < u.parts; ++k) {
+                const float w = __shfl_sync(0xFFFFFFFFu, wt, k);
+                const float *o = parts_o + slot_of(k) * kSlotFloats + r * kDims + 4 * lane;
 #pragma unroll
-            for (int k = 0; k < kFew; ++k) {
-                if (k < u.parts) {
-                    const float w = ex2(ml[k].x - M);
-                    sum += ml[k].y * w;
-#pragma unroll
-                    for (int j = 0; j < kLoads; ++j) add_scaled(acc[j], o[k][j], w);
-                }
+                for (int j = 0; j < kLoads; ++j)
+                    add_scaled(acc[j], *reinterpret_cast<const float4 *>(o + 128 * j), w);
             }
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
