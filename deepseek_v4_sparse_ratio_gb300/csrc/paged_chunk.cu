@@ -370,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int prows = min(1 << p.b.page_shift, kBlock), np = kBlock / prows;
             const int second = lane >= np, page = second ? lane - np : lane;  // (np: no page)
             uint8_t *const dst0 = sKV + second * kSlab + page * prows * 128;
+            const uint64_t pol = policy_evict_normal();  // (each half of the dims reads the keys)
             PageWalk walk(p, sStart);
             const int blocks = sStart[4];
             int row, row_next = 0, own, own_next = walk.x.part, g = 0, at = 0;
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int half = at < 2 ? own ^ 1 : own;  // of the dims
                     if (e >= 0)
                         tma_load_3d(dst0 + 2 * pair * kSlab, &tm_kv, &full[pair],
-                                    (4 * half + 2 * (at & 1) + second) * 64, row, e);
+                                    (4 * half + 2 * (at & 1) + second) * 64, row, e, pol);
                 }
                 if (!ok) break;
             }

@@ -175,6 +175,7 @@ struct Segment {
     int posf, posl;    // positions of the unit's first and last token
     int lo;            // lowest position any of its tokens sees
     bool whole;        // all of the unit's blocks
+    bool alone;        // the sequence's only unit: nothing else reads its keys
 };
 
 // Walks the segments of a CTA's run. Every role walks on its own.
@@ -214,6 +215,7 @@ struct Walk {
         x.blk = blo + at.off;
         x.nb = min(nblk - at.off, left);
         x.whole = x.nb == nblk;
+        x.alone = p.upt == 1 && q.n <= p.tpu;
         left -= x.nb;
         at.off = 0;
         if (++at.part == p.upt) {
@@ -358,12 +360,18 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, uint64_t *bar, int x,
-                                            int y, int z) {
+                                            int y, int z, uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-        "l"(tm), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+        "l"(tm), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
 }
 
