@@ -218,10 +218,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *p_full = bars + 19;
     uint64_t *pv_done = bars + 20;  // PV of a block done: P may be written, O rescaled
     uint64_t *o_full = bars + 21;
-    uint64_t *o_free = bars + 22;
-    uint64_t *stat_full = bars + 23;
-    uint64_t *drain = bars + 24;    // every product issued is done
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 25);
+    uint64_t *o_free = bars + 22;   // [2] a half of O's columns left by the stores
+    uint64_t *stat_full = bars + 24;
+    uint64_t *drain = bars + 25;    // every product issued is done
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 26);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     volatile uint32_t *sPages = tmem_holder + 2;             // [2]
     int *sStart = reinterpret_cast<int *>(tmem_holder + 4);  // [5]
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // warps on s_free, 256 softmax threads on p_full, one on the others
         int n = 1;
         uint64_t *bar = bars + lane;
-        if (bar == q_tm || bar == o_free || bar == stat_full) n = kRows;
+        if (bar == q_tm || bar == o_free || bar == o_free + 1 || bar == stat_full) n = kRows;
         if (bar == s_free) n = 8;
         if (bar == p_full) n = 256;
         if (bar <= drain) mbar_init(bar, n);
@@ -327,6 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t o[32];
                     tmem_ld32(lane_base + kOCol + 32 * k, o);
                     tmem_wait_ld();
+                    if (k % 4 == 3) {  // the next unit's PV may write this half
+                        tc_fence_before();
+                        mbar_arrive(&o_free[k / 4]);
+                    }
                     if (x.whole) {
                         float v[32];
 #pragma unroll
@@ -360,8 +364,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             store8(prow + (4 * k + j) * 8 * kRows, o + 8 * j);
                     }
                 }
-                tc_fence_before();
-                mbar_arrive(o_free);
             }
         } else if (warp == kLoadWarp) {
             // ---------------- loader: a block in four steps of two slabs, each one instruction:
@@ -493,14 +495,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                     }
                     if (pend) {
-                        if (half == 0) {
-                            ok = mbar_wait(p_full, (g - 1) & 1, abort_flag, p.status);
-                            // the segment before must have left O
-                            if (ok && pend_first && ends > 0)
-                                ok = mbar_wait(o_free, (ends - 1) & 1, abort_flag, p.status);
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
+                        if (half == 0) ok = mbar_wait(p_full, (g - 1) & 1, abort_flag, p.status);
+                        // the stores of the segment before must have left this half of O
+                        if (ok && pend_first && ends > 0)
+                            ok = mbar_wait(&o_free[half], (ends - 1) & 1, abort_flag, p.status);
+                        if (!ok) break;
+                        tc_fence_after();
                         if (elect_one()) {
                             issue_pv(smem, tmem, (g - 1) & 1, half, !pend_first);
                             mma_commit(&v_free[2 * ((g - 1) & 1) + half]);
