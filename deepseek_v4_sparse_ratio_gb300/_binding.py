@@ -275,56 +275,64 @@ def _stream_of(stream, device):
     return _raw_stream(device) if stream is None and _raw_stream is not None else _s(stream)
 
 
-def _take(where: str, name: str, t, dtype, device, want: str, fits: bool) -> int:
-    """The address of a packed tensor of this dtype on this device whose shape fits."""
-    if not (fits and t.dtype is dtype and t.get_device() == device and t.is_contiguous()):
-        raise DsaError(DSA_ERR_ARG, f"{where}: {name} has to be a packed {dtype} tensor [{want}] "
-                                    f"on cuda:{device}")
-    return t.data_ptr()
+def _refuse(where: str, name: str, dtype, want: str, device):
+    raise DsaError(DSA_ERR_ARG, f"{where}: {name} has to be a packed {dtype} tensor [{want}] on "
+                                f"cuda:{device}")
 
 
 def _paged(where: str, new_start, seq_len, page_table, pages, cos_sin, device):
-    """The arguments both paged calls share, in the ABI's order."""
-    table = tuple(page_table.shape)
-    n_seqs, max_pages = table if len(table) == 2 else (-1, -1)
-    shape, strides = tuple(pages.shape), pages.stride()
-    if not (pages.dtype is _BF16 and pages.get_device() == device and len(shape) == 3
-            and shape[2] == DIM and strides[2] == 1 and strides[1] == DIM):
+    """The arguments both paged calls share, checked, in the ABI's order."""
+    table, shape, strides = page_table.shape, pages.shape, pages.stride()
+    if not (len(table) == 2 and page_table.dtype is _I32 and page_table.get_device() == device
+            and page_table.is_contiguous()):
+        _refuse(where, "page_table", _I32, "*, *", device)
+    n_seqs, max_pages = table
+    if not (new_start.shape == (n_seqs + 1,) and new_start.dtype is _I32
+            and new_start.get_device() == device and new_start.is_contiguous()):
+        _refuse(where, "new_start", _I32, n_seqs + 1, device)
+    if not (seq_len.shape == (n_seqs,) and seq_len.dtype is _I32
+            and seq_len.get_device() == device and seq_len.is_contiguous()):
+        _refuse(where, "seq_len", _I32, n_seqs, device)
+    if not (len(shape) == 3 and shape[2] == DIM and strides[2] == 1 and strides[1] == DIM
+            and pages.dtype is _BF16 and pages.get_device() == device):
         raise DsaError(DSA_ERR_ARG, f"{where}: pages has to be a {_BF16} tensor "
                                     f"[*, *, {DIM}] on cuda:{device} with packed pages")
-    n_pages, page_size = shape[0], shape[1]
+    n_pages, page_size, _ = shape
     angles, n_pos = None, 0
     if cos_sin is not None:
-        at = tuple(cos_sin.shape)
-        angles = _take(where, "cos_sin", cos_sin, _F32, device, f"*, {ROPE_DIM // 2}, 2",
-                       at[1:] == (ROPE_DIM // 2, 2))
-        n_pos = at[0]
-    return (_take(where, "new_start", new_start, _I32, device, str(n_seqs + 1),
-                  new_start.shape == (n_seqs + 1,)),
-            _take(where, "seq_len", seq_len, _I32, device, str(n_seqs),
-                  seq_len.shape == (n_seqs,)), n_seqs,
-            _take(where, "page_table", page_table, _I32, device, "*, *", n_seqs >= 0), max_pages,
+        n_pos = cos_sin.shape[0] if cos_sin.dim() else 0
+        if not (cos_sin.shape == (n_pos, ROPE_DIM // 2, 2) and cos_sin.dtype is _F32
+                and cos_sin.get_device() == device and cos_sin.is_contiguous()):
+            _refuse(where, "cos_sin", _F32, f"*, {ROPE_DIM // 2}, 2", device)
+        angles = cos_sin.data_ptr()
+    return (new_start.data_ptr(), seq_len.data_ptr(), n_seqs, page_table.data_ptr(), max_pages,
             pages.data_ptr(), n_pages, strides[0] if n_pages > 1 else page_size * DIM, page_size,
             angles, n_pos)
 
 
 def _status(where: str, dev_status, device):
-    return None if dev_status is None else _take(where, "dev_status", dev_status, _I32, device,
-                                                 "1", dev_status.shape == (1,))
+    if dev_status is None:
+        return None
+    if not (dev_status.shape == (1,) and dev_status.dtype is _I32
+            and dev_status.get_device() == device):
+        _refuse(where, "dev_status", _I32, 1, device)
+    return dev_status.data_ptr()
 
 
 def dsa_paged_append(kv, new_start, seq_len, page_table, pages, cos_sin=None, dev_status=None,
                      stream=None) -> None:
     """Rotate the new tokens' rows kv [n_new, 512] by their positions into their pages
     [n_pages, page_size, 512]. Tensors are on the current device; see include/dsa.h."""
-    where = "dsa_paged_append"
     dev = torch.cuda.current_device()
-    rows = tuple(kv.shape)
+    shape = kv.shape
+    if not (len(shape) == 2 and shape[1] == DIM and kv.dtype is _BF16 and kv.get_device() == dev
+            and kv.is_contiguous()):
+        _refuse("dsa_paged_append", "kv", _BF16, f"*, {DIM}", dev)
     rc = (_lib or load()).dsa_paged_append(
-        _take(where, "kv", kv, _BF16, dev, f"*, {DIM}", len(rows) == 2 and rows[1] == DIM),
-        rows[0], *_paged(where, new_start, seq_len, page_table, pages, cos_sin, dev),
-        _status(where, dev_status, dev), _stream_of(stream, dev))
-    _check(rc, where)
+        kv.data_ptr(), shape[0],
+        *_paged("dsa_paged_append", new_start, seq_len, page_table, pages, cos_sin, dev),
+        _status("dsa_paged_append", dev_status, dev), _stream_of(stream, dev))
+    _check(rc, "dsa_paged_append")
 
 
 def dsa_paged_attn(q, new_start, seq_len, page_table, pages, window: int, scale: float, workspace,
@@ -334,12 +342,18 @@ def dsa_paged_attn(q, new_start, seq_len, page_table, pages, window: int, scale:
     DSA_PAGED_WORKSPACE_BYTES. Tensors are on the current device; see include/dsa.h."""
     where = "dsa_paged_attn"
     dev = torch.cuda.current_device()
-    shape = tuple(q.shape)
+    shape = q.shape
+    if not (len(shape) == 3 and shape[2] == DIM and q.dtype is _BF16 and q.get_device() == dev
+            and q.is_contiguous()):
+        _refuse(where, "q", _BF16, f"*, *, {DIM}", dev)
+    if not (out.shape == shape and out.dtype is _BF16 and out.get_device() == dev
+            and out.is_contiguous()):
+        _refuse(where, "out", _BF16, ", ".join(map(str, shape)), dev)
+    if not (workspace.get_device() == dev and workspace.is_contiguous()):
+        _refuse(where, "workspace", workspace.dtype, "*", dev)
     rc = (_lib or load()).dsa_paged_attn(
-        _take(where, "q", q, _BF16, dev, f"*, *, {DIM}", len(shape) == 3 and shape[2] == DIM),
-        shape[1], shape[0], *_paged(where, new_start, seq_len, page_table, pages, cos_sin, dev),
-        window, scale, _take(where, "workspace", workspace, workspace.dtype, dev, "*", True),
-        _nbytes(workspace),
-        _take(where, "out", out, _BF16, dev, ", ".join(map(str, shape)), out.shape == shape),
+        q.data_ptr(), shape[1], shape[0],
+        *_paged(where, new_start, seq_len, page_table, pages, cos_sin, dev), window, scale,
+        workspace.data_ptr(), _nbytes(workspace), out.data_ptr(),
         _status(where, dev_status, dev), _stream_of(stream, dev))
     _check(rc, where)

@@ -52,8 +52,8 @@ constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffKV = kQSmem * kSlab;
 constexpr uint32_t kOffMx = kOffKV + 8 * kSlab;  // [2][128] block maxima of a row's two halves
 constexpr uint32_t kOffL1 = kOffMx + 1024;       // [128] sum of the second half
-constexpr uint32_t kOffLinv = kOffL1 + 512;      // [2][128] 1/sum, by unit parity
-constexpr uint32_t kOffBar = kOffLinv + 1024;
+constexpr uint32_t kOffLinv = kOffL1 + 512;      // [128] 1/sum
+constexpr uint32_t kOffBar = kOffLinv + 512;
 constexpr uint32_t kSmem = kOffBar + 384;
 static_assert(kSmem <= 232448, "over the shared memory of one CTA");
 
@@ -220,8 +220,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *o_full = bars + 21;
     uint64_t *o_free = bars + 22;   // [2] a half of O's columns left by the stores
     uint64_t *stat_full = bars + 24;
-    uint64_t *drain = bars + 25;    // every product issued is done
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 26);
+    uint64_t *stat_free = bars + 25;  // the stores have read a segment's sums
+    uint64_t *drain = bars + 26;    // every product issued is done
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 27);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     volatile uint32_t *sPages = tmem_holder + 2;             // [2]
     int *sStart = reinterpret_cast<int *>(tmem_holder + 4);  // [5]
@@ -236,11 +237,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     if (warp == 0) {
-        // arrivals a phase takes: a thread per row on q_tm, o_free and stat_full, 8 softmax
-        // warps on s_free, 256 softmax threads on p_full, one on the others
+        // arrivals a phase takes: a thread per row on q_tm, o_free and stat_*, 8 softmax warps
+        // on s_free, 256 softmax threads on p_full, one on the others
         int n = 1;
         uint64_t *bar = bars + lane;
-        if (bar == q_tm || bar == o_free || bar == o_free + 1 || bar == stat_full) n = kRows;
+        if (bar == q_tm || bar == o_free || bar == o_free + 1 || bar == stat_full ||
+            bar == stat_free)
+            n = kRows;
         if (bar == s_free) n = 8;
         if (bar == p_full) n = 256;
         if (bar <= drain) mbar_init(bar, n);
@@ -308,9 +311,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 have = ahead.next(p, y);
                 if (have && fresh_q(y, i + 1)) stage(y, loads++);
                 wait_bar(stat_full, i & 1, abort_flag, p.status);
+                const float linv = sLinv[r];
+                mbar_arrive(stat_free);
                 const bool live = wait_bar(o_full, i & 1, abort_flag, p.status);
                 tc_fence_after();
-                const float linv = sLinv[(i & 1) * kRows + r];
                 const bool mine = r < x.nrows && live;
                 const int slot = 2 * cta + (i > 0);
                 const float4 *cs =
@@ -654,8 +658,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_pair(sp);
             if (hh == 0) {
                 const float tot = sum + sL1[r];
+                // The stores must have taken the segment before's sums: segments of one block
+                // can otherwise run two ahead of them, past the phase they wait for.
+                if (i > 0) mbar_wait(stat_free, (i - 1) & 1, abort_flag, p.status);
                 // a row that saw no key has sum 0 and O 0
-                sLinv[(i & 1) * kRows + r] = tot == 0.0f ? 0.0f : 1.0f / tot;
+                sLinv[r] = tot == 0.0f ? 0.0f : 1.0f / tot;
                 if (!x.whole)
                     reinterpret_cast<float2 *>(p.ws + kWsMl)[(2 * cta + (i > 0)) * kMaxRows + r] =
                         make_float2(m, tot);

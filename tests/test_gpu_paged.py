@@ -145,6 +145,15 @@ ATTN = [  # (sequences (new, total), heads, page, window, rope, padded rows)
     ([(64, 64), (1, 4096)], 7, 128, 5000, True, 0),
     ([(1, 30 + 7 * i) for i in range(200)], 4, 16, 0, True, 3),
     ([(150, 700)], 64, 64, 0, True, 0),
+    # more than 64 heads where most sequences are idle; the same with every one at work
+    ([(0, 10), (1, 300), (0, 5), (0, 7)], 128, 64, 0, True, 1),
+    ([(0, 10), (0, 300), (1, 500), (0, 7)], 70, 16, 100, True, 0),
+    ([(1, 260), (3, 300)], 65, 32, 0, True, 0),
+    # a long prompt beside single tokens, on average few rows per sequence
+    ([(40, 90)] + [(1, 20 + 30 * i) for i in range(60)], 16, 16, 0, True, 0),
+    # many units of one block per SM: a segment's end follows the one before at once
+    ([(100, 100)] * 12 + [(90, 128)], 64, 32, 0, True, 0),
+    ([(256, 256)] * 6, 64, 64, 3, True, 0),
     # many short units per SM, cut where a run ends
     ([(700, 900), (1, 33), (350, 350)], 16, 32, 100, True, 1),
     ([(600, 2000)], 64, 64, 128, True, 0),

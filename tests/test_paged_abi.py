@@ -107,3 +107,16 @@ def test_binding_refuses_tensors_of_another_kind(lib, monkeypatch):
         B.dsa_paged_append(kv, *common[:3], b["pages"].transpose(0, 1))
     with pytest.raises(B.DsaError, match="cos_sin"):
         B.dsa_paged_append(kv, *common, b["cos_sin"][:, :16])
+    with pytest.raises(B.DsaError, match="cos_sin"):
+        B.dsa_paged_append(kv, *common, torch.tensor(1.0))
+    with pytest.raises(B.DsaError, match="page_table"):
+        B.dsa_paged_append(kv, b["new_start"], b["seq_len"], b["page_table"][0], b["pages"])
+    with pytest.raises(B.DsaError, match="dev_status"):
+        B.dsa_paged_append(kv, *common, b["cos_sin"], torch.zeros(2, dtype=torch.int32))
+    q = torch.zeros(3, 8, 512, dtype=torch.bfloat16)
+    work = torch.zeros(4)
+    for out in (q[:2], q.float(), torch.zeros(3, 512, 8, dtype=torch.bfloat16).transpose(1, 2)):
+        with pytest.raises(B.DsaError, match="out"):
+            B.dsa_paged_attn(q, *common, 0, 0.1, work, out)
+    with pytest.raises(B.DsaError, match="workspace"):
+        B.dsa_paged_attn(q, *common, 0, 0.1, torch.zeros(8, 8).t()[::2], torch.zeros_like(q))
