@@ -169,20 +169,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             // sequences of 16K rows: the loads alone keep HBM busy.)
             const int prows = min(1 << p.b.page_shift, kBlock), np = kBlock / prows;
             PageWalk walk(p, sStart);
-            const int blocks = sStart[4];
             int row, row_next = 0, g = 0, m_at = 0;
-            bool alone, alone_next = walk.x.alone;
+            bool have = walk.have, alone, alone_next = walk.x.alone;
             int32_t e, e_next = walk.next(p, lane, prows, np, row_next);
             // Keys that no other unit reads pass through L2 without pushing out what is there
             // (q, the parts to be joined): one token at 128K 56 -> 50 us, 32 users of 8K 83 ->
             // 76. Kept for keys that others read: without, a chunk took 18 % longer.
             const uint64_t once = policy_evict_first(), keep = policy_evict_normal();
             bool ok = true;
-            for (; g < blocks; ++g) {
+            for (bool more; have; ++g, have = more) {
                 e = e_next;
                 row = row_next;
                 alone = alone_next;
                 alone_next = walk.x.alone;
+                more = walk.have;
                 e_next = walk.next(p, lane, prows, np, row_next);
                 const uint64_t pol = alone ? once : keep;
                 const int par = g & 1;
@@ -922,11 +922,13 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
         p.tpu = kChunkRows / heads;
         p.upt = 2;
         p.row_step = 0;
+        p.unit_cost = 2;
     } else {
         p.rows = kRows;
         p.tpu = heads <= kRows ? kRows / heads : 1;
         p.upt = (heads + kRows - 1) / kRows;
         p.row_step = kRows;
+        p.unit_cost = 1;
     }
     p.rpt = std::min(heads, p.rows);
     // a window no shorter than any sequence is no window

@@ -132,8 +132,8 @@ __device__ __forceinline__ void store8(void *to, const uint32_t *v) {
 // Whether segment i of a run needs other queries than the one before it: the second unit of a
 // token group follows the first with the same ones. And whether the segment after x does.
 __device__ __forceinline__ bool fresh_q(const Segment &x, int i) { return i == 0 || x.part == 0; }
-__device__ __forceinline__ bool last_of_q(const Segment &x, const Walk &w) {
-    return x.part == 1 || w.left <= 0;
+__device__ __forceinline__ bool last_of_q(const Params &p, const Segment &x, const Walk &w) {
+    return x.part == 1 || w.left <= p.unit_cost;
 }
 
 // Bits [a, b) of a 32-bit word, a and b clamped to 0..32.
@@ -378,15 +378,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t *const dst0 = sKV + second * kSlab + page * prows * 128;
             const uint64_t pol = policy_evict_normal();  // (each half of the dims reads the keys)
             PageWalk walk(p, sStart);
-            const int blocks = sStart[4];
             int row, row_next = 0, own, own_next = walk.x.part, g = 0, at = 0;
+            bool have = walk.have;
             int32_t e, e_next = walk.next(p, page, prows, np, row_next);
             bool ok = true;
-            for (; g < blocks; ++g) {
+            for (bool more; have; ++g, have = more) {
                 e = e_next;
                 row = row_next;
                 own = own_next;
                 own_next = walk.x.part;
+                more = walk.have;
                 e_next = walk.next(p, page, prows, np, row_next);
                 const int par = g & 1;
                 const uint32_t use = (g >> 1) & 1;
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         if (half == 1 && elect_one()) {
                             mma_commit(s_full);
-                            if (b == x.nb - 1 && last_of_q(x, walk)) mma_commit(q_free);
+                            if (b == x.nb - 1 && last_of_q(p, x, walk)) mma_commit(q_free);
                         }
                         __syncwarp();
                     }

@@ -4,10 +4,12 @@
 // Work. A unit is a few whole tokens of one sequence (or part of one token's heads): rows of q
 // that attend over the same rows of the cache, each up to its own position. Its keys are blocks
 // of 128 positions (aligned, so a page never straddles two blocks). All units' blocks form one
-// sequence that is cut into equal runs, one per CTA (one CTA per SM): a run takes whole units
-// where they fit and parts of a unit at its ends, so a single long sequence and a batch of
-// thousands of short ones both fill the machine, and causal triangles and ragged lengths balance
-// by themselves. A part leaves its unnormalised sum, running maximum and sum of weights in the
+// sequence, each unit's preceded by a few places for what a unit costs beside its blocks (its
+// queries, its results), and that is cut into equal runs, one per CTA (one CTA per SM): a run
+// takes whole units where they fit and parts of a unit at its ends, so a single long sequence
+// and a batch of thousands of short ones both fill the machine, and causal triangles and ragged
+// lengths balance by themselves. (Without the places the CTAs with a prompt's first tokens, many
+// units of one block, took 1,340 us where the others were done in 560: 3,021 tokens, 64 heads.) A part leaves its unnormalised sum, running maximum and sum of weights in the
 // workspace, and a second kernel joins the parts. Every CTA finds its run from the lengths on
 // the device: the blocks of a sequence's first units are sums of floors, known in closed form.
 #pragma once
@@ -64,6 +66,7 @@ struct Params {
     int32_t rows;      // rows of a unit at most
     int32_t row_step;  // rows from one part's first row to the next part's (0: same rows)
     int32_t rpt;       // rows of a token in a unit
+    int32_t unit_cost; // places of a unit before its blocks
     int32_t window;    // 0: the whole context
     float c;           // scale * log2(e)
     int32_t *status;
@@ -108,10 +111,11 @@ __device__ __forceinline__ int group_blocks(const Params &p, const PagedSeq &q, 
     return (hi >> 7) - (lo >> 7) + 1;
 }
 
-// Blocks of the first G token groups of a sequence (G = all of them: the last one may be short).
-static __device__ __noinline__ int64_t blocks_before_many(const Params &p, PagedSeq q, int64_t G) {
+// Places of the first G token groups of a sequence, for each part (G = all of them: the last one
+// may be short).
+static __device__ __noinline__ int64_t places_before_many(const Params &p, PagedSeq q, int64_t G) {
     const int64_t base = q.len - q.n, d = p.tpu;
-    int64_t sum = floor_sum(G, base + d - 1, d) + G;
+    int64_t sum = floor_sum(G, base + d - 1, d) + G * (1 + p.unit_cost);
     if (G * d > q.n) sum += ((int64_t{q.len} - 1) >> 7) - ((base + G * d - 1) >> 7);
     if (p.window > 0) {
         const int64_t a = base - p.window + 1;
@@ -121,8 +125,8 @@ static __device__ __noinline__ int64_t blocks_before_many(const Params &p, Paged
     return sum;
 }
 
-__device__ __forceinline__ int64_t blocks_before(const Params &p, const PagedSeq &q, int G) {
-    return G <= 0 ? 0 : G == 1 ? group_blocks(p, q, 0) : blocks_before_many(p, q, G);
+__device__ __forceinline__ int64_t places_before(const Params &p, const PagedSeq &q, int G) {
+    return G <= 0 ? 0 : G == 1 ? group_blocks(p, q, 0) + p.unit_cost : places_before_many(p, q, G);
 }
 
 __device__ __forceinline__ int groups_of(const Params &p, const PagedSeq &q) {
@@ -138,21 +142,21 @@ __device__ __forceinline__ int unit_rows(const Params &p, int tokens, int part) 
 }
 
 struct Place {
-    int s, g, part, off;  // sequence, token group, unit of the group, block of the unit
+    int s, g, part, off;  // sequence, token group, unit of the group, place of the unit
 };
 
-// The place of block r of sequence s's blocks.
-static __device__ __noinline__ Place find_block(const Params &p, PagedSeq q, int s, int64_t r) {
-    int lo = 0, hi = groups_of(p, q);  // upt * blocks_before(lo) <= r < upt * blocks_before(hi)
+// Place r of sequence s's places.
+static __device__ __noinline__ Place find_place(const Params &p, PagedSeq q, int s, int64_t r) {
+    int lo = 0, hi = groups_of(p, q);  // upt * places_before(lo) <= r < upt * places_before(hi)
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (p.upt * blocks_before(p, q, mid) <= r) lo = mid;
+        if (p.upt * places_before(p, q, mid) <= r) lo = mid;
         else hi = mid;
     }
-    int in = static_cast<int>(r - p.upt * blocks_before(p, q, lo)), part = 0;
-    const int nb = group_blocks(p, q, lo);
-    if (in >= nb) {  // (upt is 1 or 2)
-        in -= nb;
+    int in = static_cast<int>(r - p.upt * places_before(p, q, lo)), part = 0;
+    const int n = group_blocks(p, q, lo) + p.unit_cost;
+    if (in >= n) {  // (upt is 1 or 2)
+        in -= n;
         part = 1;
     }
     return Place{s, lo, part, in};
@@ -206,17 +210,22 @@ struct Walk {
         int hi;
         key_range(p, q, t0, x.lo, hi);
         const int blo = x.lo >> 7, nblk = (hi >> 7) - blo + 1;
+        const int before = max(0, p.unit_cost - at.off), off = max(0, at.off - p.unit_cost);
+        x.nb = min(nblk - off, left - before);
+        if (x.nb <= 0) {  // the run ends before the unit's first block
+            left = 0;
+            return false;
+        }
         x.s = at.s;
         x.posf = q.len - q.n + t0;
         x.posl = hi;
         x.row = unit_row(p, q, t0, at.part);
         x.nrows = unit_rows(p, t1 - t0, at.part);
         x.part = at.part;
-        x.blk = blo + at.off;
-        x.nb = min(nblk - at.off, left);
+        x.blk = blo + off;
         x.whole = x.nb == nblk;
         x.alone = p.upt == 1 && q.n <= p.tpu;
-        left -= x.nb;
+        left -= before + x.nb;
         at.off = 0;
         if (++at.part == p.upt) {
             at.part = 0;
@@ -266,7 +275,7 @@ __device__ __forceinline__ int row_pos(const Params &p, int posf, int r) {
     return p.tpu == 1 ? posf : posf + r / p.rpt;
 }
 
-// Finds this CTA's run, blocks [T0, T1) of all blocks: start[0..3] its first place, start[4] its
+// Finds this CTA's run, places [T0, T1) of all places: start[0..3] its first place, start[4] its
 // length (0 on entry); describes the unit that begins in it and ends beyond for the join. All
 // threads call it; `scratch` holds one value per warp. Ends with a barrier of the CTA, and one
 // inside it publishes what was set up before (TMEM, mbarriers).
@@ -282,7 +291,7 @@ __device__ __forceinline__ void find_run(const Params &p, int64_t *scratch, int 
         bool bad;
         q = paged_seq(p.b, s, bad);
         if (bad && cta == 0) report(p.status, DSA_ERR_BOUNDS);
-        nb = p.upt * blocks_before(p, q, groups_of(p, q));
+        nb = p.upt * places_before(p, q, groups_of(p, q));
         mine += nb;
     }
     int64_t incl = mine;
@@ -307,16 +316,16 @@ __device__ __forceinline__ void find_run(const Params &p, int64_t *scratch, int 
     if (T0 >= T1) {
         if (tid == 0) *desc = JoinDesc{};
     } else if (mine > 0 && T0 < incl && T1 > incl - mine) {
-        // one of this thread's sequences holds the run's first block, its last, or both
+        // one of this thread's sequences holds the run's first place, its last, or both
         int64_t acc = incl - mine;
         for (int s = s0; s < s1; ++s) {
             if (s1 - s0 > 1) {
                 bool bad;
                 q = paged_seq(p.b, s, bad);
-                nb = p.upt * blocks_before(p, q, groups_of(p, q));
+                nb = p.upt * places_before(p, q, groups_of(p, q));
             }
             if (T0 >= acc && T0 < acc + nb) {
-                const Place x = find_block(p, q, s, T0 - acc);
+                const Place x = find_place(p, q, s, T0 - acc);
                 start[0] = x.s;
                 start[1] = x.g;
                 start[2] = x.part;
@@ -324,17 +333,19 @@ __device__ __forceinline__ void find_run(const Params &p, int64_t *scratch, int 
                 start[4] = static_cast<int>(T1 - T0);
             }
             if (T1 > acc && T1 <= acc + nb) {
-                // the unit of the last block: does it begin in this run and end in a later one?
-                const Place x = find_block(p, q, s, T1 - 1 - acc);
-                const int64_t u0 = T1 - 1 - x.off, u1 = u0 + group_blocks(p, q, x.g);
+                // the unit of the last place: does its first block lie in this run, and its last
+                // one in a later run?
+                const Place x = find_place(p, q, s, T1 - 1 - acc);
+                const int64_t u0 = T1 - 1 - x.off;
+                const int64_t u1 = u0 + p.unit_cost + group_blocks(p, q, x.g);
                 JoinDesc d = {};
-                if (u0 >= T0 && u1 > T1) {
+                if (x.off >= p.unit_cost && u0 + p.unit_cost >= T0 && u1 > T1) {
                     const int t0 = x.g * p.tpu, t1 = min(t0 + p.tpu, q.n);
                     d.row = unit_row(p, q, t0, x.part);
                     d.nrows = unit_rows(p, t1 - t0, x.part);
                     d.part = x.part;
                     d.parts = static_cast<int>(div_pos(u1 - 1, run)) - cta + 1;
-                    d.slot0 = u0 == T0 ? 0 : 1;
+                    d.slot0 = u0 <= T0 ? 0 : 1;
                     d.pos = q.len - q.n + t0;
                 }
                 *desc = d;
