@@ -922,13 +922,11 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
         p.tpu = kChunkRows / heads;
         p.upt = 2;
         p.row_step = 0;
-        p.unit_cost = 2;
     } else {
         p.rows = kRows;
         p.tpu = heads <= kRows ? kRows / heads : 1;
         p.upt = (heads + kRows - 1) / kRows;
         p.row_step = kRows;
-        p.unit_cost = 1;
     }
     p.rpt = std::min(heads, p.rows);
     // a window no shorter than any sequence is no window

@@ -132,8 +132,8 @@ __device__ __forceinline__ void store8(void *to, const uint32_t *v) {
 // Whether segment i of a run needs other queries than the one before it: the second unit of a
 // token group follows the first with the same ones. And whether the segment after x does.
 __device__ __forceinline__ bool fresh_q(const Segment &x, int i) { return i == 0 || x.part == 0; }
-__device__ __forceinline__ bool last_of_q(const Params &p, const Segment &x, const Walk &w) {
-    return x.part == 1 || w.left <= p.unit_cost;
+__device__ __forceinline__ bool last_of_q(const Segment &x, const Walk &w) {
+    return x.part == 1 || w.left <= kUnitCost;
 }
 
 // Bits [a, b) of a 32-bit word, a and b clamped to 0..32.
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         if (half == 1 && elect_one()) {
                             mma_commit(s_full);
-                            if (b == x.nb - 1 && last_of_q(p, x, walk)) mma_commit(q_free);
+                            if (b == x.nb - 1 && last_of_q(x, walk)) mma_commit(q_free);
                         }
                         __syncwarp();
                     }

@@ -24,6 +24,11 @@ constexpr int kBlock = 128;        // keys in a block
 constexpr int kThreads = 512;      // of both kernels
 constexpr int kMaxCtas = 152;
 
+// Places of a unit before its blocks. (0, 2, 3 and 4 for chunks: 2,033, 1,173, 1,135 and 1,154 us
+// for a prompt of 4,096 tokens, 576, 418, 487 and 467 for 34 prompts of 208; 1, 2 and 4 for
+// single tokens: 91, 87 and 90 us for 64 users up to 8K, 73, 74 and 75 for 32 users of 8K.)
+constexpr int kUnitCost = 2;
+
 constexpr float kRescale = 8.0f;      // log2 units the running maximum may lag behind
 constexpr float kNoMax = -1.0e30f;    // running maximum of a row that has seen no key: finite,
                                       // so that (masked) -inf minus it stays -inf
@@ -66,7 +71,6 @@ struct Params {
     int32_t rows;      // rows of a unit at most
     int32_t row_step;  // rows from one part's first row to the next part's (0: same rows)
     int32_t rpt;       // rows of a token in a unit
-    int32_t unit_cost; // places of a unit before its blocks
     int32_t window;    // 0: the whole context
     float c;           // scale * log2(e)
     int32_t *status;
@@ -115,7 +119,7 @@ __device__ __forceinline__ int group_blocks(const Params &p, const PagedSeq &q, 
 // may be short).
 static __device__ __noinline__ int64_t places_before_many(const Params &p, PagedSeq q, int64_t G) {
     const int64_t base = q.len - q.n, d = p.tpu;
-    int64_t sum = floor_sum(G, base + d - 1, d) + G * (1 + p.unit_cost);
+    int64_t sum = floor_sum(G, base + d - 1, d) + G * (1 + kUnitCost);
     if (G * d > q.n) sum += ((int64_t{q.len} - 1) >> 7) - ((base + G * d - 1) >> 7);
     if (p.window > 0) {
         const int64_t a = base - p.window + 1;
@@ -126,7 +130,7 @@ static __device__ __noinline__ int64_t places_before_many(const Params &p, Paged
 }
 
 __device__ __forceinline__ int64_t places_before(const Params &p, const PagedSeq &q, int G) {
-    return G <= 0 ? 0 : G == 1 ? group_blocks(p, q, 0) + p.unit_cost : places_before_many(p, q, G);
+    return G <= 0 ? 0 : G == 1 ? group_blocks(p, q, 0) + kUnitCost : places_before_many(p, q, G);
 }
 
 __device__ __forceinline__ int groups_of(const Params &p, const PagedSeq &q) {
@@ -154,7 +158,7 @@ static __device__ __noinline__ Place find_place(const Params &p, PagedSeq q, int
         else hi = mid;
     }
     int in = static_cast<int>(r - p.upt * places_before(p, q, lo)), part = 0;
-    const int n = group_blocks(p, q, lo) + p.unit_cost;
+    const int n = group_blocks(p, q, lo) + kUnitCost;
     if (in >= n) {  // (upt is 1 or 2)
         in -= n;
         part = 1;
@@ -210,7 +214,7 @@ struct Walk {
         int hi;
         key_range(p, q, t0, x.lo, hi);
         const int blo = x.lo >> 7, nblk = (hi >> 7) - blo + 1;
-        const int before = max(0, p.unit_cost - at.off), off = max(0, at.off - p.unit_cost);
+        const int before = max(0, kUnitCost - at.off), off = max(0, at.off - kUnitCost);
         x.nb = min(nblk - off, left - before);
         if (x.nb <= 0) {  // the run ends before the unit's first block
             left = 0;
@@ -337,9 +341,9 @@ __device__ __forceinline__ void find_run(const Params &p, int64_t *scratch, int 
                 // one in a later run?
                 const Place x = find_place(p, q, s, T1 - 1 - acc);
                 const int64_t u0 = T1 - 1 - x.off;
-                const int64_t u1 = u0 + p.unit_cost + group_blocks(p, q, x.g);
+                const int64_t u1 = u0 + kUnitCost + group_blocks(p, q, x.g);
                 JoinDesc d = {};
-                if (x.off >= p.unit_cost && u0 + p.unit_cost >= T0 && u1 > T1) {
+                if (x.off >= kUnitCost && u0 + kUnitCost >= T0 && u1 > T1) {
                     const int t0 = x.g * p.tpu, t1 = min(t0 + p.tpu, q.n);
                     d.row = unit_row(p, q, t0, x.part);
                     d.nrows = unit_rows(p, t1 - t0, x.part);
