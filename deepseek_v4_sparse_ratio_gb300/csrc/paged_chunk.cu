@@ -17,9 +17,9 @@
 // own four into the same slots, where PV finds them; meanwhile the other group holds the block
 // before for its PV. TMEM: O 256 columns, S 128, P 64, q 64: all 512.
 //
-// Roles: warps 0-3 bring q's last chunks to TMEM and store finished units (so the softmax of the
-// next unit need not wait for the stores), warp 4 loads K, warp 5 issues the products, warp 6
-// loads q, warps 8-15 the softmax: TMEM lane = row, two warps per 32 rows, 64 keys each.
+// Roles: warps 0-3 store finished units (so the softmax of the next unit need not wait for the
+// stores), warp 4 loads K, warp 5 issues the products, warp 6 loads q, warps 8-15 bring q's last
+// chunks to TMEM and do the softmax: TMEM lane = row, two warps per 32 rows, 64 keys each.
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -237,15 +237,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     if (warp == 0) {
-        // arrivals a phase takes: a thread per row on q_tm, o_free and stat_*, 8 softmax warps
-        // on s_free, 256 softmax threads on p_full, one on the others
+        // arrivals a phase takes: a thread per row on o_free and stat_*, 8 softmax warps on
+        // s_free, 256 softmax threads on p_full and q_tm, one on the others
         int n = 1;
         uint64_t *bar = bars + lane;
-        if (bar == q_tm || bar == o_free || bar == o_free + 1 || bar == stat_full ||
-            bar == stat_free)
-            n = kRows;
+        if (bar == o_free || bar == o_free + 1 || bar == stat_full || bar == stat_free) n = kRows;
         if (bar == s_free) n = 8;
-        if (bar == p_full) n = 256;
+        if (bar == p_full || bar == q_tm) n = 256;
         if (bar <= drain) mbar_init(bar, n);
         if (lane == 31) {
             *abort_flag = 0;
@@ -266,50 +264,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < kSoftWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
         if (warp < kOutWarps) {
-            // ---------------- q's last two chunks to TMEM (the rotation on the way), and the
-            // finished units to memory. Thread = row.
+            // ---------------- finished units to memory. Thread = row.
             const int r = tid;
             const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-            Walk ahead(p, sStart), walk(p, sStart);
-            Segment x, y;
-            auto stage = [&](const Segment &u, int i) -> bool {
-                const bool mine = r < u.nrows;
-                const uint4 *src = reinterpret_cast<const uint4 *>(q + (u.row + r) * kD + 384);
-                const float4 *cs = reinterpret_cast<const float4 *>(
-                    p.b.cos_sin + (mine ? int64_t{row_pos(p, u.posf, r)} * kRope : 0));
-                // all of the row's loads before the wait for the previous unit's last QK
-                uint32_t v[64];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const uint4 w = mine ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-                    v[4 * k] = w.x;
-                    v[4 * k + 1] = w.y;
-                    v[4 * k + 2] = w.z;
-                    v[4 * k + 3] = w.w;
-                }
-                if (p.b.cos_sin && mine) {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float4 a = __ldg(cs + k);
-                        v[32 + 2 * k] = turn_pair(v[32 + 2 * k], a.x, a.y);
-                        v[33 + 2 * k] = turn_pair(v[33 + 2 * k], a.z, a.w);
-                    }
-                }
-                const bool ok = wait_bar(q_free, (i & 1) ^ 1, abort_flag, p.status);
-                tc_fence_after();
-                tmem_st32(lane_base + kQCol, reinterpret_cast<const uint32_t(&)[32]>(v[0]));
-                tmem_st32(lane_base + kQCol + 32, reinterpret_cast<const uint32_t(&)[32]>(v[32]));
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(q_tm);
-                return ok;
-            };
-            int loads = 0;
-            bool have = ahead.next(p, y);
-            if (have) stage(y, loads++);
+            Walk walk(p, sStart);
+            Segment x;
             for (int i = 0; walk.next(p, x); ++i) {
-                have = ahead.next(p, y);
-                if (have && fresh_q(y, i + 1)) stage(y, loads++);
                 wait_bar(stat_full, i & 1, abort_flag, p.status);
                 const float linv = sLinv[r];
                 mbar_arrive(stat_free);
@@ -550,9 +510,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         Segment x;
         int i = 0, g = 0;
         for (; walk.next(p, x); ++i) {
+            const bool mine = r < x.nrows;
+            const int pos = mine ? row_pos(p, x.posf, r) : x.posl;
+            if (fresh_q(x, i)) {
+                // q's last two chunks to TMEM, 64 dims by each of a row's two threads, dims
+                // 448..511 turned on the way. (The last unit's QK, which read what was there, is
+                // done: its last S was read above.)
+                const uint4 *src = reinterpret_cast<const uint4 *>(q + (x.row + r) * kD + 384) +
+                                   8 * hh;
+                uint32_t v[32];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint4 w = mine ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+                    v[4 * k] = w.x;
+                    v[4 * k + 1] = w.y;
+                    v[4 * k + 2] = w.z;
+                    v[4 * k + 3] = w.w;
+                }
+                if (hh == 1 && p.b.cos_sin && mine) {
+                    const float4 *cs =
+                        reinterpret_cast<const float4 *>(p.b.cos_sin + int64_t{pos} * kRope);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float4 a = __ldg(cs + k);
+                        v[2 * k] = turn_pair(v[2 * k], a.x, a.y);
+                        v[2 * k + 1] = turn_pair(v[2 * k + 1], a.z, a.w);
+                    }
+                }
+                tmem_st32(lane_base + kQCol + 32 * hh, v);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(q_tm);
+            }
             float l[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             float m = kNoMax;
-            const int pos = r < x.nrows ? row_pos(p, x.posf, r) : x.posl;
             for (int b = 0; b < x.nb; ++b, ++g) {
                 const int par = g & 1;
                 const int k0 = (x.blk + b) * kBlock;
