@@ -159,13 +159,13 @@ __device__ __forceinline__ float zero_if_finite32(const uint32_t (&s)[32]) {
     return (t[0] + t[1]) + (t[2] + t[3]);
 }
 
-// Bits of the logits among `of` that are not finite.
-__device__ __forceinline__ uint32_t odd32(const uint32_t (&s)[32], uint32_t of) {
+// Bits of the logits that are not finite.
+__device__ __forceinline__ uint32_t odd32(const uint32_t (&s)[32]) {
     uint32_t odd = 0;
 #pragma unroll
     for (int j = 0; j < 32; ++j)
         if (!(fabsf(__uint_as_float(s[j])) <= 3.4028234e38f)) odd |= 1u << j;
-    return odd & of;
+    return odd;
 }
 
 __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
@@ -387,15 +387,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         } else if (warp == kQWarp) {
-            // ---------------- q's chunks in shared memory, as soon as the last ones are read;
-            // its rows are brought to L2 before that
+            // ---------------- q's chunks in shared memory, as soon as the last ones are read.
+            // (Bringing its rows to L2 before that changed nothing.)
             const uint64_t pol_stream = policy_evict_first();
             Walk walk(p, sStart);
             Segment x;
             int loads = 0;
             for (int i = 0; walk.next(p, x); ++i) {
                 if (!fresh_q(x, i)) continue;
-                if (lane == 0) prefetch_l2(q + x.row * kD, static_cast<uint32_t>(x.nrows) * kD * 2);
                 if (!wait_bar(q_free, (loads & 1) ^ 1, abort_flag, p.status)) break;
                 if (lane == 0) {
                     mbar_expect_tx(q_full, kQSmem * kSlab);
@@ -575,12 +574,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // A row of the cache that holds an infinity or NaN makes its logit non-finite
                     // in every row of q. Where a row of q must not see the key, those elements
                     // become zero in the own slabs (0 * inf in PV would reach every row); rows
-                    // that do see the key have a NaN probability already. A key at a time: lane
-                    // = 16-byte piece of its four slabs.
+                    // that do see the key have a NaN probability already. The sub-partitions'
+                    // warps, which all see such a key, take a quarter of the keys each, one at a
+                    // time: lane = 16-byte piece of its four slabs.
                     if (__any_sync(0xFFFFFFFFu,
                                    live && !(zero_if_finite32(s0) + zero_if_finite32(s1) == 0.0f))) {
-                        uint32_t odd0 = __reduce_or_sync(0xFFFFFFFFu, odd32(s0, ~v0));
-                        uint32_t odd1 = __reduce_or_sync(0xFFFFFFFFu, odd32(s1, ~v1));
+                        const uint32_t mine4 = 0x11111111u << sp;
+                        uint32_t odd0 = __reduce_or_sync(0xFFFFFFFFu, odd32(s0)) & mine4;
+                        uint32_t odd1 = __reduce_or_sync(0xFFFFFFFFu, odd32(s1)) & mine4;
                         mbar_wait(&full[2 * par], 1, abort_flag, p.status);
                         mbar_wait(&full[2 * par + 1], 1, abort_flag, p.status);
                         uint8_t *tile = sKV + (4 * par + (lane >> 3)) * kSlab + (lane & 7) * 16;

@@ -394,11 +394,6 @@ __device__ __forceinline__ void prefetch_tmap(const CUtensorMap *tm) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(tm) : "memory");
 }
 
-// Brings `bytes` from `src` (both multiples of 16) into L2.
-__device__ __forceinline__ void prefetch_l2(const void *src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
-
 // mbar_wait with the loop out of line: its many copies would push the roles' code out of the
 // instruction caches.
 static __device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *abort,
