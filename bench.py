@@ -96,7 +96,7 @@ def score_scratch_bytes(wl, tile):
 # the sources the captured build came from; a changed source reports null.
 NCU_TRAFFIC = {
     "attn_kernel": {"bytes": 344.883e6 + 234.731e6, "files": ("attn.cu", "common.cuh", "internal.h"),
-                    "sha256_16": "babec7cc87d7dd59"},
+                    "sha256_16": "7937fd79f076a53f"},
     "score_kernel": {"bytes": 76.964e6 + 478.236e6,
                      "files": ("score_topk.cu", "common.cuh", "internal.h"),
                      "sha256_16": "0d66d1fb771e9c91"},

@@ -765,9 +765,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 // P's buffer is free once the last PV is done: it carries (m_r, l_r)
                 float *sXm = reinterpret_cast<float *>(sP);
                 float *sXl = sXm + 64;
-                if (st < 64) {
-                    sXm[st] = has ? sM[cur * 64 + st] : -INFINITY;
-                    sXl[st] = sL[st] + sL[64 + st] + sL[128 + st] + sL[192 + st];
+                // (by each half's own warp: the halves' maxima switch buffers on their own)
+                if (sp == 0) {
+                    const int hd = hb + lane;
+                    sXm[hd] = has ? sM[cur * 64 + hd] : -INFINITY;
+                    sXl[hd] = sL[hd] + sL[64 + hd] + sL[128 + hd] + sL[192 + hd];
                 }
                 cluster_sync();
                 if (st < 64) {
