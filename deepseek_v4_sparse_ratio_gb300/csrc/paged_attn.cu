@@ -7,15 +7,11 @@
 // and value of every head, so the (token, head) rows of q that share keys can be stacked into
 // one matrix product whatever token or head they come from.
 //
-// Work. A unit is up to 64 rows of q: floor(64 / heads) whole tokens of a sequence, or half
-// of one token's heads when there are more than 64. Its keys are blocks of 128 positions
-// (aligned, so pages never straddle two blocks). All units' blocks form one sequence that is
-// cut into equal runs, one per CTA (one CTA per SM): a run takes whole units where they fit
-// and parts of a unit at its ends, so a single long sequence and a batch of thousands of short
-// ones both fill the machine, and causal triangles and ragged lengths balance by themselves.
-// A part leaves its (unnormalised sum, running maximum, sum of weights) in the workspace, and
-// a second kernel joins the parts. Every CTA finds its run from the lengths on the device:
-// the blocks of a sequence's first units are a sum of floors in closed form.
+// This file holds the kernel for few rows of q per sequence (single tokens, short bands), the
+// join of cut units, and the entry point; paged_chunk.cu the kernel for chunks, paged_walk.cuh
+// the list of work that both cut evenly over the SMs. A unit here is up to 64 rows of q:
+// floor(64 / heads) whole tokens of a sequence, or 64 of a token's heads and then the rest when
+// there are more.
 //
 // A block (the layout that the window + selected attention of this library uses, with the
 // rows loaded by TMA, page by page): everything is transposed so that the 128 keys sit on the
@@ -27,6 +23,13 @@
 // one chunk of the next block land early. Chunk c holds dims 64 ((c + 2) mod 8) ..: the
 // rotated dims (448..511) are chunk 5, which the first product reaches in the middle of a
 // unit's first block, after other warps have turned that chunk of the queries in place.
+//
+// Bound: HBM for single tokens (64 heads: 128 flops a byte, against 282 of the machine). One tile
+// is all that fits beside q (64 KB) and P, so a block is a chain (PV of the block before frees
+// the slots, 1,900 cycles of load latency, the last QK products, 1,000 cycles of softmax): 6,540
+// cycles per 128 KB and SM, 5.6 TB/s, 83 % of the measured copy rate, in the steady state of 152
+// sequences of 16,384 (454 us). One token at 131,072: 46 us, of which 9 are the launch's start
+// (lengths, q, the first tile, instructions) and 8 the join; 64 users of up to 8,192: 85 us.
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -916,7 +919,13 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.ws = static_cast<uint8_t *>(workspace);
     p.heads = heads;
-    const bool chunk = n_new * heads > int64_t{n_seqs} * kRows;
+    // The chunk kernel from an average of more than 256 rows of q per sequence on. Below, a unit
+    // of 64 rows reads the keys at most four times and does not compute the logits twice. Single
+    // and chunk kernel (us): 32 sequences of 8,192 with 64 rows 74 / 126, 128 rows 130 / 132,
+    // 256 rows 232 / 240, 512 rows 415 / 407; 4 of 1,024 with 64 rows 23 / 28, 256 rows 28 / 30;
+    // 16 of up to 16,384 with 160 on average 91 / 105; 64 prompts of 100 tokens (6,400 rows) 477 /
+    // 302; one of 2,048 tokens at 16,384 4,614 / 3,764. (One token of 128 heads 60 / 58.)
+    const bool chunk = n_new * heads > int64_t{n_seqs} * 256;
     if (chunk) {
         p.rows = kChunkRows;
         p.tpu = kChunkRows / heads;

@@ -1,7 +1,7 @@
 // dsa_paged_attn for chunks: units of up to 128 rows of q (whole tokens of one sequence) and half
 // of the output dims.
 //
-// The kernel for single tokens (paged_attn.cu) keeps one 128-key tile of all 512 dims beside 64
+// The kernel for few rows (paged_attn.cu) keeps one 128-key tile of all 512 dims beside 64
 // rows of q; its block is one serial chain (load, QK, softmax, PV), and its N=64 products read
 // 6 KB of shared memory for 131,072 multiply-adds. With 128 rows the products run at full rate
 // (8 KB for 262,144), but the sums of 128 rows x 512 dims would fill TMEM alone. So a unit takes
@@ -20,6 +20,12 @@
 // Roles: warps 0-3 store finished units (so the softmax of the next unit need not wait for the
 // stores), warp 4 loads K, warp 5 issues the products, warp 6 loads q, warps 8-15 bring q's last
 // chunks to TMEM and do the softmax: TMEM lane = row, two warps per 32 rows, 64 keys each.
+//
+// Bound: the tensor pipe, 69 % active. A block takes about 4,450 cycles, 3,090 of them products
+// at full rate; the rest is issue around the waits (the softmax, 1,250 cycles, runs beside them).
+// 2,048 tokens of 64 heads at 16,384: 3.75 ms, 1,100 TFLOP/s of the result's own flops (0.57 of the
+// measured peak, 0.86 with the logits counted twice). Short units pay for their change: 64
+// prompts of 100 tokens 302 us, 4,096 tokens with a 128-row window 280 us.
 #include <cudaTypedefs.h>
 #include <math.h>
 

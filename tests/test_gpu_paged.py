@@ -151,6 +151,10 @@ ATTN = [  # (sequences (new, total), heads, page, window, rope, padded rows)
     ([(1, 260), (3, 300)], 65, 32, 0, True, 0),
     # a long prompt beside single tokens, on average few rows per sequence
     ([(40, 90)] + [(1, 20 + 30 * i) for i in range(60)], 16, 16, 0, True, 0),
+    # units of 128 rows with odd head counts
+    ([(120, 120), (200, 333)], 5, 16, 0, True, 2),
+    ([(400, 450)], 1, 64, 200, True, 0),
+    ([(5, 40), (9, 300)], 127, 32, 0, True, 0),
     # many units of one block per SM: a segment's end follows the one before at once
     ([(100, 100)] * 12 + [(90, 128)], 64, 32, 0, True, 0),
     ([(256, 256)] * 6, 64, 64, 3, True, 0),
