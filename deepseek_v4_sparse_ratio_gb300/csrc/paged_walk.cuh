@@ -149,21 +149,26 @@ struct Place {
     int s, g, part, off;  // sequence, token group, unit of the group, place of the unit
 };
 
-// Place r of sequence s's places.
-static __device__ __noinline__ Place find_place(const Params &p, PagedSeq q, int s, int64_t r) {
+// The token group of a sequence that holds its place r (of all parts' places).
+static __device__ __noinline__ int find_group(const Params &p, PagedSeq q, int64_t r) {
     int lo = 0, hi = groups_of(p, q);  // upt * places_before(lo) <= r < upt * places_before(hi)
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (p.upt * places_before(p, q, mid) <= r) lo = mid;
         else hi = mid;
     }
-    int in = static_cast<int>(r - p.upt * places_before(p, q, lo)), part = 0;
-    const int n = group_blocks(p, q, lo) + kUnitCost;
+    return lo;
+}
+
+__device__ __forceinline__ Place find_place(const Params &p, const PagedSeq &q, int s, int64_t r) {
+    const int g = q.n > p.tpu ? find_group(p, q, r) : 0;
+    int in = static_cast<int>(r - (g > 0 ? p.upt * places_before(p, q, g) : 0)), part = 0;
+    const int n = group_blocks(p, q, g) + kUnitCost;
     if (in >= n) {  // (upt is 1 or 2)
         in -= n;
         part = 1;
     }
-    return Place{s, lo, part, in};
+    return Place{s, g, part, in};
 }
 
 // a / b for a >= 0, b > 0: the 32-bit division where both fit, as they nearly always do.
@@ -308,13 +313,16 @@ __device__ __forceinline__ void find_run(const Params &p, int64_t *scratch, int 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    int64_t total = 0;
+    // (scanned once more in every warp; few instructions, as each is fetched cold)
+    int64_t upto = lane < kThreads / 32 ? scratch[lane] : 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        const int64_t v = scratch[w];
-        if (w < warp) incl += v;
-        total += v;
+    for (int w = 1; w < kThreads / 32; w <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, w);
+        if (lane >= w) upto += v;
     }
+    const int64_t total = __shfl_sync(0xFFFFFFFFu, upto, kThreads / 32 - 1);
+    const int64_t below = __shfl_sync(0xFFFFFFFFu, upto, warp > 0 ? warp - 1 : 0);
+    if (warp > 0) incl += below;
     const int64_t run = div_pos(total + gridDim.x - 1, gridDim.x);
     const int64_t T0 = run * cta, T1 = min(T0 + run, total);
     if (T0 >= T1) {

@@ -349,8 +349,9 @@ int dsa_index_score_topk_noalloc(const void *q_idx, const float *w, const void *
  *   new_start [n_seqs+1] int32: rows new_start[s] .. new_start[s+1]-1 of the new tokens'
  *     arrays belong to sequence s; they are its last n_s = new_start[s+1]-new_start[s] tokens,
  *     so row new_start[s]+i has position seq_len[s]-n_s+i. n_s may be 0.
- *   n_new: rows of the new tokens' arrays, > 0. Rows from new_start[n_seqs] on belong to no
- *     sequence (a batch padded to a captured size): they are not written.
+ *   n_new: rows of the new tokens' arrays, > 0. Rows before new_start[0] and from
+ *     new_start[n_seqs] on belong to no sequence (a batch padded to a captured size): they are
+ *     not written.
  *   cos_sin [n_pos, 32, 2] fp32 or NULL: (cos, sin) of every position and pair. A row's last
  *     64 elements are 32 adjacent pairs (x, y); position p turns them by its angles,
  *     R(p): (x, y) -> (x cos - y sin, x sin + y cos).

@@ -347,6 +347,40 @@ def test_writes_stay_inside_the_buffers(dsa):
         assert bool((buf[:guard] == 5).all()) and bool((buf[-guard:] == 5).all())
 
 
+@pytest.mark.parametrize("heads", [8, 64])
+def test_sequences_that_share_pages(dsa, workspace, heads):
+    """A common prefix of whole pages in three sequences, one of them twice in the batch."""
+    batch = R.make([(1, 200), (30, 260), (1, 200), (2, 150)], 16, seed=27)
+    for s in (1, 2, 3):
+        batch["page_table"][s, :8] = batch["page_table"][0, :8]
+    batch["page_table"][2] = batch["page_table"][0]
+    q = queries(batch, heads, 17)
+    out = run_attn(batch, q, 0, workspace)
+    check_attn(out, batch, q, 0)
+
+
+def test_thousands_of_sequences(dsa, workspace):
+    lens = [(1 if i % 3 else 0, 1 + i % 40) for i in range(3000)]
+    batch = R.make(lens, 16, seed=28)
+    q = queries(batch, 2, 18, pad=1)
+    out = run_attn(batch, q, 0, workspace)
+    check_attn(out, batch, q, 0)
+
+
+def test_rows_before_the_first_sequence_are_left(dsa, workspace):
+    batch = R.make([(3, 20), (2, 40)], 16, seed=29)
+    batch["new_start"] = torch.tensor([2, 5, 7], dtype=torch.int32)
+    kv = torch.randn(8, 512, generator=torch.Generator().manual_seed(6)).bfloat16()
+    ref, tol = R.append(batch, kv)
+    gb = to_gpu(batch)
+    B.dsa_paged_append(kv.cuda(), *args(gb), gb["cos_sin"])
+    torch.cuda.synchronize()
+    assert bool(((gb["pages"].cpu().double() - ref).abs() <= tol).all())
+    q = torch.randn(8, 16, 512, generator=torch.Generator().manual_seed(7)).bfloat16()
+    out = run_attn(batch, q, 0, workspace)
+    check_attn(out, batch, q, 0)
+
+
 # --------------------------------------------------------------------------- how it is used
 
 def _serve(batch, steps, heads, window, workspace, stream=None):
