@@ -7,7 +7,8 @@
 // (x c - y s, x s + y c) with (c, s) = cos_sin[p][i], in fp32 and rounded to bf16 once; the
 // other 448 elements are copied. Bound by HBM (a row in, a row out, 256 bytes of angles): 56,436
 // rows of 16 sequences in 17.4 us, 0.95 of the measured copy rate; up to a few thousand rows
-// by the launch (4 us). One warp per row: the row's loads are in flight while its sequence is looked up.
+// by the launch (4 us). One warp per row: the row's loads are in flight while its sequence is
+// looked up.
 #include <math.h>
 
 #include <algorithm>
@@ -37,6 +38,23 @@ __device__ __forceinline__ int find_seq(const PagedBatch &b, int64_t r, int lane
     return lo;
 }
 
+__device__ __forceinline__ bool holds(const PagedSeq &q, int64_t r) {
+    return r >= q.row0 && r < int64_t{q.row0} + q.n;
+}
+
+// The same by looking at every sequence: the last one that holds row r, -1 when none does. For
+// rows of padding, and for starts that decrease somewhere, among which find_seq may miss the
+// sequence whose numbers are right.
+__device__ __forceinline__ int find_seq_any(const PagedBatch &b, int64_t r, int lane) {
+    int at = -1;
+#pragma unroll 1
+    for (int s = lane; s < b.n_seqs; s += 32) {
+        bool bad;
+        if (holds(paged_seq(b, s, bad), r)) at = s;
+    }
+    return __reduce_max_sync(0xFFFFFFFFu, at);
+}
+
 __device__ __forceinline__ uint32_t rotate_pair(uint32_t v, float c, float s) {
     const float x = bf16lo(v), y = bf16hi(v);
     const __nv_bfloat162 r = __floats2bfloat162_rn(x * c - y * s, x * s + y * c);
@@ -44,8 +62,9 @@ __device__ __forceinline__ uint32_t rotate_pair(uint32_t v, float c, float s) {
 }
 
 // One warp per row; lane l moves 16-byte pieces l and l + 32, and the last eight pieces
-// hold the rotated pairs.
-__global__ void __launch_bounds__(kAppendWarps * 32)
+// hold the rotated pairs. The bound keeps it at 32 registers, eight CTAs an SM (with 38, six
+// CTAs: 25.6 instead of 23.6 us for 56,436 rows from a cold L2).
+__global__ void __launch_bounds__(kAppendWarps * 32, 2048 / (kAppendWarps * 32))
     paged_append_kernel(const PagedBatch b, const uint4 *kv, __nv_bfloat16 *pages,
                         int32_t *status) {
     wait_before();
@@ -61,10 +80,14 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
     if (r >= b.n_new) return;
     const uint4 *src = kv + r * (kD / 8) + lane;
     uint4 v0 = __ldg(src), v1 = __ldg(src + 32);
-    const int s = find_seq(b, r, lane);
+    int s = find_seq(b, r, lane);
     bool bad;
-    const PagedSeq q = paged_seq(b, s, bad);
-    if (r < q.row0 || r >= int64_t{q.row0} + q.n) return;
+    PagedSeq q = paged_seq(b, s, bad);
+    if (!holds(q, r)) {
+        s = find_seq_any(b, r, lane);
+        if (s < 0) return;
+        q = paged_seq(b, s, bad);
+    }
     const int32_t p = q.len - q.n + static_cast<int32_t>(r - q.row0);
     const int32_t page = __ldg(b.page_table + int64_t{s} * b.max_pages + (p >> b.page_shift));
     if (page < 0 || page >= b.n_pages) {

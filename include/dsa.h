@@ -360,6 +360,8 @@ int dsa_index_score_topk_noalloc(const void *q_idx, const float *w, const void *
  * graph replays with the lengths they hold then. A sequence whose numbers cannot be
  * (new_start decreasing, negative or beyond n_new; seq_len < n_s, > max_pages*page_size or
  * > n_pos) is skipped whole: its rows are not written, and DSA_ERR_BOUNDS goes to dev_status.
+ * (Where starts that decrease give one row to two sequences of possible numbers, either may
+ * have it.)
  * A needed page_table entry outside [0, n_pages) is reported the same way and its rows are
  * left out (not written by the append, not seen by the attention).
  */

@@ -123,6 +123,31 @@ def test_bad_starts_write_nothing_of_their_sequences(dsa, workspace, starts):
     assert bool((out[~rows] == 7.0).all())
 
 
+@pytest.mark.parametrize("at,start", [(20, -1), (20, 500), (31, -5), (1, 40), (64, -2)])
+def test_starts_that_decrease_cost_their_own_sequences_alone(dsa, workspace, at, start):
+    """65 sequences of a row each, one start out of order: those whose numbers cannot be are
+    skipped, all others are served (their rows belong to no other sequence)."""
+    batch = R.make([(1, 20 + s) for s in range(65)], 16, seed=30)
+    batch["new_start"][at] = start
+    ok = [s for s in range(65) if R.valid(batch, s, 65)]
+    spans = [tuple(batch["new_start"][s:s + 2].tolist()) for s in ok]
+    taken = torch.zeros(66, dtype=torch.int32)
+    for a, b in spans:
+        taken[a:b] += 1
+    assert 2 <= len(ok) < 65 and int(taken.max()) == 1
+    kv = torch.randn(65, 512, generator=torch.Generator().manual_seed(6)).bfloat16()
+    ref, tol = R.append(batch, kv)
+    gb = to_gpu(batch)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.dsa_paged_append(kv.cuda(), *args(gb), gb["cos_sin"], status)
+    torch.cuda.synchronize()
+    assert status.item() == B.DSA_ERR_BOUNDS
+    assert bool(((gb["pages"].cpu().double() - ref).abs() <= tol).all())
+    q = torch.randn(65, 16, 512, generator=torch.Generator().manual_seed(7)).bfloat16()
+    out = run_attn(batch, q, 0, workspace)
+    check_attn(out, batch, q, 0)
+
+
 # --------------------------------------------------------------------------- attention
 
 ATTN = [  # (sequences (new, total), heads, page, window, rope, padded rows)
