@@ -7,8 +7,8 @@ function names. There is no CPU fallback: calls raise if the library is missing.
 """
 from .buildlib import build as _build_lib
 from ._binding import (DIM, DSA_PAGED_WORKSPACE_BYTES, HEADS, INDEX_DIM, INDEX_HEADS,  # noqa: F401
-                       MAX_PAGE_SIZE, MAX_PAGED_HEADS, RATIO, ROPE_DIM, DsaError, PoolState,
-                       PrefillWorkspace, dsa_bounded_wait_selftest, dsa_index_score_topk,
+                       MAX_PAGE_SIZE, MAX_PAGED_HEADS, MAX_PAGED_TOKENS, RATIO, ROPE_DIM, DsaError,
+                       PoolState, PrefillWorkspace, dsa_bounded_wait_selftest, dsa_index_score_topk,
                        dsa_index_score_topk_noalloc, dsa_paged_append, dsa_paged_attn,
                        dsa_pool_append, dsa_prefill_chunk, dsa_prefill_chunk_host,
                        dsa_score_scratch_bytes, dsa_strerror, dsa_window_sparse_attn, load)

@@ -27,7 +27,7 @@ EXPORTS = ("dsa_pool_append", "dsa_score_scratch_bytes", "dsa_index_score_topk",
            "dsa_paged_append", "dsa_paged_attn")
 DSA_STATIC_SCRATCH_BYTES = 16 << 20
 DSA_PAGED_WORKSPACE_BYTES = 40 << 20
-ROPE_DIM, MAX_PAGE_SIZE, MAX_PAGED_HEADS = 64, 1024, 128
+ROPE_DIM, MAX_PAGE_SIZE, MAX_PAGED_HEADS, MAX_PAGED_TOKENS = 64, 1024, 128, 1 << 24
 
 
 class DsaError(RuntimeError):
@@ -351,6 +351,8 @@ def dsa_paged_attn(q, new_start, seq_len, page_table, pages, window: int, scale:
         _refuse(where, "out", _BF16, ", ".join(map(str, shape)), dev)
     if not (workspace.get_device() == dev and workspace.is_contiguous()):
         _refuse(where, "workspace", workspace.dtype, "*", dev)
+    if window >> 31:   # ctypes would drop the upper bits
+        raise DsaError(DSA_ERR_SHAPE, f"{where}: window {window} is no 32-bit count")
     rc = (_lib or load()).dsa_paged_attn(
         q.data_ptr(), shape[1], shape[0],
         *_paged(where, new_start, seq_len, page_table, pages, cos_sin, dev), window, scale,

@@ -144,7 +144,7 @@ int check_paged_batch(int64_t n_new, const int32_t *new_start, const int32_t *se
     b->n_pages = static_cast<int32_t>(n_pages);
     b->page_shift = 0;
     while ((1 << b->page_shift) < page_size) ++b->page_shift;
-    int64_t len = int64_t{max_pages} * page_size;
+    int64_t len = std::min(int64_t{max_pages} * page_size, int64_t{DSA_MAX_PAGED_TOKENS});
     if (cos_sin) len = std::min(len, n_pos);
     b->len_limit = static_cast<int32_t>(len);
     return DSA_OK;

@@ -445,8 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // A row of the cache that holds an infinity or NaN makes its logit non-finite
                     // in every row of q. Where a row of q must not see the key, those elements
                     // become zero in the tile (0 * inf in PV would reach every row); rows that
-                    // do see the key have a NaN probability already. A key at a time: lane =
-                    // 16-byte piece of four of its chunks.
+                    // do see the key have a NaN probability already, or with a logit of -inf
+                    // give it no weight. A key at a time: lane = 16-byte piece of four of its
+                    // chunks.
                     const int a = max(0, min(32, ra - hb)), e = max(0, min(32, rb - hb));
                     const uint32_t below_e = e == 32 ? 0xFFFFFFFFu : (1u << e) - 1u;
                     const uint32_t below_a = a == 32 ? 0xFFFFFFFFu : (1u << a) - 1u;
@@ -672,9 +673,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // out[row] = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M), M = max_p m_p, over the parts of a
 // unit, always added in the same order. A warp takes one row (or 32 rows x 32 dims of the chunk
 // kernel's units): up to kFew parts, what a run's ends leave of most batches, with all their
-// loads in flight at once. A row of more parts is taken in pieces of 32 dims, one per warp: four groups of eight lanes share the
-// parts, eight loads in flight each, so that one unit of 147 parts (a single token at 128K)
-// takes a few microseconds too.
+// loads in flight at once. A row of more parts is taken in pieces of 32 dims, one per warp: four
+// groups of eight lanes share the parts, eight loads in flight each, so that one unit of 147
+// parts (a single token at 128K) takes a few microseconds too.
 constexpr int kJoinWarps = 8;
 constexpr int kFew = 32;       // of 512 dims
 constexpr int kFewHalf = 16;   // of 256 dims
@@ -769,8 +770,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
             for (int j = 0; j < kLoads; ++j)
-                store_joined(p, u, r, (kDims < kD ? u.part * kDims : 0) + 128 * j + 4 * lane, acc[j],
-                             inv);
+                store_joined(p, u, r, 128 * j + 4 * lane, acc[j], inv);
         }
     } else {
         // 32 rows x 32 dims, lane = row: the slots' layout gives whole lines

@@ -580,9 +580,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // A row of the cache that holds an infinity or NaN makes its logit non-finite
                     // in every row of q. Where a row of q must not see the key, those elements
                     // become zero in the own slabs (0 * inf in PV would reach every row); rows
-                    // that do see the key have a NaN probability already. The sub-partitions'
-                    // warps, which all see such a key, take a quarter of the keys each, one at a
-                    // time: lane = 16-byte piece of its four slabs.
+                    // that do see the key have a NaN probability already, or with a logit of -inf
+                    // give it no weight. The sub-partitions' warps, which all see such a key, take
+                    // a quarter of the keys each, one at a time: lane = 16-byte piece of its four
+                    // slabs.
                     if (__any_sync(0xFFFFFFFFu,
                                    live && !(zero_if_finite32(s0) + zero_if_finite32(s1) == 0.0f))) {
                         const uint32_t mine4 = 0x11111111u << sp;

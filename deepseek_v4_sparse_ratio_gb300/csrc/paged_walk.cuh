@@ -9,9 +9,10 @@
 // takes whole units where they fit and parts of a unit at its ends, so a single long sequence
 // and a batch of thousands of short ones both fill the machine, and causal triangles and ragged
 // lengths balance by themselves. (Without the places the CTAs with a prompt's first tokens, many
-// units of one block, took 1,340 us where the others were done in 560: 3,021 tokens, 64 heads.) A part leaves its unnormalised sum, running maximum and sum of weights in the
-// workspace, and a second kernel joins the parts. Every CTA finds its run from the lengths on
-// the device: the blocks of a sequence's first units are sums of floors, known in closed form.
+// units of one block, took 1,340 us where the others were done in 560: 3,021 tokens, 64 heads.)
+// A part leaves its unnormalised sum, running maximum and sum of weights in the workspace, and a
+// second kernel joins the parts. Every CTA finds its run from the lengths on the device: the
+// blocks of a sequence's first units are sums of floors, known in closed form.
 #pragma once
 
 #include "common.cuh"
@@ -35,7 +36,8 @@ constexpr float kNoMax = -1.0e30f;    // running maximum of a row that has seen 
 
 // Workspace: descriptors, (maximum, sum) of every part's rows, the parts' O. A CTA has two
 // slots, as only the first and the last segment of a run can be parts. A slot holds 64 rows of
-// 512 dims or 128 rows of 256: eight dims (a 32-byte sector) of a row, then the next row's.
+// 512 dims, row by row, or 128 rows of 256: eight dims (a 32-byte sector) of a row, then the next
+// row's, as a thread that holds a row writes them.
 constexpr int kMaxRows = 128;
 constexpr size_t kSlotFloats = 64 * kD;
 constexpr size_t kWsDesc = 0;

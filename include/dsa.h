@@ -71,6 +71,7 @@ extern "C" {
 #define DSA_ROPE_DIM 64         /* rotated elements at the end of a paged KV row */
 #define DSA_MAX_PAGE_SIZE 1024  /* rows of a page: a power of two from 16 to this */
 #define DSA_MAX_PAGED_HEADS 128
+#define DSA_MAX_PAGED_TOKENS (1 << 24) /* of a sequence in pages */
 
 enum dsa_status {
     DSA_OK = 0,
@@ -358,10 +359,10 @@ int dsa_index_score_topk_noalloc(const void *q_idx, const float *w, const void *
  *
  * These arrays (all but the sizes) are read on the device when the kernels run, so a captured
  * graph replays with the lengths they hold then. A sequence whose numbers cannot be
- * (new_start decreasing, negative or beyond n_new; seq_len < n_s, > max_pages*page_size or
- * > n_pos) is skipped whole: its rows are not written, and DSA_ERR_BOUNDS goes to dev_status.
- * (Where starts that decrease give one row to two sequences of possible numbers, either may
- * have it.)
+ * (new_start decreasing, negative or beyond n_new; seq_len < n_s, > max_pages*page_size,
+ * > n_pos or > DSA_MAX_PAGED_TOKENS, up to which a kernel's bounded waits last) is skipped
+ * whole: its rows are not written, and DSA_ERR_BOUNDS goes to dev_status. (Where starts that
+ * decrease give one row to two sequences of possible numbers, either may have it.)
  * A needed page_table entry outside [0, n_pages) is reported the same way and its rows are
  * left out (not written by the append, not seen by the attention).
  */
@@ -401,7 +402,9 @@ int dsa_paged_append(const void *kv, int64_t n_new, const int32_t *new_start,
  *   run at the same time need one each.
  * A token that sees no row (every page of its keys left out) gets zeros. Rows of a page that
  * a token does not see (past seq_len, later tokens, before the window) do not touch its
- * output, whatever they hold, infinities and NaN among it.
+ * output, whatever they hold, infinities and NaN among it. A row that it does see has to be
+ * finite: a NaN in it, or an infinity whose logit is +inf, makes the output NaN; with a logit of
+ * -inf the elements at the infinity's place are unspecified.
  * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE, DSA_ERR_SCRATCH, DSA_ERR_CUDA.
  */
 int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new, const int32_t *new_start,

@@ -346,6 +346,59 @@ def test_pages_far_apart_pass_32_bit_offsets(dsa, workspace):
     check_attn(out.cpu(), batch, q, 0)
 
 
+def _over_and_over(len_, n_new):
+    """A sequence whose table names the same four pages of 1,024 rows over and over."""
+    g = torch.Generator().manual_seed(31)
+    pages = torch.randn(4, 1024, 512, generator=g).bfloat16()
+    table = (torch.arange(-(-len_ // 1024)) % 4).int()[None]
+    return dict(pages=pages, page_table=table, cos_sin=None,
+                new_start=torch.tensor([0, n_new], dtype=torch.int32),
+                seq_len=torch.tensor([len_], dtype=torch.int32))
+
+
+@pytest.mark.parametrize("n_new,heads", [(1, 64), (3, 128)])
+def test_the_longest_sequence(dsa, workspace, n_new, heads):
+    """The largest length there is, each key at many positions. Beside the bounds of the module
+    for few keys, every fp32 sum is a chain over a CTA's share of the keys (a 152nd, of all units;
+    then 152 parts): 2^-24 a step."""
+    length = B.MAX_PAGED_TOKENS - 5
+    batch = _over_and_over(length, n_new)
+    q = torch.randn(n_new, heads, 512, generator=torch.Generator().manual_seed(32)).bfloat16()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = run_attn(batch, q, 0, workspace, status=status)
+    assert status.item() == 0
+    kv = batch["pages"].double().view(4096, 512)
+    share = 2 * n_new * length / 152 + 152
+    for i in range(n_new):
+        seen = length - n_new + i + 1
+        times = torch.full((4096,), float(seen // 4096), dtype=torch.float64)
+        times[:seen % 4096] += 1
+        qr = q[i].double()
+        logits = SCALE * qr @ kv.T
+        w = torch.softmax(logits + times.log(), -1)
+        ref, big = w @ kv, w @ kv.abs()
+        size = SCALE * (qr.abs() @ kv.abs().T).amax(-1)
+        e = 512 * 2.0 ** -23 * size + 2.0 ** -22 * 1.45 * (logits.abs().amax(-1) + 16)
+        spread = torch.expm1(2 * e) + 2.02 * R.U + 2.0 ** -20 + 2 * share * 2.0 ** -24
+        err = (out[i].double() - ref).abs()
+        assert bool((err <= R.U * ref.abs() + big * spread[:, None]).all())
+
+
+def test_a_sequence_over_the_largest_length_is_skipped(dsa, workspace):
+    batch = _over_and_over(B.MAX_PAGED_TOKENS + 1, 1)
+    q = torch.randn(1, 64, 512, generator=torch.Generator().manual_seed(33)).bfloat16()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = run_attn(batch, q, 0, workspace, status=status)
+    assert status.item() == B.DSA_ERR_BOUNDS
+    assert bool((out == 7.0).all())
+    gb = to_gpu(batch)
+    status.zero_()
+    B.dsa_paged_append(q[:, 0].contiguous().cuda(), *args(gb), None, status)
+    torch.cuda.synchronize()
+    assert status.item() == B.DSA_ERR_BOUNDS
+    assert torch.equal(gb["pages"].cpu(), batch["pages"])
+
+
 def test_writes_stay_inside_the_buffers(dsa):
     """Canaries around the output, the workspace and the pages."""
     guard = 4096

@@ -75,6 +75,8 @@ def test_limits_match_the_header():
     assert get("DSA_ROPE_DIM") == B.ROPE_DIM
     assert get("DSA_MAX_PAGE_SIZE") == B.MAX_PAGE_SIZE
     assert get("DSA_MAX_PAGED_HEADS") == B.MAX_PAGED_HEADS
+    m = re.search(r"#define\s+DSA_MAX_PAGED_TOKENS\s+\((\d+) << (\d+)\)", text)
+    assert B.MAX_PAGED_TOKENS == int(m.group(1)) << int(m.group(2))
     m = re.search(r"#define\s+DSA_PAGED_WORKSPACE_BYTES\s+\(\(size_t\)(\d+)\s*<<\s*(\d+)\)", text)
     assert B.DSA_PAGED_WORKSPACE_BYTES == int(m.group(1)) << int(m.group(2))
 
@@ -118,5 +120,9 @@ def test_binding_refuses_tensors_of_another_kind(lib, monkeypatch):
     for out in (q[:2], q.float(), torch.zeros(3, 512, 8, dtype=torch.bfloat16).transpose(1, 2)):
         with pytest.raises(B.DsaError, match="out"):
             B.dsa_paged_attn(q, *common, 0, 0.1, work, out)
+    for window in (1 << 31, 1 << 40, -1):
+        with pytest.raises(B.DsaError, match="window") as e:
+            B.dsa_paged_attn(q, *common, window, 0.1, work, torch.zeros_like(q))
+        assert e.value.code == B.DSA_ERR_SHAPE
     with pytest.raises(B.DsaError, match="workspace"):
         B.dsa_paged_attn(q, *common, 0, 0.1, torch.zeros(8, 8).t()[::2], torch.zeros_like(q))
