@@ -917,7 +917,9 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
     if (!workspace || !aligned16(workspace) || workspace_bytes < DSA_PAGED_WORKSPACE_BYTES)
         return DSA_ERR_SCRATCH;
     p.out = static_cast<__nv_bfloat16 *>(out);
-    p.ws = static_cast<uint8_t *>(workspace);
+    // whole lines (the caller's buffer begins on 16 bytes at least)
+    p.ws = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(workspace) + (kWsAlign - 1)) &
+                                       ~uintptr_t{kWsAlign - 1});
     p.heads = heads;
     // The chunk kernel from an average of more than 256 rows of q per sequence on. Below, a unit
     // of 64 rows reads the keys at most four times and does not compute the logits twice. Single
@@ -925,7 +927,9 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
     // 256 rows 232 / 240, 512 rows 415 / 407; 4 of 1,024 with 64 rows 23 / 28, 256 rows 28 / 30;
     // 16 of up to 16,384 with 160 on average 91 / 105; 64 prompts of 100 tokens (6,400 rows) 477 /
     // 302; one of 2,048 tokens at 16,384 4,614 / 3,764. (One token of 128 heads 60 / 58.)
-    const bool chunk = n_new * heads > int64_t{n_seqs} * 256;
+    // It stores out 32 bytes at a time, so an out that begins between (a view at an odd multiple of
+    // eight elements) is left to the other kernel, which is right for every batch.
+    const bool chunk = n_new * heads > int64_t{n_seqs} * 256 && (oa & 31u) == 0;
     if (chunk) {
         p.rows = kChunkRows;
         p.tpu = kChunkRows / heads;

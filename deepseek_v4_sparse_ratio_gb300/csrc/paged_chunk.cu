@@ -128,7 +128,7 @@ __device__ __forceinline__ void bar_pair(int sp) {
     asm volatile("bar.sync %0, 64;" ::"r"(1 + sp) : "memory");
 }
 
-// 32 bytes to global memory: a whole sector per lane.
+// 32 bytes to global memory, at a multiple of 32: a whole sector per lane.
 __device__ __forceinline__ void store8(void *to, const uint32_t *v) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]),
                  "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])

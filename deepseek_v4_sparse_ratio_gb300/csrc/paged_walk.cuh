@@ -43,7 +43,10 @@ constexpr size_t kSlotFloats = 64 * kD;
 constexpr size_t kWsDesc = 0;
 constexpr size_t kWsMl = 8192;
 constexpr size_t kWsO = kWsMl + size_t{2 * kMaxCtas} * kMaxRows * 2 * sizeof(float);
-static_assert(kWsO + size_t{2 * kMaxCtas} * kSlotFloats * sizeof(float) <= DSA_PAGED_WORKSPACE_BYTES,
+constexpr size_t kWsAlign = 128;   // the layout begins at the buffer's first multiple of this
+static_assert(kWsMl % kWsAlign == 0 && kWsO % kWsAlign == 0, "parts begin lines");
+static_assert(kWsO + size_t{2 * kMaxCtas} * kSlotFloats * sizeof(float) + kWsAlign <=
+                  DSA_PAGED_WORKSPACE_BYTES,
               "over the workspace");
 
 // Where dim `dim` of row r is in a slot of `rows` rows.

@@ -425,6 +425,35 @@ def test_writes_stay_inside_the_buffers(dsa):
         assert bool((buf[:guard] == 5).all()) and bool((buf[-guard:] == 5).all())
 
 
+@pytest.mark.parametrize("off_q,off_out,off_work", [(8, 8, 16), (0, 8, 0), (0, 0, 16), (8, 0, 48)])
+@pytest.mark.parametrize("lens", [[(1, 900), (1, 40)], [(300, 700), (40, 40)]])
+def test_buffers_on_odd_multiples_of_16_bytes(dsa, lens, off_q, off_out, off_work):
+    """Every tensor 16 bytes into its allocation (queries, output: elements; workspace: bytes),
+    with single tokens and with chunks, whose units are cut into parts."""
+    batch = R.make(lens, 32, seed=34)
+    gb = to_gpu(batch)
+    q = queries(batch, 32, 19)
+    n = q.numel()
+
+    def at(offset, size, dtype, fill):
+        buf = torch.full((offset + size + 64,), fill, dtype=dtype, device="cuda")
+        return buf, buf[offset:offset + size]
+
+    _, qd = at(off_q, n, torch.bfloat16, 0.0)
+    ob, out = at(off_out, n, torch.bfloat16, 7.0)
+    wb, work = at(off_work, B.DSA_PAGED_WORKSPACE_BYTES, torch.uint8, 5)
+    _, pages = at(8, batch["pages"].numel(), torch.bfloat16, 0.0)
+    pages = pages.view(batch["pages"].shape).copy_(batch["pages"])
+    assert out.data_ptr() % 32 == 2 * off_out % 32 and pages.data_ptr() % 32 == 16
+    qd = qd.view(q.shape).copy_(q)
+    B.dsa_paged_attn(qd, gb["new_start"], gb["seq_len"], gb["page_table"], pages, 0, SCALE, work,
+                     out.view(q.shape), gb["cos_sin"])
+    torch.cuda.synchronize()
+    check_attn(out.view(q.shape).cpu(), batch, q, 0)
+    assert bool((ob[:off_out] == 7.0).all()) and bool((ob[off_out + n:] == 7.0).all())
+    assert bool((wb[:off_work] == 5).all()) and bool((wb[-64:] == 5).all())
+
+
 @pytest.mark.parametrize("heads", [8, 64])
 def test_sequences_that_share_pages(dsa, workspace, heads):
     """A common prefix of whole pages in three sequences, one of them twice in the batch."""
