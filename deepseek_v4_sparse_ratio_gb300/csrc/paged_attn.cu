@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             if (r < u.nrows) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    store_joined(p, u, r, u.part * kDims + dim0 + 4 * j, acc[j], inv);
+                    store_joined(p, u, r, half_of(u.part) * kDims + dim0 + 4 * j, acc[j], inv);
             }
         }
     }
@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             acc.w += __shfl_xor_sync(0xFFFFFFFFu, acc.w, w);
         }
         if (grp == 0)
-            store_joined(p, u, r, (kDims < kD ? u.part * kDims : 0) + dim, acc,
+            store_joined(p, u, r, (kDims < kD ? half_of(u.part) * kDims : 0) + dim, acc,
                          sum == 0.0f ? 0.0f : 1.0f / sum);
     }
 }
@@ -926,10 +926,10 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
     // and chunk kernel (us): 32 sequences of 8,192 with 64 rows 74 / 126, 128 rows 130 / 132,
     // 256 rows 232 / 240, 512 rows 415 / 407; 4 of 1,024 with 64 rows 23 / 28, 256 rows 28 / 30;
     // 16 of up to 16,384 with 160 on average 91 / 105; 64 prompts of 100 tokens (6,400 rows) 477 /
-    // 302; one of 2,048 tokens at 16,384 4,614 / 3,764. (One token of 128 heads 60 / 58.)
-    // It stores out 32 bytes at a time, so an out that begins between (a view at an odd multiple of
-    // eight elements) is left to the other kernel, which is right for every batch.
-    const bool chunk = n_new * heads > int64_t{n_seqs} * 256 && (oa & 31u) == 0;
+    // 276; one of 2,048 tokens at 16,384 4,614 / 3,764. (One token of 128 heads 60 / 58.)
+    // It loads q and stores out 32 bytes at a time, so arrays that begin between (views at an odd
+    // multiple of eight elements) are left to the other kernel, which is right for every batch.
+    const bool chunk = n_new * heads > int64_t{n_seqs} * 256 && ((qa | oa) & 31u) == 0;
     if (chunk) {
         p.rows = kChunkRows;
         p.tpu = kChunkRows / heads;

@@ -25,7 +25,8 @@
 // at full rate; the rest is issue around the waits (the softmax, 1,250 cycles, runs beside them).
 // 2,048 tokens of 64 heads at 16,384: 3.75 ms, 1,100 TFLOP/s of the result's own flops (0.57 of the
 // measured peak, 0.86 with the logits counted twice). Short units pay for their change: 64
-// prompts of 100 tokens 302 us, 4,096 tokens with a 128-row window 280 us.
+// prompts of 100 tokens 276 us, 4,096 tokens with a 128-row window 260 us (303 and 281 while new
+// queries' products began with the dims that go through TMEM and those were read 16 bytes a load).
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -133,6 +134,17 @@ __device__ __forceinline__ void store8(void *to, const uint32_t *v) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]),
                  "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
+}
+
+// 32 bytes from global memory, at a multiple of 32; zeros without `in`.
+__device__ __forceinline__ void load8(uint32_t *v, const void *from, bool in) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0;
+    if (in)
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                       "=r"(v[6]), "=r"(v[7])
+                     : "l"(from));
 }
 
 // Whether segment i of a run needs other queries than the one before it: the second unit of a
@@ -284,11 +296,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool mine = r < x.nrows && live;
                 const int slot = 2 * cta + (i > 0);
                 const float4 *cs =
-                    p.b.cos_sin && x.part == 1 && r < x.nrows
+                    p.b.cos_sin && half_of(x.part) == 1 && r < x.nrows
                         ? reinterpret_cast<const float4 *>(
                               p.b.cos_sin + int64_t{row_pos(p, x.posf, r)} * kRope)
                         : nullptr;
-                __nv_bfloat16 *orow = p.out + (x.row + r) * kD + x.part * kHalf;
+                __nv_bfloat16 *orow = p.out + (x.row + r) * kD + half_of(x.part) * kHalf;
                 // a part's slot: eight dims of a row are 32 bytes, then the next row's, so that a
                 // warp writes whole lines
                 float *prow = reinterpret_cast<float *>(p.ws + kWsO) + slot * kSlotFloats + r * 8;
@@ -344,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t *const dst0 = sKV + second * kSlab + page * prows * 128;
             const uint64_t pol = policy_evict_normal();  // (each half of the dims reads the keys)
             PageWalk walk(p, sStart);
-            int row, row_next = 0, own, own_next = walk.x.part, g = 0, at = 0;
+            int row, row_next = 0, own, own_next = half_of(walk.x.part), g = 0, at = 0;
             bool have = walk.have;
             int32_t e, e_next = walk.next(p, page, prows, np, row_next);
             bool ok = true;
@@ -352,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 e = e_next;
                 row = row_next;
                 own = own_next;
-                own_next = walk.x.part;
+                own_next = half_of(walk.x.part);
                 more = walk.have;
                 e_next = walk.next(p, page, prows, np, row_next);
                 const int par = g & 1;
@@ -433,7 +445,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (qk) {
                     if (wait_q) {
                         if (!(ok = mbar_wait(q_full, loads & 1, abort_flag, p.status))) break;
-                        if (!(ok = mbar_wait(q_tm, loads & 1, abort_flag, p.status))) break;
                         ++loads;
                         wait_q = false;
                     }
@@ -447,12 +458,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int h = 0; h < 2; ++h) {
                             if (!(ok = mbar_wait(&full[2 * par + h], half, abort_flag, p.status)))
                                 break;
+                            // (looked at in every block: a flag that says whether this is the
+                            // queries' first one costs registers, 271 us where this takes 261)
+                            if (h == 1 && (half ^ x.part)) {
+                                if (!(ok = mbar_wait(q_tm, (loads - 1) & 1, abort_flag, p.status)))
+                                    break;
+                            }
                             tc_fence_after();
                             if (elect_one()) {
                                 if (half ^ x.part)
-                                    issue_qk(smem, tmem, 2 * h, 4 * par + 2 * h, half | h);
-                                else
                                     issue_qk(smem, tmem, 4 + 2 * h, 4 * par + 2 * h, half | h);
+                                else
+                                    issue_qk(smem, tmem, 2 * h, 4 * par + 2 * h, half | h);
                                 if (half == 0) mma_commit(&f_free[2 * par + h]);
                             }
                             __syncwarp();
@@ -521,17 +538,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // q's last two chunks to TMEM, 64 dims by each of a row's two threads, dims
                 // 448..511 turned on the way. (The last unit's QK, which read what was there, is
                 // done: its last S was read above.)
-                const uint4 *src = reinterpret_cast<const uint4 *>(q + (x.row + r) * kD + 384) +
-                                   8 * hh;
+                const __nv_bfloat16 *src = q + (x.row + r) * kD + 384 + 64 * hh;
                 uint32_t v[32];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint4 w = mine ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-                    v[4 * k] = w.x;
-                    v[4 * k + 1] = w.y;
-                    v[4 * k + 2] = w.z;
-                    v[4 * k + 3] = w.w;
-                }
+                for (int k = 0; k < 4; ++k) load8(v + 8 * k, src + 16 * k, mine);
                 if (hh == 1 && p.b.cos_sin && mine) {
                     const float4 *cs =
                         reinterpret_cast<const float4 *>(p.b.cos_sin + int64_t{pos} * kRope);

@@ -182,6 +182,12 @@ __device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
     return a / b;
 }
 
+// Half of the dims (0: dims 0..255) that is the output of a token group's unit `part`, where a
+// group has a unit per half. The upper one comes first: its products with new queries begin with
+// the dims below 256, which lie in shared memory, and end with those that go through TMEM, which
+// arrive last.
+__device__ __forceinline__ int half_of(int part) { return part ^ 1; }
+
 // A run of blocks of one unit.
 struct Segment {
     int64_t row;       // first row of q / out
