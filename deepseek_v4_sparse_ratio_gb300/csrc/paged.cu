@@ -6,7 +6,7 @@
 // page_table[s][p / page_size]. Pairs (x, y) = elements (448 + 2i, 449 + 2i) become
 // (x c - y s, x s + y c) with (c, s) = cos_sin[p][i], in fp32 and rounded to bf16 once; the
 // other 448 elements are copied. Bound by HBM (a row in, a row out, 256 bytes of angles): 56,436
-// rows of 16 sequences in 17.4 us, 0.95 of the measured copy rate; up to a few thousand rows
+// rows of 16 sequences in 20.1 us, 0.95 of the measured copy rate; up to a few thousand rows
 // by the launch (4 us). One warp per row: the row's loads are in flight while its sequence is
 // looked up.
 #include <math.h>

@@ -23,10 +23,11 @@
 //
 // Bound: the tensor pipe, 69 % active. A block takes about 4,450 cycles, 3,090 of them products
 // at full rate; the rest is issue around the waits (the softmax, 1,250 cycles, runs beside them).
-// 2,048 tokens of 64 heads at 16,384: 3.75 ms, 1,100 TFLOP/s of the result's own flops (0.57 of the
-// measured peak, 0.86 with the logits counted twice). Short units pay for their change: 64
-// prompts of 100 tokens 276 us, 4,096 tokens with a 128-row window 260 us (303 and 281 while new
-// queries' products began with the dims that go through TMEM and those were read 16 bytes a load).
+// 2,048 tokens of 64 heads at 16,384: 3.74 to 3.88 ms by the clocks, 1,060 to 1,100 TFLOP/s of the
+// result's own flops (0.55 to 0.57 of the measured peak, 0.83 to 0.86 with the logits counted
+// twice). Short units pay for their change: 64 prompts of 100 tokens 276 us, 4,096 tokens with a
+// 128-row window 260 us (303 and 281 while new queries' products began with the dims that go
+// through TMEM and those were read 16 bytes a load).
 #include <cudaTypedefs.h>
 #include <math.h>
 
