@@ -83,22 +83,24 @@ struct Params {
 
 // ------------------------------------------------------------------ the list of units
 
+// a / b for a >= 0, b > 0: the 32-bit division where both fit, as they nearly always do.
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
+    if (((a | b) >> 31) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // sum_{i < n} floor((a + d i) / 128) for a, d >= 0 (the Euclid-like reduction of such sums).
 static __device__ __noinline__ int64_t floor_sum(int64_t n, int64_t a, int64_t d) {
     int64_t m = kBlock, ans = 0;
     while (n > 0) {
-        if (d >= m) {
-            ans += (n - 1) * n / 2 * (d / m);
-            d %= m;
-        }
-        if (a >= m) {
-            ans += n * (a / m);
-            a %= m;
-        }
+        const int64_t dq = div_pos(d, m), aq = div_pos(a, m);
+        ans += (n - 1) * n / 2 * dq + n * aq;
+        d -= dq * m;
+        a -= aq * m;
         const int64_t y = d * n + a;
         if (y < m) break;
-        n = y / m;
-        a = y % m;
+        n = div_pos(y, m);
+        a = y - n * m;
         const int64_t t = m;
         m = d;
         d = t;
@@ -122,14 +124,14 @@ __device__ __forceinline__ int group_blocks(const Params &p, const PagedSeq &q, 
 
 // Places of the first G token groups of a sequence, for each part (G = all of them: the last one
 // may be short).
-static __device__ __noinline__ int64_t places_before_many(const Params &p, PagedSeq q, int64_t G) {
-    const int64_t base = q.len - q.n, d = p.tpu;
-    int64_t sum = floor_sum(G, base + d - 1, d) + G * (1 + kUnitCost);
-    if (G * d > q.n) sum += ((int64_t{q.len} - 1) >> 7) - ((base + G * d - 1) >> 7);
+static __device__ __noinline__ int64_t places_before_many(const Params &p, PagedSeq q, int G) {
+    const int base = q.len - q.n, d = p.tpu;
+    int64_t sum = floor_sum(G, base + d - 1, d) + int64_t{G} * (1 + kUnitCost);
+    if (G * d > q.n) sum += ((q.len - 1) >> 7) - ((base + G * d - 1) >> 7);
     if (p.window > 0) {
-        const int64_t a = base - p.window + 1;
-        const int64_t g0 = a >= 0 ? 0 : (-a + d - 1) / d;
-        sum -= floor_sum(G - g0, a + g0 * d, d);
+        const int a = base - p.window + 1;  // (a window is shorter than the longest sequence)
+        const int g0 = a >= 0 ? 0 : (-a + d - 1) / d;
+        if (G > g0) sum -= floor_sum(G - g0, a + g0 * d, d);
     }
     return sum;
 }
@@ -154,17 +156,22 @@ struct Place {
     int s, g, part, off;  // sequence, token group, unit of the group, place of the unit
 };
 
-// The token group of a sequence that holds its place r (of all parts' places).
+// The token group of a sequence that holds its place r (of all parts' places), by a warp: a round
+// looks at 32 groups (a thread that halved 2,048 groups took 35 us of a launch's start).
 static __device__ __noinline__ int find_group(const Params &p, PagedSeq q, int64_t r) {
+    const int lane = threadIdx.x & 31;
     int lo = 0, hi = groups_of(p, q);  // upt * places_before(lo) <= r < upt * places_before(hi)
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.upt * places_before(p, q, mid) <= r) lo = mid;
-        else hi = mid;
+        const int step = (hi - lo + 31) >> 5, g = lo + lane * step;
+        const bool le = g < hi && p.upt * places_before(p, q, g) <= r;
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, le) | 1u;
+        lo += (31 - __clz(m)) * step;
+        hi = min(hi, lo + step);
     }
     return lo;
 }
 
+// (all lanes of a warp, with the same arguments)
 __device__ __forceinline__ Place find_place(const Params &p, const PagedSeq &q, int s, int64_t r) {
     const int g = q.n > p.tpu ? find_group(p, q, r) : 0;
     int in = static_cast<int>(r - (g > 0 ? p.upt * places_before(p, q, g) : 0)), part = 0;
@@ -174,12 +181,6 @@ __device__ __forceinline__ Place find_place(const Params &p, const PagedSeq &q, 
         part = 1;
     }
     return Place{s, g, part, in};
-}
-
-// a / b for a >= 0, b > 0: the 32-bit division where both fit, as they nearly always do.
-__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
-    if (((a | b) >> 31) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
 }
 
 // Half of the dims (0: dims 0..255) that is the output of a token group's unit `part`, where a
@@ -297,8 +298,8 @@ __device__ __forceinline__ int row_pos(const Params &p, int posf, int r) {
 
 // Finds this CTA's run, places [T0, T1) of all places: start[0..3] its first place, start[4] its
 // length (0 on entry); describes the unit that begins in it and ends beyond for the join. All
-// threads call it; `scratch` holds one value per warp. Ends with a barrier of the CTA, and one
-// inside it publishes what was set up before (TMEM, mbarriers).
+// threads call it; `scratch` holds a value per warp and four more. Ends with a barrier of the CTA,
+// and one inside it publishes what was set up before (TMEM, mbarriers).
 __device__ __forceinline__ void find_run(const Params &p, int64_t *scratch, int *start) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = static_cast<int>(blockIdx.x);
@@ -336,10 +337,10 @@ __device__ __forceinline__ void find_run(const Params &p, int64_t *scratch, int 
     if (warp > 0) incl += below;
     const int64_t run = div_pos(total + gridDim.x - 1, gridDim.x);
     const int64_t T0 = run * cta, T1 = min(T0 + run, total);
-    if (T0 >= T1) {
-        if (tid == 0) *desc = JoinDesc{};
-    } else if (mine > 0 && T0 < incl && T1 > incl - mine) {
-        // one of this thread's sequences holds the run's first place, its last, or both
+    int64_t *const ends = scratch + kThreads / 32;  // sequence and place in it: the run's first
+                                                    // place, its last
+    if (mine > 0 && T0 < T1 && T0 < incl && T1 > incl - mine) {
+        // one of this thread's sequences holds the first, the last, or both
         int64_t acc = incl - mine;
         for (int s = s0; s < s1; ++s) {
             if (s1 - s0 > 1) {
@@ -348,32 +349,47 @@ __device__ __forceinline__ void find_run(const Params &p, int64_t *scratch, int 
                 nb = p.upt * places_before(p, q, groups_of(p, q));
             }
             if (T0 >= acc && T0 < acc + nb) {
-                const Place x = find_place(p, q, s, T0 - acc);
-                start[0] = x.s;
-                start[1] = x.g;
-                start[2] = x.part;
-                start[3] = x.off;
-                start[4] = static_cast<int>(T1 - T0);
+                ends[0] = s;
+                ends[1] = T0 - acc;
             }
             if (T1 > acc && T1 <= acc + nb) {
-                // the unit of the last place: does its first block lie in this run, and its last
-                // one in a later run?
-                const Place x = find_place(p, q, s, T1 - 1 - acc);
-                const int64_t u0 = T1 - 1 - x.off;
-                const int64_t u1 = u0 + kUnitCost + group_blocks(p, q, x.g);
-                JoinDesc d = {};
-                if (x.off >= kUnitCost && u0 + kUnitCost >= T0 && u1 > T1) {
-                    const int t0 = x.g * p.tpu, t1 = min(t0 + p.tpu, q.n);
-                    d.row = unit_row(p, q, t0, x.part);
-                    d.nrows = unit_rows(p, t1 - t0, x.part);
-                    d.part = x.part;
-                    d.parts = static_cast<int>(div_pos(u1 - 1, run)) - cta + 1;
-                    d.slot0 = u0 <= T0 ? 0 : 1;
-                    d.pos = q.len - q.n + t0;
-                }
-                *desc = d;
+                ends[2] = s;
+                ends[3] = T1 - 1 - acc;
             }
             acc += nb;
+        }
+    }
+    __syncthreads();
+    if (T0 >= T1) {
+        if (tid == 0) *desc = JoinDesc{};
+    } else if (warp < 2) {
+        const int s = static_cast<int>(ends[2 * warp]);
+        bool bad;
+        q = paged_seq(p.b, s, bad);
+        const Place x = find_place(p, q, s, ends[2 * warp + 1]);
+        if (warp == 0 && lane == 0) {
+            start[0] = x.s;
+            start[1] = x.g;
+            start[2] = x.part;
+            start[3] = x.off;
+            start[4] = static_cast<int>(T1 - T0);
+        }
+        if (warp == 1 && lane == 0) {
+            // the unit of the last place: does its first block lie in this run, and its last one
+            // in a later run?
+            const int64_t u0 = T1 - 1 - x.off;
+            const int64_t u1 = u0 + kUnitCost + group_blocks(p, q, x.g);
+            JoinDesc d = {};
+            if (x.off >= kUnitCost && u0 + kUnitCost >= T0 && u1 > T1) {
+                const int t0 = x.g * p.tpu, t1 = min(t0 + p.tpu, q.n);
+                d.row = unit_row(p, q, t0, x.part);
+                d.nrows = unit_rows(p, t1 - t0, x.part);
+                d.part = x.part;
+                d.parts = static_cast<int>(div_pos(u1 - 1, run)) - cta + 1;
+                d.slot0 = u0 <= T0 ? 0 : 1;
+                d.pos = q.len - q.n + t0;
+            }
+            *desc = d;
         }
     }
     fence_proxy_async_smem();  // the scratch's tile is next written by TMA
