@@ -89,23 +89,29 @@ __device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
     return a / b;
 }
 
-// sum_{i < n} floor((a + d i) / 128) for a, d >= 0 (the Euclid-like reduction of such sums).
+// sum_{i < n} floor((a + d i) / 128) for a, d >= 0 (the Euclid-like reduction of such sums; its
+// first step, and the only one of many where d is a power of two, divides by 128).
 static __device__ __noinline__ int64_t floor_sum(int64_t n, int64_t a, int64_t d) {
-    int64_t m = kBlock, ans = 0;
-    while (n > 0) {
+    if (n <= 0) return 0;
+    int64_t ans = (n - 1) * n / 2 * (d >> 7) + n * (a >> 7);
+    int64_t m = d & 127, y = m * n + (a & 127);
+    if (y < kBlock) return ans;
+    n = y >> 7;
+    a = y & 127;
+    d = kBlock;
+    for (;;) {
         const int64_t dq = div_pos(d, m), aq = div_pos(a, m);
         ans += (n - 1) * n / 2 * dq + n * aq;
         d -= dq * m;
         a -= aq * m;
-        const int64_t y = d * n + a;
-        if (y < m) break;
+        y = d * n + a;
+        if (y < m) return ans;
         n = div_pos(y, m);
         a = y - n * m;
         const int64_t t = m;
         m = d;
         d = t;
     }
-    return ans;
 }
 
 // Keys of the tokens [t0, t1) of a sequence: positions lo .. hi, blocks lo / 128 .. hi / 128.
@@ -131,7 +137,7 @@ static __device__ __noinline__ int64_t places_before_many(const Params &p, Paged
     if (p.window > 0) {
         const int a = base - p.window + 1;  // (a window is shorter than the longest sequence)
         const int g0 = a >= 0 ? 0 : (-a + d - 1) / d;
-        if (G > g0) sum -= floor_sum(G - g0, a + g0 * d, d);
+        sum -= floor_sum(G - g0, a + g0 * d, d);
     }
     return sum;
 }
@@ -158,23 +164,28 @@ struct Place {
 
 // The token group of a sequence that holds its place r (of all parts' places), by a warp: a round
 // looks at 32 groups (a thread that halved 2,048 groups took 35 us of a launch's start).
-static __device__ __noinline__ int find_group(const Params &p, PagedSeq q, int64_t r) {
+// Returns it and, above its 32 bits, the place in it.
+static __device__ __noinline__ int64_t find_group(const Params &p, PagedSeq q, int64_t r) {
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = groups_of(p, q);  // upt * places_before(lo) <= r < upt * places_before(hi)
+    int64_t before = 0;
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) >> 5, g = lo + lane * step;
-        const bool le = g < hi && p.upt * places_before(p, q, g) <= r;
-        const uint32_t m = __ballot_sync(0xFFFFFFFFu, le) | 1u;
-        lo += (31 - __clz(m)) * step;
+        const int64_t mine = g < hi ? p.upt * places_before(p, q, g) : 0;
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, g < hi && mine <= r) | 1u;
+        const int k = 31 - __clz(m);
+        before = __shfl_sync(0xFFFFFFFFu, mine, k);
+        lo += k * step;
         hi = min(hi, lo + step);
     }
-    return lo;
+    return (r - before) << 32 | lo;
 }
 
 // (all lanes of a warp, with the same arguments)
 __device__ __forceinline__ Place find_place(const Params &p, const PagedSeq &q, int s, int64_t r) {
-    const int g = q.n > p.tpu ? find_group(p, q, r) : 0;
-    int in = static_cast<int>(r - (g > 0 ? p.upt * places_before(p, q, g) : 0)), part = 0;
+    const int64_t at = q.n > p.tpu ? find_group(p, q, r) : r << 32;
+    const int g = static_cast<int>(at);
+    int in = static_cast<int>(at >> 32), part = 0;
     const int n = group_blocks(p, q, g) + kUnitCost;
     if (in >= n) {  // (upt is 1 or 2)
         in -= n;
