@@ -25,9 +25,10 @@ constexpr int kBlock = 128;        // keys in a block
 constexpr int kThreads = 512;      // of both kernels
 constexpr int kMaxCtas = 152;
 
-// Places of a unit before its blocks. (0, 2, 3 and 4 for chunks: 2,033, 1,173, 1,135 and 1,154 us
-// for a prompt of 4,096 tokens, 576, 418, 487 and 467 for 34 prompts of 208; 1, 2 and 4 for
-// single tokens: 91, 87 and 90 us for 64 users up to 8K, 73, 74 and 75 for 32 users of 8K.)
+// Places of a unit before its blocks. (1, 2 and 3 for chunks: 1,127, 1,085 and 1,104 us for a prompt
+// of 4,096 tokens, 346, 341 and 352 for 34 prompts of 208, 149, 134 and 145 for 32 users of 64
+// tokens with a window of 128; for single tokens: 90, 87 and 90 us for 64 users up to 8K. None at
+// all: 2,033 us for the prompt of 4,096.)
 constexpr int kUnitCost = 2;
 
 constexpr float kRescale = 8.0f;      // log2 units the running maximum may lag behind
