@@ -82,24 +82,26 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
 }
 
 // S (+)= Q . K^T over two slabs, dims 64 c .. 64 c + 127, in slots `slot` and the next.
+// (Four products a loop, and one copy for the first pair whichever half it is: unrolled whole the
+// kernel's code outgrows the instruction caches, which units of few blocks feel. A window of 128
+// 238 us, so 209; half the loops, one step for both halves, 218 but 11 % more for a chunk.)
+template <bool kTmem>
 __device__ __forceinline__ void issue_qk(const uint8_t *smem, uint32_t tmem, int c, int slot,
                                          uint32_t acc0) {
     constexpr uint32_t idesc = idesc_bf16(kRows, kBlock, false, false);
     const uint64_t kd = desc_sw128(smem_u32(smem + kOffKV) + slot * kSlab, 16, 1024);
-    if (c < kQSmem) {
-        const uint64_t qd = desc_sw128(smem_u32(smem + kOffQ) + c * kSlab, 16, 1024);
+    const uint64_t qd = desc_sw128(smem_u32(smem + kOffQ) + c * kSlab, 16, 1024);
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t step = ((k / 4 * kSlab) >> 4) + 2 * (k % 4);
-            mma_bf16(tmem + kSCol, qd + step, kd + step, idesc, k > 0 ? 1u : acc0);
+        for (int kk = 0; kk < 4; ++kk) {
+            const int k = 4 * e + kk;
+            const uint32_t step = e * (kSlab >> 4) + 2 * kk, acc = k > 0 ? 1u : acc0;
+            if (kTmem)
+                mma_bf16_ta(tmem + kSCol, tmem + kQCol + 8 * k, kd + step, idesc, acc);
+            else
+                mma_bf16(tmem + kSCol, qd + step, kd + step, idesc, acc);
         }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t step = ((k / 4 * kSlab) >> 4) + 2 * (k % 4);
-            mma_bf16_ta(tmem + kSCol, tmem + kQCol + 8 * k, kd + step, idesc, k > 0 ? 1u : acc0);
-        }
-    }
 }
 
 // O (+)= P . V over the block's keys and 128 of the unit's dims (own slabs 2 half, 2 half + 1).
@@ -108,7 +110,7 @@ __device__ __forceinline__ void issue_pv(const uint8_t *smem, uint32_t tmem, int
     constexpr uint32_t idesc = idesc_bf16(kRows, 128, false, true);
     const uint64_t vd =
         desc_sw128(smem_u32(smem + kOffKV) + (4 * par + 2 * half) * kSlab, kSlab, 1024);
-#pragma unroll
+#pragma unroll 4
     for (int kk = 0; kk < 8; ++kk)
         mma_bf16_ta(tmem + kOCol + 128 * half, tmem + kPCol + 8 * kk, vd + ((kk * 2048) >> 4),
                     idesc, kk > 0 ? 1u : acc0);
@@ -172,10 +174,12 @@ __device__ __forceinline__ void mask32(uint32_t (&s)[32], uint32_t vis) {
 
 // 0 when all 32 logits are finite, else NaN.
 __device__ __forceinline__ float zero_if_finite32(const uint32_t (&s)[32]) {
-    float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    uint64_t t[2] = {0, 0};
 #pragma unroll
-    for (int j = 0; j < 32; ++j) t[j & 3] = fmaf(__uint_as_float(s[j]), 0.0f, t[j & 3]);
-    return (t[0] + t[1]) + (t[2] + t[3]);
+    for (int j = 0; j < 16; ++j)
+        t[j & 1] = fma_pair(pair_of(s[2 * j], s[2 * j + 1]), 0, t[j & 1]);
+    t[0] = add_pair(t[0], t[1]);
+    return first_of(t[0]) + second_of(t[0]);
 }
 
 // Bits of the logits that are not finite.
@@ -201,15 +205,14 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
 
 // exp2(s c - m) of 32 logits as 16 bf16 pairs; adds the rounded values to l.
 __device__ __forceinline__ void exp32(const uint32_t (&s)[32], float c, float m, uint32_t *out,
-                                      float (&l)[4]) {
+                                      uint64_t (&l)[2]) {
+    const uint64_t c2 = pair_of(c), m2 = pair_of(-m);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-        const float a = ex2(fmaf(__uint_as_float(s[2 * j]), c, -m));
-        const float b = ex2(fmaf(__uint_as_float(s[2 * j + 1]), c, -m));
-        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        const uint64_t x = fma_pair(pair_of(s[2 * j], s[2 * j + 1]), c2, m2);
+        const __nv_bfloat162 v = __floats2bfloat162_rn(ex2(first_of(x)), ex2(second_of(x)));
         out[j] = *reinterpret_cast<const uint32_t *>(&v);
-        l[(2 * j) & 3] += bf16lo(out[j]);
-        l[(2 * j + 1) & 3] += bf16hi(out[j]);
+        l[j & 1] = add_pair(l[j & 1], pair_of(out[j] << 16, out[j] & 0xFFFF0000u));
     }
 }
 
@@ -467,10 +470,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             tc_fence_after();
                             if (elect_one()) {
-                                if (half ^ x.part)
-                                    issue_qk(smem, tmem, 4 + 2 * h, 4 * par + 2 * h, half | h);
+                                if (h == 0)
+                                    issue_qk<false>(smem, tmem, 4 * (half ^ x.part), 4 * par, half);
+                                else if (half ^ x.part)
+                                    issue_qk<true>(smem, tmem, 6, 4 * par + 2, 1);
                                 else
-                                    issue_qk(smem, tmem, 2 * h, 4 * par + 2 * h, half | h);
+                                    issue_qk<false>(smem, tmem, 2, 4 * par + 2, 1);
                                 if (half == 0) mma_commit(&f_free[2 * par + h]);
                             }
                             __syncwarp();
@@ -558,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 mbar_arrive(q_tm);
             }
-            float l[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            uint64_t l[2] = {0, 0};  // two sums each
             float m = kNoMax;
             for (int b = 0; b < x.nb; ++b, ++g) {
                 const int par = g & 1;
@@ -634,8 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         fmaxf(m, fmaxf(mx, sMx[(hh ^ 1) * kRows + r]) * p.c);
                     const float alpha = ex2(m - m_new);
                     m = m_new;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) l[k] *= alpha;
+                    l[0] = fma_pair(l[0], pair_of(alpha), 0);
+                    l[1] = fma_pair(l[1], pair_of(alpha), 0);
                     if (b > 0) {
                         mbar_wait(pv_done, par ^ 1, abort_flag, p.status);
                         tc_fence_after();
@@ -664,7 +669,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 mbar_arrive(p_full);
             }
-            const float sum = (l[0] + l[1]) + (l[2] + l[3]);
+            const uint64_t l2 = add_pair(l[0], l[1]);
+            const float sum = first_of(l2) + second_of(l2);
             if (hh == 1) sL1[r] = sum;
             bar_pair(sp);
             if (hh == 0) {
