@@ -362,7 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t acc0 = b > 0;
                     const uint32_t lbo3 = (g & 1) ? kLbo7Spare : 16384u;
                     if (elect_one()) {
-#pragma unroll
+                        // (one tile's code four times over: 152 sequences of 16,384 457 -> 445 us
+                        // against four copies)
+#pragma unroll 1
                         for (int m = 0; m < 4; ++m) {
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk)

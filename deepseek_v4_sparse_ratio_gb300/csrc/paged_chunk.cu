@@ -110,7 +110,7 @@ __device__ __forceinline__ void issue_pv(const uint8_t *smem, uint32_t tmem, int
     constexpr uint32_t idesc = idesc_bf16(kRows, 128, false, true);
     const uint64_t vd =
         desc_sw128(smem_u32(smem + kOffKV) + (4 * par + 2 * half) * kSlab, kSlab, 1024);
-#pragma unroll 4
+#pragma unroll 2
     for (int kk = 0; kk < 8; ++kk)
         mma_bf16_ta(tmem + kOCol + 128 * half, tmem + kPCol + 8 * kk, vd + ((kk * 2048) >> 4),
                     idesc, kk > 0 ? 1u : acc0);
