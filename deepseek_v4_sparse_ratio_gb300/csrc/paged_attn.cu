@@ -28,8 +28,8 @@
 // is all that fits beside q (64 KB) and P, so a block is a chain (PV of the block before frees
 // the slots, 1,900 cycles of load latency, the last QK products, 1,000 cycles of softmax): 6,540
 // cycles per 128 KB and SM, 5.6 TB/s, 83 % of the measured copy rate, in the steady state of 152
-// sequences of 16,384 (454 us). One token at 131,072: 46 us, of which 9 are the launch's start
-// (lengths, q, the first tile, instructions) and 8 the join; 64 users of up to 8,192: 85 us.
+// sequences of 16,384 (445 us). One token at 131,072: 45 us, of which 9 are the launch's start
+// (lengths, q, the first tile, instructions) and 8 the join; 64 users of up to 8,192: 82 us.
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -925,10 +925,10 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
     p.heads = heads;
     // The chunk kernel from an average of more than 256 rows of q per sequence on. Below, a unit
     // of 64 rows reads the keys at most four times and does not compute the logits twice. Single
-    // and chunk kernel (us): 32 sequences of 8,192 with 64 rows 74 / 126, 128 rows 130 / 132,
-    // 256 rows 232 / 240, 512 rows 415 / 407; 4 of 1,024 with 64 rows 23 / 28, 256 rows 28 / 30;
-    // 16 of up to 16,384 with 160 on average 91 / 105; 64 prompts of 100 tokens (6,400 rows) 477 /
-    // 276; one of 2,048 tokens at 16,384 4,614 / 3,764. (One token of 128 heads 60 / 58.)
+    // and chunk kernel (us): 32 sequences of 8,192 with 64 rows 70 / 124, 128 rows 128 / 130,
+    // 256 rows 226 / 237, 512 rows 402 / 402; 4 of 1,024 with 64 rows 21 / 26, 256 rows 26 / 28;
+    // 16 of up to 16,384 with 160 on average 89 / 102; 64 prompts of 100 tokens (6,400 rows) 460 /
+    // 249; one of 2,048 tokens at 16,384 4,343 / 3,688; 32 of one token of 128 heads 59 / 62.
     // It loads q and stores out 32 bytes at a time, so arrays that begin between (views at an odd
     // multiple of eight elements) are left to the other kernel, which is right for every batch.
     const bool chunk = n_new * heads > int64_t{n_seqs} * 256 && ((qa | oa) & 31u) == 0;
