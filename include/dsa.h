@@ -371,7 +371,7 @@ int dsa_index_score_topk_noalloc(const void *q_idx, const float *w, const void *
  * Append the new tokens' rows: row p mod page_size of page page_table[s][p / page_size] :=
  * R(p) kv[r] for every row r of a sequence, p its position (a plain copy when cos_sin is
  * NULL). The rotation is taken in fp32 and rounded to bf16 once.
- *   kv [n_new, 512] bf16. Two rows for one place (a page that two sequences of the batch
+ *   kv [n_new, 512] bf16, apart from the pages. Two rows for one place (a page that two sequences of the batch
  *   write) are the caller's mistake: either may end up there.
  * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE, DSA_ERR_CUDA.
  */

@@ -590,6 +590,26 @@ def test_captured_step_replays_with_other_lengths(dsa):
             check_attn(st["out"].cpu(), b, q, 0)
 
 
+def test_calls_on_two_streams_at_once(dsa, workspace):
+    """Chunks on one stream and single tokens on another, a workspace each, with nothing between
+    them: the bits of the calls made one after the other."""
+    work = torch.empty(B.DSA_PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    jobs = []
+    for lens, seed, w in (([(300, 900), (200, 200)], 35, workspace), ([(1, 5000), (1, 70)], 36, work)):
+        batch = R.make(lens, 64, seed=seed)
+        gb, q = to_gpu(batch), queries(batch, 64, seed).cuda()
+        want = torch.empty_like(q)
+        B.dsa_paged_attn(q, *args(gb), 0, SCALE, w, want, gb["cos_sin"])
+        jobs.append((gb, q, w, want, [torch.zeros_like(q) for _ in range(8)], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for k in range(8):
+        for gb, q, w, want, outs, stream in jobs:
+            B.dsa_paged_attn(q, *args(gb), 0, SCALE, w, outs[k], gb["cos_sin"], stream=stream)
+    torch.cuda.synchronize()
+    for gb, q, w, want, outs, stream in jobs:
+        assert all(torch.equal(want, o) for o in outs)
+
+
 def test_same_call_twice_gives_the_same_bits(dsa, workspace):
     batch = R.make([(1, 3000), (30, 500), (1, 64)], 64, seed=25)
     q = queries(batch, 64, 14)
