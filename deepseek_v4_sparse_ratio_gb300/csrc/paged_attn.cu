@@ -481,13 +481,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                // xv = scale * log2e * logit - running maximum: decides the rescale, feeds exp2
+                // xv = (product - running maximum) * c: decides the rescale, feeds exp2
                 float xv[32];
                 float xmax;
                 {
 #pragma unroll
                     for (int h = 0; h < 32; ++h)
-                        xv[h] = fmaf(__uint_as_float(sa[h]), p.c, -__uint_as_float(mv[h]));
+                        xv[h] = (__uint_as_float(sa[h]) - __uint_as_float(mv[h])) * p.c;
                     float t16[16];
 #pragma unroll
                     for (int h = 0; h < 16; ++h) t16[h] = fmaxf(xv[h], xv[h + 16]);
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // exact block maxima -> new running maximum; sums and O^T rescaled
 #pragma unroll
                     for (int h = 0; h < 32; ++h) {
-                        const float wm = redux_max(__uint_as_float(sa[h]) * p.c);
+                        const float wm = redux_max(__uint_as_float(sa[h]));
                         if (lane == h) sRed[sp * 64 + hb + h] = wm;
                     }
                     bar_group(hh);
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float m_old = sM[cur * 64 + r];
                         const float m_new = fmaxf(m_old, bm);
                         sM[(cur ^ 1) * 64 + r] = m_new;
-                        sAlpha[r] = ex2(m_old - m_new);
+                        sAlpha[r] = ex2((m_old - m_new) * p.c);
                     }
                     bar_group(hh);
                     cur ^= 1;
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int h = 0; h < 32; ++h) {
                         mv[h] = __float_as_uint(m_now[h]);
                         l[h] *= sAlpha[hb + h];
-                        xv[h] = fmaf(__uint_as_float(sa[h]), p.c, -m_now[h]);
+                        xv[h] = (__uint_as_float(sa[h]) - m_now[h]) * p.c;
                     }
                     tmem_st32(lane_base + kMCol + hb, mv);
                     tmem_wait_st();
@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ the join
 
-// out[row] = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M), M = max_p m_p, over the parts of a
+// out[row] = sum_p O_p w_p / sum_p l_p w_p, w_p = 2^((m_p - M) c), M = max_p m_p, over the parts of a
 // unit, always added in the same order. A warp takes one row (or 32 rows x 32 dims of the chunk
 // kernel's units): up to kFew parts, what a run's ends leave of most batches, with all their
 // loads in flight at once. A row of more parts is taken in pieces of 32 dims, one per warp: four
@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             // lane k holds part k's maximum and sum
             const float2 ml = lane < u.parts ? parts_ml[slot_of(lane) * kMaxRows + r]
                                              : make_float2(kNoMax, 0.0f);
-            const float wt = ex2(ml.x - redux_max(ml.x));
+            const float wt = ex2((ml.x - redux_max(ml.x)) * p.c);
             float sum = lane < u.parts ? ml.y * wt : 0.0f;
 #pragma unroll
             for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, w);
@@ -792,7 +792,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             for (int k = 0; k < u.parts; ++k) {
                 const int slot = slot_of(k);
                 const float2 ml = parts_ml[slot * kMaxRows + r];
-                const float w = ex2(ml.x - M);
+                const float w = ex2((ml.x - M) * p.c);
                 sum += ml.y * w;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -830,7 +830,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < kWords; ++j) {
-            const float w = ex2(v[j].x - M);
+            const float w = ex2((v[j].x - M) * p.c);
             weight[warp][32 * j + lane] = w;
             sum += v[j].y * w;
         }

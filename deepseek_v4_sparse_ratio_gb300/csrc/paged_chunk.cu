@@ -204,13 +204,13 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
     return t[0];
 }
 
-// exp2(s c - m) of 32 logits as 16 bf16 pairs; adds the rounded values to l.
+// exp2((s - m) c) of 32 products as 16 bf16 pairs; adds the rounded values to l.
 __device__ __forceinline__ void exp32(const uint32_t (&s)[32], float c, float m, uint32_t *out,
                                       uint64_t (&l)[2]) {
     const uint64_t c2 = pair_of(c), m2 = pair_of(-m);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-        const uint64_t x = fma_pair(pair_of(s[2 * j], s[2 * j + 1]), c2, m2);
+        const uint64_t x = mul_pair(add_pair(pair_of(s[2 * j], s[2 * j + 1]), m2), c2);
         const __nv_bfloat162 v = __floats2bfloat162_rn(ex2(first_of(x)), ex2(second_of(x)));
         out[j] = *reinterpret_cast<const uint32_t *>(&v);
         l[j & 1] = add_pair(l[j & 1], pair_of(out[j] << 16, out[j] & 0xFFFF0000u));
@@ -632,13 +632,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mask32(s1, v1);
                 }
                 const float mx = fmaxf(max32(s0), max32(s1));
-                if (vote_any_pair(fmaf(mx, p.c, -m) > kRescale, sp)) {
+                if (vote_any_pair((mx - m) * p.c > kRescale, sp)) {
                     // the row's block maximum from both halves; sums and O rescaled
                     sMx[hh * kRows + r] = mx;
                     bar_pair(sp);
-                    const float m_new =
-                        fmaxf(m, fmaxf(mx, sMx[(hh ^ 1) * kRows + r]) * p.c);
-                    const float alpha = ex2(m - m_new);
+                    const float m_new = fmaxf(m, fmaxf(mx, sMx[(hh ^ 1) * kRows + r]));
+                    const float alpha = ex2((m - m_new) * p.c);
                     m = m_new;
                     l[0] = fma_pair(l[0], pair_of(alpha), 0);
                     l[1] = fma_pair(l[1], pair_of(alpha), 0);

@@ -31,9 +31,14 @@ constexpr int kMaxCtas = 152;
 // all: 2,033 us for the prompt of 4,096.)
 constexpr int kUnitCost = 2;
 
-constexpr float kRescale = 8.0f;      // log2 units the running maximum may lag behind
-constexpr float kNoMax = -1.0e30f;    // running maximum of a row that has seen no key: finite,
-                                      // so that (masked) -inf minus it stays -inf
+// Softmax. The running maximum m of a row is one of its products s = q . row, unscaled, and a weight
+// is exp2((s - m) c), c = scale log2(e): the largest key's is 1 whatever the size of s c. (With
+// m = fl(s c) and exp2(fma(s, c, -m)) it is off by 2 to half an ulp of m, a factor that cancels in
+// the division by the sum but is zero or infinite from |m| = 2^31 on.)
+constexpr float kRescale = 8.0f;          // log2 units the running maximum may lag behind
+constexpr float kNoMax = -3.4028235e38f;  // the maximum of a row that has seen no key: the lowest
+                                          // finite value, so that (masked) -inf minus it stays
+                                          // -inf and any product replaces it
 
 // Workspace: descriptors, (maximum, sum) of every part's rows, the parts' O. A CTA has two
 // slots, as only the first and the last segment of a run can be parts. A slot holds 64 rows of
@@ -493,6 +498,12 @@ __device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
 __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
     uint64_t v;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
     return v;
 }
 

@@ -404,7 +404,9 @@ int dsa_paged_append(const void *kv, int64_t n_new, const int32_t *new_start,
  * a token does not see (past seq_len, later tokens, before the window) do not touch its
  * output, whatever they hold, infinities and NaN among it. A row that it does see has to be
  * finite: a NaN in it, or an infinity whose logit is +inf, makes the output NaN; with a logit of
- * -inf the elements at the infinity's place are unspecified.
+ * -inf the elements at the infinity's place are unspecified. Logits may have any size: the products
+ * q . row are held in fp32 and weights taken from their differences (a product beyond fp32's
+ * range counts as an infinity in its row).
  * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE, DSA_ERR_SCRATCH, DSA_ERR_CUDA.
  */
 int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new, const int32_t *new_start,
