@@ -910,8 +910,9 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
     int rc = check_paged_batch(n_new, new_start, seq_len, n_seqs, page_table, max_pages, pages,
                                n_pages, page_stride, page_size, cos_sin, n_pos, &p.b);
     if (rc != DSA_OK) return rc;
-    if (heads < 1 || heads > DSA_MAX_PAGED_HEADS || window < 0 || !(scale > 0.0f) ||
-        isinf(scale) || n_new * heads > (int64_t{1} << 31) - 1)
+    const float c = scale * 1.4426950408889634f;
+    if (heads < 1 || heads > DSA_MAX_PAGED_HEADS || window < 0 || !(scale > 0.0f) || isinf(c) ||
+        n_new * heads > (int64_t{1} << 31) - 1)
         return DSA_ERR_SHAPE;
     const uintptr_t qa = reinterpret_cast<uintptr_t>(q), oa = reinterpret_cast<uintptr_t>(out);
     const uintptr_t bytes = static_cast<uintptr_t>(n_new) * heads * kD * 2;
@@ -946,7 +947,7 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
     p.rpt = std::min(heads, p.rows);
     // a window no shorter than any sequence is no window
     p.window = window >= p.b.len_limit ? 0 : window;
-    p.c = scale * 1.4426950408889634f;
+    p.c = c;
     p.status = dev_status;
     int sms = 0;
     rc = setup(&sms);

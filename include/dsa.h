@@ -396,7 +396,8 @@ int dsa_paged_append(const void *kv, int64_t n_new, const int32_t *new_start,
  * rotated queries are rounded to bf16 for the matrix products, the output once to bf16.
  *
  *   q [n_new, heads, 512] bf16; out the same, not overlapping q; heads from 1 to
- *   DSA_MAX_PAGED_HEADS (64 for the whole model, fewer on a shard of it); scale > 0;
+ *   DSA_MAX_PAGED_HEADS (64 for the whole model, fewer on a shard of it); scale > 0 and
+ *   scale * log2(e) within fp32;
  *   workspace: device buffer of workspace_bytes >= DSA_PAGED_WORKSPACE_BYTES; nothing in it
  *   needs to start at zero and nothing is kept in it. Calls (and captured graphs) that may
  *   run at the same time need one each.
