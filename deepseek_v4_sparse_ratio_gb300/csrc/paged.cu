@@ -133,6 +133,8 @@ int check_paged_batch(int64_t n_new, const int32_t *new_start, const int32_t *se
     const int64_t limit = (int64_t{1} << 31) - 1;
     if (n_new > limit || n_pages > limit || int64_t{max_pages} * page_size > limit)
         return DSA_ERR_SHAPE;
+    // the kernels' walks over the sequences step past the last one, in 32 bits
+    if (n_seqs > DSA_MAX_PAGED_SEQS) return DSA_ERR_SHAPE;
     b->new_start = new_start;
     b->seq_len = seq_len;
     b->page_table = page_table;

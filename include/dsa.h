@@ -72,6 +72,7 @@ extern "C" {
 #define DSA_MAX_PAGE_SIZE 1024  /* rows of a page: a power of two from 16 to this */
 #define DSA_MAX_PAGED_HEADS 128
 #define DSA_MAX_PAGED_TOKENS (1 << 24) /* of a sequence in pages */
+#define DSA_MAX_PAGED_SEQS (1 << 30)   /* of a ragged batch */
 
 enum dsa_status {
     DSA_OK = 0,
@@ -346,6 +347,7 @@ int dsa_index_score_topk_noalloc(const void *q_idx, const float *w, const void *
  *     a power of two from 16 to DSA_MAX_PAGE_SIZE. A row is key and value of every head.
  *   page_table [n_seqs, max_pages] int32: entry [s][j] is the page of positions
  *     j*page_size .. of sequence s. Entries that hold no position a call needs are not read.
+ *   n_seqs: from 1 to DSA_MAX_PAGED_SEQS.
  *   seq_len [n_seqs] int32: tokens of each sequence, its new ones included.
  *   new_start [n_seqs+1] int32: rows new_start[s] .. new_start[s+1]-1 of the new tokens'
  *     arrays belong to sequence s; they are its last n_s = new_start[s+1]-new_start[s] tokens,

@@ -31,3 +31,10 @@ APART = 9 << 40
 def test_a_scale_that_leaves_fp32_in_log2_units(lib, scale):
     """scale * log2(e) is the factor of every logit: infinite, it makes 0 * inf of the largest."""
     assert attn(lib, out=APART, scale=scale) == B.DSA_ERR_SHAPE
+
+
+@pytest.mark.parametrize("n_seqs", [(1 << 30) + 1, (1 << 31) - 200, (1 << 31) - 1])
+def test_more_sequences_than_the_kernels_can_count(lib, n_seqs):
+    """Their loops step past n_seqs by up to a block of threads: the sum has to stay in 32 bits."""
+    assert append(lib, n_seqs=n_seqs) == B.DSA_ERR_SHAPE
+    assert attn(lib, n_seqs=n_seqs, out=APART) == B.DSA_ERR_SHAPE
