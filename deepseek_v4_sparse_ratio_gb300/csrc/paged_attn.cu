@@ -870,6 +870,14 @@ struct Setup {
 std::mutex g_mu;
 Setup g_setup[kMaxDevices];
 
+// Places that a CTA's run may have (of a GB300's 152), from the sizes alone (lengths are the
+// device's): the kernels count them in 32 bits.
+int64_t run_bound(const Params &p) {
+    const int64_t groups = std::min(p.b.n_new, p.b.n_new / p.tpu + p.b.n_seqs);
+    const int64_t keys = p.window > 0 ? std::min(p.b.len_limit, p.window + p.tpu) : p.b.len_limit;
+    return groups * p.upt * (keys / kBlock + 2 + kUnitCost) / kMaxCtas + 1;
+}
+
 // Per-device one-time set-up: the raised shared-memory limit and the register split's check.
 int setup(int *sms) {
     const int dev = current_device();
@@ -917,12 +925,6 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
     const uintptr_t qa = reinterpret_cast<uintptr_t>(q), oa = reinterpret_cast<uintptr_t>(out);
     const uintptr_t bytes = static_cast<uintptr_t>(n_new) * heads * kD * 2;
     if (qa < oa + bytes && oa < qa + bytes) return DSA_ERR_ARG;
-    if (!workspace || !aligned16(workspace) || workspace_bytes < DSA_PAGED_WORKSPACE_BYTES)
-        return DSA_ERR_SCRATCH;
-    p.out = static_cast<__nv_bfloat16 *>(out);
-    // whole lines (the caller's buffer begins on 16 bytes at least)
-    p.ws = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(workspace) + (kWsAlign - 1)) &
-                                       ~uintptr_t{kWsAlign - 1});
     p.heads = heads;
     // The chunk kernel from an average of more than 256 rows of q per sequence on. Below, a unit
     // of 64 rows reads the keys at most four times and does not compute the logits twice. Single
@@ -947,6 +949,13 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
     p.rpt = std::min(heads, p.rows);
     // a window no shorter than any sequence is no window
     p.window = window >= p.b.len_limit ? 0 : window;
+    if (run_bound(p) > (int64_t{1} << 31) - 1) return DSA_ERR_SHAPE;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < DSA_PAGED_WORKSPACE_BYTES)
+        return DSA_ERR_SCRATCH;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    // whole lines (the caller's buffer begins on 16 bytes at least)
+    p.ws = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(workspace) + (kWsAlign - 1)) &
+                                       ~uintptr_t{kWsAlign - 1});
     p.c = c;
     p.status = dev_status;
     int sms = 0;

@@ -410,6 +410,8 @@ int dsa_paged_append(const void *kv, int64_t n_new, const int32_t *new_start,
  * -inf the elements at the infinity's place are unspecified. Logits may have any size: the products
  * q . row are held in fp32 and weights taken from their differences (a product beyond fp32's
  * range counts as an infinity in its row).
+ * Sizes that would allow one SM 2^31 blocks of 128 keys (2.5 million units of 64 or 128 rows of q
+ * over sequences of DSA_MAX_PAGED_TOKENS: hours) get DSA_ERR_SHAPE.
  * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE, DSA_ERR_SCRATCH, DSA_ERR_CUDA.
  */
 int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new, const int32_t *new_start,

@@ -38,3 +38,25 @@ def test_more_sequences_than_the_kernels_can_count(lib, n_seqs):
     """Their loops step past n_seqs by up to a block of threads: the sum has to stay in 32 bits."""
     assert append(lib, n_seqs=n_seqs) == B.DSA_ERR_SHAPE
     assert attn(lib, n_seqs=n_seqs, out=APART) == B.DSA_ERR_SHAPE
+
+
+LONG = dict(page_size=1024, page_stride=1024 * 512, max_pages=1 << 14, cos_sin=None, out=APART)
+
+
+@pytest.mark.parametrize("change", [
+    dict(n_new=5_000_000, heads=33, n_seqs=1),            # two units per three tokens
+    dict(n_new=2_600_000, heads=65, n_seqs=1),            # two per token
+    dict(n_new=3_000_000, heads=1, n_seqs=3_000_000)])    # a unit per sequence
+def test_more_blocks_than_a_cta_can_count(lib, change):
+    """131,072 blocks for each of more than 2.5 million units: a 152nd passes 32 bits."""
+    assert attn(lib, **LONG, **change) == B.DSA_ERR_SHAPE
+
+
+@pytest.mark.parametrize("change", [
+    dict(n_new=5_000_000, heads=33, n_seqs=1, window=4096),
+    dict(n_new=1_000_000, heads=65, n_seqs=1),
+    dict(n_new=3_000_000, heads=1, n_seqs=1)])
+def test_long_work_that_can_be_counted_is_not_refused(lib, change):
+    """It gets past the checks of the arguments: to the workspace's, here one byte short."""
+    short = B.DSA_PAGED_WORKSPACE_BYTES - 1
+    assert attn(lib, **LONG, **change, workspace_bytes=short) == B.DSA_ERR_SCRATCH
