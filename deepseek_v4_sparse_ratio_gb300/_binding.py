@@ -298,6 +298,9 @@ def _paged(where: str, new_start, seq_len, page_table, pages, cos_sin, device):
         raise DsaError(DSA_ERR_ARG, f"{where}: pages has to be a {_BF16} tensor "
                                     f"[*, *, {DIM}] on cuda:{device} with packed pages")
     n_pages, page_size, _ = shape
+    if (n_seqs | max_pages | page_size) >> 31:   # ctypes would drop the upper bits
+        raise DsaError(DSA_ERR_SHAPE, f"{where}: {n_seqs} sequences of {max_pages} pages of "
+                                      f"{page_size} rows are no 32-bit counts")
     angles, n_pos = None, 0
     if cos_sin is not None:
         n_pos = cos_sin.shape[0] if cos_sin.dim() else 0
@@ -351,8 +354,9 @@ def dsa_paged_attn(q, new_start, seq_len, page_table, pages, window: int, scale:
         _refuse(where, "out", _BF16, ", ".join(map(str, shape)), dev)
     if not (workspace.get_device() == dev and workspace.is_contiguous()):
         _refuse(where, "workspace", workspace.dtype, "*", dev)
-    if window >> 31:   # ctypes would drop the upper bits
-        raise DsaError(DSA_ERR_SHAPE, f"{where}: window {window} is no 32-bit count")
+    if (window | shape[1]) >> 31:   # ctypes would drop the upper bits
+        raise DsaError(DSA_ERR_SHAPE, f"{where}: window {window} or heads {shape[1]} is no 32-bit "
+                                      "count")
     rc = (_lib or load()).dsa_paged_attn(
         q.data_ptr(), shape[1], shape[0],
         *_paged(where, new_start, seq_len, page_table, pages, cos_sin, dev), window, scale,
