@@ -152,6 +152,15 @@ int check_paged_batch(int64_t n_new, const int32_t *new_start, const int32_t *se
     return DSA_OK;
 }
 
+bool touches_pages(const PagedBatch &b, const void *pages, const void *p, uint64_t bytes) {
+    const uint64_t base = reinterpret_cast<uintptr_t>(pages), at = reinterpret_cast<uintptr_t>(p);
+    const uint64_t stride = static_cast<uint64_t>(b.page_stride) * 2;
+    const uint64_t page = (uint64_t{kD} * 2) << b.page_shift;
+    // the first page that ends behind `at`: does it begin before the end?
+    const uint64_t k = at < base + page ? 0 : (at - base - page) / stride + 1;
+    return k < static_cast<uint64_t>(b.n_pages) && base + k * stride < at + bytes;
+}
+
 }  // namespace dsa
 
 extern "C" int dsa_paged_append(const void *kv, int64_t n_new, const int32_t *new_start,
@@ -165,6 +174,7 @@ extern "C" int dsa_paged_append(const void *kv, int64_t n_new, const int32_t *ne
     int rc = check_paged_batch(n_new, new_start, seq_len, n_seqs, page_table, max_pages, pages,
                                n_pages, page_stride, page_size, cos_sin, n_pos, &b);
     if (rc != DSA_OK) return rc;
+    if (touches_pages(b, pages, kv, static_cast<uint64_t>(n_new) * kD * 2)) return DSA_ERR_ARG;
     const unsigned grid = static_cast<unsigned>((n_new + kAppendWarps - 1) / kAppendWarps);
     return launch_overlapped(paged_append_kernel, grid, kAppendWarps * 32, 0,
                              static_cast<cudaStream_t>(stream), b, static_cast<const uint4 *>(kv),

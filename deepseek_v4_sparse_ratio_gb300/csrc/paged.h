@@ -32,6 +32,9 @@ int check_paged_batch(int64_t n_new, const int32_t *new_start, const int32_t *se
                       const void *pages, int64_t n_pages, int64_t page_stride, int32_t page_size,
                       const float *cos_sin, int64_t n_pos, PagedBatch *b);
 
+// Whether [p, p + bytes) touches a page (between pages lies what the caller likes).
+bool touches_pages(const PagedBatch &b, const void *pages, const void *p, uint64_t bytes);
+
 bool make_tmap_pages(CUtensorMap *map, const void *pages, const PagedBatch &b);
 
 // One sequence of the batch: rows [row0, row0 + n) are its new tokens, the last n of its len.

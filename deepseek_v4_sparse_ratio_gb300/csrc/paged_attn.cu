@@ -924,7 +924,10 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
         return DSA_ERR_SHAPE;
     const uintptr_t qa = reinterpret_cast<uintptr_t>(q), oa = reinterpret_cast<uintptr_t>(out);
     const uintptr_t bytes = static_cast<uintptr_t>(n_new) * heads * kD * 2;
-    if (qa < oa + bytes && oa < qa + bytes) return DSA_ERR_ARG;
+    auto overlap = [](uintptr_t a, uintptr_t na, uintptr_t b, uintptr_t nb) {
+        return a < b + nb && b < a + na;
+    };
+    if (overlap(qa, bytes, oa, bytes) || touches_pages(p.b, pages, out, bytes)) return DSA_ERR_ARG;
     p.heads = heads;
     // The chunk kernel from an average of more than 256 rows of q per sequence on. Below, a unit
     // of 64 rows reads the keys at most four times and does not compute the logits twice. Single
@@ -952,6 +955,10 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
     if (run_bound(p) > (int64_t{1} << 31) - 1) return DSA_ERR_SHAPE;
     if (!workspace || !aligned16(workspace) || workspace_bytes < DSA_PAGED_WORKSPACE_BYTES)
         return DSA_ERR_SCRATCH;
+    const uintptr_t wa = reinterpret_cast<uintptr_t>(workspace), used = DSA_PAGED_WORKSPACE_BYTES;
+    if (overlap(wa, used, qa, bytes) || overlap(wa, used, oa, bytes) ||
+        touches_pages(p.b, pages, workspace, used))
+        return DSA_ERR_ARG;
     p.out = static_cast<__nv_bfloat16 *>(out);
     // whole lines (the caller's buffer begins on 16 bytes at least)
     p.ws = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(workspace) + (kWsAlign - 1)) &

@@ -373,8 +373,9 @@ int dsa_index_score_topk_noalloc(const void *q_idx, const float *w, const void *
  * Append the new tokens' rows: row p mod page_size of page page_table[s][p / page_size] :=
  * R(p) kv[r] for every row r of a sequence, p its position (a plain copy when cos_sin is
  * NULL). The rotation is taken in fp32 and rounded to bf16 once.
- *   kv [n_new, 512] bf16, apart from the pages. Two rows for one place (a page that two sequences of the batch
- *   write) are the caller's mistake: either may end up there.
+ *   kv [n_new, 512] bf16, apart from the pages (DSA_ERR_ARG; it may lie between two). Two rows
+ *   for one place (a page that two sequences of the batch write) are the caller's mistake: either
+ *   may end up there.
  * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE, DSA_ERR_CUDA.
  */
 int dsa_paged_append(const void *kv, int64_t n_new, const int32_t *new_start,
@@ -397,9 +398,10 @@ int dsa_paged_append(const void *kv, int64_t n_new, const int32_t *new_start,
  * read from the pages: append them first. Accumulated in fp32; the probabilities and the
  * rotated queries are rounded to bf16 for the matrix products, the output once to bf16.
  *
- *   q [n_new, heads, 512] bf16; out the same, not overlapping q; heads from 1 to
- *   DSA_MAX_PAGED_HEADS (64 for the whole model, fewer on a shard of it); scale > 0 and
- *   scale * log2(e) within fp32;
+ *   q [n_new, heads, 512] bf16; out the same. out and the workspace's first
+ *   DSA_PAGED_WORKSPACE_BYTES lie apart from q, the pages and each other (else DSA_ERR_ARG; between
+ *   two pages is apart). heads from 1 to DSA_MAX_PAGED_HEADS (64 for the whole model, fewer on a
+ *   shard of it); scale > 0 and scale * log2(e) within fp32;
  *   workspace: device buffer of workspace_bytes >= DSA_PAGED_WORKSPACE_BYTES; nothing in it
  *   needs to start at zero and nothing is kept in it. Calls (and captured graphs) that may
  *   run at the same time need one each.

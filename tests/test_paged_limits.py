@@ -60,3 +60,36 @@ def test_long_work_that_can_be_counted_is_not_refused(lib, change):
     """It gets past the checks of the arguments: to the workspace's, here one byte short."""
     short = B.DSA_PAGED_WORKSPACE_BYTES - 1
     assert attn(lib, **LONG, **change, workspace_bytes=short) == B.DSA_ERR_SCRATCH
+
+
+STRIDE = 3 * 64 * 512                     # two thirds of every stride is other data
+PAGE, NEXT = 64 * 512 * 2, STRIDE * 2     # bytes of a page, and from one to the next
+POOL = 5 << 40
+
+
+@pytest.mark.parametrize("at,hit", [
+    (POOL - 4 * 1024, False), (POOL - 4 * 1024 + 16, True), (POOL, True), (POOL + PAGE - 16, True),
+    (POOL + PAGE, False), (POOL + NEXT - 4 * 1024, False), (POOL + NEXT - 16, True),
+    (POOL + 9 * NEXT + PAGE - 16, True), (POOL + 9 * NEXT + PAGE, False),
+    (POOL + 10 * NEXT, False), (POOL + (1 << 30), False)])
+def test_rows_inside_the_pages_are_refused(lib, at, hit):
+    """kv read while pages are written, out written while pages are read: whichever comes first.
+    Between the pages, where another layer's may lie, either is fine (the call then gets to
+    its workspace, which is missing: none of these reaches a GPU)."""
+    pool = dict(pages=POOL, page_stride=STRIDE)
+    code = B.DSA_ERR_ARG if hit else B.DSA_ERR_SCRATCH
+    assert attn(lib, **pool, out=at, heads=1, workspace=None) == code
+    if hit:
+        assert append(lib, **pool, kv=at) == code
+
+
+WORK = ATTN["workspace"]
+
+
+@pytest.mark.parametrize("change", [
+    dict(out=WORK), dict(out=WORK + B.DSA_PAGED_WORKSPACE_BYTES - 16),
+    dict(out=APART, q=WORK + 4096), dict(out=APART, pages=WORK + 4096),
+    dict(out=APART, pages=WORK - 9 * 64 * 1024 - 16)])
+def test_a_workspace_that_holds_other_arguments_is_refused(lib, change):
+    """Parts of cut units would be written over what other SMs still read or write."""
+    assert attn(lib, **change) == B.DSA_ERR_ARG
