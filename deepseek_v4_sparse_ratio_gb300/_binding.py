@@ -201,9 +201,10 @@ def dsa_index_score_topk_noalloc(q_idx, w, pooled_ik, n_pooled: int, chunk: int,
     _check(rc, "dsa_index_score_topk_noalloc")
 
 
-def dsa_bounded_wait_selftest(arrive: bool, dev_status, stream=None) -> None:
-    """Run the library's bounded mbarrier wait on a barrier that gets its arrival or none."""
-    rc = load().dsa_bounded_wait_selftest(1 if arrive else 0, _p(dev_status), _s(stream))
+def dsa_bounded_wait_selftest(arrive: int, dev_status, stream=None) -> None:
+    """Run the library's bounded mbarrier waits on a barrier that gets its arrival (1) or none (0),
+    or gets it late while blocks of work move on (2) or stand still (3)."""
+    rc = load().dsa_bounded_wait_selftest(int(arrive), _p(dev_status), _s(stream))
     _check(rc, "dsa_bounded_wait_selftest")
 
 

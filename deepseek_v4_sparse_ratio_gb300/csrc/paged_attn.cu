@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     volatile uint32_t *sPages = tmem_holder + 2;  // [2] pages of a block that were loaded
     int *sStart = reinterpret_cast<int *>(tmem_holder + 4);  // [5] start of this CTA's run
+    volatile uint32_t *sBlocks = tmem_holder + 9;            // blocks begun, for the long waits
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (warp == 0) {
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 31) {
             *abort_flag = 0;
             sStart[4] = 0;
+            *sBlocks = 0;
         }
         fence_barrier_init();
     }
@@ -195,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // chunk 7 first, into the slot that the block two back released
                 if (lane == 0) {
                     sPages[par] = mask;
+                    *sBlocks = static_cast<uint32_t>(g) + 1;
                     mbar_expect_tx(&x_full[par], bytes);
                 }
                 __syncwarp();
@@ -248,7 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 8; ++k) cs[k] = __ldg(src + k);
                     }
-                    if (!wait_bar(q_full, i & 1, abort_flag, p.status)) break;
+                    // (lasts as long as the unit before)
+                    if (!wait_units(q_full, i & 1, abort_flag, sBlocks, p.status)) break;
                     if (mine) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {

@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     volatile uint32_t *sPages = tmem_holder + 2;             // [2]
     int *sStart = reinterpret_cast<int *>(tmem_holder + 4);  // [5]
+    volatile uint32_t *sBlocks = tmem_holder + 9;            // blocks begun, for the long waits
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (smem_u32(smem) & 1023u) {  // the tiles' swizzle counts on it
@@ -271,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 31) {
             *abort_flag = 0;
             sStart[4] = 0;
+            *sBlocks = 0;
         }
         fence_barrier_init();
     }
@@ -293,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Walk walk(p, sStart);
             Segment x;
             for (int i = 0; walk.next(p, x); ++i) {
-                wait_bar(stat_full, i & 1, abort_flag, p.status);
+                wait_units(stat_full, i & 1, abort_flag, sBlocks, p.status);  // a unit
                 const float linv = sLinv[r];
                 mbar_arrive(stat_free);
                 const bool live = wait_bar(o_full, i & 1, abort_flag, p.status);
@@ -388,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) {
                         if (at == 0) {
                             sPages[par] = mask & ((1u << np) - 1u);
+                            *sBlocks = static_cast<uint32_t>(g) + 1;
                             mbar_arrive(&pg_full[par]);
                         }
                         mbar_expect_tx(&full[pair], bytes);
@@ -418,7 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int loads = 0;
             for (int i = 0; walk.next(p, x); ++i) {
                 if (!fresh_q(x, i)) continue;
-                if (!wait_bar(q_free, (loads & 1) ^ 1, abort_flag, p.status)) break;
+                // (a token group: two units)
+                if (!wait_units(q_free, (loads & 1) ^ 1, abort_flag, sBlocks, p.status)) break;
                 if (lane == 0) {
                     mbar_expect_tx(q_full, kQSmem * kSlab);
                     for (int c = 0; c < kQSmem; ++c)

@@ -17,6 +17,7 @@
 
 #include "common.cuh"
 #include "paged.h"
+#include "waits.cuh"
 
 namespace dsa {
 namespace paged {
@@ -456,6 +457,12 @@ static __device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, vo
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort,
                                          int32_t *status) {
     return mbar_test(smem_u32(bar), parity) || wait_long(bar, parity, abort, status);
+}
+
+// The same for a wait that spans whole units.
+__device__ __forceinline__ bool wait_units(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                           const volatile uint32_t *blocks, int32_t *status) {
+    return mbar_test(smem_u32(bar), parity) || wait_moving(bar, parity, abort, blocks, status);
 }
 
 // One lane of a converged warp, the same one every time. A branch on it (rather than on

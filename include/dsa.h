@@ -362,8 +362,7 @@ int dsa_index_score_topk_noalloc(const void *q_idx, const float *w, const void *
  * These arrays (all but the sizes) are read on the device when the kernels run, so a captured
  * graph replays with the lengths they hold then. A sequence whose numbers cannot be
  * (new_start decreasing, negative or beyond n_new; seq_len < n_s, > max_pages*page_size,
- * > n_pos or > DSA_MAX_PAGED_TOKENS, up to which a kernel's bounded waits last) is skipped
- * whole: its rows are not written, and DSA_ERR_BOUNDS goes to dev_status. (Where starts that
+ * > n_pos or > DSA_MAX_PAGED_TOKENS) is skipped whole: its rows are not written, and DSA_ERR_BOUNDS goes to dev_status. (Where starts that
  * decrease give one row to two sequences of possible numbers, either may have it.)
  * A needed page_table entry outside [0, n_pages) is reported the same way and its rows are
  * left out (not written by the append, not seen by the attention).
@@ -428,13 +427,19 @@ int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new, const int32_t *n
  * Every kernel of this library waits on shared-memory mbarriers with a bounded
  * wait: after about 2^31 SM cycles (about a second) it gives up, records
  * DSA_ERR_TIMEOUT in dev_status, lets the other warps of its CTA leave, and
- * the kernel returns, so the CUDA context stays usable. This call launches one
- * 32-thread CTA that initialises an mbarrier expecting one arrival and waits on
- * it with that same bounded wait:
- *   arrive != 0: a thread arrives first; the wait completes at once and
- *                dev_status is left as it is;
+ * the kernel returns, so the CUDA context stays usable. Waits of the paged kernels
+ * that span whole units of work count the second from the CTA's last block of
+ * keys. This call launches one CTA of two warps that initialises an mbarrier
+ * expecting one arrival and waits on it with those same bounded waits:
+ *   arrive == 1 (or any value not named here): a thread arrives first; the wait
+ *                completes at once and dev_status is left as it is;
  *   arrive == 0: nothing arrives; about a second later DSA_ERR_TIMEOUT is
- *                written to dev_status (if it held DSA_OK) and the kernel ends.
+ *                written to dev_status (if it held DSA_OK) and the kernel ends;
+ *   arrive == 2: a thread moves the count of blocks four times a second and
+ *                arrives after one and a half: the long wait completes then and
+ *                dev_status is left as it is;
+ *   arrive == 3: the same with a count that stands still: DSA_ERR_TIMEOUT after
+ *                about a second (the kernel ends when the thread has arrived).
  * dev_status: device int32, caller-owned. Enqueued on `stream`; returns
  * DSA_ERR_ARG for a null dev_status, DSA_ERR_CUDA if the launch fails.
  * The pages have no counterpart to this entry point: it is an addition of this
