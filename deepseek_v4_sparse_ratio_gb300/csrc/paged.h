@@ -51,6 +51,19 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatch &b, int s, bool &
     return PagedSeq{r0, bad ? 0 : r1 - r0, len};
 }
 
+// What a kernel needs once per device: the raised shared-memory limit, and that it was compiled to
+// the registers its warps' split counts on.
+template <typename... Args>
+int prepare_kernel(void (*kernel)(Args...), int regs, int smem) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kernel) == cudaSuccess && fa.numRegs == regs &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
+            cudaSuccess)
+        return DSA_OK;
+    (void)cudaGetLastError();  // the caller has the code; its own next call is not to find it
+    return DSA_ERR_CUDA;
+}
+
 // For kernels launched by launch_overlapped: waits until the kernels before this one in the
 // stream are done and their writes can be read.
 __device__ __forceinline__ void wait_before() {

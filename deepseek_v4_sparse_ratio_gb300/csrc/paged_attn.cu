@@ -866,13 +866,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 
 // ------------------------------------------------------------------ host
 
-struct Setup {
-    bool done = false;
-    int rc = DSA_OK;
-    int sms = 0;
-};
 std::mutex g_mu;
-Setup g_setup[kMaxDevices];
+int g_sms[kMaxDevices];   // 0: not set up yet
 
 // Places that a CTA's run may have (of a GB300's 152), from the sizes alone (lengths are the
 // device's): the kernels count them in 32 bits.
@@ -882,26 +877,19 @@ int64_t run_bound(const Params &p) {
     return groups * p.upt * (keys / kBlock + 2 + kUnitCost) / kMaxCtas + 1;
 }
 
-// Per-device one-time set-up: the raised shared-memory limit and the register split's check.
+// Per-device one-time set-up. A failure is not kept: it may pass (memory for the module's code).
 int setup(int *sms) {
     const int dev = current_device();
     if (dev < 0) return DSA_ERR_CUDA;
     std::lock_guard<std::mutex> lock(g_mu);
-    Setup &st = g_setup[dev];
-    if (!st.done) {
-        cudaFuncAttributes fa;
-        st.sms = sm_count();
-        st.rc = st.sms > 0 && cudaFuncGetAttributes(&fa, paged_attn_kernel) == cudaSuccess &&
-                        fa.numRegs == kRegsLaunch &&
-                        cudaFuncSetAttribute(paged_attn_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kSmem) == cudaSuccess
-                    ? DSA_OK
-                    : DSA_ERR_CUDA;
-        st.done = true;
+    if (!g_sms[dev]) {
+        const int n = sm_count();
+        const int rc = n > 0 ? prepare_kernel(paged_attn_kernel, kRegsLaunch, kSmem) : DSA_ERR_CUDA;
+        if (rc != DSA_OK) return rc;
+        g_sms[dev] = n;
     }
-    *sms = st.sms;
-    return st.rc;
+    *sms = g_sms[dev];
+    return DSA_OK;
 }
 
 }  // namespace

@@ -700,7 +700,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 std::mutex g_mu;
-int g_rc[kMaxDevices];
 bool g_done[kMaxDevices];
 
 }  // namespace
@@ -710,17 +709,11 @@ int prepare_paged_chunk() {
     if (dev < 0) return DSA_ERR_CUDA;
     std::lock_guard<std::mutex> lock(g_mu);
     if (!g_done[dev]) {
-        cudaFuncAttributes fa;
-        g_rc[dev] = cudaFuncGetAttributes(&fa, paged_chunk_kernel) == cudaSuccess &&
-                            fa.numRegs == kRegsLaunch &&
-                            cudaFuncSetAttribute(paged_chunk_kernel,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 kSmem) == cudaSuccess
-                        ? DSA_OK
-                        : DSA_ERR_CUDA;
+        const int rc = prepare_kernel(paged_chunk_kernel, kRegsLaunch, kSmem);
+        if (rc != DSA_OK) return rc;
         g_done[dev] = true;
     }
-    return g_rc[dev];
+    return DSA_OK;
 }
 
 int enqueue_paged_chunk(const CUtensorMap &tm_q, const CUtensorMap &tm_kv,
