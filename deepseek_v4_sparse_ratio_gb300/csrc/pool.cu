@@ -302,35 +302,42 @@ static PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
     return g_encode;
 }
 
+// A bf16 tensor map whose box steps over every element. The driver encodes for the calling
+// thread's context, and a thread that has made no runtime call yet (another one did this library's
+// set-up) has none: cudaSetDevice binds its device's.
+static bool encode_bf16(CUtensorMap *map, const void *base, uint32_t rank, const cuuint64_t *dims,
+                        const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swz) {
+    const auto encode = tmap_encoder();
+    if (!encode) return false;
+    const cuuint32_t estr[3] = {1, 1, 1};
+    auto try_encode = [&] {
+        return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims,
+                      strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (try_encode()) return true;
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && try_encode();
+}
+
 bool make_tmap_bf16(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,
                     uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, bool swizzle128) {
-    if (!tmap_encoder()) return false;
-    cuuint64_t dims[2] = {inner, rows};
-    cuuint64_t strides[1] = {row_bytes};
-    cuuint32_t box[2] = {box_inner, box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims,
-                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
+    const cuuint64_t dims[2] = {inner, rows};
+    const cuuint64_t strides[1] = {row_bytes};
+    const cuuint32_t box[2] = {box_inner, box_rows};
+    return encode_bf16(map, base, 2, dims, strides, box,
+                       swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 // The pages as [n_pages][page_size][512]; a box is 64 dims of one page, or of 128 rows of a
 // longer one, with the 128-byte swizzle.
 bool make_tmap_pages(CUtensorMap *map, const void *pages, const PagedBatch &b) {
-    if (!tmap_encoder()) return false;
     const cuuint64_t rows = cuuint64_t{1} << b.page_shift;
-    cuuint64_t dims[3] = {kD, rows, static_cast<cuuint64_t>(b.n_pages)};
-    cuuint64_t strides[2] = {kD * 2, static_cast<cuuint64_t>(b.page_stride) * 2};
-    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows < 128 ? rows : 128), 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(pages),
-                          dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
+    const cuuint64_t dims[3] = {kD, rows, static_cast<cuuint64_t>(b.n_pages)};
+    const cuuint64_t strides[2] = {kD * 2, static_cast<cuuint64_t>(b.page_stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows < 128 ? rows : 128), 1};
+    return encode_bf16(map, pages, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 int current_device() {
