@@ -6,7 +6,7 @@
 #include <cuda.h>
 #include <stdint.h>
 
-#include "internal.h"
+#include "common.cuh"
 
 namespace dsa {
 
@@ -49,6 +49,13 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatch &b, int s, bool &
     const int32_t len = __ldg(b.seq_len + s);
     bad = r0 < 0 || r1 < r0 || r1 > b.n_new || len < r1 - r0 || len > b.len_limit;
     return PagedSeq{r0, bad ? 0 : r1 - r0, len};
+}
+
+// A pair (x, y) turned by an angle, in fp32 and rounded to bf16 once.
+__device__ __forceinline__ uint32_t turn_pair(uint32_t v, float c, float s) {
+    const float x = bf16lo(v), y = bf16hi(v);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(x * c - y * s, x * s + y * c);
+    return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 // What a kernel needs once per device: the raised shared-memory limit, and that it was compiled to

@@ -529,12 +529,6 @@ __device__ __forceinline__ uint32_t finite2(uint32_t v) {
     return v;
 }
 
-__device__ __forceinline__ uint32_t turn_pair(uint32_t v, float c, float s) {
-    const float x = bf16lo(v), y = bf16hi(v);
-    const __nv_bfloat162 r = __floats2bfloat162_rn(x * c - y * s, x * s + y * c);
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-
 }  // namespace paged
 
 // The chunk kernel (paged_chunk.cu): one-time set-up, and its launch.
