@@ -204,6 +204,8 @@ int dsa_index_score_topk(const void *q_idx, const float *w, const void *pooled_i
  *   entries are read; among them -1 is skipped, and an index outside
  *   [0, n_vis(t)) is skipped and reported as DSA_ERR_BOUNDS in dev_status;
  *   window > 0; scale > 0; out [chunk, 64, 512] bf16.
+ *   Logits may be up to 1e9 in size: the exponent is the difference of two values
+ *   rounded at their own size, from 2^31 in log2 units on by more than fp32 can scale.
  * Launch shape: one 512-thread CTA per SM, each taking whole tokens; for a
  * chunk of at most (SM count / 8) rows whose tokens span more than one
  * 128-key block (decode steps, short bands), thread-block clusters of 8 CTAs
@@ -338,9 +340,9 @@ int dsa_index_score_topk_noalloc(const void *q_idx, const float *w, const void *
 
 /*
  * The paged cache of a ragged batch, as dsa_paged_append and dsa_paged_attn take it. The
- * pages have no counterpart to these two calls: they are additions of this library, for the
- * layers of the same model that attend densely (their whole context, or the local window
- * alone) when many sequences are served at once.
+ * pages have no counterpart to these two calls: they are additions of this library, for many
+ * sequences served at once: their layers that attend over the local window alone, and layers
+ * with rows of this kind that attend over the whole context (the pages name no such layer).
  *
  *   pages [n_pages] of [page_size, 512] bf16, page_stride elements from one page to the next
  *     (>= page_size*512, a multiple of 8; larger where other data lies between). page_size is
