@@ -11,21 +11,19 @@ namespace dsa {
 
 __global__ void __launch_bounds__(64) wait_selftest_kernel(int32_t arrive, int32_t *status) {
     __shared__ __align__(8) uint64_t bar;
-    __shared__ int abort_flag;
-    __shared__ uint32_t blocks;
+    __shared__ int words[1 + kBlocksAt];  // the abort flag, and the count of blocks
     if (threadIdx.x == 0) {
         mbar_init(&bar, 1);
-        abort_flag = 0;
-        blocks = 0;
+        words[0] = words[kBlocksAt] = 0;
         fence_barrier_init();
     }
     __syncthreads();
     if (arrive == 2 || arrive == 3) {
         if (threadIdx.x == 0) {
-            wait_moving(&bar, 0, &abort_flag, &blocks, status);
+            wait_moving(&bar, 0, words, status);
         } else if (threadIdx.x == 32) {
             // six steps of a quarter of a budget each: moving ones, or one count for all
-            volatile uint32_t *count = &blocks;
+            volatile int *count = words + kBlocksAt;
             for (int k = 0; k < 6; ++k) {
                 const long long t0 = clock64();
                 while (clock64() - t0 < kWaitBudget / 4) {
@@ -36,7 +34,7 @@ __global__ void __launch_bounds__(64) wait_selftest_kernel(int32_t arrive, int32
         }
     } else if (threadIdx.x == 0) {
         if (arrive) mbar_arrive(&bar);
-        mbar_wait(&bar, 0, &abort_flag, status);
+        mbar_wait(&bar, 0, words, status);
     }
 }
 

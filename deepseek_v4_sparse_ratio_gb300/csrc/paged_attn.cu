@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     volatile uint32_t *sPages = tmem_holder + 2;  // [2] pages of a block that were loaded
     int *sStart = reinterpret_cast<int *>(tmem_holder + 4);  // [5] start of this CTA's run
-    volatile uint32_t *sBlocks = tmem_holder + 9;            // blocks begun, for the long waits
+    volatile uint32_t *sBlocks = tmem_holder + 1 + kBlocksAt;  // blocks begun
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (warp == 0) {
@@ -251,8 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 8; ++k) cs[k] = __ldg(src + k);
                     }
-                    // (lasts as long as the unit before)
-                    if (!wait_units(q_full, i & 1, abort_flag, sBlocks, p.status)) break;
+                    if (!wait_bar(q_full, i & 1, abort_flag, p.status)) break;
                     if (mine) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {

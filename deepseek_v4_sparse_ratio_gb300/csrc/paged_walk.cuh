@@ -447,22 +447,10 @@ __device__ __forceinline__ void prefetch_tmap(const CUtensorMap *tm) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(tm) : "memory");
 }
 
-// mbar_wait with the loop out of line: its many copies would push the roles' code out of the
-// instruction caches.
-static __device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *abort,
-                                       int32_t *status) {
-    return mbar_wait(bar, parity, abort, status);
-}
-
+// mbar_wait whose loop is out of line and whose budget counts from the last block.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort,
                                          int32_t *status) {
-    return mbar_test(smem_u32(bar), parity) || wait_long(bar, parity, abort, status);
-}
-
-// The same for a wait that spans whole units.
-__device__ __forceinline__ bool wait_units(uint64_t *bar, uint32_t parity, volatile int *abort,
-                                           const volatile uint32_t *blocks, int32_t *status) {
-    return mbar_test(smem_u32(bar), parity) || wait_moving(bar, parity, abort, blocks, status);
+    return mbar_test(smem_u32(bar), parity) || wait_moving(bar, parity, abort, status);
 }
 
 // One lane of a converged warp, the same one every time. A branch on it (rather than on

@@ -430,8 +430,8 @@ int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new, const int32_t *n
  * wait: after about 2^31 SM cycles (about a second) it gives up, records
  * DSA_ERR_TIMEOUT in dev_status, lets the other warps of its CTA leave, and
  * the kernel returns, so the CUDA context stays usable. Waits of the paged kernels
- * that span whole units of work count the second from the CTA's last block of
- * keys. This call launches one CTA of two warps that initialises an mbarrier
+ * that may span whole units of work start the second anew while blocks of keys
+ * are begun. This call launches one CTA of two warps that initialises an mbarrier
  * expecting one arrival and waits on it with those same bounded waits:
  *   arrive == 1 (or any value not named here): a thread arrives first; the wait
  *                completes at once and dev_status is left as it is;
