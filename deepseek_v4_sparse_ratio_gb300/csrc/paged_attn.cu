@@ -26,10 +26,11 @@
 //
 // Bound: HBM for single tokens (64 heads: 128 flops a byte, against 282 of the machine). One tile
 // is all that fits beside q (64 KB) and P, so a block is a chain (PV of the block before frees
-// the slots, 1,900 cycles of load latency, the last QK products, 1,000 cycles of softmax): 6,540
-// cycles per 128 KB and SM, 5.6 TB/s, 83 % of the measured copy rate, in the steady state of 152
-// sequences of 16,384 (445 us). One token at 131,072: 45 us, of which 9 are the launch's start
-// (lengths, q, the first tile, instructions) and 8 the join; 64 users of up to 8,192: 82 us.
+// the slots, 1,900 cycles of load latency, the last QK products, 1,000 cycles of softmax). 152
+// sequences of 16,384, a unit of 128 blocks for each SM: 441 us from start to join, 5.8 TB/s of
+// keys, 85 % of the measured copy rate. One token at 131,072: 44.5 us, 37 without the launch of the
+// join; 64 users of up to 8,192: 82.6, 77.4 without. (The compiler spills 100 bytes a thread, 128
+// read back, to fit all roles into the launch's 128 registers.)
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -922,10 +923,12 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
     p.heads = heads;
     // The chunk kernel from an average of more than 256 rows of q per sequence on. Below, a unit
     // of 64 rows reads the keys at most four times and does not compute the logits twice. Single
-    // and chunk kernel (us): 32 sequences of 8,192 with 64 rows 70 / 124, 128 rows 128 / 130,
-    // 256 rows 226 / 237, 512 rows 402 / 402; 4 of 1,024 with 64 rows 21 / 26, 256 rows 26 / 28;
-    // 16 of up to 16,384 with 160 on average 89 / 102; 64 prompts of 100 tokens (6,400 rows) 460 /
-    // 249; one of 2,048 tokens at 16,384 4,343 / 3,688; 32 of one token of 128 heads 59 / 62.
+    // and chunk kernel (us): 32 sequences of 8,192 with 64 rows 67 / 120, 128 rows 122 / 125,
+    // 256 rows 222 / 233, 512 rows 398 / 401; 4 of 1,024 with 64 rows 16 / 22, 256 rows 20 / 24;
+    // 16 of up to 16,384 with 160 on average 84 / 97; 64 prompts of 100 tokens (6,400 rows) 460 /
+    // 249; one of 2,048 tokens at 16,384 4,360 / 3,796; 32 of one token of 128 heads 54 / 58.
+    // (An average: 64 single tokens of up to 8,192 beside a prompt of 512 all go to the chunk
+    // kernel, 187 us where the two apart take 83 and 52.)
     // It loads q and stores out 32 bytes at a time, so arrays that begin between (views at an odd
     // multiple of eight elements) are left to the other kernel, which is right for every batch.
     const bool chunk = n_new * heads > int64_t{n_seqs} * 256 && ((qa | oa) & 31u) == 0;

@@ -21,13 +21,13 @@
 // stores), warp 4 loads K, warp 5 issues the products, warp 6 loads q, warps 8-15 bring q's last
 // chunks to TMEM and do the softmax: TMEM lane = row, two warps per 32 rows, 64 keys each.
 //
-// Bound: the tensor pipe, 72 % active. A block takes about 4,300 cycles, 3,090 of them products
+// Bound: the tensor pipe, 71 % active. A block takes about 4,400 cycles, 3,090 of them products
 // at full rate; the rest is issue around the waits (the softmax, some 1,000 cycles, runs beside
 // them).
-// 2,048 tokens of 64 heads at 16,384: 3.65 to 3.73 ms by the clocks, 1,100 to 1,130 TFLOP/s of the
-// result's own flops (0.58 to 0.59 of the measured peak, 0.87 to 0.88 with the logits counted
-// twice). Short units pay for their change: 64 prompts of 100 tokens 249 us, 4,096 tokens with a
-// 128-row window 196 us (303 and 281 while new queries' products began with the dims that go
+// 2,048 tokens of 64 heads at 16,384: 3.74 to 3.81 ms by the clocks, 1,080 to 1,100 TFLOP/s of the
+// result's own flops (0.56 to 0.57 of the measured peak, 0.85 to 0.86 with the logits counted
+// twice). Short units pay for their change: 64 prompts of 100 tokens 250 us, 4,096 tokens with a
+// 128-row window 200 us (303 and 281 while new queries' products began with the dims that go
 // through TMEM, those were read 16 bytes a load, and every product had its own code).
 #include <cudaTypedefs.h>
 #include <math.h>

@@ -26,16 +26,23 @@ constexpr int kBlock = 128;        // keys in a block
 constexpr int kThreads = 512;      // of both kernels
 constexpr int kMaxCtas = 152;
 
-// Places of a unit before its blocks. (1, 2 and 3 for chunks: 1,127, 1,085 and 1,104 us for a prompt
-// of 4,096 tokens, 346, 341 and 352 for 34 prompts of 208, 149, 134 and 145 for 32 users of 64
-// tokens with a window of 128; for single tokens: 90, 87 and 90 us for 64 users up to 8K. None at
-// all: 2,033 us for the prompt of 4,096.)
+// Places of a unit before its blocks. (0, 1, 2 and 3 for chunks: 1,534, 1,107, 1,110 and 1,137 us
+// for a prompt of 4,096 tokens, 363, 314, 305 and 321 for 34 prompts of 208, 143, 134, 113 and 129
+// for 32 users of 64 tokens with a window of 128; for single tokens: 88, 82.5, 83 and 81 us for 64
+// users up to 8K.)
 constexpr int kUnitCost = 2;
 
 // Softmax. The running maximum m of a row is one of its products s = q . row, unscaled, and a weight
 // is exp2((s - m) c), c = scale log2(e): the largest key's is 1 whatever the size of s c. (With
 // m = fl(s c) and exp2(fma(s, c, -m)) it is off by 2 to half an ulp of m, a factor that cancels in
 // the division by the sum but is zero or infinite from |m| = 2^31 on.)
+//
+// Two roundings to bf16 are by choice: of the weights and of the rotated dims of the queries, which
+// were bf16 when they came in. Both operands of a product have one type, and the rows of the cache
+// are bf16; with the weights and rows in tf32 every tile would take twice the shared memory at half
+// the rate. The sums of weights take the rounded values, so the weights still add up to one, and
+// sums, maxima and outputs stay in fp32 up to the store. An output is off by 0.0018 to 0.0022 of its
+// size (2-norm) where rounding it alone gives 0.0017.
 constexpr float kRescale = 8.0f;          // log2 units the running maximum may lag behind
 constexpr float kNoMax = -3.4028235e38f;  // the maximum of a row that has seen no key: the lowest
                                           // finite value, so that (masked) -inf minus it stays
@@ -96,8 +103,10 @@ __device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
     return a / b;
 }
 
-// sum_{i < n} floor((a + d i) / 128) for a, d >= 0 (the Euclid-like reduction of such sums; its
-// first step, and the only one of many where d is a power of two, divides by 128).
+// sum_{i < n} floor((a + d i) / 128) for a, d >= 0: the whole parts of the slope and the offset in
+// closed form, the rest counted along the other axis, where slope and offset are smaller (Graham,
+// Knuth and Patashnik, Concrete Mathematics, section 3.5, repeated as in Euclid's algorithm). The
+// first step, and the only one of many where d is a power of two, divides by 128.
 static __device__ __noinline__ int64_t floor_sum(int64_t n, int64_t a, int64_t d) {
     if (n <= 0) return 0;
     int64_t ans = (n - 1) * n / 2 * (d >> 7) + n * (a >> 7);
