@@ -2,8 +2,10 @@
 
 Argument marshalling only: every step of the path runs in the library's CUDA
 kernels. Tensors are torch CUDA tensors (their data pointers are passed);
-``stream`` defaults to torch's current stream. A non-zero return code raises
-DsaError. If libdsa.so cannot be built or loaded, every call raises.
+``stream`` defaults to torch's current stream; with another one, the caller orders
+it after the work that made the tensors and keeps them alive until it is done. A
+non-zero return code raises DsaError. If libdsa.so cannot be built or loaded, every
+call raises.
 """
 from __future__ import annotations
 

@@ -340,8 +340,8 @@ int dsa_index_score_topk_noalloc(const void *q_idx, const float *w, const void *
 
 /*
  * The paged cache of a ragged batch, as dsa_paged_append and dsa_paged_attn take it. The
- * pages have no counterpart to these two calls: they are additions of this library, for many
- * sequences served at once: their layers that attend over the local window alone, and layers
+ * pages have no counterpart to these two calls. They are additions of this library for many
+ * sequences served at once, in layers that attend over the local window alone and in layers
  * with rows of this kind that attend over the whole context (the pages name no such layer).
  *
  *   pages [n_pages] of [page_size, 512] bf16, page_stride elements from one page to the next
@@ -364,8 +364,9 @@ int dsa_index_score_topk_noalloc(const void *q_idx, const float *w, const void *
  * These arrays (all but the sizes) are read on the device when the kernels run, so a captured
  * graph replays with the lengths they hold then. A sequence whose numbers cannot be
  * (new_start decreasing, negative or beyond n_new; seq_len < n_s, > max_pages*page_size,
- * > n_pos or > DSA_MAX_PAGED_TOKENS) is skipped whole: its rows are not written, and DSA_ERR_BOUNDS goes to dev_status. (Where starts that
- * decrease give one row to two sequences of possible numbers, either may have it.)
+ * > n_pos or > DSA_MAX_PAGED_TOKENS) is skipped whole: its rows are not written, and
+ * DSA_ERR_BOUNDS goes to dev_status. (Where starts that decrease give one row to two sequences of
+ * possible numbers, either may have it.)
  * A needed page_table entry outside [0, n_pages) is reported the same way and its rows are
  * left out (not written by the append, not seen by the attention).
  */
