@@ -414,6 +414,10 @@ int dsa_paged_append(const void *kv, int64_t n_new, const int32_t *new_start,
  * -inf the elements at the infinity's place are unspecified. Logits may have any size: the products
  * q . row are held in fp32 and weights taken from their differences (a product beyond fp32's
  * range counts as an infinity in its row).
+ * Launch shape: one CTA per SM, all keys of the batch cut evenly over them, and a join of what
+ * was cut. Units of 64 rows of q, or of 128 where n_new*heads > 256*n_seqs and q and out begin on
+ * 32 bytes (decided from the arguments, so a captured graph keeps it); both are right for every
+ * batch and differ by rounding only. The same call gives the same bits.
  * Sizes that would allow one SM 2^31 blocks of 128 keys (2.5 million units of 64 or 128 rows of q
  * over sequences of DSA_MAX_PAGED_TOKENS: hours) get DSA_ERR_SHAPE.
  * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE, DSA_ERR_SCRATCH, DSA_ERR_CUDA.
