@@ -6,7 +6,7 @@ position, writes the KV rows into pages in 4 bits, reads rows back where a packe
 and attends over the pages: the whole context, or a sliding window and the first few tokens.
 
 A row of the cache is 384 bytes: 448 elements in 4 bits with a scale per 16, and the 64 rotated
-ones in bf16. With A the row's largest of the 448 magnitudes and E = floor(log2 A) - 10 (-124 at
+ones in bf16. With A the row's largest of the 448 magnitudes and E = floor(log2 A) - 10 (-123 at
 least), a group's scale is s = amax / 7 / 2^E in e4m3 and an element n = x / (s 2^E) rounded to a
 whole number of -7 .. 7, ties to even; it stands for n s 2^E. Twelve 32-byte places hold
   bytes 32 j + 16 h + ..: half h (32 dims) of chunk c (64 dims)
@@ -139,7 +139,7 @@ def _pack(x):
     v = x[:, :NOPE].float()
     group = v.view(n, NOPE // GROUP, GROUP).abs().amax(-1)
     top = group.amax(-1, keepdim=True)
-    e = ((top.view(torch.int32) >> 23) - 127).clamp(min=-114)     # of the row
+    e = ((top.view(torch.int32) >> 23) - 127).clamp(min=-113)     # of the row
     # (tensors: a division by a number may be a product with its reciprocal)
     s = (_times_two(group, 10 - e) / torch.full_like(group, 7)).to(torch.float8_e4m3fn)
     unit = s.float().repeat_interleave(GROUP, 1)
@@ -378,7 +378,7 @@ def _exact_row(x):
     """What a row [n, 512] float64 stands for in the cache: from the definition, in float64."""
     g = x[:, :NOPE].reshape(-1, NOPE // GROUP, GROUP)
     amax = g.abs().amax(-1)
-    e = (torch.frexp(amax.amax(-1)).exponent - 1).clamp(min=-114)
+    e = (torch.frexp(amax.amax(-1)).exponent - 1).clamp(min=-113)
     s = amax / torch.full_like(amax, 7) * _power(10 - e)[:, None]
     # e4m3: steps of 2^-3 of the power of two below, 2^-9 at least
     step = _power((torch.frexp(s).exponent - 1).clamp(min=-6) - 3)
