@@ -26,10 +26,12 @@ DSA_ERR_BOUNDS, DSA_ERR_RAW_RANGE = -9, -10
 EXPORTS = ("dsa_pool_append", "dsa_score_scratch_bytes", "dsa_index_score_topk",
            "dsa_window_sparse_attn", "dsa_prefill_chunk", "dsa_strerror",
            "dsa_index_score_topk_noalloc", "dsa_bounded_wait_selftest", "dsa_prefill_chunk_host",
-           "dsa_paged_append", "dsa_paged_attn")
+           "dsa_paged_append", "dsa_paged_attn", "dsa_qk_norm_rope", "dsa_paged_q4_append",
+           "dsa_paged_q4_read", "dsa_paged_q4_attn")
 DSA_STATIC_SCRATCH_BYTES = 16 << 20
 DSA_PAGED_WORKSPACE_BYTES = 40 << 20
 ROPE_DIM, MAX_PAGE_SIZE, MAX_PAGED_HEADS, MAX_PAGED_TOKENS = 64, 1024, 128, 1 << 24
+Q4_ROW_BYTES, MAX_SINKS = 384, 128
 
 
 class DsaError(RuntimeError):
@@ -82,11 +84,18 @@ def load(path: str | None = None):
     lib.dsa_paged_append.argtypes = [P, i64, P, P, i32, P, i32, P, i64, i64, i32, P, i64, P, P]
     lib.dsa_paged_attn.argtypes = [P, i32, i64, P, P, i32, P, i32, P, i64, i64, i32, P, i64, i32,
                                    ctypes.c_float, P, sz, P, P, P]
+    lib.dsa_qk_norm_rope.argtypes = [P, i32, P, i64, P, P, i32, P, P, ctypes.c_float, P, i64, P, P,
+                                     P, P]
+    lib.dsa_paged_q4_append.argtypes = lib.dsa_paged_append.argtypes
+    lib.dsa_paged_q4_read.argtypes = [P, P, i32, P, i32, P, i64, i64, i32, P, i64, P, i64, P, P]
+    lib.dsa_paged_q4_attn.argtypes = [P, i32, i64, P, P, i32, P, i32, P, i64, i64, i32, P, i64, i32,
+                                      i32, i32, ctypes.c_float, P, sz, P, P, P]
     lib.dsa_strerror.argtypes = [ctypes.c_int]
     lib.dsa_strerror.restype = ctypes.c_char_p
     for f in ("dsa_pool_append", "dsa_index_score_topk", "dsa_window_sparse_attn",
               "dsa_prefill_chunk", "dsa_index_score_topk_noalloc", "dsa_bounded_wait_selftest",
-              "dsa_prefill_chunk_host", "dsa_paged_append", "dsa_paged_attn"):
+              "dsa_prefill_chunk_host", "dsa_paged_append", "dsa_paged_attn", "dsa_qk_norm_rope",
+              "dsa_paged_q4_append", "dsa_paged_q4_read", "dsa_paged_q4_attn"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -269,7 +278,7 @@ def dsa_prefill_chunk_host(state: "PoolState", ws: PrefillWorkspace, raw_kv_h, r
     _check(rc, "dsa_prefill_chunk_host")
 
 
-_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # absent from CPU builds
 
 
@@ -283,37 +292,47 @@ def _refuse(where: str, name: str, dtype, want: str, device):
                                 f"cuda:{device}")
 
 
-def _paged(where: str, new_start, seq_len, page_table, pages, cos_sin, device):
-    """The arguments both paged calls share, checked, in the ABI's order."""
-    table, shape, strides = page_table.shape, pages.shape, pages.stride()
-    if not (len(table) == 2 and page_table.dtype is _I32 and page_table.get_device() == device
-            and page_table.is_contiguous()):
-        _refuse(where, "page_table", _I32, "*, *", device)
-    n_seqs, max_pages = table
+def _angles(where: str, cos_sin, device):
+    """(address, positions) of the table of angles."""
+    if cos_sin is None:
+        return None, 0
+    n_pos = cos_sin.shape[0] if cos_sin.dim() else 0
+    if not (cos_sin.shape == (n_pos, ROPE_DIM // 2, 2) and cos_sin.dtype is _F32
+            and cos_sin.get_device() == device and cos_sin.is_contiguous()):
+        _refuse(where, "cos_sin", _F32, f"*, {ROPE_DIM // 2}, 2", device)
+    return cos_sin.data_ptr(), n_pos
+
+
+def _starts(where: str, new_start, seq_len, n_seqs, device):
     if not (new_start.shape == (n_seqs + 1,) and new_start.dtype is _I32
             and new_start.get_device() == device and new_start.is_contiguous()):
         _refuse(where, "new_start", _I32, n_seqs + 1, device)
     if not (seq_len.shape == (n_seqs,) and seq_len.dtype is _I32
             and seq_len.get_device() == device and seq_len.is_contiguous()):
         _refuse(where, "seq_len", _I32, n_seqs, device)
-    if not (len(shape) == 3 and shape[2] == DIM and strides[2] == 1 and strides[1] == DIM
-            and pages.dtype is _BF16 and pages.get_device() == device):
-        raise DsaError(DSA_ERR_ARG, f"{where}: pages has to be a {_BF16} tensor "
-                                    f"[*, *, {DIM}] on cuda:{device} with packed pages")
+
+
+def _paged(where: str, new_start, seq_len, page_table, pages, cos_sin, device, width=DIM,
+           dtype=_BF16):
+    """The arguments the paged calls share, checked, in the ABI's order. A row of the pages is
+    `width` elements of `dtype`."""
+    table, shape, strides = page_table.shape, pages.shape, pages.stride()
+    if not (len(table) == 2 and page_table.dtype is _I32 and page_table.get_device() == device
+            and page_table.is_contiguous()):
+        _refuse(where, "page_table", _I32, "*, *", device)
+    n_seqs, max_pages = table
+    _starts(where, new_start, seq_len, n_seqs, device)
+    if not (len(shape) == 3 and shape[2] == width and strides[2] == 1 and strides[1] == width
+            and pages.dtype is dtype and pages.get_device() == device):
+        raise DsaError(DSA_ERR_ARG, f"{where}: pages has to be a {dtype} tensor "
+                                    f"[*, *, {width}] on cuda:{device} with packed pages")
     n_pages, page_size, _ = shape
     if (n_seqs | max_pages | page_size) >> 31:   # ctypes would drop the upper bits
         raise DsaError(DSA_ERR_SHAPE, f"{where}: {n_seqs} sequences of {max_pages} pages of "
                                       f"{page_size} rows are no 32-bit counts")
-    angles, n_pos = None, 0
-    if cos_sin is not None:
-        n_pos = cos_sin.shape[0] if cos_sin.dim() else 0
-        if not (cos_sin.shape == (n_pos, ROPE_DIM // 2, 2) and cos_sin.dtype is _F32
-                and cos_sin.get_device() == device and cos_sin.is_contiguous()):
-            _refuse(where, "cos_sin", _F32, f"*, {ROPE_DIM // 2}, 2", device)
-        angles = cos_sin.data_ptr()
     return (new_start.data_ptr(), seq_len.data_ptr(), n_seqs, page_table.data_ptr(), max_pages,
-            pages.data_ptr(), n_pages, strides[0] if n_pages > 1 else page_size * DIM, page_size,
-            angles, n_pos)
+            pages.data_ptr(), n_pages, strides[0] if n_pages > 1 else page_size * width, page_size,
+            *_angles(where, cos_sin, device))
 
 
 def _status(where: str, dev_status, device):
@@ -365,4 +384,96 @@ def dsa_paged_attn(q, new_start, seq_len, page_table, pages, window: int, scale:
         *_paged(where, new_start, seq_len, page_table, pages, cos_sin, dev), window, scale,
         workspace.data_ptr(), _nbytes(workspace), out.data_ptr(),
         _status(where, dev_status, dev), _stream_of(stream, dev))
+    _check(rc, where)
+
+
+def _rows(where: str, name: str, t, device, shape=None):
+    """A packed bf16 tensor [*, 512] or [*, *, 512], of `shape` where one is given."""
+    have = t.shape
+    if not ((have == shape if shape is not None else len(have) == 2 and have[1] == DIM)
+            and t.dtype is _BF16 and t.get_device() == device and t.is_contiguous()):
+        _refuse(where, name, _BF16, ", ".join(map(str, shape or ("*", DIM))), device)
+
+
+def dsa_qk_norm_rope(q, kv, new_start, seq_len, q_out, kv_out, cos_sin=None, q_weight=None,
+                     kv_weight=None, eps: float = 1e-6, dev_status=None, stream=None) -> None:
+    """Normalise the new tokens' query heads q [n_new, heads, 512] and rows kv [n_new, 512] and
+    rotate them by position into q_out and kv_out (which may be q and kv). Weights are fp32 [512]
+    or None. Tensors are on the current device; see include/dsa.h."""
+    where = "dsa_qk_norm_rope"
+    dev = torch.cuda.current_device()
+    shape = q.shape
+    if not (len(shape) == 3 and shape[2] == DIM and q.dtype is _BF16 and q.get_device() == dev
+            and q.is_contiguous()):
+        _refuse(where, "q", _BF16, f"*, *, {DIM}", dev)
+    _rows(where, "kv", kv, dev, (shape[0], DIM))
+    _rows(where, "q_out", q_out, dev, tuple(shape))
+    _rows(where, "kv_out", kv_out, dev, (shape[0], DIM))
+    for name, w in (("q_weight", q_weight), ("kv_weight", kv_weight)):
+        if w is not None and not (w.shape == (DIM,) and w.dtype is _F32 and w.get_device() == dev
+                                  and w.is_contiguous()):
+            _refuse(where, name, _F32, DIM, dev)
+    n_seqs = seq_len.shape[0] if seq_len.dim() else 0
+    _starts(where, new_start, seq_len, n_seqs, dev)
+    if (n_seqs | shape[1]) >> 31:   # ctypes would drop the upper bits
+        raise DsaError(DSA_ERR_SHAPE, f"{where}: {n_seqs} sequences or {shape[1]} heads are no "
+                                      "32-bit counts")
+    rc = (_lib or load()).dsa_qk_norm_rope(
+        q.data_ptr(), shape[1], kv.data_ptr(), shape[0], new_start.data_ptr(), seq_len.data_ptr(),
+        n_seqs, _p(q_weight), _p(kv_weight), eps, *_angles(where, cos_sin, dev), q_out.data_ptr(),
+        kv_out.data_ptr(), _status(where, dev_status, dev), _stream_of(stream, dev))
+    _check(rc, where)
+
+
+def dsa_paged_q4_append(kv, new_start, seq_len, page_table, pages, cos_sin=None, dev_status=None,
+                        stream=None) -> None:
+    """dsa_paged_append into pages [n_pages, page_size, 384] uint8 of 4-bit rows. Tensors are on
+    the current device; see include/dsa.h."""
+    where = "dsa_paged_q4_append"
+    dev = torch.cuda.current_device()
+    _rows(where, "kv", kv, dev)
+    rc = (_lib or load()).dsa_paged_q4_append(
+        kv.data_ptr(), kv.shape[0],
+        *_paged(where, new_start, seq_len, page_table, pages, cos_sin, dev, Q4_ROW_BYTES, _U8),
+        _status(where, dev_status, dev), _stream_of(stream, dev))
+    _check(rc, where)
+
+
+def dsa_paged_q4_read(new_start, seq_len, page_table, pages, out, cos_sin=None, dev_status=None,
+                      stream=None) -> None:
+    """What the sequences' 4-bit rows stand for into out [n_new, 512] bf16, turned back with
+    cos_sin. Tensors are on the current device; see include/dsa.h."""
+    where = "dsa_paged_q4_read"
+    dev = torch.cuda.current_device()
+    _rows(where, "out", out, dev)
+    rc = (_lib or load()).dsa_paged_q4_read(
+        *_paged(where, new_start, seq_len, page_table, pages, cos_sin, dev, Q4_ROW_BYTES, _U8),
+        out.data_ptr(), out.shape[0], _status(where, dev_status, dev), _stream_of(stream, dev))
+    _check(rc, where)
+
+
+def dsa_paged_q4_attn(q, new_start, seq_len, page_table, pages, window: int, sinks: int,
+                      scale: float, workspace, out, cos_sin=None, q_turned: bool = False,
+                      dev_status=None, stream=None) -> None:
+    """Attention of the new tokens q [n_new, heads, 512] over their sequences' 4-bit rows into
+    out: all of them (window 0), or the last `window` and the first `sinks`. q_turned: q comes
+    turned by its positions. `workspace` as for dsa_paged_attn. Tensors are on the current device;
+    see include/dsa.h."""
+    where = "dsa_paged_q4_attn"
+    dev = torch.cuda.current_device()
+    shape = q.shape
+    if not (len(shape) == 3 and shape[2] == DIM and q.dtype is _BF16 and q.get_device() == dev
+            and q.is_contiguous()):
+        _refuse(where, "q", _BF16, f"*, *, {DIM}", dev)
+    _rows(where, "out", out, dev, tuple(shape))
+    if not (workspace.get_device() == dev and workspace.is_contiguous()):
+        _refuse(where, "workspace", workspace.dtype, "*", dev)
+    if (window | sinks | shape[1]) >> 31:   # ctypes would drop the upper bits
+        raise DsaError(DSA_ERR_SHAPE, f"{where}: window {window}, sinks {sinks} or heads "
+                                      f"{shape[1]} is no 32-bit count")
+    rc = (_lib or load()).dsa_paged_q4_attn(
+        q.data_ptr(), shape[1], shape[0],
+        *_paged(where, new_start, seq_len, page_table, pages, cos_sin, dev, Q4_ROW_BYTES, _U8),
+        window, sinks, bool(q_turned), scale, workspace.data_ptr(), _nbytes(workspace),
+        out.data_ptr(), _status(where, dev_status, dev), _stream_of(stream, dev))
     _check(rc, where)

@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdsa.so")
 SOURCES = ["pool.cu", "score_topk.cu", "attn.cu", "prefill.cu", "diag.cu", "paged.cu",
-           "paged_attn.cu", "paged_chunk.cu"]
+           "paged_attn.cu", "paged_chunk.cu", "norm.cu", "q4.cu", "q4_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -22,39 +22,6 @@ namespace {
 
 constexpr int kAppendWarps = 8;
 
-// The sequence that holds row r: the last s with new_start[s] <= r (0 when there is none).
-// One round looks at 32 evenly spaced entries, so 1,024 sequences take two rounds.
-__device__ __forceinline__ int find_seq(const PagedBatch &b, int64_t r, int lane) {
-    int lo = 0, hi = b.n_seqs;  // new_start[lo] <= r (taken for lo = 0), r < new_start[hi]
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) >> 5;
-        const int s = lo + lane * step;
-        const bool le = s < hi && __ldg(b.new_start + s) <= r;
-        const uint32_t m = __ballot_sync(0xFFFFFFFFu, le) | 1u;
-        const int k = 31 - __clz(m);
-        lo += k * step;
-        hi = min(hi, lo + step);
-    }
-    return lo;
-}
-
-__device__ __forceinline__ bool holds(const PagedSeq &q, int64_t r) {
-    return r >= q.row0 && r < int64_t{q.row0} + q.n;
-}
-
-// The same by looking at every sequence: the last one that holds row r, -1 when none does. For
-// rows of padding, and for starts that decrease somewhere, among which find_seq may miss the
-// sequence whose numbers are right.
-__device__ __forceinline__ int find_seq_any(const PagedBatch &b, int64_t r, int lane) {
-    int at = -1;
-#pragma unroll 1
-    for (int s = lane; s < b.n_seqs; s += 32) {
-        bool bad;
-        if (holds(paged_seq(b, s, bad), r)) at = s;
-    }
-    return __reduce_max_sync(0xFFFFFFFFu, at);
-}
-
 // One warp per row; lane l moves 16-byte pieces l and l + 32, and the last eight pieces
 // hold the rotated pairs. The bound keeps it at 32 registers, eight CTAs an SM (with 38, six
 // CTAs: 25.6 instead of 23.6 us for 56,436 rows from a cold L2).
@@ -104,52 +71,59 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 2048 / (kAppendWarps * 32))
     dst[32] = v1;
 }
 
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
 }  // namespace
 
-int check_paged_batch(int64_t n_new, const int32_t *new_start, const int32_t *seq_len,
-                      int32_t n_seqs, const int32_t *page_table, int32_t max_pages,
-                      const void *pages, int64_t n_pages, int64_t page_stride, int32_t page_size,
-                      const float *cos_sin, int64_t n_pos, PagedBatch *b) {
-    if (!new_start || !seq_len || !page_table || !pages) return DSA_ERR_ARG;
-    if (n_new <= 0 || n_seqs <= 0 || max_pages <= 0 || n_pages <= 0) return DSA_ERR_ARG;
-    if (!aligned4(new_start) || !aligned4(seq_len) || !aligned4(page_table) ||
-        !aligned16(pages) || !aligned16(cos_sin))
-        return DSA_ERR_ARG;
+int check_batch(int64_t n_new, const int32_t *new_start, const int32_t *seq_len, int32_t n_seqs,
+                const float *cos_sin, int64_t n_pos, PagedBatch *b) {
+    if (!new_start || !seq_len || n_new <= 0 || n_seqs <= 0) return DSA_ERR_ARG;
+    if (!aligned4(new_start) || !aligned4(seq_len) || !aligned16(cos_sin)) return DSA_ERR_ARG;
     if (cos_sin && n_pos <= 0) return DSA_ERR_ARG;
-    if (page_size < 16 || page_size > DSA_MAX_PAGE_SIZE || (page_size & (page_size - 1)) != 0)
-        return DSA_ERR_SHAPE;
-    // a page stride is a byte stride of the tensor map: a multiple of 16 below 2^40
-    if (page_stride < int64_t{page_size} * kD || page_stride % 8 != 0 ||
-        page_stride >= (int64_t{1} << 39))
-        return DSA_ERR_SHAPE;
-    const int64_t limit = (int64_t{1} << 31) - 1;
-    if (n_new > limit || n_pages > limit || int64_t{max_pages} * page_size > limit)
-        return DSA_ERR_SHAPE;
     // the kernels' walks over the sequences step past the last one, in 32 bits
-    if (n_seqs > DSA_MAX_PAGED_SEQS) return DSA_ERR_SHAPE;
+    if (n_new > (int64_t{1} << 31) - 1 || n_seqs > DSA_MAX_PAGED_SEQS) return DSA_ERR_SHAPE;
     b->new_start = new_start;
     b->seq_len = seq_len;
-    b->page_table = page_table;
     b->cos_sin = cos_sin;
     b->n_new = n_new;
-    b->page_stride = page_stride;
     b->n_seqs = n_seqs;
-    b->max_pages = max_pages;
-    b->n_pages = static_cast<int32_t>(n_pages);
-    b->page_shift = 0;
-    while ((1 << b->page_shift) < page_size) ++b->page_shift;
-    int64_t len = std::min(int64_t{max_pages} * page_size, int64_t{DSA_MAX_PAGED_TOKENS});
+    int64_t len = DSA_MAX_PAGED_TOKENS;
     if (cos_sin) len = std::min(len, n_pos);
     b->len_limit = static_cast<int32_t>(len);
     return DSA_OK;
 }
 
-bool touches_pages(const PagedBatch &b, const void *pages, const void *p, uint64_t bytes) {
+int check_paged_batch(int64_t n_new, const int32_t *new_start, const int32_t *seq_len,
+                      int32_t n_seqs, const int32_t *page_table, int32_t max_pages,
+                      const void *pages, int64_t n_pages, int64_t page_stride, int32_t page_size,
+                      const float *cos_sin, int64_t n_pos, PagedBatch *b, PageRow row) {
+    // (null pointers, counts and alignments of all arguments before any limit)
+    if (!page_table || !pages || max_pages <= 0 || n_pages <= 0) return DSA_ERR_ARG;
+    if (!aligned4(page_table) || !aligned16(pages)) return DSA_ERR_ARG;
+    const int rc = check_batch(n_new, new_start, seq_len, n_seqs, cos_sin, n_pos, b);
+    if (rc != DSA_OK) return rc;
+    if (page_size < 16 || page_size > DSA_MAX_PAGE_SIZE || (page_size & (page_size - 1)) != 0)
+        return DSA_ERR_SHAPE;
+    // a page stride is a byte stride of the tensor map: a multiple of 16 below 2^40
+    if (page_stride < int64_t{page_size} * row.size || page_stride % (16 / row.unit) != 0 ||
+        page_stride >= (int64_t{1} << 39))
+        return DSA_ERR_SHAPE;
+    const int64_t limit = (int64_t{1} << 31) - 1;
+    if (n_pages > limit || int64_t{max_pages} * page_size > limit) return DSA_ERR_SHAPE;
+    b->page_table = page_table;
+    b->page_stride = page_stride;
+    b->max_pages = max_pages;
+    b->n_pages = static_cast<int32_t>(n_pages);
+    b->page_shift = 0;
+    while ((1 << b->page_shift) < page_size) ++b->page_shift;
+    b->len_limit = static_cast<int32_t>(
+        std::min(int64_t{max_pages} * page_size, int64_t{b->len_limit}));
+    return DSA_OK;
+}
+
+bool touches_pages(const PagedBatch &b, const void *pages, const void *p, uint64_t bytes,
+                   PageRow row) {
     const uint64_t base = reinterpret_cast<uintptr_t>(pages), at = reinterpret_cast<uintptr_t>(p);
-    const uint64_t stride = static_cast<uint64_t>(b.page_stride) * 2;
-    const uint64_t page = (uint64_t{kD} * 2) << b.page_shift;
+    const uint64_t stride = static_cast<uint64_t>(b.page_stride) * row.unit;
+    const uint64_t page = static_cast<uint64_t>(row.size) * row.unit << b.page_shift;
     // the first page that ends behind `at`: does it begin before the end?
     const uint64_t k = at < base + page ? 0 : (at - base - page) / stride + 1;
     return k < static_cast<uint64_t>(b.n_pages) && base + k * stride < at + bytes;

@@ -19,21 +19,44 @@ struct PagedBatch {
     const int32_t *page_table;  // [n_seqs, max_pages]
     const float *cos_sin;       // [n_pos, 32, 2] or null
     int64_t n_new;              // rows of the new tokens' arrays
-    int64_t page_stride;        // elements
+    int64_t page_stride;        // elements (bytes where a row is in 4 bits)
     int32_t n_seqs, max_pages;
     int32_t n_pages;
     int32_t page_shift;         // log2(rows of a page)
     int32_t len_limit;          // longest sequence the table (and cos_sin) can hold
 };
 
-// Checks every argument the two calls share and fills `b`; DSA_OK or a DSA_ERR_* code.
+// A row of the pages as their stride counts it: `size` units of `unit` bytes, pages on 16 bytes.
+struct PageRow {
+    int32_t size, unit;
+};
+constexpr PageRow kBf16Row = {kD, 2};
+constexpr PageRow kQ4PageRow = {DSA_Q4_ROW_BYTES, 1};
+
+// Checks the arguments that say which rows belong to which sequence at which positions, and fills
+// that part of `b` (a sequence may be as long as there are angles, or DSA_MAX_PAGED_TOKENS); DSA_OK
+// or a DSA_ERR_* code.
+int check_batch(int64_t n_new, const int32_t *new_start, const int32_t *seq_len, int32_t n_seqs,
+                const float *cos_sin, int64_t n_pos, PagedBatch *b);
+
+// Checks every argument the paged calls share and fills `b`; DSA_OK or a DSA_ERR_* code.
 int check_paged_batch(int64_t n_new, const int32_t *new_start, const int32_t *seq_len,
                       int32_t n_seqs, const int32_t *page_table, int32_t max_pages,
                       const void *pages, int64_t n_pages, int64_t page_stride, int32_t page_size,
-                      const float *cos_sin, int64_t n_pos, PagedBatch *b);
+                      const float *cos_sin, int64_t n_pos, PagedBatch *b,
+                      PageRow row = kBf16Row);
 
 // Whether [p, p + bytes) touches a page (between pages lies what the caller likes).
-bool touches_pages(const PagedBatch &b, const void *pages, const void *p, uint64_t bytes);
+bool touches_pages(const PagedBatch &b, const void *pages, const void *p, uint64_t bytes,
+                   PageRow row = kBf16Row);
+
+inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Whether [a, a + na) and [b, b + nb) share a byte.
+inline bool overlaps(const void *a, uint64_t na, const void *b, uint64_t nb) {
+    const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
 
 bool make_tmap_pages(CUtensorMap *map, const void *pages, const PagedBatch &b);
 
@@ -49,6 +72,39 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatch &b, int s, bool &
     const int32_t len = __ldg(b.seq_len + s);
     bad = r0 < 0 || r1 < r0 || r1 > b.n_new || len < r1 - r0 || len > b.len_limit;
     return PagedSeq{r0, bad ? 0 : r1 - r0, len};
+}
+
+// The sequence that holds row r: the last s with new_start[s] <= r (0 when there is none).
+// One round looks at 32 evenly spaced entries, so 1,024 sequences take two rounds.
+__device__ __forceinline__ int find_seq(const PagedBatch &b, int64_t r, int lane) {
+    int lo = 0, hi = b.n_seqs;  // new_start[lo] <= r (taken for lo = 0), r < new_start[hi]
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) >> 5;
+        const int s = lo + lane * step;
+        const bool le = s < hi && __ldg(b.new_start + s) <= r;
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, le) | 1u;
+        const int k = 31 - __clz(m);
+        lo += k * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
+}
+
+__device__ __forceinline__ bool holds(const PagedSeq &q, int64_t r) {
+    return r >= q.row0 && r < int64_t{q.row0} + q.n;
+}
+
+// The same by looking at every sequence: the last one that holds row r, -1 when none does. For
+// rows of padding, and for starts that decrease somewhere, among which find_seq may miss the
+// sequence whose numbers are right.
+__device__ __forceinline__ int find_seq_any(const PagedBatch &b, int64_t r, int lane) {
+    int at = -1;
+#pragma unroll 1
+    for (int s = lane; s < b.n_seqs; s += 32) {
+        bool bad;
+        if (holds(paged_seq(b, s, bad), r)) at = s;
+    }
+    return __reduce_max_sync(0xFFFFFFFFu, at);
 }
 
 // A pair (x, y) turned by an angle, in fp32 and rounded to bf16 once.

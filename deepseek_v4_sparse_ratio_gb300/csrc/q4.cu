@@ -1,0 +1,219 @@
+// dsa_paged_q4_append and dsa_paged_q4_read: KV rows of a ragged batch into pages of 4-bit rows,
+// and back.
+//
+// A row of 512 bf16 becomes 384 bytes (the header has the layout): 448 whole numbers n of -7 .. 7,
+// a scale s in e4m3 for each 16, a power of two 2^E for the row, x ~ n s 2^E; and the 64 rotated
+// dims in bf16. Both calls take one warp per row, as the bf16 append does, and are bound by HBM
+// (1,408 bytes a row), or by the launch up to a few thousand rows.
+#include <math.h>
+
+#include "common.cuh"
+#include "paged.h"
+#include "q4.h"
+
+namespace dsa {
+
+namespace {
+
+constexpr int kQ4Warps = 8;
+constexpr uint32_t kQ4Limit = (124u + 127u) << 23;  // the bits of 2^124
+constexpr int kQ4LeastExp = -113;
+
+// The row of the pages that holds position p of sequence s; null (and a report) for a bad entry.
+__device__ __forceinline__ uint8_t *row_of(const PagedBatch &b, uint8_t *pages, int s, int32_t p,
+                                           int lane, int32_t *status) {
+    const int32_t page = __ldg(b.page_table + int64_t{s} * b.max_pages + (p >> b.page_shift));
+    if (page < 0 || page >= b.n_pages) {
+        if (lane == 0) report(status, DSA_ERR_BOUNDS);
+        return nullptr;
+    }
+    return pages + page * b.page_stride + int64_t{p & ((1 << b.page_shift) - 1)} * kQ4Row;
+}
+
+__device__ __forceinline__ void report_bad(const PagedBatch &b, int32_t *status) {
+    if (blockIdx.x != 0) return;
+    for (int s = threadIdx.x; s < b.n_seqs; s += blockDim.x) {
+        bool bad;
+        paged_seq(b, s, bad);
+        if (bad) report(status, DSA_ERR_BOUNDS);
+    }
+}
+
+// The sequence and position of row r; false where it belongs to none.
+__device__ __forceinline__ bool find_row(const PagedBatch &b, int64_t r, int lane, int &s,
+                                         int32_t &p) {
+    s = find_seq(b, r, lane);
+    bool bad;
+    PagedSeq q = paged_seq(b, s, bad);
+    if (!holds(q, r)) {
+        s = find_seq_any(b, r, lane);
+        if (s < 0) return false;
+        q = paged_seq(b, s, bad);
+    }
+    p = q.len - q.n + static_cast<int32_t>(r - q.row0);
+    return true;
+}
+
+// Lane l has dims 16 l ..: a group of the 448, or (lanes 28 to 31) a quarter of the rotated ones.
+__global__ void __launch_bounds__(kQ4Warps * 32)
+    q4_append_kernel(const PagedBatch b, const uint4 *kv, uint8_t *pages, int32_t *status) {
+    wait_before();
+    const int lane = threadIdx.x & 31;
+    const int64_t r = int64_t{blockIdx.x} * kQ4Warps + (threadIdx.x >> 5);
+    report_bad(b, status);
+    if (r >= b.n_new) return;
+    const uint4 *src = kv + r * (kD / 8) + 2 * lane;
+    const uint4 v0 = __ldg(src), v1 = __ldg(src + 1);
+    int s;
+    int32_t p;
+    if (!find_row(b, r, lane, s, p)) return;
+    uint8_t *row = row_of(b, pages, s, p, lane, status);
+    if (!row) return;
+    uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    const bool rope = lane >= 28;
+    // magnitudes as the bits of an fp32: whole numbers in the same order, NaN above all
+    uint32_t amax = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        amax = max(amax, max((w[k] << 16) & 0x7FFF0000u, w[k] & 0x7FFF0000u));
+    const bool finite = amax < kQ4Limit;
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, rope || !finite ? 0u : amax);
+    const int e = max(static_cast<int>(top >> 23) - 127, kQ4LeastExp);
+    const float up = pow2(10 - e);
+    // 0 <= amax 2^-E / 7 < 293; the division's rounding never meets a border of e4m3 (amax has
+    // eight significant bits, seven times a border as well)
+    const uint32_t scale =
+        finite ? __nv_cvt_float_to_fp8(__uint_as_float(amax) * up / 7.0f, __NV_SATFINITE,
+                                       __NV_E4M3)
+               : 0x7Fu;
+    if (!rope) {
+        const float unit = finite ? e4m3(scale) : 0.0f;
+        uint32_t code[2] = {0, 0};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            // (quotients that end in a half are exact: ties go to even numbers)
+            const float x0 = bf16lo(w[k]) * up / unit, x1 = bf16hi(w[k]) * up / unit;
+            const int n0 = unit > 0.0f ? max(-7, min(7, __float2int_rn(x0))) : 0;
+            const int n1 = unit > 0.0f ? max(-7, min(7, __float2int_rn(x1))) : 0;
+            code[k / 4] |= static_cast<uint32_t>(n0 + 8) << (4 * (k % 4));
+            code[k / 4] |= static_cast<uint32_t>(n1 + 8) << (4 * (k % 4) + 16);
+        }
+        *reinterpret_cast<uint2 *>(row + 32 + 8 * lane) = make_uint2(code[0], code[1]);
+    } else {
+        if (b.cos_sin) {
+            const float4 *cs = reinterpret_cast<const float4 *>(b.cos_sin + int64_t{p} * kRope) +
+                               (lane - 28) * 4;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 a = __ldg(cs + k);
+                w[2 * k] = turn_pair(w[2 * k], a.x, a.y);
+                w[2 * k + 1] = turn_pair(w[2 * k + 1], a.z, a.w);
+            }
+        }
+        uint4 *to = reinterpret_cast<uint4 *>(row + kQ4Rope) + 2 * (lane - 28);
+        to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    // the first 32 bytes: chunk lane / 4, half (lane / 2) % 2, group lane % 2 of the half
+    const int half = rope ? lane & 1 : (lane >> 1) & 1;
+    const int at = rope ? (lane < 30 ? 14 : 15) : 2 * (lane >> 2) + (lane & 1);
+    row[16 * half + at] = static_cast<uint8_t>(!rope ? scale : lane < 30 ? e + 127 : 0);
+}
+
+// Lane l has dims 8 l .. and 256 + 8 l ..: words l and l + 32 of the codes, or (lanes 24 to 31) an
+// eighth of the rotated dims.
+__global__ void __launch_bounds__(kQ4Warps * 32)
+    q4_read_kernel(const PagedBatch b, uint8_t *pages, uint4 *out, int32_t *status) {
+    wait_before();
+    const int lane = threadIdx.x & 31;
+    const int64_t r = int64_t{blockIdx.x} * kQ4Warps + (threadIdx.x >> 5);
+    report_bad(b, status);
+    if (r >= b.n_new) return;
+    int s;
+    int32_t p;
+    if (!find_row(b, r, lane, s, p)) return;
+    const uint8_t *row = row_of(b, pages, s, p, lane, status);
+    if (!row) return;
+    const bool rope = lane >= 24;
+    const uint32_t first = __ldg(reinterpret_cast<const uint32_t *>(row + 32) + lane);
+    uint32_t second = 0;
+    uint4 v1 = {};
+    if (rope)
+        v1 = __ldg(reinterpret_cast<const uint4 *>(row + kQ4Rope) + lane - 24);
+    else
+        second = __ldg(reinterpret_cast<const uint32_t *>(row + 32) + 32 + lane);
+    const uint32_t head = __ldg(row + lane);   // the scales, a byte a lane
+    const uint32_t exponent = __shfl_sync(0xFFFFFFFFu, head, 14);
+    auto words = [&](uint32_t code, int word) {
+        // chunk word / 8, half word / 4 % 2, group word / 2 % 2
+        const uint32_t scale = __shfl_sync(0xFFFFFFFFu, head,
+                                           (16 * ((word >> 2) & 1) + 2 * (word >> 3) +
+                                            ((word >> 1) & 1)) & 31);
+        const float u = q4_unit(scale, exponent);
+        const __nv_bfloat162 half = __float2bfloat162_rn(0.5f * u);
+        const __nv_bfloat162 off = __float2bfloat162_rn(-72.0f * u);
+        return make_uint4(q4_pair(code, 0, half, off), q4_pair(code, 1, half, off),
+                          q4_pair(code, 2, half, off), q4_pair(code, 3, half, off));
+    };
+    const uint4 v0 = words(first, lane);
+    const uint4 v2 = words(second, lane + 32);
+    if (!rope) {
+        v1 = v2;
+    } else if (b.cos_sin) {
+        const float4 *cs =
+            reinterpret_cast<const float4 *>(b.cos_sin + int64_t{p} * kRope) + (lane - 24) * 2;
+        const float4 a = __ldg(cs), c = __ldg(cs + 1);
+        v1.x = turn_pair(v1.x, a.x, -a.y);
+        v1.y = turn_pair(v1.y, a.z, -a.w);
+        v1.z = turn_pair(v1.z, c.x, -c.y);
+        v1.w = turn_pair(v1.w, c.z, -c.w);
+    }
+    uint4 *dst = out + r * (kD / 8) + lane;
+    dst[0] = v0;
+    dst[32] = v1;
+}
+
+}  // namespace
+}  // namespace dsa
+
+extern "C" int dsa_paged_q4_append(const void *kv, int64_t n_new, const int32_t *new_start,
+                                   const int32_t *seq_len, int32_t n_seqs,
+                                   const int32_t *page_table, int32_t max_pages, void *pages,
+                                   int64_t n_pages, int64_t page_stride, int32_t page_size,
+                                   const float *cos_sin, int64_t n_pos, int32_t *dev_status,
+                                   void *stream) {
+    using namespace dsa;
+    if (!kv || !aligned16(kv) || !aligned4(dev_status)) return DSA_ERR_ARG;
+    PagedBatch b;
+    const int rc = check_paged_batch(n_new, new_start, seq_len, n_seqs, page_table, max_pages,
+                                     pages, n_pages, page_stride, page_size, cos_sin, n_pos, &b,
+                                     kQ4PageRow);
+    if (rc != DSA_OK) return rc;
+    if (touches_pages(b, pages, kv, static_cast<uint64_t>(n_new) * kD * 2, kQ4PageRow))
+        return DSA_ERR_ARG;
+    const unsigned grid = static_cast<unsigned>((n_new + kQ4Warps - 1) / kQ4Warps);
+    return launch_overlapped(q4_append_kernel, grid, kQ4Warps * 32, 0,
+                             static_cast<cudaStream_t>(stream), b, static_cast<const uint4 *>(kv),
+                             static_cast<uint8_t *>(pages), dev_status);
+}
+
+extern "C" int dsa_paged_q4_read(const int32_t *new_start, const int32_t *seq_len, int32_t n_seqs,
+                                 const int32_t *page_table, int32_t max_pages, const void *pages,
+                                 int64_t n_pages, int64_t page_stride, int32_t page_size,
+                                 const float *cos_sin, int64_t n_pos, void *out, int64_t n_new,
+                                 int32_t *dev_status, void *stream) {
+    using namespace dsa;
+    if (!out || !aligned16(out) || !aligned4(dev_status)) return DSA_ERR_ARG;
+    PagedBatch b;
+    const int rc = check_paged_batch(n_new, new_start, seq_len, n_seqs, page_table, max_pages,
+                                     pages, n_pages, page_stride, page_size, cos_sin, n_pos, &b,
+                                     kQ4PageRow);
+    if (rc != DSA_OK) return rc;
+    if (touches_pages(b, pages, out, static_cast<uint64_t>(n_new) * kD * 2, kQ4PageRow))
+        return DSA_ERR_ARG;
+    const unsigned grid = static_cast<unsigned>((n_new + kQ4Warps - 1) / kQ4Warps);
+    return launch_overlapped(q4_read_kernel, grid, kQ4Warps * 32, 0,
+                             static_cast<cudaStream_t>(stream), b,
+                             static_cast<uint8_t *>(const_cast<void *>(pages)),
+                             static_cast<uint4 *>(out), dev_status);
+}

@@ -16,7 +16,12 @@
  * Beside it, for a ragged batch of sequences whose KV rows live in pages:
  *   dsa_paged_append           the new tokens' rows, rotated by position, into the pages;
  *   dsa_paged_attn             attention of the new tokens over their sequences' rows
- *                              (prompt chunks, short bands, single tokens).
+ *                              (prompt chunks, short bands, single tokens);
+ *   dsa_qk_norm_rope           the new tokens' query heads and KV rows normalised and rotated;
+ *   dsa_paged_q4_append        the KV rows into pages of 4-bit rows,
+ *   dsa_paged_q4_read          rows read back from them,
+ *   dsa_paged_q4_attn          attention over them: the whole context, or a sliding window and
+ *                              the first few tokens.
  *
  * Shapes are fixed by the model: indexer heads H_I=64 of dim d_I=128, query
  * heads H=64, one shared KV row of dim D=512 (key and value for every head),
@@ -73,6 +78,8 @@ extern "C" {
 #define DSA_MAX_PAGED_HEADS 128
 #define DSA_MAX_PAGED_TOKENS (1 << 24) /* of a sequence in pages */
 #define DSA_MAX_PAGED_SEQS (1 << 30)   /* of a ragged batch */
+#define DSA_Q4_ROW_BYTES 384    /* of a row of the 4-bit pages */
+#define DSA_MAX_SINKS 128       /* first tokens that stay visible beside a window */
 
 enum dsa_status {
     DSA_OK = 0,
@@ -428,6 +435,101 @@ int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new, const int32_t *n
                    int32_t page_size, const float *cos_sin, int64_t n_pos, int32_t window,
                    float scale, void *workspace, size_t workspace_bytes, void *out,
                    int32_t *dev_status, void *stream);
+
+/*
+ * The new tokens' query heads and KV rows normalised, and rotated by position in the same pass:
+ *   y = R(p) (x / sqrt(mean_i x_i^2 + eps) * weight)
+ * for every head of q and for kv, p the row's position. The pages have no counterpart to this
+ * call; it is an addition of this library and prepares what dsa_window_sparse_attn,
+ * dsa_paged_append, dsa_paged_q4_append and dsa_paged_q4_attn (q_turned = 1) take.
+ *   q, q_out [n_new, heads, 512] bf16, kv, kv_out [n_new, 512] bf16; q_out may be q and kv_out may
+ *   be kv (in place), and otherwise the outputs lie apart from the inputs and each other (else
+ *   DSA_ERR_ARG); heads from 1 to DSA_MAX_PAGED_HEADS;
+ *   q_weight, kv_weight [512] fp32 or NULL (ones); eps > 0 and finite;
+ *   n_new, new_start, seq_len, n_seqs, cos_sin, n_pos as for the paged calls (one sequence with
+ *   seq_len = offset + chunk for a chunk of the prefill); a sequence may be DSA_MAX_PAGED_TOKENS
+ *   long. Rows of no sequence, or of one whose numbers cannot be, are not written.
+ * In fp32, rounded to bf16 once. Elements are up to 2^59 in size: the sum of a row's squares has
+ * to be within fp32 (beyond, the row becomes zeros; a NaN in it makes it NaN).
+ * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE, DSA_ERR_CUDA.
+ */
+int dsa_qk_norm_rope(const void *q, int32_t heads, const void *kv, int64_t n_new,
+                     const int32_t *new_start, const int32_t *seq_len, int32_t n_seqs,
+                     const float *q_weight, const float *kv_weight, float eps,
+                     const float *cos_sin, int64_t n_pos, void *q_out, void *kv_out,
+                     int32_t *dev_status, void *stream);
+
+/*
+ * The paged cache in 4 bits: the same batch, page tables and positions with rows of
+ * DSA_Q4_ROW_BYTES = 384 bytes, where a bf16 row takes 1,024. The pages have no counterpart.
+ *
+ *   pages [n_pages] of [page_size] rows, page_stride BYTES from one page to the next
+ *     (>= page_size*384, a multiple of 16).
+ *   A row: its dims 0..447 in 4 bits with a scale for each 16 of them, and its last 64 dims, the
+ *   rotated ones, in bf16 (positions live there). With A the largest of the 448 magnitudes and
+ *   E = max(floor(log2 A), -113) - 10, a group of 16 has the scale s = (its largest magnitude)
+ *   / 7 / 2^E rounded to e4m3 (to nearest, ties to even; at most 288), and an element x is held
+ *   as n = x / (s 2^E) rounded to a whole number of -7 .. 7 (ties to even; 0 where s is 0). It
+ *   stands for n s 2^E, which bf16 holds exactly. (For Gaussian rows 0.086 of their size off in
+ *   the mean square; with fp4 codes of one mantissa bit in the place of whole numbers, 0.095.)
+ *   Groups down to 2^-14 of the row's largest element keep their whole precision. A group that
+ *   holds a NaN, an infinity or an element of 2^124 or more has a NaN for its scale and reads back
+ *   as NaN; the others of its row are as without it (A is taken over the others).
+ *   Bytes 32 j + 16 h .. 32 j + 16 h + 15, h = 0 and 1 the half (32 dims) of a chunk of 64 dims:
+ *     j = 0       the half's 14 scales, two a chunk; one byte E + 137; one byte 0;
+ *     j = 1 .. 7  chunk j - 1 in four words of eight dims; dim 2 k of a word is its nibble k and
+ *                 dim 2 k + 1 its nibble k + 4, as n + 8;
+ *     j = 8 .. 11 the last 64 dims in order, two bytes each.
+ */
+
+/*
+ * Append the new tokens' rows in 4 bits: dsa_paged_append with the row R(p) kv[r] written as
+ * above (the 448 dims are quantised as they come; R(p) is taken in fp32 and rounded to bf16 once).
+ *   kv [n_new, 512] bf16, apart from the pages (DSA_ERR_ARG).
+ * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE, DSA_ERR_CUDA.
+ */
+int dsa_paged_q4_append(const void *kv, int64_t n_new, const int32_t *new_start,
+                        const int32_t *seq_len, int32_t n_seqs, const int32_t *page_table,
+                        int32_t max_pages, void *pages, int64_t n_pages, int64_t page_stride,
+                        int32_t page_size, const float *cos_sin, int64_t n_pos,
+                        int32_t *dev_status, void *stream);
+
+/*
+ * Read rows back: out[r] := what the row of r's position stands for, in bf16 (exact), turned back
+ * by R(-p) with cos_sin (fp32, rounded once) and as it is held without. new_start and seq_len say
+ * which rows as they do for new tokens: out's rows new_start[s] .. are the last ones of the
+ * seq_len[s] first tokens of sequence s.
+ *   out [n_new, 512] bf16, apart from the pages (DSA_ERR_ARG). Rows of no sequence, and rows whose
+ *   page_table entry is out of range, are not written.
+ * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE, DSA_ERR_CUDA.
+ */
+int dsa_paged_q4_read(const int32_t *new_start, const int32_t *seq_len, int32_t n_seqs,
+                      const int32_t *page_table, int32_t max_pages, const void *pages,
+                      int64_t n_pages, int64_t page_stride, int32_t page_size,
+                      const float *cos_sin, int64_t n_pos, void *out, int64_t n_new,
+                      int32_t *dev_status, void *stream);
+
+/*
+ * Attention of the new tokens over their sequences' 4-bit rows: dsa_paged_attn, where the token
+ * of position t sees the rows u <= t with u > t - window or u < sinks (window > 0), or all
+ * u <= t (window = 0).
+ *   sinks: first tokens that stay visible beside a window, 0 to DSA_MAX_SINKS (no meaning
+ *   without a window);
+ *   q_turned: 1 where q comes turned by its positions (dsa_qk_norm_rope), 0 where this call turns
+ *   it; the output is turned back with cos_sin in either case, and without cos_sin nothing is
+ *   turned.
+ * The other arguments, the workspace, roundings, logits of any size and what rows that are not seen
+ * (whatever they hold) or not finite do: as for dsa_paged_attn. A token that sees no row gets
+ * zeros. The same call gives the same bits.
+ * Sizes that would allow one SM 2^31 blocks of 128 keys get DSA_ERR_SHAPE.
+ * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE, DSA_ERR_SCRATCH, DSA_ERR_CUDA.
+ */
+int dsa_paged_q4_attn(const void *q, int32_t heads, int64_t n_new, const int32_t *new_start,
+                      const int32_t *seq_len, int32_t n_seqs, const int32_t *page_table,
+                      int32_t max_pages, const void *pages, int64_t n_pages, int64_t page_stride,
+                      int32_t page_size, const float *cos_sin, int64_t n_pos, int32_t window,
+                      int32_t sinks, int32_t q_turned, float scale, void *workspace,
+                      size_t workspace_bytes, void *out, int32_t *dev_status, void *stream);
 
 /*
  * Self-check of the error path behind DSA_ERR_TIMEOUT, for failure detection.
