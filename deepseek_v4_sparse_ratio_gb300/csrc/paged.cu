@@ -97,13 +97,14 @@ int check_paged_batch(int64_t n_new, const int32_t *new_start, const int32_t *se
                       const float *cos_sin, int64_t n_pos, PagedBatch *b, PageRow row) {
     // (null pointers, counts and alignments of all arguments before any limit)
     if (!page_table || !pages || max_pages <= 0 || n_pages <= 0) return DSA_ERR_ARG;
-    if (!aligned4(page_table) || !aligned16(pages)) return DSA_ERR_ARG;
+    if (!aligned4(page_table) || reinterpret_cast<uintptr_t>(pages) % row.align != 0)
+        return DSA_ERR_ARG;
     const int rc = check_batch(n_new, new_start, seq_len, n_seqs, cos_sin, n_pos, b);
     if (rc != DSA_OK) return rc;
     if (page_size < 16 || page_size > DSA_MAX_PAGE_SIZE || (page_size & (page_size - 1)) != 0)
         return DSA_ERR_SHAPE;
-    // a page stride is a byte stride of the tensor map: a multiple of 16 below 2^40
-    if (page_stride < int64_t{page_size} * row.size || page_stride % (16 / row.unit) != 0 ||
+    // a page stride is a byte stride of the tensor map: a multiple of 16 (32) below 2^40
+    if (page_stride < int64_t{page_size} * row.size || page_stride % (row.align / row.unit) != 0 ||
         page_stride >= (int64_t{1} << 39))
         return DSA_ERR_SHAPE;
     const int64_t limit = (int64_t{1} << 31) - 1;

@@ -26,12 +26,13 @@ struct PagedBatch {
     int32_t len_limit;          // longest sequence the table (and cos_sin) can hold
 };
 
-// A row of the pages as their stride counts it: `size` units of `unit` bytes, pages on 16 bytes.
+// A row of the pages as their stride counts it: `size` units of `unit` bytes; pages begin on
+// multiples of `align` bytes.
 struct PageRow {
-    int32_t size, unit;
+    int32_t size, unit, align;
 };
-constexpr PageRow kBf16Row = {kD, 2};
-constexpr PageRow kQ4PageRow = {DSA_Q4_ROW_BYTES, 1};
+constexpr PageRow kBf16Row = {kD, 2, 16};
+constexpr PageRow kQ4PageRow = {DSA_Q4_ROW_BYTES, 1, 32};  // (read in sectors)
 
 // Checks the arguments that say which rows belong to which sequence at which positions, and fills
 // that part of `b` (a sequence may be as long as there are angles, or DSA_MAX_PAGED_TOKENS); DSA_OK
@@ -58,7 +59,9 @@ inline bool overlaps(const void *a, uint64_t na, const void *b, uint64_t nb) {
     return x < y + nb && y < x + na;
 }
 
-bool make_tmap_pages(CUtensorMap *map, const void *pages, const PagedBatch &b);
+// The rows of the pages in bf16 elements, boxes of 64 of them (128 bytes) by the rows of a page.
+bool make_tmap_pages(CUtensorMap *map, const void *pages, const PagedBatch &b,
+                     PageRow row = kBf16Row);
 
 // One sequence of the batch: rows [row0, row0 + n) are its new tokens, the last n of its len.
 struct PagedSeq {

@@ -869,14 +869,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 std::mutex g_mu;
 int g_sms[kMaxDevices];   // 0: not set up yet
 
-// Places that a CTA's run may have (of a GB300's 152), from the sizes alone (lengths are the
-// device's): the kernels count them in 32 bits.
-int64_t run_bound(const Params &p) {
-    const int64_t groups = std::min(p.b.n_new, p.b.n_new / p.tpu + p.b.n_seqs);
-    const int64_t keys = p.window > 0 ? std::min(p.b.len_limit, p.window + p.tpu) : p.b.len_limit;
-    return groups * p.upt * (keys / kBlock + 2 + kUnitCost) / kMaxCtas + 1;
-}
-
 // Per-device one-time set-up. A failure is not kept: it may pass (memory for the module's code).
 int setup(int *sms) {
     const int dev = current_device();
@@ -893,6 +885,16 @@ int setup(int *sms) {
 }
 
 }  // namespace
+
+int64_t paged_run_bound(const Params &p, int64_t keys) {
+    const int64_t groups = std::min(p.b.n_new, p.b.n_new / p.tpu + p.b.n_seqs);
+    return groups * p.upt * (keys / kBlock + 2 + kUnitCost) / kMaxCtas + 1;
+}
+
+int enqueue_paged_join(const Params &p, int ctas, cudaStream_t s) {
+    return launch_overlapped(paged_join_kernel<kD>, 4 * ctas, kJoinWarps * 32, 0, s, p, ctas);
+}
+
 }  // namespace dsa
 
 extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
@@ -946,7 +948,9 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
     p.rpt = std::min(heads, p.rows);
     // a window no shorter than any sequence is no window
     p.window = window >= p.b.len_limit ? 0 : window;
-    if (run_bound(p) > (int64_t{1} << 31) - 1) return DSA_ERR_SHAPE;
+    const int64_t keys =
+        p.window > 0 ? std::min(p.b.len_limit, p.window + p.tpu) : p.b.len_limit;
+    if (paged_run_bound(p, keys) > (int64_t{1} << 31) - 1) return DSA_ERR_SHAPE;
     if (!workspace || !aligned16(workspace) || workspace_bytes < DSA_PAGED_WORKSPACE_BYTES)
         return DSA_ERR_SCRATCH;
     const uintptr_t wa = reinterpret_cast<uintptr_t>(workspace), used = DSA_PAGED_WORKSPACE_BYTES;
@@ -975,6 +979,5 @@ extern "C" int dsa_paged_attn(const void *q, int32_t heads, int64_t n_new,
     if (rc != DSA_OK) return rc;
     return chunk ? launch_overlapped(paged_join_kernel<kD / 2>, 4 * ctas, kJoinWarps * 32, 0, s,
                                      p, ctas)
-                 : launch_overlapped(paged_join_kernel<kD>, 4 * ctas, kJoinWarps * 32, 0, s, p,
-                                     ctas);
+                 : enqueue_paged_join(p, ctas, s);
 }

@@ -23,7 +23,7 @@ namespace dsa {
 namespace paged {
 
 constexpr int kBlock = 128;        // keys in a block
-constexpr int kThreads = 512;      // of both kernels
+constexpr int kThreads = 512;      // of both kernels of dsa_paged_attn
 constexpr int kMaxCtas = 152;
 
 // Places of a unit before its blocks. (0, 1, 2 and 3 for chunks: 1,534, 1,107, 1,110 and 1,137 us
@@ -93,9 +93,20 @@ struct Params {
     int32_t window;    // 0: the whole context
     float c;           // scale * log2(e)
     int32_t *status;
+    static constexpr bool kSinks = false;
 };
 
+// With first tokens that stay visible beside a window: the keys of a unit whose window begins
+// behind block 0 are block 0 and then the window's blocks.
+struct SinkParams : Params {
+    int32_t sinks;     // 0 without a window; within block 0
+    int32_t turn_q;    // q is to be turned by its positions
+    static constexpr bool kSinks = true;
+};
+static_assert(DSA_MAX_SINKS <= kBlock, "the first tokens are in block 0");
+
 // ------------------------------------------------------------------ the list of units
+// (each function for both kinds of parameters)
 
 // a / b for a >= 0, b > 0: the 32-bit division where both fit, as they nearly always do.
 __device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
@@ -131,22 +142,34 @@ static __device__ __noinline__ int64_t floor_sum(int64_t n, int64_t a, int64_t d
 }
 
 // Keys of the tokens [t0, t1) of a sequence: positions lo .. hi, blocks lo / 128 .. hi / 128.
-__device__ __forceinline__ void key_range(const Params &p, const PagedSeq &q, int t0, int &lo,
+template <class P>
+__device__ __forceinline__ void key_range(const P &p, const PagedSeq &q, int t0, int &lo,
                                           int &hi) {
     const int first = q.len - q.n + t0;
     lo = p.window > 0 ? max(0, first - p.window + 1) : 0;
     hi = q.len - q.n + min(t0 + p.tpu, q.n) - 1;
 }
 
-__device__ __forceinline__ int group_blocks(const Params &p, const PagedSeq &q, int g) {
+// Whether block 0 stands before the blocks of a window that begins at lo.
+template <class P>
+__device__ __forceinline__ bool sink_block(const P &p, int lo) {
+    if constexpr (P::kSinks)
+        return p.sinks > 0 && lo >= kBlock;
+    else
+        return false;
+}
+
+template <class P>
+__device__ __forceinline__ int group_blocks(const P &p, const PagedSeq &q, int g) {
     int lo, hi;
     key_range(p, q, g * p.tpu, lo, hi);
-    return (hi >> 7) - (lo >> 7) + 1;
+    return (hi >> 7) - (lo >> 7) + 1 + sink_block(p, lo);
 }
 
 // Places of the first G token groups of a sequence, for each part (G = all of them: the last one
 // may be short).
-static __device__ __noinline__ int64_t places_before_many(const Params &p, PagedSeq q, int G) {
+template <class P>
+static __device__ __noinline__ int64_t places_before_many(const P &p, PagedSeq q, int G) {
     const int base = q.len - q.n, d = p.tpu;
     int64_t sum = floor_sum(G, base + d - 1, d) + int64_t{G} * (1 + kUnitCost);
     if (G * d > q.n) sum += ((q.len - 1) >> 7) - ((base + G * d - 1) >> 7);
@@ -154,11 +177,16 @@ static __device__ __noinline__ int64_t places_before_many(const Params &p, Paged
         const int a = base - p.window + 1;  // (a window is shorter than the longest sequence)
         const int g0 = a >= 0 ? 0 : (-a + d - 1) / d;
         sum -= floor_sum(G - g0, a + g0 * d, d);
+        if constexpr (P::kSinks) {  // the groups whose windows begin behind block 0
+            const int g1 = a >= kBlock ? 0 : (kBlock - a + d - 1) / d;
+            if (p.sinks > 0) sum += max(0, G - g1);
+        }
     }
     return sum;
 }
 
-__device__ __forceinline__ int64_t places_before(const Params &p, const PagedSeq &q, int G) {
+template <class P>
+__device__ __forceinline__ int64_t places_before(const P &p, const PagedSeq &q, int G) {
     return G <= 0 ? 0 : G == 1 ? group_blocks(p, q, 0) + kUnitCost : places_before_many(p, q, G);
 }
 
@@ -181,7 +209,8 @@ struct Place {
 // The token group of a sequence that holds its place r (of all parts' places), by a warp: a round
 // looks at 32 groups (a thread that halved 2,048 groups took 35 us of a launch's start).
 // Returns it and, above its 32 bits, the place in it.
-static __device__ __noinline__ int64_t find_group(const Params &p, PagedSeq q, int64_t r) {
+template <class P>
+static __device__ __noinline__ int64_t find_group(const P &p, PagedSeq q, int64_t r) {
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = groups_of(p, q);  // upt * places_before(lo) <= r < upt * places_before(hi)
     int64_t before = 0;
@@ -198,7 +227,8 @@ static __device__ __noinline__ int64_t find_group(const Params &p, PagedSeq q, i
 }
 
 // (all lanes of a warp, with the same arguments)
-__device__ __forceinline__ Place find_place(const Params &p, const PagedSeq &q, int s, int64_t r) {
+template <class P>
+__device__ __forceinline__ Place find_place(const P &p, const PagedSeq &q, int s, int64_t r) {
     const int64_t at = q.n > p.tpu ? find_group(p, q, r) : r << 32;
     const int g = static_cast<int>(at);
     int in = static_cast<int>(at >> 32), part = 0;
@@ -228,6 +258,12 @@ struct Segment {
     int lo;            // lowest position any of its tokens sees
     bool whole;        // all of the unit's blocks
     bool alone;        // the sequence's only unit: nothing else reads its keys
+    bool jump;         // the first block is block 0, the next one blk + 1
+
+    // The first position of block b.
+    __device__ __forceinline__ int block_pos(int b) const {
+        return jump && b == 0 ? 0 : (blk + b) * kBlock;
+    }
 };
 
 // Walks the segments of a CTA's run. Every role walks on its own.
@@ -236,7 +272,8 @@ struct Walk {
     PagedSeq q;
     int left;
 
-    __device__ __forceinline__ Walk(const Params &p, const int *start) {
+    template <class P>
+    __device__ __forceinline__ Walk(const P &p, const int *start) {
         at = Place{start[0], start[1], start[2], start[3]};
         left = start[4];
         q.n = 0;
@@ -246,7 +283,8 @@ struct Walk {
         }
     }
 
-    __device__ __forceinline__ bool next(const Params &p, Segment &x) {
+    template <class P>
+    __device__ __forceinline__ bool next(const P &p, Segment &x) {
         if (left <= 0) return false;
         while (at.g * p.tpu >= q.n) {
             if (++at.s >= p.b.n_seqs) return false;
@@ -257,7 +295,8 @@ struct Walk {
         const int t0 = at.g * p.tpu, t1 = min(t0 + p.tpu, q.n);
         int hi;
         key_range(p, q, t0, x.lo, hi);
-        const int blo = x.lo >> 7, nblk = (hi >> 7) - blo + 1;
+        const int sink = sink_block(p, x.lo);
+        const int blo = (x.lo >> 7) - sink, nblk = (hi >> 7) - blo + 1;
         const int before = max(0, kUnitCost - at.off), off = max(0, at.off - kUnitCost);
         x.nb = min(nblk - off, left - before);
         if (x.nb <= 0) {  // the run ends before the unit's first block
@@ -271,6 +310,7 @@ struct Walk {
         x.nrows = unit_rows(p, t1 - t0, at.part);
         x.part = at.part;
         x.blk = blo + off;
+        x.jump = sink > 0 && off == 0;
         x.whole = x.nb == nblk;
         x.alone = p.upt == 1 && q.n <= p.tpu;
         left -= before + x.nb;
@@ -290,19 +330,23 @@ struct PageWalk {
     int b;
     bool have;
 
-    __device__ __forceinline__ PageWalk(const Params &p, const int *start) : walk(p, start), b(0) {
+    template <class P>
+    __device__ __forceinline__ PageWalk(const P &p, const int *start) : walk(p, start), b(0) {
         have = walk.next(p, x);
     }
 
     // The page that holds this lane's rows [pos, pos + prows) of the next block (-1: no token
     // needs one, or a bad table entry), and the row of the page they begin at.
-    __device__ __forceinline__ int32_t next(const Params &p, int page, int prows, int pages,
+    template <class P>
+    __device__ __forceinline__ int32_t next(const P &p, int page, int prows, int pages,
                                             int &row) {
         int32_t e = -1;
         if (have) {
-            const int pos = (x.blk + b) * kBlock + page * prows;
+            const int pos = x.block_pos(b) + page * prows;
             row = pos & ((1 << p.b.page_shift) - 1);
-            if (page < pages && pos <= x.posl && pos > x.lo - prows) {
+            bool seen = pos > x.lo - prows;
+            if constexpr (P::kSinks) seen |= pos < p.sinks;
+            if (page < pages && pos <= x.posl && seen) {
                 e = __ldg(p.b.page_table + int64_t{x.s} * p.b.max_pages + (pos >> p.b.page_shift));
                 if (e < 0 || e >= p.b.n_pages) {
                     report(p.status, DSA_ERR_BOUNDS);
@@ -327,11 +371,13 @@ __device__ __forceinline__ int row_pos(const Params &p, int posf, int r) {
 // length (0 on entry); describes the unit that begins in it and ends beyond for the join. All
 // threads call it; `scratch` holds a value per warp and four more. Ends with a barrier of the CTA,
 // and one inside it publishes what was set up before (TMEM, mbarriers).
-__device__ __forceinline__ void find_run(const Params &p, int64_t *scratch, int *start) {
+template <int kT = kThreads, class P>
+__device__ __forceinline__ void find_run(const P &p, int64_t *scratch, int *start) {
+    constexpr int kWarps = kT / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = static_cast<int>(blockIdx.x);
     JoinDesc *desc = reinterpret_cast<JoinDesc *>(p.ws + kWsDesc) + cta;
-    const int per = (p.b.n_seqs + kThreads - 1) / kThreads;
+    const int per = (p.b.n_seqs + kT - 1) / kT;
     const int s0 = min(tid * per, p.b.n_seqs), s1 = min(s0 + per, p.b.n_seqs);
     int64_t mine = 0, nb = 0;
     PagedSeq q = {};
@@ -353,18 +399,18 @@ __device__ __forceinline__ void find_run(const Params &p, int64_t *scratch, int 
     __syncthreads();
     tc_fence_after();
     // (scanned once more in every warp; few instructions, as each is fetched cold)
-    int64_t upto = lane < kThreads / 32 ? scratch[lane] : 0;
+    int64_t upto = lane < kWarps ? scratch[lane] : 0;
 #pragma unroll
-    for (int w = 1; w < kThreads / 32; w <<= 1) {
+    for (int w = 1; w < kWarps; w <<= 1) {
         const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, w);
         if (lane >= w) upto += v;
     }
-    const int64_t total = __shfl_sync(0xFFFFFFFFu, upto, kThreads / 32 - 1);
+    const int64_t total = __shfl_sync(0xFFFFFFFFu, upto, kWarps - 1);
     const int64_t below = __shfl_sync(0xFFFFFFFFu, upto, warp > 0 ? warp - 1 : 0);
     if (warp > 0) incl += below;
     const int64_t run = div_pos(total + gridDim.x - 1, gridDim.x);
     const int64_t T0 = run * cta, T1 = min(T0 + run, total);
-    int64_t *const ends = scratch + kThreads / 32;  // sequence and place in it: the run's first
+    int64_t *const ends = scratch + kWarps;  // sequence and place in it: the run's first
                                                     // place, its last
     if (mine > 0 && T0 < T1 && T0 < incl && T1 > incl - mine) {
         // one of this thread's sequences holds the first, the last, or both
@@ -531,6 +577,13 @@ __device__ __forceinline__ uint32_t finite2(uint32_t v) {
 // The chunk kernel (paged_chunk.cu): one-time set-up, and its launch.
 constexpr int kChunkRows = 128;
 int prepare_paged_chunk();
+
+// The join of the units that paged_attn_kernel (or one that leaves the same parts) cut.
+int enqueue_paged_join(const paged::Params &p, int ctas, cudaStream_t s);
+
+// Places that a CTA's run may have (of a GB300's 152), from the sizes alone (lengths are the
+// device's): the kernels count them in 32 bits. `keys`: the longest range of a unit's keys.
+int64_t paged_run_bound(const paged::Params &p, int64_t keys);
 
 int enqueue_paged_chunk(const CUtensorMap &tm_q, const CUtensorMap &tm_kv,
                         const paged::Params &p, const void *q, int ctas, cudaStream_t s);

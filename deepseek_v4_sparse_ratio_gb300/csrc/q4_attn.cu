@@ -3,125 +3,928 @@
 //
 //   out[r,h] = R(-t) sum_u p_u v_u,   p = softmax_u(scale * (R(t) q[r,h]) . v_u)
 //
-// The simplest form: a warp per row of q, one key after the other, lane l with dims 16 l ...
+// Units of up to 64 rows of q and blocks of 128 keys, one list of both cut evenly over the SMs and
+// joined, as for single tokens over bf16 pages (paged_walk.cuh, paged_attn.cu). A block, keys on
+// the MMA's M:
+//   S^T[key, row]  = K_blk[128 x 512] . Q^T        (M=128, N=64, K=512)
+//   O^T[d, row]   += V_blk^T[512 x 128] . P^T       (4 x (M=128, N=64, K=128))
+// in bf16, which holds what a 4-bit element stands for exactly. What bounds it is shared memory:
+// with both operands there a product of N=64 takes 48 cycles for 32 of the tensor pipe, and the
+// unpacked rows are written on top. So six of the eight 64-dim chunks of K are unpacked into TMEM,
+// where the first product takes them from (32 cycles), and from there into shared memory when the
+// block before has left it; the second product needs them there, transposed. That also takes the
+// unpacking and the first product of a block out of the chain: they run beside the softmax and the
+// second product of the block before.
+//   chunks 0-5: TMEM for QK, shared memory for PV;  chunk 6: shared memory for both, unpacked when
+//   PV of the block before has used it (the first tile of PV);  chunk 7, the rotated dims (bf16 in
+//   the pages): TMA into two slots in turn.
+//
+// Roles (640 threads): warp 0 finds each block's pages for the unpackers and loads chunk 7; warp 1
+// issues the products, in the order QK chunks 0-5 (b), PV 1st and 2nd tile (b - 1), QK chunks 6-7
+// (b), PV 3rd and 4th (b - 1); warp 2 loads q, 2 and 3 turn it; warps 4-11 unpack: thread = key,
+// each half of the warps every other chunk; warps 12-19 softmax and results, 32 rows of 32 keys a
+// warp.
+#include <cudaTypedefs.h>
 #include <math.h>
 
-#include "paged.h"
+#include <algorithm>
+#include <mutex>
+
+#include "paged_walk.cuh"
 #include "q4.h"
 
 namespace dsa {
 
 namespace {
 
-struct Q4Args {
-    PagedBatch b;
-    const uint4 *q;
-    const uint8_t *pages;
-    uint4 *out;
-    int32_t heads, window, sinks, q_turned;
-    float c;   // scale log2(e)
-    int32_t *status;
+using namespace paged;
+
+constexpr int kT = 640;
+constexpr int kMmaWarp = 1;
+constexpr int kTurnWarp0 = 2;      // two warps: a row of q a thread
+constexpr int kUnpackWarp0 = 4;
+constexpr int kSoftWarp0 = 12;
+constexpr int kRegsLaunch = 96;
+constexpr int kRegsMisc = 80;
+constexpr int kRegsUnpack = 80;
+constexpr int kRegsSoft = 120;     // 128*80 + 256*80 + 256*120 = 640*96, the launch allocation
+
+constexpr int kRows = 64;          // rows of q in a unit (MMA N)
+constexpr int kDescs = 4;          // blocks whose pages are known ahead
+
+// shared memory
+constexpr uint32_t kChunk = 16384;                // [128 keys x 64 dims]
+constexpr uint32_t kOffQ = 0;                     // 8 chunks x [64 rows x 128 B]
+constexpr uint32_t kOffV = 65536;                 // chunks 0-5, for PV
+constexpr uint32_t kOff6 = kOffV + 6 * kChunk;    // chunk 6
+constexpr uint32_t kOff7 = kOff6 + kChunk;        // chunk 7, by block parity
+constexpr uint32_t kOffP = kOff7 + 2 * kChunk;    // P^T [128 keys x 64 rows] bf16
+constexpr uint32_t kOffRed = kOffP + 16384;       // [4][64] block maxima | partial sums
+constexpr uint32_t kOffLinv = kOffRed + 1024;     // [64] rescale factors | 1/sum
+constexpr uint32_t kOffM = kOffLinv + 256;        // [2][64] running maximum, double-buffered
+constexpr uint32_t kOffDesc = kOffM + 512;        // [kDescs] pages of a block
+constexpr uint32_t kOffBar = kOffDesc + kDescs * 80;
+constexpr uint32_t kSmem = kOffBar + 384;
+static_assert(kSmem <= 232448, "over the shared memory of one CTA");
+
+// TMEM columns
+constexpr uint32_t kOCol = 0;      // O^T: 4 d-tiles x 64
+constexpr uint32_t kSCol = 256;    // S^T
+constexpr uint32_t kKCol = 320;    // chunks 0-5 of K, 32 columns each
+
+// The pages of a block, for the unpackers.
+struct Desc {
+    const uint8_t *row[8];  // the first row that the block has in each page (null: none needed)
+    int a, b, c;            // keys [a, b) and those below c are seen by some token
+    int more;               // 0: the run has ended
 };
+static_assert(sizeof(Desc) == 80, "descriptors");
 
-__device__ __forceinline__ void turn16(float *x, const float *cs, float sign) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const float c = __ldg(cs + 2 * k), s = sign * __ldg(cs + 2 * k + 1);
-        const float a = x[2 * k] * c - x[2 * k + 1] * s;
-        x[2 * k + 1] = x[2 * k] * s + x[2 * k + 1] * c;
-        x[2 * k] = a;
-    }
+// D[tmem] (+)= A[tmem] * B[smem]^T; A: lane = row, a column holds two bf16 along K.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
-__device__ __forceinline__ void floats16(const uint4 &a, const uint4 &b, float *x) {
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        x[2 * k] = bf16lo(w[k]);
-        x[2 * k + 1] = bf16hi(w[k]);
-    }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
 
-__global__ void __launch_bounds__(256) q4_attn_kernel(const __grid_constant__ Q4Args p) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+        "%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
+}
+
+// A 32-byte sector of a row (zeros without one).
+__device__ __forceinline__ void load_sector(uint32_t *v, const uint8_t *row, int at) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0;
+    if (row)
+        asm volatile(
+            "ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+              "=r"(v[7])
+            : "l"(row + at));
+}
+
+// Two scales (e4m3, 16 bits) times the row's power of two: for either group u / 2 and -72 u, twice.
+struct Units {
+    __nv_bfloat162 half[2], off[2];
+};
+__device__ __forceinline__ Units units_of(uint32_t two, float half_pow) {
+    const __half2_raw h =
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+    const float2 s = __half22float2(__half2(h));
+    Units u;
+    u.half[0] = __float2bfloat162_rn(s.x * half_pow);
+    u.half[1] = __float2bfloat162_rn(s.y * half_pow);
+    const __nv_bfloat162 k = __float2bfloat162_rn(-144.0f);   // (144 u / 2: eight bits, exact)
+    u.off[0] = __hmul2(u.half[0], k);
+    u.off[1] = __hmul2(u.half[1], k);
+    return u;
+}
+
+// Four words (32 dims) as 16 pairs of bf16.
+__device__ __forceinline__ void unpack32(const uint32_t *w, const Units &u, uint32_t *out) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out[4 * j + k] = q4_pair(w[j], k, u.half[j / 2], u.off[j / 2]);
+}
+
+// Whether a word holds an e4m3 NaN (0x7F or 0xFF) in its bytes under `mask`.
+__device__ __forceinline__ bool has_nan(uint32_t w) {
+    const uint32_t x = ~w & 0x7F7F7F7Fu;   // a byte 0 where all seven bits are set
+    return ((x - 0x01010101u) & ~x & 0x80808080u) != 0;
+}
+
+// The softmax warps form two groups of four, one per half of the rows (named barriers 1 and
+// 2, 128 threads each).
+__device__ __forceinline__ bool vote_any_group(bool pred, int hh) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, %2, 128, p;\n"
+        " selp.b32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(pred)), "r"(1 + hh)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void bar_group(int hh) {
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + hh) : "memory");
+}
+
+// ------------------------------------------------------------------ the kernel
+
+__global__ void __launch_bounds__(kT, 1)
+    q4_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
+                   const __grid_constant__ CUtensorMap tm_kv,
+                   const __grid_constant__ SinkParams p, const uint8_t *pages) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *sQ = smem + kOffQ;
+    uint8_t *sV = smem + kOffV;
+    uint8_t *s6 = smem + kOff6;
+    uint8_t *sP = smem + kOffP;
+    float *sRed = reinterpret_cast<float *>(smem + kOffRed);
+    float *sL = sRed;
+    float *sLinv = reinterpret_cast<float *>(smem + kOffLinv);
+    float *sAlpha = sLinv;
+    float *sM = reinterpret_cast<float *>(smem + kOffM);
+    Desc *sDesc = reinterpret_cast<Desc *>(smem + kOffDesc);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBar);
+    uint64_t *tm_full = bars + 0;   // [3] pair of chunks 0-5 in TMEM
+    uint64_t *v_full = bars + 3;    // [3] pair of chunks 0-5 in shared memory
+    uint64_t *v_free = bars + 6;    // [4] pair of chunks used by PV
+    uint64_t *k6_full = bars + 10;  // chunk 6 unpacked, sValid written
+    uint64_t *r_full = bars + 11;   // [2] chunk 7 landed, by block parity
+    uint64_t *qa_done = bars + 13;  // QK has read the chunks in TMEM
+    uint64_t *q_full = bars + 14;
+    uint64_t *q_free = bars + 15;
+    uint64_t *q_turned = bars + 16;
+    uint64_t *s_full = bars + 17;
+    uint64_t *s_free = bars + 18;
+    uint64_t *p_full = bars + 19;
+    uint64_t *pv_done = bars + 20;  // P may be written, O rescaled
+    uint64_t *o_full = bars + 21;
+    uint64_t *o_free = bars + 22;
+    uint64_t *drain = bars + 23;
+    uint64_t *d_full = bars + 24;   // [kDescs]
+    uint64_t *d_free = bars + 28;   // [kDescs]
+    constexpr int kBars = 32;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + kBars);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    int *sStart = reinterpret_cast<int *>(tmem_holder + 2);    // [5] start of this CTA's run
+    volatile uint32_t *sBlocks = tmem_holder + 1 + kBlocksAt;  // blocks begun
+    volatile uint32_t *sValid = tmem_holder + 12;              // [2][4] keys that were loaded
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (smem_u32(smem) & 1023u) {  // the tiles' swizzle counts on it
+        wait_before();
+        if (tid == 0) {
+            report(p.status, DSA_ERR_CUDA);
+            reinterpret_cast<JoinDesc *>(p.ws + kWsDesc)[blockIdx.x] = JoinDesc{};
+        }
+        return;
+    }
+    if (warp == 0) {
+        // arrivals a phase takes: 8 unpacking warps on tm_full, v_full, k6_full and d_free, 64
+        // turning threads on q_turned, 8 softmax warps on s_free, p_full and o_free, one on the
+        // others
+        int n = 1;
+        uint64_t *bar = bars + lane;
+        if (bar < v_free || bar == k6_full || bar >= d_free) n = 8;
+        if (bar == q_turned) n = 64;
+        if (bar == s_free || bar == o_free || bar == p_full) n = 8;
+        mbar_init(bar, n);
+        if (lane == 31) {
+            *abort_flag = 0;
+            sStart[4] = 0;
+            *sBlocks = 0;
+        }
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc(tmem_holder, 512);
+    if (tid == 32 * kTurnWarp0) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_kv);
+    }
     wait_before();
-    const int lane = threadIdx.x & 31;
-    const int64_t item = int64_t{blockIdx.x} * 8 + (threadIdx.x >> 5);
-    if (blockIdx.x == 0) {
-        for (int s = threadIdx.x; s < p.b.n_seqs; s += blockDim.x) {
-            bool bad;
-            paged_seq(p.b, s, bad);
-            if (bad) report(p.status, DSA_ERR_BOUNDS);
-        }
-    }
-    const int64_t r = item / p.heads;
-    if (r >= p.b.n_new) return;
-    const int s = find_seq_any(p.b, r, lane);
-    if (s < 0) return;
-    bool bad;
-    const PagedSeq sq = paged_seq(p.b, s, bad);
-    const int t = sq.len - sq.n + static_cast<int>(r - sq.row0);
-    const float *cs = p.b.cos_sin && lane >= 28
-                          ? p.b.cos_sin + int64_t{t} * kRope + 16 * (lane - 28)
-                          : nullptr;
-    float q[16], o[16];
-    floats16(p.q[item * 64 + 2 * lane], p.q[item * 64 + 2 * lane + 1], q);
-    if (cs && !p.q_turned) turn16(q, cs, 1.0f);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) o[k] = 0.0f;
-    float m = -INFINITY, sum = 0.0f;
-    const int low = p.window > 0 ? max(0, t - p.window + 1) : 0;
-    const int sinks = min(p.sinks, low);
-    for (int j = 0; j < sinks + t + 1 - low; ++j) {
-        const int u = j < sinks ? j : low + j - sinks;
-        const int32_t page = __ldg(p.b.page_table + int64_t{s} * p.b.max_pages +
-                                   (u >> p.b.page_shift));
-        if (page < 0 || page >= p.b.n_pages) {
-            if (lane == 0) report(p.status, DSA_ERR_BOUNDS);
-            continue;
-        }
-        const uint8_t *row = p.pages + page * p.b.page_stride +
-                             int64_t{u & ((1 << p.b.page_shift) - 1)} * kQ4Row;
-        float x[16];
-        if (lane >= 28) {
-            const uint4 *at = reinterpret_cast<const uint4 *>(row + kQ4Rope) + 2 * (lane - 28);
-            floats16(__ldg(at), __ldg(at + 1), x);
-        } else {
-            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(row + 32) + lane);
-            const float unit = q4_unit(
-                __ldg(row + 16 * ((lane >> 1) & 1) + 2 * (lane >> 2) + (lane & 1)),
-                __ldg(row + 14));
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const uint32_t word = k < 8 ? w.x : w.y;
-                const int at = 4 * (k % 8 / 2) + 16 * (k & 1);
-                x[k] = (static_cast<int>((word >> at) & 15u) - 8) * unit;
+    const int cta = static_cast<int>(blockIdx.x);
+    find_run<kT>(p, reinterpret_cast<int64_t *>(sV), sStart);
+    const uint32_t tmem = *tmem_holder;
+
+    if (warp < kUnpackWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMisc));
+        if (warp == 0) {
+            // ---------------- pages: lane i < np has page i of a block. Descriptors run two
+            // blocks ahead of the loads of chunk 7 (which wait for PV), as the unpackers do.
+            const int prows = min(1 << p.b.page_shift, kBlock), np = kBlock / prows;
+            PageWalk walk(p, sStart);
+            // (entry, row) of the block whose chunk 7 is loaded next and of the one behind it
+            int32_t e0 = -1, e1 = -1, e2 = -1;
+            int row0 = 0, row1 = 0, row2 = 0;
+            bool ok = true;
+            int t = -2, last_load = -1;
+            bool have0 = false, have1 = false;
+            for (;; ++t) {
+                const bool have2 = walk.have;
+                if (t + 2 >= 0 && ok) {
+                    // block t + 2
+                    const int d = (t + 2) & (kDescs - 1);
+                    const uint32_t use = ((t + 2) / kDescs) & 1;
+                    ok = __all_sync(0xFFFFFFFFu,
+                                    wait_bar(&d_free[d], use ^ 1, abort_flag, p.status));
+                    if (!ok) break;
+                    if (have2) {
+                        const int pos = walk.x.block_pos(walk.b);
+                        const int lo = walk.x.lo - pos, end = walk.x.posl - pos + 1;
+                        e2 = walk.next(p, lane, prows, np, row2);
+                        if (lane < 8)
+                            sDesc[d].row[lane] =
+                                e2 >= 0 ? pages + e2 * p.b.page_stride + int64_t{row2} * kQ4Row
+                                        : nullptr;
+                        if (lane == 8) {
+                            sDesc[d].a = lo;
+                            sDesc[d].b = end;
+                            sDesc[d].c = p.sinks - pos;
+                        }
+                    }
+                    if (lane == 9) sDesc[d].more = have2;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&d_full[d]);
+                }
+                if (t >= 0 && have0) {
+                    // chunk 7 of block t, when PV of the block two back has used the slot
+                    const int par = t & 1;
+                    ok = __all_sync(0xFFFFFFFFu, t < 2 || wait_bar(&v_free[3], t & 1, abort_flag,
+                                                                   p.status));
+                    if (!ok) break;
+                    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, e0 >= 0);
+                    *sBlocks = static_cast<uint32_t>(t) + 1;
+                    if (lane == 0)
+                        mbar_expect_tx(&r_full[par],
+                                       static_cast<uint32_t>(__popc(mask)) * prows * 128);
+                    __syncwarp();
+                    if (e0 >= 0)
+                        tma_load_3d(smem + kOff7 + par * kChunk + lane * prows * 128, &tm_kv,
+                                    &r_full[par], kQ4Rope / 2, row0, e0, policy_evict_normal());
+                    last_load = t;
+                }
+                if (t >= 0 && !have0) break;
+                have0 = have1;
+                have1 = have2;
+                e0 = e1;
+                row0 = row1;
+                e1 = e2;
+                row1 = row2;
             }
+            // no copy into this CTA's shared memory may still be in flight at exit
+            if (lane == 0)
+                for (int l = last_load; l >= 0 && l >= last_load - 1; --l)
+                    drain_wait(&r_full[l & 1], (l >> 1) & 1);
+            __syncwarp();
+        } else if (warp == kMmaWarp) {
+            // ---------------- the products. PV of a block follows QK of the next one's chunks in
+            // TMEM, and QK of its last two chunks stands between the tiles of PV; where the next
+            // block needs new queries, PV goes first.
+            constexpr uint32_t idesc_qk = idesc_bf16(kBlock, kRows, false, false);
+            constexpr uint32_t idesc_pv = idesc_bf16(128, kRows, true, true);
+            Walk walk(p, sStart);
+            Segment x;
+            int i = -1, g = 0;                 // unit and block of QK
+            bool ok = true, pend = false, pend_first = false, pend_last = false;
+            int ends = 0;                      // units whose PV is all issued
+            bool have = walk.next(p, x);
+            const bool turn = p.b.cos_sin && p.turn_q;
+
+            auto pv_tile = [&](int m, int gb, bool first) {
+                // tile m of PV of block gb: dims 128 m ..
+                const uint32_t base =
+                    smem_u32(smem) + (m < 3 ? kOffV + 2 * m * kChunk : kOff6);
+                const uint32_t lbo = m < 3 || !(gb & 1) ? kChunk : 2 * kChunk;
+                if (elect_one()) {
+                    const uint64_t ad = desc_sw128(base, lbo, 1024);
+                    const uint64_t bd = desc_sw128(smem_u32(sP), 8192, 1024);
+#pragma unroll 4
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_bf16(tmem + kOCol + 64 * m, ad + ((kk * 2048) >> 4),
+                                 bd + ((kk * 2048) >> 4), idesc_pv, kk > 0 || !first);
+                    mma_commit(&v_free[m]);
+                }
+                __syncwarp();
+            };
+            // PV's last tile first: its chunk 6 is what QK of the next block waits for
+            auto pv_begin = [&]() -> bool {
+                const int gb = g - 1;
+                if (!wait_bar(p_full, gb & 1, abort_flag, p.status)) return false;
+                if (pend_first && ends > 0 &&
+                    !wait_bar(o_free, (ends - 1) & 1, abort_flag, p.status))
+                    return false;
+                tc_fence_after();
+                pv_tile(3, gb, pend_first);
+                if (!wait_bar(&v_full[0], gb & 1, abort_flag, p.status)) return false;
+                tc_fence_after();
+                pv_tile(0, gb, pend_first);
+                return true;
+            };
+            auto pv_end = [&]() -> bool {
+                const int gb = g - 1;
+#pragma unroll 1
+                for (int m = 1; m < 3; ++m) {
+                    if (!wait_bar(&v_full[m], gb & 1, abort_flag, p.status)) return false;
+                    tc_fence_after();
+                    pv_tile(m, gb, pend_first);
+                }
+                if (elect_one()) {
+                    mma_commit(pv_done);
+                    if (pend_last) mma_commit(o_full);
+                }
+                __syncwarp();
+                if (pend_last) ++ends;
+                return true;
+            };
+
+            for (int b = 0; ok && have;) {
+                const bool fresh = b == 0;
+                if (fresh) {
+                    ++i;
+                    if (pend && !(ok = pv_begin() && pv_end())) break;
+                    pend = false;
+                    if (!(ok = wait_bar(q_full, i & 1, abort_flag, p.status))) break;
+                }
+                // QK, chunks 0-5
+                if (!(ok = wait_bar(s_free, (g & 1) ^ 1, abort_flag, p.status))) break;
+#pragma unroll 1
+                for (int m = 0; m < 3 && ok; ++m) {
+                    if (!(ok = wait_bar(&tm_full[m], g & 1, abort_flag, p.status))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t bd = desc_sw128(smem_u32(sQ) + 2 * m * 8192, 16, 1024);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_bf16_ta(tmem + kSCol, tmem + kKCol + 64 * m + 8 * k,
+                                        bd + (k / 4) * (8192 >> 4) + 2 * (k % 4), idesc_qk,
+                                        m > 0 || k > 0);
+                        if (m == 2) mma_commit(qa_done);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (pend && !(ok = pv_begin())) break;
+                // QK, chunk 6 and chunk 7
+                if (!(ok = wait_bar(k6_full, g & 1, abort_flag, p.status) &&
+                           wait_bar(&r_full[g & 1], (g >> 1) & 1, abort_flag, p.status)))
+                    break;
+                if (fresh && turn && !(ok = wait_bar(q_turned, i & 1, abort_flag, p.status)))
+                    break;
+                tc_fence_after();
+                const bool last = b == x.nb - 1;
+                if (elect_one()) {
+                    const uint64_t bd = desc_sw128(smem_u32(sQ) + 6 * 8192, 16, 1024);
+                    const uint64_t a6 = desc_sw128(smem_u32(s6), 16, 1024);
+                    const uint64_t a7 = desc_sw128(smem_u32(smem) + kOff7 + (g & 1) * kChunk, 16,
+                                                   1024);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_bf16(tmem + kSCol, (k < 4 ? a6 : a7) + 2 * (k % 4),
+                                 bd + (k / 4) * (8192 >> 4) + 2 * (k % 4), idesc_qk, 1u);
+                    mma_commit(s_full);
+                    if (last) mma_commit(q_free);
+                }
+                __syncwarp();
+                if (pend && !(ok = pv_end())) break;
+                pend = true;
+                pend_first = fresh;
+                pend_last = last;
+                ++g;
+                if (++b == x.nb) {
+                    b = 0;
+                    have = walk.next(p, x);
+                }
+            }
+            if (ok && pend) ok = pv_begin() && pv_end();
+            if (elect_one()) {
+                mma_commit(drain);
+                drain_wait(drain, 0);
+            }
+            __syncwarp();
+        } else {
+            // ---------------- the queries: loaded when the last unit's products have read theirs,
+            // and turned in place, a row a thread
+            const bool turn = p.b.cos_sin && p.turn_q;
+            const uint64_t pol_stream = policy_evict_first();
+            const int r = tid - 32 * kTurnWarp0;
+            uint8_t *row = sQ + 7 * 8192 + r * 128;
+            Walk walk(p, sStart);
+            Segment x;
+            int i = 0;
+            for (; walk.next(p, x); ++i) {
+                if (warp == kTurnWarp0) {
+                    if (!__all_sync(0xFFFFFFFFu,
+                                    wait_bar(q_free, (i & 1) ^ 1, abort_flag, p.status)))
+                        break;
+                    if (lane == 0) {
+                        mbar_expect_tx(q_full, 65536);
+                        for (int c = 0; c < 8; ++c)
+                            tma_load_2d(sQ + c * 8192, &tm_q, q_full, c * 64,
+                                        static_cast<int>(x.row), pol_stream);
+                    }
+                    __syncwarp();
+                }
+                if (!turn) continue;
+                const bool mine = r < x.nrows;
+                const float4 *src = reinterpret_cast<const float4 *>(
+                    p.b.cos_sin + int64_t{mine ? row_pos(p, x.posf, r) : x.posl} * kRope);
+                if (!__all_sync(0xFFFFFFFFu, wait_bar(q_full, i & 1, abort_flag, p.status))) break;
+                if (mine) {
+#pragma unroll 2
+                    for (int k = 0; k < 8; ++k) {
+                        const float4 c0 = __ldg(src + 2 * k), c1 = __ldg(src + 2 * k + 1);
+                        uint4 *at = reinterpret_cast<uint4 *>(row + ((k ^ (r & 7)) << 4));
+                        uint4 v = *at;
+                        v.x = turn_pair(v.x, c0.x, c0.y);
+                        v.y = turn_pair(v.y, c0.z, c0.w);
+                        v.z = turn_pair(v.z, c1.x, c1.y);
+                        v.w = turn_pair(v.w, c1.z, c1.w);
+                        *at = v;
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(q_turned);
+            }
+            // no copy into this CTA's shared memory may still be in flight at exit
+            __syncwarp();
+            if (tid == 32 * kTurnWarp0 && i > 0) drain_wait(q_full, (i - 1) & 1);
+            __syncwarp();
         }
-        float dot = 0.0f;
+    } else if (warp < kSoftWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
+        // ---------------- unpacking. Step t: chunk 6 of block t - 1, then pair by pair the chunks
+        // of block t - 1 from TMEM to shared memory and those of block t into TMEM; behind each
+        // of them the load of the same chunk of block t + 1.
+        const int sp = warp & 3, h = (warp - kUnpackWarp0) >> 2;
+        const int key = 32 * sp + lane;
+        const uint32_t k_col = tmem + (static_cast<uint32_t>(sp * 32) << 16) + kKCol + 32 * h;
+        uint8_t *const to6 = s6 + key * 128;
+        uint8_t *const to_v = sV + h * kChunk + key * 128;
+        const int swz = key & 7;
+        const int page_shift = min(p.b.page_shift, 7);
+
+        uint32_t raw[3][8], raw6[4] = {}, head[8];
+        uint32_t two[3] = {}, two6 = 0, two6_next = 0;   // scales of a chunk's halves, of chunk 6
+        float pow = 0.0f, pow6 = 0.0f;                   // half of the row's power of two
+        bool odd = false, odd_next = false;              // a scale that is NaN
+
+        // The row of block t (null: not to be read) and which keys of the warp have one.
+        auto fetch = [&](int t, bool &have, uint32_t &valid) -> const uint8_t * {
+            const int d = t & (kDescs - 1);
+            const bool ok = __all_sync(0xFFFFFFFFu, wait_bar(&d_full[d], (t / kDescs) & 1,
+                                                             abort_flag, p.status));
+            const Desc &x = sDesc[d];
+            have = ok && x.more;
+            const uint8_t *row = nullptr;
+            if (have && key < x.b && (key >= x.a || key < x.c)) {
+                row = x.row[key >> page_shift];
+                if (row) row += (key & ((1 << page_shift) - 1)) * kQ4Row;
+            }
+            valid = __ballot_sync(0xFFFFFFFFu, row != nullptr);
+            if (lane == 0) mbar_arrive(&d_free[d]);
+            return row;
+        };
+
+        bool have, have_next;
+        uint32_t valid = 0, valid_next = 0, valid_before = 0;
+        const uint8_t *at = fetch(0, have, valid);
+        load_sector(head, at, 0);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) dot = fmaf(q[k], x[k], dot);
+        for (int m = 0; m < 3; ++m) load_sector(raw[m], at, 32 * (2 * m + h + 1));
+        bool ok = true, before = false;                  // before: block t - 1 is to be copied
+        for (int t = 0; ok && (have || before); ++t) {
+            // the scales of block t
+            if (have) {
 #pragma unroll
-        for (int k = 16; k >= 1; k >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, k);
-        const float m_new = fmaxf(m, dot);
-        const float alpha = m == m_new ? 1.0f : exp2f((m - m_new) * p.c);
-        const float w = dot == -INFINITY ? 0.0f : exp2f((dot - m_new) * p.c);
-        m = m_new;
-        sum = sum * alpha + w;
+                for (int m = 0; m < 3; ++m)   // chunk 2 m + h: bytes 4 m + 2 h of either half
+                    two[m] = __byte_perm(head[m], head[4 + m], h ? 0x7632 : 0x5410);
+                // chunk 6, half h: bytes 12 and 13
+                two6_next = h ? head[7] : head[3];
+                odd_next = has_nan(two[0]) || has_nan(two[1]) || has_nan(two[2]);
+                pow = pow2(max(static_cast<int>((head[3] >> 16) & 0xFFu), 11) - 138);
+            }
+            const uint8_t *const at_next =
+                have ? fetch(t + 1, have_next, valid_next) : (have_next = false, nullptr);
+            if (have_next) load_sector(head, at_next, 0);
+            if (t > 0) {
+                // chunk 6 of block t - 1, in the place that PV of block t - 2 has left
+                ok = __all_sync(0xFFFFFFFFu,
+                                t < 2 || wait_bar(&v_free[3], t & 1, abort_flag, p.status));
+                if (!ok) break;
+                const Units u = units_of(two6 & 0xFFFFu, pow6);
+                uint32_t v[16];
+                unpack32(raw6, u, v);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) o[k] = o[k] * alpha + w * x[k];
+                for (int w = 0; w < 4; ++w)
+                    *reinterpret_cast<uint4 *>(to6 + (((4 * h + w) ^ swz) << 4)) =
+                        make_uint4(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3]);
+                if (h == 0 && lane == 0) sValid[4 * ((t - 1) & 1) + sp] = valid_before;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(k6_full);
+            }
+            two6 = two6_next;
+            pow6 = pow;
+            if (have) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (at) v = __ldg(reinterpret_cast<const uint4 *>(at + 32 * 7 + 16 * h));
+                raw6[0] = v.x;
+                raw6[1] = v.y;
+                raw6[2] = v.z;
+                raw6[3] = v.w;
+            }
+#pragma unroll
+            for (int m = 0; m < 3; ++m) {
+                if (before) {
+                    ok = __all_sync(0xFFFFFFFFu,
+                                    t < 2 || wait_bar(&v_free[m], t & 1, abort_flag, p.status));
+                    if (!ok) break;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t v[16];
+                        tmem_ld16(k_col + 64 * m + 16 * half, v);
+                        tmem_wait_ld();
+                        if (odd) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j] = finite2(v[j]);
+                        }
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            *reinterpret_cast<uint4 *>(to_v + 2 * m * kChunk +
+                                                       (((4 * half + w) ^ swz) << 4)) =
+                                make_uint4(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3]);
+                    }
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&v_full[m]);
+                }
+                if (have) {
+                    if (m == 0 && t > 0) {   // QK of block t - 1 has read what is overwritten
+                        ok = __all_sync(0xFFFFFFFFu, wait_bar(qa_done, (t - 1) & 1, abort_flag,
+                                                              p.status));
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const Units u = units_of((two[m] >> (16 * half)) & 0xFFFFu, pow);
+                        uint32_t v[16];
+                        unpack32(raw[m] + 4 * half, u, v);
+                        tmem_st16(k_col + 64 * m + 16 * half, v);
+                    }
+                    if (have_next) load_sector(raw[m], at_next, 32 * (2 * m + h + 1));
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tm_full[m]);
+                }
+            }
+            odd = odd_next;
+            before = have;
+            have = have_next;
+            at = at_next;
+            valid_before = valid;
+            valid = valid_next;
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        // ---------------- softmax + epilogue, 8 warps: TMEM lanes of sub-partition sp (keys,
+        // later dims) x rows [32 hh, 32 hh + 32)
+        const int sp = warp & 3;
+        const int hh = (warp - kSoftWarp0) >> 2;
+        const int hb = 32 * hh;
+        const int kl = sp * 32 + lane;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(sp * 32) << 16);
+        Walk walk(p, sStart);
+        Segment x;
+        int i = 0, g = 0, cur = 0;
+        for (; walk.next(p, x); ++i) {
+            uint64_t l[16];   // sums of rows 2 j and 2 j + 1, over this lane's keys
+#pragma unroll
+            for (int j = 0; j < 16; ++j) l[j] = 0;
+            if (sp == 0) sM[cur * 64 + hb + lane] = kNoMax;
+            bar_group(hh);
+            for (int b = 0; b < x.nb; ++b, ++g) {
+                const int k0 = x.block_pos(b);
+                const bool live = __all_sync(
+                    0xFFFFFFFFu, mbar_wait(s_full, g & 1, abort_flag, p.status));
+                // (complete since QK of this block waited for it: orders sValid before here)
+                mbar_wait(k6_full, g & 1, abort_flag, p.status);
+                tc_fence_after();
+                uint32_t sa[32];
+                if (live) tmem_ld32(lane_base + kSCol + hb, sa);
+                const uint32_t valid = sValid[4 * (g & 1) + sp];
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free);
+                // every row sees every key of the warp, unless ...
+                if (k0 + 32 * sp + 31 > x.posf || (p.window > 0 && k0 <= x.posl - p.window) ||
+                    valid != 0xFFFFFFFFu || !live) {
+                    // rows [ra, rb) of the unit see key k0 + kl: their token is not before it
+                    // and less than `window` after it, or it is one of the first
+                    const int64_t ahead = int64_t{k0} + kl - x.posf;
+                    const int ta = static_cast<int>(max(int64_t{0}, min(ahead, int64_t{64})));
+                    const int64_t gone =
+                        p.window > 0 && k0 + kl >= p.sinks ? ahead + p.window : 64;
+                    const int tb = static_cast<int>(max(int64_t{0}, min(gone, int64_t{64})));
+                    const int ra = min(64, ta * p.rpt);
+                    int rb = min(64, tb * p.rpt);
+                    if (!((valid >> lane) & 1u) || !live) rb = 0;
+                    // A row of the cache that holds an infinity or NaN makes its logit non-finite
+                    // in every row of q. Where a row of q must not see the key, those elements
+                    // become zero in the tile (0 * inf in PV would reach every row); rows that
+                    // do see the key have a NaN probability already, or with a logit of -inf
+                    // give it no weight. Chunks 0-5 are finite in shared memory; the others a key
+                    // at a time: lane = 16-byte piece of the two.
+                    const int a = max(0, min(32, ra - hb)), e = max(0, min(32, rb - hb));
+                    const uint32_t below_e = e == 32 ? 0xFFFFFFFFu : (1u << e) - 1u;
+                    const uint32_t below_a = a == 32 ? 0xFFFFFFFFu : (1u << a) - 1u;
+                    const uint32_t vis = below_e & ~below_a;
+                    uint64_t t2[2] = {0, 0};  // NaN if any is not finite
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        t2[j & 1] = fma_pair(pair_of(sa[2 * j], sa[2 * j + 1]), 0, t2[j & 1]);
+                    t2[0] = add_pair(t2[0], t2[1]);
+                    const bool odd = !(first_of(t2[0]) + second_of(t2[0]) == 0.0f);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (!((vis >> j) & 1u)) sa[j] = __float_as_uint(-INFINITY);
+                    uint32_t keys =
+                        __ballot_sync(0xFFFFFFFFu, odd && live && (ra > 0 || rb < x.nrows));
+                    if (keys) {
+                        mbar_wait(&r_full[g & 1], (g >> 1) & 1, abort_flag, p.status);
+                        uint8_t *tile = (lane & 8 ? smem + kOff7 + (g & 1) * kChunk : s6) +
+                                        sp * 4096 + (lane & 7) * 16;
+                        for (; keys && lane < 16; keys &= keys - 1) {
+                            uint4 *at = reinterpret_cast<uint4 *>(tile + (__ffs(keys) - 1) * 128);
+                            uint4 v = *at;
+                            v.x = finite2(v.x);
+                            v.y = finite2(v.y);
+                            v.z = finite2(v.z);
+                            v.w = finite2(v.w);
+                            *at = v;
+                        }
+                        __syncwarp();
+                    }
+                }
+                // how far the products lie above the running maximum: decides the rescale
+                const float4 *m4 = reinterpret_cast<const float4 *>(sM + cur * 64 + hb);
+                float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 m = m4[j];
+                    t[0] = fmaxf(t[0], __uint_as_float(sa[4 * j]) - m.x);
+                    t[1] = fmaxf(t[1], __uint_as_float(sa[4 * j + 1]) - m.y);
+                    t[2] = fmaxf(t[2], __uint_as_float(sa[4 * j + 2]) - m.z);
+                    t[3] = fmaxf(t[3], __uint_as_float(sa[4 * j + 3]) - m.w);
+                }
+                const float over = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+                if (vote_any_group(over * p.c > kRescale, hh)) {
+                    // exact block maxima -> new running maximum; sums and O^T rescaled
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float wm = redux_max(__uint_as_float(sa[j]));
+                        if (lane == j) sRed[sp * 64 + hb + j] = wm;
+                    }
+                    bar_group(hh);
+                    if (sp == 0) {
+                        const int r = hb + lane;
+                        const float bm = fmaxf(fmaxf(sRed[r], sRed[64 + r]),
+                                               fmaxf(sRed[128 + r], sRed[192 + r]));
+                        const float m_old = sM[cur * 64 + r];
+                        const float m_new = fmaxf(m_old, bm);
+                        sM[(cur ^ 1) * 64 + r] = m_new;
+                        sAlpha[r] = ex2((m_old - m_new) * p.c);
+                    }
+                    bar_group(hh);
+                    cur ^= 1;
+                    const uint64_t *alpha = reinterpret_cast<const uint64_t *>(sAlpha + hb);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) l[j] = mul_pair(l[j], alpha[j]);
+                    if (b > 0 && live) {
+                        mbar_wait(pv_done, (g & 1) ^ 1, abort_flag, p.status);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int m = 0; m < 8; ++m) {
+                            uint32_t oa[16];
+                            const uint32_t col = lane_base + kOCol + 64 * (m / 2) + hb + 16 * (m & 1);
+                            tmem_ld16(col, oa);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                oa[j] = __float_as_uint(__uint_as_float(oa[j]) *
+                                                        sAlpha[hb + 16 * (m & 1) + j]);
+                            tmem_st16(col, oa);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                // this thread's 32 rows of P^T for key kl. The sums take P as rounded to bf16, the
+                // values that PV multiplies.
+                uint32_t pk[16];
+                {
+                    const ulonglong2 *m2 =
+                        reinterpret_cast<const ulonglong2 *>(sM + cur * 64 + hb);
+                    const uint64_t c2 = pair_of(p.c), minus = pair_of(-1.0f);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const ulonglong2 m = m2[j];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint64_t s2 = pair_of(sa[4 * j + 2 * e], sa[4 * j + 2 * e + 1]);
+                            const uint64_t d = fma_pair(e ? m.y : m.x, minus, s2);
+                            const uint64_t y = mul_pair(d, c2);
+                            const __nv_bfloat162 v =
+                                __floats2bfloat162_rn(ex2(first_of(y)), ex2(second_of(y)));
+                            const uint32_t w = *reinterpret_cast<const uint32_t *>(&v);
+                            pk[2 * j + e] = w;
+                            l[2 * j + e] =
+                                add_pair(l[2 * j + e], pair_of(w << 16, w & 0xFFFF0000u));
+                        }
+                    }
+                }
+                // PV of the block before has used P
+                mbar_wait(pv_done, (g & 1) ^ 1, abort_flag, p.status);
+                {
+                    uint8_t *prow = sP + kl * 128;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint4 *>(prow + (((4 * hh + q) ^ (kl & 7)) << 4)) =
+                            make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full);
+            }
+            // ---- end of the segment: sums over the keys. Transpose-reduce the 32 partial
+            // sums across the warp: lane ends with the warp's total for row hb + lane
+            float lf[32];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                lf[2 * j] = first_of(l[j]);
+                lf[2 * j + 1] = second_of(l[j]);
+            }
+#pragma unroll
+            for (int w = 16; w >= 1; w >>= 1) {
+                const bool up = (lane & w) != 0;
+#pragma unroll
+                for (int j = 0; j < w; ++j) {
+                    const float send = up ? lf[j] : lf[j + w];
+                    const float keep = up ? lf[j + w] : lf[j];
+                    lf[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, w);
+                }
+            }
+            sL[sp * 64 + hb + lane] = lf[0];
+            bar_group(hh);
+            const int slot = 2 * cta + (i > 0);
+            if (sp == 0) {
+                // (each half's own warp: `cur` goes by the half)
+                const int r = hb + lane;
+                const float tot = sL[r] + sL[64 + r] + sL[128 + r] + sL[192 + r];
+                // a row that saw no key has sum 0 and O 0
+                sLinv[r] = tot == 0.0f ? 0.0f : 1.0f / tot;
+                if (!x.whole)
+                    reinterpret_cast<float2 *>(p.ws + kWsMl)[slot * kMaxRows + r] =
+                        make_float2(sM[cur * 64 + r], tot);
+            }
+            bar_group(hh);
+            // O^T into registers one d-tile at a time: lane holds dim 128 m + 32 sp + lane of
+            // rows hb .. hb + 31, so a warp writes 32 consecutive dims of each row
+            const bool live = mbar_wait(o_full, i & 1, abort_flag, p.status);
+            tc_fence_after();
+            const int rows = min(32, x.nrows - hb);
+            if (x.whole) {
+                __nv_bfloat16 *orow = p.out + (x.row + hb) * kD + 32 * sp + lane;
+#pragma unroll 1
+                for (int m = 0; m < 4; ++m) {
+                    uint32_t oa[32];
+                    if (!__all_sync(0xFFFFFFFFu, live)) break;
+                    tmem_ld32(lane_base + kOCol + 64 * m + hb, oa);
+                    tmem_wait_ld();
+                    __nv_bfloat16 *o = orow + 128 * m;
+                    if (p.b.cos_sin && m == 3 && sp >= 2) {
+                        // turned back by the token's position; a pair is in two adjacent lanes
+                        const float2 *cs = reinterpret_cast<const float2 *>(p.b.cos_sin) +
+                                           ((sp - 2) * 16 + (lane >> 1));
+                        // (a unit of one token's heads has one position)
+                        int pos = p.tpu == 1 ? x.posf : x.posf + hb / p.rpt;
+                        int left = p.tpu == 1 ? 32 : p.rpt - hb % p.rpt;  // rows at pos
+                        float2 a = __ldg(cs + int64_t{pos <= x.posl ? pos : x.posl} * kRopePairs);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float v = __uint_as_float(oa[j]) * sLinv[hb + j];
+                            const float w = __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+                            if (j < rows) {
+                                if (left == 0) {
+                                    ++pos;
+                                    left = p.rpt;
+                                    a = __ldg(cs + int64_t{pos} * kRopePairs);
+                                }
+                                --left;
+                                o[j * kD] = __float2bfloat16_rn(v * a.x + (lane & 1 ? -w : w) * a.y);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < rows)
+                                o[j * kD] =
+                                    __float2bfloat16_rn(__uint_as_float(oa[j]) * sLinv[hb + j]);
+                    }
+                }
+            } else {
+                float *orow = reinterpret_cast<float *>(p.ws + kWsO) +
+                              (int64_t{slot} * kRows + hb) * kD + 32 * sp + lane;
+#pragma unroll 1
+                for (int m = 0; m < 4; ++m) {
+                    uint32_t oa[32];
+                    if (!__all_sync(0xFFFFFFFFu, live)) break;
+                    tmem_ld32(lane_base + kOCol + 64 * m + hb, oa);
+                    tmem_wait_ld();
+                    float *o = orow + 128 * m;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j < rows) o[j * kD] = __uint_as_float(oa[j]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free);
+        }
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) o[k] *= inv;
-    if (cs) turn16(o, cs, -1.0f);
-    uint32_t w[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * k], o[2 * k + 1]);
-        w[k] = *reinterpret_cast<const uint32_t *>(&v);
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
     }
-    p.out[item * 64 + 2 * lane] = make_uint4(w[0], w[1], w[2], w[3]);
-    p.out[item * 64 + 2 * lane + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// ------------------------------------------------------------------ host
+
+std::mutex g_mu;
+int g_sms[kMaxDevices];   // 0: not set up yet
+
+// Per-device one-time set-up. A failure is not kept: it may pass (memory for the module's code).
+int setup(int *sms) {
+    const int dev = current_device();
+    if (dev < 0) return DSA_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (!g_sms[dev]) {
+        const int n = sm_count();
+        const int rc = n > 0 ? prepare_kernel(q4_attn_kernel, kRegsLaunch, kSmem) : DSA_ERR_CUDA;
+        if (rc != DSA_OK) return rc;
+        g_sms[dev] = n;
+    }
+    *sms = g_sms[dev];
+    return DSA_OK;
 }
 
 }  // namespace
@@ -138,10 +941,9 @@ extern "C" int dsa_paged_q4_attn(const void *q, int32_t heads, int64_t n_new,
     using namespace dsa;
     if (!q || !out || !aligned16(q) || !aligned16(out) || !aligned4(dev_status))
         return DSA_ERR_ARG;
-    Q4Args p;
-    const int rc = check_paged_batch(n_new, new_start, seq_len, n_seqs, page_table, max_pages,
-                                     pages, n_pages, page_stride, page_size, cos_sin, n_pos, &p.b,
-                                     kQ4PageRow);
+    SinkParams p;
+    int rc = check_paged_batch(n_new, new_start, seq_len, n_seqs, page_table, max_pages, pages,
+                               n_pages, page_stride, page_size, cos_sin, n_pos, &p.b, kQ4PageRow);
     if (rc != DSA_OK) return rc;
     const float c = scale * 1.4426950408889634f;
     if (heads < 1 || heads > DSA_MAX_PAGED_HEADS || window < 0 || sinks < 0 ||
@@ -152,19 +954,39 @@ extern "C" int dsa_paged_q4_attn(const void *q, int32_t heads, int64_t n_new,
     const uint64_t used = DSA_PAGED_WORKSPACE_BYTES;
     if (overlaps(q, bytes, out, bytes) || touches_pages(p.b, pages, out, bytes, kQ4PageRow))
         return DSA_ERR_ARG;
+    p.heads = heads;
+    p.rows = kRows;
+    p.tpu = heads <= kRows ? kRows / heads : 1;
+    p.upt = (heads + kRows - 1) / kRows;
+    p.row_step = kRows;
+    p.rpt = std::min(heads, p.rows);
+    // a window no shorter than any sequence is no window
+    p.window = window >= p.b.len_limit ? 0 : window;
+    p.sinks = p.window > 0 ? sinks : 0;
+    p.turn_q = !q_turned;
+    const int64_t keys =
+        p.window > 0 ? std::min(p.b.len_limit, p.window + p.tpu) + kBlock : p.b.len_limit;
+    if (paged_run_bound(p, keys) > (int64_t{1} << 31) - 1) return DSA_ERR_SHAPE;
     if (!workspace || !aligned16(workspace) || workspace_bytes < used) return DSA_ERR_SCRATCH;
     if (overlaps(workspace, used, q, bytes) || overlaps(workspace, used, out, bytes) ||
         touches_pages(p.b, pages, workspace, used, kQ4PageRow))
         return DSA_ERR_ARG;
-    p.q = static_cast<const uint4 *>(q);
-    p.pages = static_cast<const uint8_t *>(pages);
-    p.out = static_cast<uint4 *>(out);
-    p.heads = heads;
-    p.window = window;
-    p.sinks = window > 0 ? sinks : 0;
-    p.q_turned = q_turned;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    // whole lines (the caller's buffer begins on 16 bytes at least)
+    p.ws = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(workspace) + (kWsAlign - 1)) &
+                                       ~uintptr_t{kWsAlign - 1});
     p.c = c;
     p.status = dev_status;
-    return launch_overlapped(q4_attn_kernel, static_cast<unsigned>((n_new * heads + 7) / 8), 256, 0,
-                             static_cast<cudaStream_t>(stream), p);
+    int sms = 0;
+    rc = setup(&sms);
+    if (rc != DSA_OK) return rc;
+    CUtensorMap tm_q, tm_kv;
+    if (!make_tmap_bf16(&tm_q, q, kD, static_cast<uint64_t>(n_new) * heads, kD * 2, 64, p.rows) ||
+        !make_tmap_pages(&tm_kv, pages, p.b, kQ4PageRow))
+        return DSA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int ctas = std::min(sms, kMaxCtas);
+    rc = launch_overlapped(q4_attn_kernel, ctas, kT, kSmem, s, tm_q, tm_kv, p,
+                           static_cast<const uint8_t *>(pages));
+    return rc == DSA_OK ? enqueue_paged_join(p, ctas, s) : rc;
 }

@@ -463,8 +463,8 @@ int dsa_qk_norm_rope(const void *q, int32_t heads, const void *kv, int64_t n_new
  * The paged cache in 4 bits: the same batch, page tables and positions with rows of
  * DSA_Q4_ROW_BYTES = 384 bytes, where a bf16 row takes 1,024. The pages have no counterpart.
  *
- *   pages [n_pages] of [page_size] rows, page_stride BYTES from one page to the next
- *     (>= page_size*384, a multiple of 16).
+ *   pages [n_pages] of [page_size] rows, 32-byte aligned, page_stride BYTES from one page to the
+ *     next (>= page_size*384, a multiple of 32).
  *   A row: its dims 0..447 in 4 bits with a scale for each 16 of them, and its last 64 dims, the
  *   rotated ones, in bf16 (positions live there). With A the largest of the 448 magnitudes and
  *   E = max(floor(log2 A), -113) - 10, a group of 16 has the scale s = (its largest magnitude)

@@ -478,7 +478,7 @@ def test_pages_far_apart_pass_32_bit_offsets(dsa, workspace):
     lens = [(3, 150), (1, 64)]
     batch = Q.make(lens, 64, extra_pages=0, seed=17)
     n_pages = batch["pages"].shape[0]
-    stride = (1 << 33) // (n_pages - 1) // 16 * 16 + 64 * 384
+    stride = (1 << 33) // (n_pages - 1) // 32 * 32 + 64 * 384
     store = torch.empty(n_pages * stride, dtype=torch.uint8, device="cuda")
     pages = store.as_strided((n_pages, 64, 384), (stride, 384, 1))
     pages.copy_(batch["pages"])
@@ -499,13 +499,13 @@ def test_pages_far_apart_pass_32_bit_offsets(dsa, workspace):
 
 
 def test_writes_stay_inside_the_buffers(dsa):
-    """Canaries around the outputs, the workspace and the pages, each 16 bytes off 32."""
-    guard = 4096 + 16
+    """Canaries around the outputs, the workspace and the pages, each 16 bytes off 32 (the pages 32
+    off 64)."""
     batch = Q.make([(1, 900), (3, 129), (40, 77)], 32, seed=18)
     gb = to_gpu(batch)
     q = queries(batch, 24, 11)
 
-    def guarded(shape, dtype):
+    def guarded(shape, dtype, guard=4096 + 16):
         n = math.prod(shape) * dtype.itemsize
         buf = torch.full((n + 2 * guard,), 5, dtype=torch.uint8, device="cuda")
         return buf, buf[guard:guard + n].view(dtype).view(shape)
@@ -513,7 +513,7 @@ def test_writes_stay_inside_the_buffers(dsa):
     ob, out = guarded(q.shape, torch.bfloat16)
     rb, rows = guarded((q.shape[0], 512), torch.bfloat16)
     wb, work = guarded((B.DSA_PAGED_WORKSPACE_BYTES,), torch.uint8)
-    pb, pages = guarded(batch["pages"].shape, torch.uint8)
+    pb, pages = guarded(batch["pages"].shape, torch.uint8, 4096 + 32)
     kb, kv = guarded((q.shape[0], 512), torch.bfloat16)
     qb, qd = guarded(q.shape, torch.bfloat16)
     qd.copy_(q)
@@ -525,7 +525,7 @@ def test_writes_stay_inside_the_buffers(dsa):
     B.dsa_paged_q4_attn(qd, *a, 0, 0, SCALE, work, out, gb["cos_sin"])
     torch.cuda.synchronize()
     for buf in (ob, rb, wb, pb, kb, qb):
-        assert bool((buf[:guard] == 5).all()) and bool((buf[-guard:] == 5).all())
+        assert bool((buf[:4112] == 5).all()) and bool((buf[-4112:] == 5).all())
     ref, tol = Q.append(batch, kv.cpu())
     check_pages(pages.cpu(), ref, tol)
     batch["pages"] = pages.cpu()

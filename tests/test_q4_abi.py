@@ -46,12 +46,13 @@ BATCH = [
 PAGES = BATCH + [
     (dict(page_table=None), B.DSA_ERR_ARG), (dict(pages=None), B.DSA_ERR_ARG),
     (dict(max_pages=0), B.DSA_ERR_ARG), (dict(n_pages=0), B.DSA_ERR_ARG),
-    (dict(pages=FAKE + 8), B.DSA_ERR_ARG),
+    (dict(pages=FAKE + 8), B.DSA_ERR_ARG), (dict(pages=FAKE + 16), B.DSA_ERR_ARG),
     (dict(page_size=8, page_stride=8 * 384), B.DSA_ERR_SHAPE),
     (dict(page_size=48), B.DSA_ERR_SHAPE),
     (dict(page_size=2048, page_stride=2048 * 384), B.DSA_ERR_SHAPE),
-    (dict(page_stride=64 * 384 - 16), B.DSA_ERR_SHAPE),
+    (dict(page_stride=64 * 384 - 32), B.DSA_ERR_SHAPE),
     (dict(page_stride=64 * 384 + 8), B.DSA_ERR_SHAPE),
+    (dict(page_stride=64 * 384 + 16), B.DSA_ERR_SHAPE),
     (dict(page_stride=1 << 39), B.DSA_ERR_SHAPE), (dict(n_pages=1 << 31), B.DSA_ERR_SHAPE),
     (dict(max_pages=1 << 25), B.DSA_ERR_SHAPE),
 ]
