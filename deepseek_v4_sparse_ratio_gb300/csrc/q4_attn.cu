@@ -45,9 +45,6 @@ constexpr int kTurnWarp0 = 2;      // two warps: a row of q a thread
 constexpr int kUnpackWarp0 = 4;
 constexpr int kSoftWarp0 = 12;
 constexpr int kRegsLaunch = 96;
-constexpr int kRegsMisc = 80;
-constexpr int kRegsUnpack = 80;
-constexpr int kRegsSoft = 120;     // 128*80 + 256*80 + 256*120 = 640*96, the launch allocation
 
 constexpr int kRows = 64;          // rows of q in a unit (MMA N)
 constexpr int kDescs = 4;          // blocks whose pages are known ahead
@@ -61,7 +58,7 @@ constexpr uint32_t kOff7 = kOff6 + kChunk;        // chunk 7, by block parity
 constexpr uint32_t kOffP = kOff7 + 2 * kChunk;    // P^T [128 keys x 64 rows] bf16
 constexpr uint32_t kOffRed = kOffP + 16384;       // [4][64] block maxima | partial sums
 constexpr uint32_t kOffLinv = kOffRed + 1024;     // [64] rescale factors | 1/sum
-constexpr uint32_t kOffM = kOffLinv + 256;        // [2][64] running maximum, double-buffered
+constexpr uint32_t kOffM = kOffLinv + 256;        // [2][64] running maximum, negated, double-buffered
 constexpr uint32_t kOffDesc = kOffM + 512;        // [kDescs] pages of a block
 constexpr uint32_t kOffBar = kOffDesc + kDescs * 80;
 constexpr uint32_t kSmem = kOffBar + 384;
@@ -73,7 +70,7 @@ constexpr uint32_t kSCol = 256;    // S^T
 constexpr uint32_t kKCol = 320;    // chunks 0-5 of K, 32 columns each
 
 // The pages of a block, for the unpackers.
-struct Desc {
+struct alignas(16) Desc {
     const uint8_t *row[8];  // the first row that the block has in each page (null: none needed)
     int a, b, c;            // keys [a, b) and those below c are seen by some token
     int more;               // 0: the run has ended
@@ -90,15 +87,26 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r) {
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *r) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15}, [%16];"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+          "=r"(r[7])
         : "r"(taddr)
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
@@ -123,35 +131,41 @@ __device__ __forceinline__ void load_sector(uint32_t *v, const uint8_t *row, int
             : "l"(row + at));
 }
 
-// Two scales (e4m3, 16 bits) times the row's power of two: for either group u / 2 and -72 u, twice.
-struct Units {
-    __nv_bfloat162 half[2], off[2];
-};
-__device__ __forceinline__ Units units_of(uint32_t two, float half_pow) {
+// Four words (32 dims) as 16 pairs of bf16. `two`: the scales of their two groups (e4m3, the lower
+// 16 bits); half_pow: half of the row's power of two.
+__device__ __forceinline__ void unpack32(const uint32_t *w, uint32_t two, float half_pow,
+                                         uint32_t *out) {
     const __half2_raw h =
         __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
     const float2 s = __half22float2(__half2(h));
-    Units u;
-    u.half[0] = __float2bfloat162_rn(s.x * half_pow);
-    u.half[1] = __float2bfloat162_rn(s.y * half_pow);
-    const __nv_bfloat162 k = __float2bfloat162_rn(-144.0f);   // (144 u / 2: eight bits, exact)
-    u.off[0] = __hmul2(u.half[0], k);
-    u.off[1] = __hmul2(u.half[1], k);
-    return u;
-}
-
-// Four words (32 dims) as 16 pairs of bf16.
-__device__ __forceinline__ void unpack32(const uint32_t *w, const Units &u, uint32_t *out) {
+    const __nv_bfloat162 half[2] = {__float2bfloat162_rn(s.x * half_pow),
+                                    __float2bfloat162_rn(s.y * half_pow)};
+    const __nv_bfloat162 k144 = __float2bfloat162_rn(-144.0f);   // (144 u / 2: eight bits, exact)
+    const __nv_bfloat162 off[2] = {__hmul2(half[0], k144), __hmul2(half[1], k144)};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) out[4 * j + k] = q4_pair(w[j], k, u.half[j / 2], u.off[j / 2]);
+        for (int k = 0; k < 4; ++k) out[4 * j + k] = q4_pair(w[j], k, half[j / 2], off[j / 2]);
 }
 
 // Whether a word holds an e4m3 NaN (0x7F or 0xFF) in its bytes under `mask`.
 __device__ __forceinline__ bool has_nan(uint32_t w) {
     const uint32_t x = ~w & 0x7F7F7F7Fu;   // a byte 0 where all seven bits are set
     return ((x - 0x01010101u) & ~x & 0x80808080u) != 0;
+}
+
+// A chunk's row of a key in shared memory without its infinities and NaN.
+static __device__ __noinline__ void make_finite(uint8_t *row) {
+#pragma unroll 1
+    for (int w = 0; w < 8; ++w) {
+        uint4 *at = reinterpret_cast<uint4 *>(row) + w;
+        uint4 v = *at;
+        v.x = finite2(v.x);
+        v.y = finite2(v.y);
+        v.z = finite2(v.z);
+        v.w = finite2(v.w);
+        *at = v;
+    }
 }
 
 // The softmax warps form two groups of four, one per half of the rows (named barriers 1 and
@@ -169,6 +183,32 @@ __device__ __forceinline__ bool vote_any_group(bool pred, int hh) {
 
 __device__ __forceinline__ void bar_group(int hh) {
     asm volatile("bar.sync %0, 128;" ::"r"(1 + hh) : "memory");
+}
+
+// Products that a row of q must not see become -inf.
+__device__ __forceinline__ void hide32(uint32_t (&s)[32], uint32_t vis) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (!((vis >> j) & 1u)) s[j] = __float_as_uint(-INFINITY);
+}
+
+// s += the negated running maxima; the largest of the 32.
+__device__ __forceinline__ float less_max(uint32_t (&s)[32], const float *minus_m) {
+    const ulonglong2 *m2 = reinterpret_cast<const ulonglong2 *>(minus_m);
+    float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const ulonglong2 m = m2[j];
+        const uint64_t a = add_pair(pair_of(s[4 * j], s[4 * j + 1]), m.x);
+        const uint64_t b = add_pair(pair_of(s[4 * j + 2], s[4 * j + 3]), m.y);
+        t[j & 1] = max3(t[j & 1], first_of(a), second_of(a));
+        t[2 + (j & 1)] = max3(t[2 + (j & 1)], first_of(b), second_of(b));
+        s[4 * j] = __float_as_uint(first_of(a));
+        s[4 * j + 1] = __float_as_uint(second_of(a));
+        s[4 * j + 2] = __float_as_uint(first_of(b));
+        s[4 * j + 3] = __float_as_uint(second_of(b));
+    }
+    return max3(fmaxf(t[0], t[1]), t[2], t[3]);
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -251,7 +291,6 @@ __global__ void __launch_bounds__(kT, 1)
     const uint32_t tmem = *tmem_holder;
 
     if (warp < kUnpackWarp0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMisc));
         if (warp == 0) {
             // ---------------- pages: lane i < np has page i of a block. Descriptors run two
             // blocks ahead of the loads of chunk 7 (which wait for PV), as the unpackers do.
@@ -334,112 +373,106 @@ __global__ void __launch_bounds__(kT, 1)
             bool have = walk.next(p, x);
             const bool turn = p.b.cos_sin && p.turn_q;
 
-            auto pv_tile = [&](int m, int gb, bool first) {
-                // tile m of PV of block gb: dims 128 m ..
-                const uint32_t base =
-                    smem_u32(smem) + (m < 3 ? kOffV + 2 * m * kChunk : kOff6);
-                const uint32_t lbo = m < 3 || !(gb & 1) ? kChunk : 2 * kChunk;
-                if (elect_one()) {
-                    const uint64_t ad = desc_sw128(base, lbo, 1024);
-                    const uint64_t bd = desc_sw128(smem_u32(sP), 8192, 1024);
-#pragma unroll 4
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16(tmem + kOCol + 64 * m, ad + ((kk * 2048) >> 4),
-                                 bd + ((kk * 2048) >> 4), idesc_pv, kk > 0 || !first);
-                    mma_commit(&v_free[m]);
-                }
-                __syncwarp();
-            };
-            // PV's last tile first: its chunk 6 is what QK of the next block waits for
-            auto pv_begin = [&]() -> bool {
-                const int gb = g - 1;
-                if (!wait_bar(p_full, gb & 1, abort_flag, p.status)) return false;
-                if (pend_first && ends > 0 &&
-                    !wait_bar(o_free, (ends - 1) & 1, abort_flag, p.status))
-                    return false;
-                tc_fence_after();
-                pv_tile(3, gb, pend_first);
-                if (!wait_bar(&v_full[0], gb & 1, abort_flag, p.status)) return false;
-                tc_fence_after();
-                pv_tile(0, gb, pend_first);
-                return true;
-            };
-            auto pv_end = [&]() -> bool {
-                const int gb = g - 1;
-#pragma unroll 1
-                for (int m = 1; m < 3; ++m) {
-                    if (!wait_bar(&v_full[m], gb & 1, abort_flag, p.status)) return false;
-                    tc_fence_after();
-                    pv_tile(m, gb, pend_first);
-                }
-                if (elect_one()) {
-                    mma_commit(pv_done);
-                    if (pend_last) mma_commit(o_full);
-                }
-                __syncwarp();
-                if (pend_last) ++ends;
-                return true;
-            };
-
-            for (int b = 0; ok && have;) {
+            // One pass per block, and one more where PV of the last block has no QK to go with:
+            // before new queries, and at the end. (One copy of each product's code: every byte of
+            // it is fetched anew in every pass.)
+            for (int b = 0; ok && (have || pend);) {
                 const bool fresh = b == 0;
-                if (fresh) {
-                    ++i;
-                    if (pend && !(ok = pv_begin() && pv_end())) break;
-                    pend = false;
-                    if (!(ok = wait_bar(q_full, i & 1, abort_flag, p.status))) break;
-                }
-                // QK, chunks 0-5
-                if (!(ok = wait_bar(s_free, (g & 1) ^ 1, abort_flag, p.status))) break;
-#pragma unroll 1
-                for (int m = 0; m < 3 && ok; ++m) {
-                    if (!(ok = wait_bar(&tm_full[m], g & 1, abort_flag, p.status))) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t bd = desc_sw128(smem_u32(sQ) + 2 * m * 8192, 16, 1024);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_bf16_ta(tmem + kSCol, tmem + kKCol + 64 * m + 8 * k,
-                                        bd + (k / 4) * (8192 >> 4) + 2 * (k % 4), idesc_qk,
-                                        m > 0 || k > 0);
-                        if (m == 2) mma_commit(qa_done);
+                const bool qk = have && !(fresh && pend);
+                const bool last = b == x.nb - 1;
+                if (qk) {
+                    if (fresh) {
+                        ++i;
+                        if (!(ok = wait_bar(q_full, i & 1, abort_flag, p.status))) break;
                     }
-                    __syncwarp();
+                    // QK, chunks 0-5
+                    if (!(ok = wait_bar(s_free, (g & 1) ^ 1, abort_flag, p.status))) break;
+#pragma unroll 1
+                    for (int m = 0; m < 3; ++m) {
+                        if (!(ok = wait_bar(&tm_full[m], g & 1, abort_flag, p.status))) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t bd = desc_sw128(smem_u32(sQ) + 2 * m * 8192, 16, 1024);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                mma_bf16_ta(tmem + kSCol, tmem + kKCol + 64 * m + 8 * k,
+                                            bd + (k / 4) * (8192 >> 4) + 2 * (k % 4), idesc_qk,
+                                            m > 0 || k > 0);
+                            if (m == 2) mma_commit(qa_done);
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                }
+#pragma unroll 1
+                for (int st = 0; st < 4; ++st) {
+                    if (pend) {
+                        // tile m of PV of block g - 1, dims 128 m ..; the last one first, as its
+                        // chunk 6 is what QK of the next block waits for
+                        const int gb = g - 1, m = (st + 3) & 3;
+                        if (st == 0) {
+                            ok = wait_bar(p_full, gb & 1, abort_flag, p.status);
+                            if (ok && pend_first && ends > 0)
+                                ok = wait_bar(o_free, (ends - 1) & 1, abort_flag, p.status);
+                        } else {
+                            ok = wait_bar(&v_full[m], gb & 1, abort_flag, p.status);
+                        }
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t ad = desc_sw128(
+                                smem_u32(smem) + (st > 0 ? kOffV + 2 * m * kChunk : kOff6),
+                                st > 0 || !(gb & 1) ? kChunk : 2 * kChunk, 1024);
+                            const uint64_t bd = desc_sw128(smem_u32(sP), 8192, 1024);
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                mma_bf16(tmem + kOCol + 64 * m, ad + ((kk * 2048) >> 4),
+                                         bd + ((kk * 2048) >> 4), idesc_pv,
+                                         kk > 0 || !pend_first);
+                            mma_commit(&v_free[m]);
+                            if (st == 3) {
+                                mma_commit(pv_done);
+                                if (pend_last) mma_commit(o_full);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (st == 1 && qk) {
+                        // QK, chunk 6 and chunk 7
+                        ok = wait_bar(k6_full, g & 1, abort_flag, p.status) &&
+                             wait_bar(&r_full[g & 1], (g >> 1) & 1, abort_flag, p.status);
+                        if (ok && fresh && turn)
+                            ok = wait_bar(q_turned, i & 1, abort_flag, p.status);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t bd = desc_sw128(smem_u32(sQ) + 6 * 8192, 16, 1024);
+                            const uint64_t a6 = desc_sw128(smem_u32(s6), 16, 1024);
+                            const uint64_t a7 = desc_sw128(
+                                smem_u32(smem) + kOff7 + (g & 1) * kChunk, 16, 1024);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                mma_bf16(tmem + kSCol, (k < 4 ? a6 : a7) + 2 * (k % 4),
+                                         bd + (k / 4) * (8192 >> 4) + 2 * (k % 4), idesc_qk, 1u);
+                            mma_commit(s_full);
+                            if (last) mma_commit(q_free);
+                        }
+                        __syncwarp();
+                    }
                 }
                 if (!ok) break;
-                if (pend && !(ok = pv_begin())) break;
-                // QK, chunk 6 and chunk 7
-                if (!(ok = wait_bar(k6_full, g & 1, abort_flag, p.status) &&
-                           wait_bar(&r_full[g & 1], (g >> 1) & 1, abort_flag, p.status)))
-                    break;
-                if (fresh && turn && !(ok = wait_bar(q_turned, i & 1, abort_flag, p.status)))
-                    break;
-                tc_fence_after();
-                const bool last = b == x.nb - 1;
-                if (elect_one()) {
-                    const uint64_t bd = desc_sw128(smem_u32(sQ) + 6 * 8192, 16, 1024);
-                    const uint64_t a6 = desc_sw128(smem_u32(s6), 16, 1024);
-                    const uint64_t a7 = desc_sw128(smem_u32(smem) + kOff7 + (g & 1) * kChunk, 16,
-                                                   1024);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_bf16(tmem + kSCol, (k < 4 ? a6 : a7) + 2 * (k % 4),
-                                 bd + (k / 4) * (8192 >> 4) + 2 * (k % 4), idesc_qk, 1u);
-                    mma_commit(s_full);
-                    if (last) mma_commit(q_free);
-                }
-                __syncwarp();
-                if (pend && !(ok = pv_end())) break;
-                pend = true;
-                pend_first = fresh;
-                pend_last = last;
-                ++g;
-                if (++b == x.nb) {
-                    b = 0;
-                    have = walk.next(p, x);
+                if (pend && pend_last) ++ends;
+                pend = qk;
+                if (qk) {
+                    pend_first = fresh;
+                    pend_last = last;
+                    ++g;
+                    if (++b == x.nb) {
+                        b = 0;
+                        have = walk.next(p, x);
+                    }
                 }
             }
-            if (ok && pend) ok = pv_begin() && pv_end();
             if (elect_one()) {
                 mma_commit(drain);
                 drain_wait(drain, 0);
@@ -495,7 +528,6 @@ __global__ void __launch_bounds__(kT, 1)
             __syncwarp();
         }
     } else if (warp < kSoftWarp0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
         // ---------------- unpacking. Step t: chunk 6 of block t - 1, then pair by pair the chunks
         // of block t - 1 from TMEM to shared memory and those of block t into TMEM; behind each
         // of them the load of the same chunk of block t + 1.
@@ -508,9 +540,9 @@ __global__ void __launch_bounds__(kT, 1)
         const int page_shift = min(p.b.page_shift, 7);
 
         uint32_t raw[3][8], raw6[4] = {}, head[8];
-        uint32_t two[3] = {}, two6 = 0, two6_next = 0;   // scales of a chunk's halves, of chunk 6
-        float pow = 0.0f, pow6 = 0.0f;                   // half of the row's power of two
-        bool odd = false, odd_next = false;              // a scale that is NaN
+        uint32_t two[3] = {}, two6 = 0;      // scales of a chunk's halves, of chunk 6
+        float pow = 0.0f;                    // half of the row's power of two
+        bool odd = false;                    // a scale that is NaN, in the block to be copied
 
         // The row of block t (null: not to be read) and which keys of the warp have one.
         auto fetch = [&](int t, bool &have, uint32_t &valid) -> const uint8_t * {
@@ -518,46 +550,32 @@ __global__ void __launch_bounds__(kT, 1)
             const bool ok = __all_sync(0xFFFFFFFFu, wait_bar(&d_full[d], (t / kDescs) & 1,
                                                              abort_flag, p.status));
             const Desc &x = sDesc[d];
-            have = ok && x.more;
-            const uint8_t *row = nullptr;
-            if (have && key < x.b && (key >= x.a || key < x.c)) {
-                row = x.row[key >> page_shift];
-                if (row) row += (key & ((1 << page_shift) - 1)) * kQ4Row;
-            }
+            const int4 range = *reinterpret_cast<const int4 *>(&x.a);   // a, b, c, more
+            const uint8_t *row = x.row[key >> page_shift];
+            have = ok && range.w;
+            if (!have || key >= range.y || (key < range.x && key >= range.z)) row = nullptr;
             valid = __ballot_sync(0xFFFFFFFFu, row != nullptr);
+            if (row) row += (key & ((1 << page_shift) - 1)) * kQ4Row;
             if (lane == 0) mbar_arrive(&d_free[d]);
             return row;
         };
 
-        bool have, have_next;
-        uint32_t valid = 0, valid_next = 0, valid_before = 0;
+        bool have, before = false;           // block t is there, block t - 1 is to be copied
+        uint32_t valid;
         const uint8_t *at = fetch(0, have, valid);
         load_sector(head, at, 0);
 #pragma unroll
         for (int m = 0; m < 3; ++m) load_sector(raw[m], at, 32 * (2 * m + h + 1));
-        bool ok = true, before = false;                  // before: block t - 1 is to be copied
-        for (int t = 0; ok && (have || before); ++t) {
-            // the scales of block t
-            if (have) {
-#pragma unroll
-                for (int m = 0; m < 3; ++m)   // chunk 2 m + h: bytes 4 m + 2 h of either half
-                    two[m] = __byte_perm(head[m], head[4 + m], h ? 0x7632 : 0x5410);
-                // chunk 6, half h: bytes 12 and 13
-                two6_next = h ? head[7] : head[3];
-                odd_next = has_nan(two[0]) || has_nan(two[1]) || has_nan(two[2]);
-                pow = pow2(max(static_cast<int>((head[3] >> 16) & 0xFFu), 11) - 138);
-            }
-            const uint8_t *const at_next =
-                have ? fetch(t + 1, have_next, valid_next) : (have_next = false, nullptr);
-            if (have_next) load_sector(head, at_next, 0);
-            if (t > 0) {
+        uint32_t valid_before = 0;
+        bool ok = true;
+        for (int t = 0; have || before; ++t) {
+            if (before) {
                 // chunk 6 of block t - 1, in the place that PV of block t - 2 has left
                 ok = __all_sync(0xFFFFFFFFu,
                                 t < 2 || wait_bar(&v_free[3], t & 1, abort_flag, p.status));
                 if (!ok) break;
-                const Units u = units_of(two6 & 0xFFFFu, pow6);
                 uint32_t v[16];
-                unpack32(raw6, u, v);
+                unpack32(raw6, two6 & 0xFFFFu, pow, v);
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
                     *reinterpret_cast<uint4 *>(to6 + (((4 * h + w) ^ swz) << 4)) =
@@ -567,8 +585,9 @@ __global__ void __launch_bounds__(kT, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(k6_full);
             }
-            two6 = two6_next;
-            pow6 = pow;
+            // block t: its chunk 6 and scales; the row and the scales of block t + 1
+            bool odd_next = false, have_next = false;
+            valid_before = valid;
             if (have) {
                 uint4 v = make_uint4(0, 0, 0, 0);
                 if (at) v = __ldg(reinterpret_cast<const uint4 *>(at + 32 * 7 + 16 * h));
@@ -576,6 +595,14 @@ __global__ void __launch_bounds__(kT, 1)
                 raw6[1] = v.y;
                 raw6[2] = v.z;
                 raw6[3] = v.w;
+#pragma unroll
+                for (int m = 0; m < 3; ++m)   // chunk 2 m + h: bytes 4 m + 2 h of either half
+                    two[m] = __byte_perm(head[m], head[4 + m], h ? 0x7632 : 0x5410);
+                two6 = h ? head[7] : head[3];  // chunk 6, half h: bytes 12 and 13
+                odd_next = has_nan(two[0]) || has_nan(two[1]) || has_nan(two[2]);
+                pow = pow2(max(static_cast<int>((head[3] >> 16) & 0xFFu), 11) - 138);
+                at = fetch(t + 1, have_next, valid);
+                if (have_next) load_sector(head, at, 0);
             }
 #pragma unroll
             for (int m = 0; m < 3; ++m) {
@@ -583,28 +610,21 @@ __global__ void __launch_bounds__(kT, 1)
                     ok = __all_sync(0xFFFFFFFFu,
                                     t < 2 || wait_bar(&v_free[m], t & 1, abort_flag, p.status));
                     if (!ok) break;
+                    uint32_t v[32];
+                    tmem_ld32(k_col + 64 * m, v);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t v[16];
-                        tmem_ld16(k_col + 64 * m + 16 * half, v);
-                        tmem_wait_ld();
-                        if (odd) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) v[j] = finite2(v[j]);
-                        }
-#pragma unroll
-                        for (int w = 0; w < 4; ++w)
-                            *reinterpret_cast<uint4 *>(to_v + 2 * m * kChunk +
-                                                       (((4 * half + w) ^ swz) << 4)) =
-                                make_uint4(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3]);
-                    }
+                    for (int w = 0; w < 8; ++w)
+                        *reinterpret_cast<uint4 *>(to_v + 2 * m * kChunk + ((w ^ swz) << 4)) =
+                            make_uint4(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3]);
+                    if (odd) make_finite(to_v + 2 * m * kChunk);
                     fence_proxy_async_smem();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&v_full[m]);
                 }
                 if (have) {
-                    if (m == 0 && t > 0) {   // QK of block t - 1 has read what is overwritten
+                    if (m == 0 && before) {   // QK of block t - 1 has read what is overwritten
                         ok = __all_sync(0xFFFFFFFFu, wait_bar(qa_done, (t - 1) & 1, abort_flag,
                                                               p.status));
                         if (!ok) break;
@@ -612,27 +632,23 @@ __global__ void __launch_bounds__(kT, 1)
                     }
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        const Units u = units_of((two[m] >> (16 * half)) & 0xFFFFu, pow);
                         uint32_t v[16];
-                        unpack32(raw[m] + 4 * half, u, v);
+                        unpack32(raw[m] + 4 * half, (two[m] >> (16 * half)) & 0xFFFFu, pow, v);
                         tmem_st16(k_col + 64 * m + 16 * half, v);
                     }
-                    if (have_next) load_sector(raw[m], at_next, 32 * (2 * m + h + 1));
+                    if (have_next) load_sector(raw[m], at, 32 * (2 * m + h + 1));
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&tm_full[m]);
                 }
             }
+            if (!ok) break;
             odd = odd_next;
             before = have;
             have = have_next;
-            at = at_next;
-            valid_before = valid;
-            valid = valid_next;
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
         // ---------------- softmax + epilogue, 8 warps: TMEM lanes of sub-partition sp (keys,
         // later dims) x rows [32 hh, 32 hh + 32)
         const int sp = warp & 3;
@@ -647,7 +663,7 @@ __global__ void __launch_bounds__(kT, 1)
             uint64_t l[16];   // sums of rows 2 j and 2 j + 1, over this lane's keys
 #pragma unroll
             for (int j = 0; j < 16; ++j) l[j] = 0;
-            if (sp == 0) sM[cur * 64 + hb + lane] = kNoMax;
+            if (sp == 0) sM[cur * 64 + hb + lane] = -kNoMax;
             bar_group(hh);
             for (int b = 0; b < x.nb; ++b, ++g) {
                 const int k0 = x.block_pos(b);
@@ -656,18 +672,19 @@ __global__ void __launch_bounds__(kT, 1)
                 // (complete since QK of this block waited for it: orders sValid before here)
                 mbar_wait(k6_full, g & 1, abort_flag, p.status);
                 tc_fence_after();
+                const uint32_t s_col = lane_base + kSCol + hb;
                 uint32_t sa[32];
-                if (live) tmem_ld32(lane_base + kSCol + hb, sa);
                 const uint32_t valid = sValid[4 * (g & 1) + sp];
-                tmem_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(s_free);
+                if (live) tmem_ld32(s_col, sa);
+                uint32_t vis = 0xFFFFFFFFu;   // rows hb + j that see key k0 + kl
                 // every row sees every key of the warp, unless ...
-                if (k0 + 32 * sp + 31 > x.posf || (p.window > 0 && k0 <= x.posl - p.window) ||
-                    valid != 0xFFFFFFFFu || !live) {
-                    // rows [ra, rb) of the unit see key k0 + kl: their token is not before it
-                    // and less than `window` after it, or it is one of the first
+                const bool masked = k0 + 32 * sp + 31 > x.posf ||
+                                    (p.window > 0 && k0 <= x.posl - p.window) ||
+                                    valid != 0xFFFFFFFFu || !live;
+                tmem_wait_ld();
+                if (masked) {
+                    // rows [ra, rb) of the unit see the key: their token is not before it and
+                    // less than `window` after it, or it is one of the first
                     const int64_t ahead = int64_t{k0} + kl - x.posf;
                     const int ta = static_cast<int>(max(int64_t{0}, min(ahead, int64_t{64})));
                     const int64_t gone =
@@ -676,31 +693,30 @@ __global__ void __launch_bounds__(kT, 1)
                     const int ra = min(64, ta * p.rpt);
                     int rb = min(64, tb * p.rpt);
                     if (!((valid >> lane) & 1u) || !live) rb = 0;
+                    const int a = max(0, min(32, ra - hb)), e = max(0, min(32, rb - hb));
+                    const uint32_t below_e = e == 32 ? 0xFFFFFFFFu : (1u << e) - 1u;
+                    const uint32_t below_a = a == 32 ? 0xFFFFFFFFu : (1u << a) - 1u;
+                    vis = below_e & ~below_a;
                     // A row of the cache that holds an infinity or NaN makes its logit non-finite
                     // in every row of q. Where a row of q must not see the key, those elements
                     // become zero in the tile (0 * inf in PV would reach every row); rows that
                     // do see the key have a NaN probability already, or with a logit of -inf
                     // give it no weight. Chunks 0-5 are finite in shared memory; the others a key
                     // at a time: lane = 16-byte piece of the two.
-                    const int a = max(0, min(32, ra - hb)), e = max(0, min(32, rb - hb));
-                    const uint32_t below_e = e == 32 ? 0xFFFFFFFFu : (1u << e) - 1u;
-                    const uint32_t below_a = a == 32 ? 0xFFFFFFFFu : (1u << a) - 1u;
-                    const uint32_t vis = below_e & ~below_a;
                     uint64_t t2[2] = {0, 0};  // NaN if any is not finite
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         t2[j & 1] = fma_pair(pair_of(sa[2 * j], sa[2 * j + 1]), 0, t2[j & 1]);
                     t2[0] = add_pair(t2[0], t2[1]);
                     const bool odd = !(first_of(t2[0]) + second_of(t2[0]) == 0.0f);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (!((vis >> j) & 1u)) sa[j] = __float_as_uint(-INFINITY);
+                    hide32(sa, vis);
                     uint32_t keys =
                         __ballot_sync(0xFFFFFFFFu, odd && live && (ra > 0 || rb < x.nrows));
                     if (keys) {
                         mbar_wait(&r_full[g & 1], (g >> 1) & 1, abort_flag, p.status);
                         uint8_t *tile = (lane & 8 ? smem + kOff7 + (g & 1) * kChunk : s6) +
                                         sp * 4096 + (lane & 7) * 16;
+#pragma unroll 1
                         for (; keys && lane < 16; keys &= keys - 1) {
                             uint4 *at = reinterpret_cast<uint4 *>(tile + (__ffs(keys) - 1) * 128);
                             uint4 v = *at;
@@ -713,20 +729,13 @@ __global__ void __launch_bounds__(kT, 1)
                         __syncwarp();
                     }
                 }
-                // how far the products lie above the running maximum: decides the rescale
-                const float4 *m4 = reinterpret_cast<const float4 *>(sM + cur * 64 + hb);
-                float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float4 m = m4[j];
-                    t[0] = fmaxf(t[0], __uint_as_float(sa[4 * j]) - m.x);
-                    t[1] = fmaxf(t[1], __uint_as_float(sa[4 * j + 1]) - m.y);
-                    t[2] = fmaxf(t[2], __uint_as_float(sa[4 * j + 2]) - m.z);
-                    t[3] = fmaxf(t[3], __uint_as_float(sa[4 * j + 3]) - m.w);
-                }
-                const float over = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-                if (vote_any_group(over * p.c > kRescale, hh)) {
+                // how far the products lie above the running maximum: decides the rescale, and
+                // times c is the exponent
+                if (vote_any_group(less_max(sa, sM + cur * 64 + hb) * p.c > kRescale, hh)) {
                     // exact block maxima -> new running maximum; sums and O^T rescaled
+                    if (live) tmem_ld32(s_col, sa);
+                    tmem_wait_ld();
+                    if (masked) hide32(sa, vis);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         const float wm = redux_max(__uint_as_float(sa[j]));
@@ -737,13 +746,14 @@ __global__ void __launch_bounds__(kT, 1)
                         const int r = hb + lane;
                         const float bm = fmaxf(fmaxf(sRed[r], sRed[64 + r]),
                                                fmaxf(sRed[128 + r], sRed[192 + r]));
-                        const float m_old = sM[cur * 64 + r];
+                        const float m_old = -sM[cur * 64 + r];
                         const float m_new = fmaxf(m_old, bm);
-                        sM[(cur ^ 1) * 64 + r] = m_new;
+                        sM[(cur ^ 1) * 64 + r] = -m_new;
                         sAlpha[r] = ex2((m_old - m_new) * p.c);
                     }
                     bar_group(hh);
                     cur ^= 1;
+                    less_max(sa, sM + cur * 64 + hb);
                     const uint64_t *alpha = reinterpret_cast<const uint64_t *>(sAlpha + hb);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) l[j] = mul_pair(l[j], alpha[j]);
@@ -751,43 +761,35 @@ __global__ void __launch_bounds__(kT, 1)
                         mbar_wait(pv_done, (g & 1) ^ 1, abort_flag, p.status);
                         tc_fence_after();
 #pragma unroll 1
-                        for (int m = 0; m < 8; ++m) {
-                            uint32_t oa[16];
-                            const uint32_t col = lane_base + kOCol + 64 * (m / 2) + hb + 16 * (m & 1);
-                            tmem_ld16(col, oa);
+                        for (int m = 0; m < 16; ++m) {
+                            uint32_t oa[8];
+                            const uint32_t col = lane_base + kOCol + 64 * (m / 4) + hb + 8 * (m & 3);
+                            tmem_ld8(col, oa);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
+                            for (int j = 0; j < 8; ++j)
                                 oa[j] = __float_as_uint(__uint_as_float(oa[j]) *
-                                                        sAlpha[hb + 16 * (m & 1) + j]);
-                            tmem_st16(col, oa);
+                                                        sAlpha[hb + 8 * (m & 3) + j]);
+                            tmem_st8(col, oa);
                         }
                         tmem_wait_st();
                     }
                 }
+                // S may take QK of the next block
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free);
                 // this thread's 32 rows of P^T for key kl. The sums take P as rounded to bf16, the
                 // values that PV multiplies.
                 uint32_t pk[16];
-                {
-                    const ulonglong2 *m2 =
-                        reinterpret_cast<const ulonglong2 *>(sM + cur * 64 + hb);
-                    const uint64_t c2 = pair_of(p.c), minus = pair_of(-1.0f);
+                const uint64_t c2 = pair_of(p.c);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const ulonglong2 m = m2[j];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint64_t s2 = pair_of(sa[4 * j + 2 * e], sa[4 * j + 2 * e + 1]);
-                            const uint64_t d = fma_pair(e ? m.y : m.x, minus, s2);
-                            const uint64_t y = mul_pair(d, c2);
-                            const __nv_bfloat162 v =
-                                __floats2bfloat162_rn(ex2(first_of(y)), ex2(second_of(y)));
-                            const uint32_t w = *reinterpret_cast<const uint32_t *>(&v);
-                            pk[2 * j + e] = w;
-                            l[2 * j + e] =
-                                add_pair(l[2 * j + e], pair_of(w << 16, w & 0xFFFF0000u));
-                        }
-                    }
+                for (int j = 0; j < 16; ++j) {
+                    const uint64_t y = mul_pair(pair_of(sa[2 * j], sa[2 * j + 1]), c2);
+                    const __nv_bfloat162 v =
+                        __floats2bfloat162_rn(ex2(first_of(y)), ex2(second_of(y)));
+                    pk[j] = *reinterpret_cast<const uint32_t *>(&v);
+                    l[j] = add_pair(l[j], pair_of(pk[j] << 16, pk[j] & 0xFFFF0000u));
                 }
                 // PV of the block before has used P
                 mbar_wait(pv_done, (g & 1) ^ 1, abort_flag, p.status);
@@ -832,7 +834,7 @@ __global__ void __launch_bounds__(kT, 1)
                 sLinv[r] = tot == 0.0f ? 0.0f : 1.0f / tot;
                 if (!x.whole)
                     reinterpret_cast<float2 *>(p.ws + kWsMl)[slot * kMaxRows + r] =
-                        make_float2(sM[cur * 64 + r], tot);
+                        make_float2(-sM[cur * 64 + r], tot);
             }
             bar_group(hh);
             // O^T into registers one d-tile at a time: lane holds dim 128 m + 32 sp + lane of
