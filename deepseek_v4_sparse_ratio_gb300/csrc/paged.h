@@ -59,9 +59,10 @@ inline bool overlaps(const void *a, uint64_t na, const void *b, uint64_t nb) {
     return x < y + nb && y < x + na;
 }
 
-// The rows of the pages in bf16 elements, boxes of 64 of them (128 bytes) by the rows of a page.
+// The rows of the pages in bf16 elements, boxes of 64 (or 32) of them by the rows of a page (128 at
+// most), swizzled over their 128 (64) bytes.
 bool make_tmap_pages(CUtensorMap *map, const void *pages, const PagedBatch &b,
-                     PageRow row = kBf16Row);
+                     PageRow row = kBf16Row, uint32_t box_inner = 64);
 
 // One sequence of the batch: rows [row0, row0 + n) are its new tokens, the last n of its len.
 struct PagedSeq {

@@ -332,13 +332,15 @@ bool make_tmap_bf16(CUtensorMap *map, const void *base, uint64_t inner, uint64_t
 
 // The pages as [n_pages][page_size][512]; a box is 64 dims of one page, or of 128 rows of a
 // longer one, with the 128-byte swizzle.
-bool make_tmap_pages(CUtensorMap *map, const void *pages, const PagedBatch &b, PageRow row) {
+bool make_tmap_pages(CUtensorMap *map, const void *pages, const PagedBatch &b, PageRow row,
+                     uint32_t box_inner) {
     const cuuint64_t rows = cuuint64_t{1} << b.page_shift;
     const cuuint64_t bytes = static_cast<cuuint64_t>(row.size) * row.unit;
     const cuuint64_t dims[3] = {bytes / 2, rows, static_cast<cuuint64_t>(b.n_pages)};
     const cuuint64_t strides[2] = {bytes, static_cast<cuuint64_t>(b.page_stride) * row.unit};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows < 128 ? rows : 128), 1};
-    return encode_bf16(map, pages, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    const cuuint32_t box[3] = {box_inner, static_cast<cuuint32_t>(rows < 128 ? rows : 128), 1};
+    return encode_bf16(map, pages, 3, dims, strides, box,
+                       box_inner == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 int current_device() {

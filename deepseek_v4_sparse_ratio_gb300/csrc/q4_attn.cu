@@ -17,13 +17,16 @@
 // second product of the block before.
 //   chunks 0-5: TMEM for QK, shared memory for PV;  chunk 6: shared memory for both, unpacked when
 //   PV of the block before has used it (the first tile of PV);  chunk 7, the rotated dims (bf16 in
-//   the pages): TMA into two slots in turn.
+//   the pages): TMA into their place as soon as the same tile has left it.
+// The 4-bit bytes come by TMA too, 64 of a row's first 256 at a time (the scales and chunk 0, chunks
+// 1-2, 3-4, 5-6), into two slots in turn. (Loaded by the unpacking threads themselves, a key's
+// bytes each, a sector and a line for every lane of a load keep the load unit busy for longer than
+// the products take.)
 //
-// Roles (640 threads): warp 0 finds each block's pages for the unpackers and loads chunk 7; warp 1
-// issues the products, in the order QK chunks 0-5 (b), PV 1st and 2nd tile (b - 1), QK chunks 6-7
-// (b), PV 3rd and 4th (b - 1); warp 2 loads q, 2 and 3 turn it; warps 4-11 unpack: thread = key,
-// each half of the warps every other chunk; warps 12-19 softmax and results, 32 rows of 32 keys a
-// warp.
+// Roles (640 threads): warp 0 loads the 4-bit bytes, warp 3 chunk 7; warp 1 issues the products, in
+// the order QK chunks 0-5 (b), three tiles of PV (b - 1), QK chunks 6-7 (b), the last tile of PV
+// (b - 1); warp 2 loads q and turns it; warps 4-11 unpack: thread = key, each half of the warps
+// every other chunk; warps 12-19 softmax and results, 32 rows of 32 keys a warp.
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -41,26 +44,28 @@ using namespace paged;
 
 constexpr int kT = 640;
 constexpr int kMmaWarp = 1;
-constexpr int kTurnWarp0 = 2;      // two warps: a row of q a thread
+constexpr int kQWarp = 2;
+constexpr int kRopeWarp = 3;
 constexpr int kUnpackWarp0 = 4;
 constexpr int kSoftWarp0 = 12;
 constexpr int kRegsLaunch = 96;
 
 constexpr int kRows = 64;          // rows of q in a unit (MMA N)
-constexpr int kDescs = 4;          // blocks whose pages are known ahead
+constexpr int kRing = 4;           // blocks whose valid keys are kept
 
 // shared memory
 constexpr uint32_t kChunk = 16384;                // [128 keys x 64 dims]
 constexpr uint32_t kOffQ = 0;                     // 8 chunks x [64 rows x 128 B]
 constexpr uint32_t kOffV = 65536;                 // chunks 0-5, for PV
 constexpr uint32_t kOff6 = kOffV + 6 * kChunk;    // chunk 6
-constexpr uint32_t kOff7 = kOff6 + kChunk;        // chunk 7, by block parity
-constexpr uint32_t kOffP = kOff7 + 2 * kChunk;    // P^T [128 keys x 64 rows] bf16
+constexpr uint32_t kOff7 = kOff6 + kChunk;        // chunk 7
+constexpr uint32_t kOffRaw = kOff7 + kChunk;      // [2][128 keys x 64 B] of the pages
+constexpr uint32_t kOffP = kOffRaw + 16384;       // P^T [128 keys x 64 rows] bf16
 constexpr uint32_t kOffRed = kOffP + 16384;       // [4][64] block maxima | partial sums
 constexpr uint32_t kOffLinv = kOffRed + 1024;     // [64] rescale factors | 1/sum
 constexpr uint32_t kOffM = kOffLinv + 256;        // [2][64] running maximum, negated, double-buffered
-constexpr uint32_t kOffDesc = kOffM + 512;        // [kDescs] pages of a block
-constexpr uint32_t kOffBar = kOffDesc + kDescs * 80;
+constexpr uint32_t kOffWalk = kOffM + 512;        // [2] where the softmax is, by half
+constexpr uint32_t kOffBar = kOffWalk + 2 * 192;
 constexpr uint32_t kSmem = kOffBar + 384;
 static_assert(kSmem <= 232448, "over the shared memory of one CTA");
 
@@ -69,13 +74,13 @@ constexpr uint32_t kOCol = 0;      // O^T: 4 d-tiles x 64
 constexpr uint32_t kSCol = 256;    // S^T
 constexpr uint32_t kKCol = 320;    // chunks 0-5 of K, 32 columns each
 
-// The pages of a block, for the unpackers.
-struct alignas(16) Desc {
-    const uint8_t *row[8];  // the first row that the block has in each page (null: none needed)
-    int a, b, c;            // keys [a, b) and those below c are seen by some token
-    int more;               // 0: the run has ended
+// Where a half of the softmax warps is: its segment and, in turn with it, the next one.
+struct SoftWalk {
+    Walk walk;
+    Segment x[2];
+    int more[2];
 };
-static_assert(sizeof(Desc) == 80, "descriptors");
+static_assert(sizeof(SoftWalk) <= 192, "walks");
 
 // D[tmem] (+)= A[tmem] * B[smem]^T; A: lane = row, a column holds two bf16 along K.
 __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
@@ -119,16 +124,9 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
         : "memory");
 }
 
-// A 32-byte sector of a row (zeros without one).
-__device__ __forceinline__ void load_sector(uint32_t *v, const uint8_t *row, int at) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0;
-    if (row)
-        asm volatile(
-            "ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-              "=r"(v[7])
-            : "l"(row + at));
+// Bytes brought to L2.
+__device__ __forceinline__ void prefetch_rows(const uint8_t *at, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
 }
 
 // Four words (32 dims) as 16 pairs of bf16. `two`: the scales of their two groups (e4m3, the lower
@@ -154,17 +152,30 @@ __device__ __forceinline__ bool has_nan(uint32_t w) {
     return ((x - 0x01010101u) & ~x & 0x80808080u) != 0;
 }
 
+// 16 bytes to shared memory.
+__device__ __forceinline__ void store_piece(uint32_t at, const uint32_t *v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
+
+// 16 bytes from shared memory.
+__device__ __forceinline__ void load_piece(uint32_t *v, uint32_t at) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(at)
+                 : "memory");
+}
+
 // A chunk's row of a key in shared memory without its infinities and NaN.
-static __device__ __noinline__ void make_finite(uint8_t *row) {
+static __device__ __noinline__ void make_finite(uint32_t row) {
 #pragma unroll 1
     for (int w = 0; w < 8; ++w) {
-        uint4 *at = reinterpret_cast<uint4 *>(row) + w;
-        uint4 v = *at;
-        v.x = finite2(v.x);
-        v.y = finite2(v.y);
-        v.z = finite2(v.z);
-        v.w = finite2(v.w);
-        *at = v;
+        uint32_t v[4];
+        load_piece(v, row ^ (16 * w));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = finite2(v[j]);
+        store_piece(row ^ (16 * w), v);
     }
 }
 
@@ -215,7 +226,8 @@ __device__ __forceinline__ float less_max(uint32_t (&s)[32], const float *minus_
 
 __global__ void __launch_bounds__(kT, 1)
     q4_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
-                   const __grid_constant__ CUtensorMap tm_kv,
+                   const __grid_constant__ CUtensorMap tm_raw,
+                   const __grid_constant__ CUtensorMap tm_rope,
                    const __grid_constant__ SinkParams p, const uint8_t *pages) {
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *sQ = smem + kOffQ;
@@ -227,32 +239,32 @@ __global__ void __launch_bounds__(kT, 1)
     float *sLinv = reinterpret_cast<float *>(smem + kOffLinv);
     float *sAlpha = sLinv;
     float *sM = reinterpret_cast<float *>(smem + kOffM);
-    Desc *sDesc = reinterpret_cast<Desc *>(smem + kOffDesc);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBar);
     uint64_t *tm_full = bars + 0;   // [3] pair of chunks 0-5 in TMEM
     uint64_t *v_full = bars + 3;    // [3] pair of chunks 0-5 in shared memory
     uint64_t *v_free = bars + 6;    // [4] pair of chunks used by PV
-    uint64_t *k6_full = bars + 10;  // chunk 6 unpacked, sValid written
-    uint64_t *r_full = bars + 11;   // [2] chunk 7 landed, by block parity
-    uint64_t *qa_done = bars + 13;  // QK has read the chunks in TMEM
-    uint64_t *q_full = bars + 14;
-    uint64_t *q_free = bars + 15;
-    uint64_t *q_turned = bars + 16;
-    uint64_t *s_full = bars + 17;
-    uint64_t *s_free = bars + 18;
-    uint64_t *p_full = bars + 19;
-    uint64_t *pv_done = bars + 20;  // P may be written, O rescaled
-    uint64_t *o_full = bars + 21;
-    uint64_t *o_free = bars + 22;
-    uint64_t *drain = bars + 23;
-    uint64_t *d_full = bars + 24;   // [kDescs]
-    uint64_t *d_free = bars + 28;   // [kDescs]
-    constexpr int kBars = 32;
+    uint64_t *k6_full = bars + 10;  // chunk 6 unpacked
+    uint64_t *raw_free = bars + 11; // [2] 4-bit bytes taken
+    uint64_t *raw_full = bars + 13; // [2] 4-bit bytes landed
+    uint64_t *r_full = bars + 15;   // chunk 7 landed
+    uint64_t *qa_done = bars + 16;  // QK has read the chunks in TMEM
+    uint64_t *q_full = bars + 17;
+    uint64_t *q_free = bars + 18;
+    uint64_t *q_turned = bars + 19;
+    uint64_t *s_full = bars + 20;
+    uint64_t *s_free = bars + 21;
+    uint64_t *p_full = bars + 22;
+    uint64_t *pv_done = bars + 23;  // P may be written, O rescaled
+    uint64_t *o_full = bars + 24;
+    uint64_t *o_free = bars + 25;
+    uint64_t *drain = bars + 26;
+    constexpr int kBars = 27;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *sStart = reinterpret_cast<int *>(tmem_holder + 2);    // [5] start of this CTA's run
     volatile uint32_t *sBlocks = tmem_holder + 1 + kBlocksAt;  // blocks begun
-    volatile uint32_t *sValid = tmem_holder + 12;              // [2][4] keys that were loaded
+    volatile uint32_t *sMore = tmem_holder + 10;               // [kRing] 0: the run has ended
+    volatile uint32_t *sValid = sMore + kRing;                 // [kRing][4] keys that are there
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (smem_u32(smem) & 1023u) {  // the tiles' swizzle counts on it
@@ -264,15 +276,15 @@ __global__ void __launch_bounds__(kT, 1)
         return;
     }
     if (warp == 0) {
-        // arrivals a phase takes: 8 unpacking warps on tm_full, v_full, k6_full and d_free, 64
-        // turning threads on q_turned, 8 softmax warps on s_free, p_full and o_free, one on the
-        // others
+        // arrivals a phase takes: 8 unpacking warps on tm_full, v_full, k6_full and raw_free, the
+        // turning warp's threads on q_turned, 8 softmax warps on s_free, p_full and o_free, one on
+        // the others
         int n = 1;
         uint64_t *bar = bars + lane;
-        if (bar < v_free || bar == k6_full || bar >= d_free) n = 8;
-        if (bar == q_turned) n = 64;
+        if (bar < v_free || (bar >= k6_full && bar < raw_full)) n = 8;
+        if (bar == q_turned) n = 32;
         if (bar == s_free || bar == o_free || bar == p_full) n = 8;
-        mbar_init(bar, n);
+        if (bar <= drain) mbar_init(bar, n);
         if (lane == 31) {
             *abort_flag = 0;
             sStart[4] = 0;
@@ -281,9 +293,10 @@ __global__ void __launch_bounds__(kT, 1)
         fence_barrier_init();
     }
     if (warp == kMmaWarp) tmem_alloc(tmem_holder, 512);
-    if (tid == 32 * kTurnWarp0) {
+    if (tid == 32 * kQWarp) {
         prefetch_tmap(&tm_q);
-        prefetch_tmap(&tm_kv);
+        prefetch_tmap(&tm_raw);
+        prefetch_tmap(&tm_rope);
     }
     wait_before();
     const int cta = static_cast<int>(blockIdx.x);
@@ -292,72 +305,111 @@ __global__ void __launch_bounds__(kT, 1)
 
     if (warp < kUnpackWarp0) {
         if (warp == 0) {
-            // ---------------- pages: lane i < np has page i of a block. Descriptors run two
-            // blocks ahead of the loads of chunk 7 (which wait for PV), as the unpackers do.
+            // ---------------- the 4-bit bytes, 64 of a row at a time. Lane i < np loads page i;
+            // a block's table entries are read, and its rows brought to L2, one block ahead.
             const int prows = min(1 << p.b.page_shift, kBlock), np = kBlock / prows;
+            const int key_shift = min(p.b.page_shift, 7);
+            const uint64_t once = policy_evict_first(), keep = policy_evict_normal();
             PageWalk walk(p, sStart);
-            // (entry, row) of the block whose chunk 7 is loaded next and of the one behind it
-            int32_t e0 = -1, e1 = -1, e2 = -1;
-            int row0 = 0, row1 = 0, row2 = 0;
-            bool ok = true;
-            int t = -2, last_load = -1;
-            bool have0 = false, have1 = false;
-            for (;; ++t) {
-                const bool have2 = walk.have;
-                if (t + 2 >= 0 && ok) {
-                    // block t + 2
-                    const int d = (t + 2) & (kDescs - 1);
-                    const uint32_t use = ((t + 2) / kDescs) & 1;
-                    ok = __all_sync(0xFFFFFFFFu,
-                                    wait_bar(&d_free[d], use ^ 1, abort_flag, p.status));
-                    if (!ok) break;
-                    if (have2) {
-                        const int pos = walk.x.block_pos(walk.b);
-                        const int lo = walk.x.lo - pos, end = walk.x.posl - pos + 1;
-                        e2 = walk.next(p, lane, prows, np, row2);
-                        if (lane < 8)
-                            sDesc[d].row[lane] =
-                                e2 >= 0 ? pages + e2 * p.b.page_stride + int64_t{row2} * kQ4Row
-                                        : nullptr;
-                        if (lane == 8) {
-                            sDesc[d].a = lo;
-                            sDesc[d].b = end;
-                            sDesc[d].c = p.sinks - pos;
-                        }
-                    }
-                    if (lane == 9) sDesc[d].more = have2;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&d_full[d]);
+            bool have = false, have_next, ok = true;
+            int32_t e = -1, e_next = -1;
+            int row = 0, row_next = 0;
+            // keys [a, b) and those below c of a block are seen by some token
+            int a = 0, b = 0, c = 0, a_next = 0, b_next = 0, c_next = 0;
+            bool alone = false, alone_next = false;
+            int uses0 = 0, uses1 = 0;   // of either slot, the end's among them
+            for (int t = -1;; ++t) {
+                have_next = walk.have;
+                if (have_next) {
+                    const int pos = walk.x.block_pos(walk.b);
+                    a_next = walk.x.lo - pos;
+                    b_next = walk.x.posl - pos + 1;
+                    c_next = p.sinks - pos;
+                    alone_next = walk.x.alone;
+                    e_next = walk.next(p, lane, prows, np, row_next);
+                    if (e_next >= 0)
+                        prefetch_rows(pages + e_next * p.b.page_stride + int64_t{row_next} * kQ4Row,
+                                      prows * kQ4Row);
                 }
-                if (t >= 0 && have0) {
-                    // chunk 7 of block t, when PV of the block two back has used the slot
-                    const int par = t & 1;
-                    ok = __all_sync(0xFFFFFFFFu, t < 2 || wait_bar(&v_free[3], t & 1, abort_flag,
-                                                                   p.status));
-                    if (!ok) break;
-                    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, e0 >= 0);
+                if (t >= 0) {
                     *sBlocks = static_cast<uint32_t>(t) + 1;
-                    if (lane == 0)
-                        mbar_expect_tx(&r_full[par],
-                                       static_cast<uint32_t>(__popc(mask)) * prows * 128);
-                    __syncwarp();
-                    if (e0 >= 0)
-                        tma_load_3d(smem + kOff7 + par * kChunk + lane * prows * 128, &tm_kv,
-                                    &r_full[par], kQ4Rope / 2, row0, e0, policy_evict_normal());
-                    last_load = t;
+                    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, e >= 0);
+                    const uint32_t bytes = static_cast<uint32_t>(__popc(mask)) * prows * 64;
+#pragma unroll 1
+                    for (int j = 0; j < 4; ++j) {
+                        ok = __all_sync(0xFFFFFFFFu, wait_bar(&raw_free[j & 1], (j >> 1) ^ 1,
+                                                              abort_flag, p.status));
+                        if (!ok) break;
+                        if (j == 0) {
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) {
+                                const int key = 32 * w + lane;
+                                const uint32_t there = __ballot_sync(
+                                    0xFFFFFFFFu, ((mask >> (key >> key_shift)) & 1u) && key < b &&
+                                                     (key >= a || key < c));
+                                if (lane == w) sValid[4 * (t & (kRing - 1)) + w] = there;
+                            }
+                            if (lane == 4) sMore[t & (kRing - 1)] = have;
+                            __syncwarp();
+                        }
+                        uses0 += ~j & 1;
+                        uses1 += j & 1;
+                        if (!have) {
+                            if (lane == 0) mbar_arrive(&raw_full[0]);
+                            break;
+                        }
+                        if (lane == 0) mbar_expect_tx(&raw_full[j & 1], bytes);
+                        __syncwarp();
+                        if (e >= 0)
+                            tma_load_3d(smem + kOffRaw + (j & 1) * 8192 + lane * prows * 64,
+                                        &tm_raw, &raw_full[j & 1], 32 * j, row, e,
+                                        alone ? once : keep);
+                    }
+                    if (!ok || !have) break;
                 }
-                if (t >= 0 && !have0) break;
-                have0 = have1;
-                have1 = have2;
-                e0 = e1;
-                row0 = row1;
-                e1 = e2;
-                row1 = row2;
+                have = have_next;
+                e = have_next ? e_next : -1;
+                row = row_next;
+                a = a_next;
+                b = b_next;
+                c = c_next;
+                alone = alone_next;
             }
             // no copy into this CTA's shared memory may still be in flight at exit
-            if (lane == 0)
-                for (int l = last_load; l >= 0 && l >= last_load - 1; --l)
-                    drain_wait(&r_full[l & 1], (l >> 1) & 1);
+            __syncwarp();
+            if (lane == 0) {
+                if (uses0 > 0) drain_wait(&raw_full[0], (uses0 - 1) & 1);
+                if (uses1 > 0) drain_wait(&raw_full[1], (uses1 - 1) & 1);
+            }
+            __syncwarp();
+        } else if (warp == kRopeWarp) {
+            // ---------------- chunk 7 of each block, when PV of the block before has used it
+            const int prows = min(1 << p.b.page_shift, kBlock), np = kBlock / prows;
+            const uint64_t once = policy_evict_first(), keep = policy_evict_normal();
+            PageWalk walk(p, sStart);
+            int row, row_next = 0, t = 0;
+            bool have = walk.have, alone, alone_next = walk.x.alone;
+            int32_t e, e_next = walk.next(p, lane, prows, np, row_next);
+            for (bool more; have; ++t, have = more) {
+                e = e_next;
+                row = row_next;
+                alone = alone_next;
+                alone_next = walk.x.alone;
+                more = walk.have;
+                e_next = walk.next(p, lane, prows, np, row_next);
+                if (!__all_sync(0xFFFFFFFFu, t == 0 || wait_bar(&v_free[3], (t - 1) & 1, abort_flag,
+                                                                p.status)))
+                    break;
+                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, e >= 0);
+                if (lane == 0)
+                    mbar_expect_tx(r_full, static_cast<uint32_t>(__popc(mask)) * prows * 128);
+                __syncwarp();
+                if (e >= 0)
+                    tma_load_3d(smem + kOff7 + lane * prows * 128, &tm_rope, r_full, kQ4Rope / 2,
+                                row, e, alone ? once : keep);
+            }
+            // no copy into this CTA's shared memory may still be in flight at exit
+            if (lane == 0 && t > 0) drain_wait(r_full, (t - 1) & 1);
             __syncwarp();
         } else if (warp == kMmaWarp) {
             // ---------------- the products. PV of a block follows QK of the next one's chunks in
@@ -422,7 +474,7 @@ __global__ void __launch_bounds__(kT, 1)
                         if (elect_one()) {
                             const uint64_t ad = desc_sw128(
                                 smem_u32(smem) + (st > 0 ? kOffV + 2 * m * kChunk : kOff6),
-                                st > 0 || !(gb & 1) ? kChunk : 2 * kChunk, 1024);
+                                kChunk, 1024);
                             const uint64_t bd = desc_sw128(smem_u32(sP), 8192, 1024);
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk)
@@ -437,10 +489,10 @@ __global__ void __launch_bounds__(kT, 1)
                         }
                         __syncwarp();
                     }
-                    if (st == 1 && qk) {
+                    if (st == 2 && qk) {
                         // QK, chunk 6 and chunk 7
                         ok = wait_bar(k6_full, g & 1, abort_flag, p.status) &&
-                             wait_bar(&r_full[g & 1], (g >> 1) & 1, abort_flag, p.status);
+                             wait_bar(r_full, g & 1, abort_flag, p.status);
                         if (ok && fresh && turn)
                             ok = wait_bar(q_turned, i & 1, abort_flag, p.status);
                         if (!ok) break;
@@ -448,11 +500,9 @@ __global__ void __launch_bounds__(kT, 1)
                         if (elect_one()) {
                             const uint64_t bd = desc_sw128(smem_u32(sQ) + 6 * 8192, 16, 1024);
                             const uint64_t a6 = desc_sw128(smem_u32(s6), 16, 1024);
-                            const uint64_t a7 = desc_sw128(
-                                smem_u32(smem) + kOff7 + (g & 1) * kChunk, 16, 1024);
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                mma_bf16(tmem + kSCol, (k < 4 ? a6 : a7) + 2 * (k % 4),
+                                mma_bf16(tmem + kSCol, a6 + (k / 4) * (kChunk >> 4) + 2 * (k % 4),
                                          bd + (k / 4) * (8192 >> 4) + 2 * (k % 4), idesc_qk, 1u);
                             mma_commit(s_full);
                             if (last) mma_commit(q_free);
@@ -480,34 +530,33 @@ __global__ void __launch_bounds__(kT, 1)
             __syncwarp();
         } else {
             // ---------------- the queries: loaded when the last unit's products have read theirs,
-            // and turned in place, a row a thread
+            // and turned in place, two rows a thread
             const bool turn = p.b.cos_sin && p.turn_q;
             const uint64_t pol_stream = policy_evict_first();
-            const int r = tid - 32 * kTurnWarp0;
-            uint8_t *row = sQ + 7 * 8192 + r * 128;
             Walk walk(p, sStart);
             Segment x;
             int i = 0;
             for (; walk.next(p, x); ++i) {
-                if (warp == kTurnWarp0) {
-                    if (!__all_sync(0xFFFFFFFFu,
-                                    wait_bar(q_free, (i & 1) ^ 1, abort_flag, p.status)))
-                        break;
-                    if (lane == 0) {
-                        mbar_expect_tx(q_full, 65536);
-                        for (int c = 0; c < 8; ++c)
-                            tma_load_2d(sQ + c * 8192, &tm_q, q_full, c * 64,
-                                        static_cast<int>(x.row), pol_stream);
-                    }
-                    __syncwarp();
+                if (!__all_sync(0xFFFFFFFFu, wait_bar(q_free, (i & 1) ^ 1, abort_flag, p.status)))
+                    break;
+                if (lane == 0) {
+                    mbar_expect_tx(q_full, 65536);
+                    for (int c = 0; c < 8; ++c)
+                        tma_load_2d(sQ + c * 8192, &tm_q, q_full, c * 64, static_cast<int>(x.row),
+                                    pol_stream);
                 }
+                __syncwarp();
                 if (!turn) continue;
-                const bool mine = r < x.nrows;
-                const float4 *src = reinterpret_cast<const float4 *>(
-                    p.b.cos_sin + int64_t{mine ? row_pos(p, x.posf, r) : x.posl} * kRope);
-                if (!__all_sync(0xFFFFFFFFu, wait_bar(q_full, i & 1, abort_flag, p.status))) break;
-                if (mine) {
-#pragma unroll 2
+                if (!__all_sync(0xFFFFFFFFu, wait_bar(q_full, i & 1, abort_flag, p.status))) {
+                    ++i;
+                    break;
+                }
+#pragma unroll 1
+                for (int r = lane; r < x.nrows; r += 32) {
+                    uint8_t *row = sQ + 7 * 8192 + r * 128;
+                    const float4 *src = reinterpret_cast<const float4 *>(
+                        p.b.cos_sin + int64_t{row_pos(p, x.posf, r)} * kRope);
+#pragma unroll 4
                     for (int k = 0; k < 8; ++k) {
                         const float4 c0 = __ldg(src + 2 * k), c1 = __ldg(src + 2 * k + 1);
                         uint4 *at = reinterpret_cast<uint4 *>(row + ((k ^ (r & 7)) << 4));
@@ -523,130 +572,112 @@ __global__ void __launch_bounds__(kT, 1)
                 mbar_arrive(q_turned);
             }
             // no copy into this CTA's shared memory may still be in flight at exit
-            __syncwarp();
-            if (tid == 32 * kTurnWarp0 && i > 0) drain_wait(q_full, (i - 1) & 1);
+            if (lane == 0 && i > 0) drain_wait(q_full, (i - 1) & 1);
             __syncwarp();
         }
     } else if (warp < kSoftWarp0) {
         // ---------------- unpacking. Step t: chunk 6 of block t - 1, then pair by pair the chunks
-        // of block t - 1 from TMEM to shared memory and those of block t into TMEM; behind each
-        // of them the load of the same chunk of block t + 1.
+        // of block t - 1 from TMEM to shared memory and those of block t into TMEM. (Once the kernel
+        // gives up no wait lasts, and the next block does not come.)
         const int sp = warp & 3, h = (warp - kUnpackWarp0) >> 2;
         const int key = 32 * sp + lane;
         const uint32_t k_col = tmem + (static_cast<uint32_t>(sp * 32) << 16) + kKCol + 32 * h;
-        uint8_t *const to6 = s6 + key * 128;
-        uint8_t *const to_v = sV + h * kChunk + key * 128;
-        const int swz = key & 7;
-        const int page_shift = min(p.b.page_shift, 7);
+        // (piece w of a swizzled row lies at the row's place ^ 16 w)
+        const uint32_t row_at = key * 128 + ((key & 7) << 4);
+        const uint32_t to6 = (smem_u32(s6) + row_at) ^ (64 * h);
+        const uint32_t to_v = smem_u32(sV) + h * kChunk + row_at;
+        const uint32_t from = smem_u32(smem) + kOffRaw + key * 64 + (((key >> 1) & 3) << 4);
 
-        uint32_t raw[3][8], raw6[4] = {}, head[8];
-        uint32_t two[3] = {}, two6 = 0;      // scales of a chunk's halves, of chunk 6
+        uint32_t raw6[4], two[3], two6;      // bytes of chunk 6's half; scales of the chunks' halves
         float pow = 0.0f;                    // half of the row's power of two
         bool odd = false;                    // a scale that is NaN, in the block to be copied
-
-        // The row of block t (null: not to be read) and which keys of the warp have one.
-        auto fetch = [&](int t, bool &have, uint32_t &valid) -> const uint8_t * {
-            const int d = t & (kDescs - 1);
-            const bool ok = __all_sync(0xFFFFFFFFu, wait_bar(&d_full[d], (t / kDescs) & 1,
-                                                             abort_flag, p.status));
-            const Desc &x = sDesc[d];
-            const int4 range = *reinterpret_cast<const int4 *>(&x.a);   // a, b, c, more
-            const uint8_t *row = x.row[key >> page_shift];
-            have = ok && range.w;
-            if (!have || key >= range.y || (key < range.x && key >= range.z)) row = nullptr;
-            valid = __ballot_sync(0xFFFFFFFFu, row != nullptr);
-            if (row) row += (key & ((1 << page_shift) - 1)) * kQ4Row;
-            if (lane == 0) mbar_arrive(&d_free[d]);
-            return row;
-        };
-
-        bool have, before = false;           // block t is there, block t - 1 is to be copied
-        uint32_t valid;
-        const uint8_t *at = fetch(0, have, valid);
-        load_sector(head, at, 0);
-#pragma unroll
-        for (int m = 0; m < 3; ++m) load_sector(raw[m], at, 32 * (2 * m + h + 1));
-        uint32_t valid_before = 0;
-        bool ok = true;
-        for (int t = 0; have || before; ++t) {
+        bool have = true, before = false;    // block t is there, block t - 1 is to be copied
+        for (int t = 0;; ++t) {
             if (before) {
                 // chunk 6 of block t - 1, in the place that PV of block t - 2 has left
-                ok = __all_sync(0xFFFFFFFFu,
-                                t < 2 || wait_bar(&v_free[3], t & 1, abort_flag, p.status));
-                if (!ok) break;
                 uint32_t v[16];
                 unpack32(raw6, two6 & 0xFFFFu, pow, v);
+                if (t > 1) wait_bar(&v_free[3], t & 1, abort_flag, p.status);
 #pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    *reinterpret_cast<uint4 *>(to6 + (((4 * h + w) ^ swz) << 4)) =
-                        make_uint4(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3]);
-                if (h == 0 && lane == 0) sValid[4 * ((t - 1) & 1) + sp] = valid_before;
+                for (int w = 0; w < 4; ++w) store_piece(to6 ^ (16 * w), v + 4 * w);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(k6_full);
             }
-            // block t: its chunk 6 and scales; the row and the scales of block t + 1
-            bool odd_next = false, have_next = false;
-            valid_before = valid;
+            bool odd_next = false;
             if (have) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (at) v = __ldg(reinterpret_cast<const uint4 *>(at + 32 * 7 + 16 * h));
-                raw6[0] = v.x;
-                raw6[1] = v.y;
-                raw6[2] = v.z;
-                raw6[3] = v.w;
+                const bool ok =
+                    __all_sync(0xFFFFFFFFu, wait_bar(&raw_full[0], 0, abort_flag, p.status));
+                have = ok && sMore[t & (kRing - 1)];
+            }
+            if (!have && !before) break;
+            if (have) {
+                // the scales (of a key that is not there: zeros, and so are its values)
+                uint32_t head[8];
+                load_piece(head, from);
+                load_piece(head + 4, from ^ 16);
+                if (h == 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&raw_free[0]);
+                }
+                const bool there = (sValid[4 * (t & (kRing - 1)) + sp] >> lane) & 1u;
 #pragma unroll
                 for (int m = 0; m < 3; ++m)   // chunk 2 m + h: bytes 4 m + 2 h of either half
-                    two[m] = __byte_perm(head[m], head[4 + m], h ? 0x7632 : 0x5410);
-                two6 = h ? head[7] : head[3];  // chunk 6, half h: bytes 12 and 13
+                    two[m] = there ? __byte_perm(head[m], head[4 + m], h ? 0x7632 : 0x5410) : 0u;
+                two6 = there ? (h ? head[7] : head[3]) : 0u;  // chunk 6, half h: bytes 12 and 13
                 odd_next = has_nan(two[0]) || has_nan(two[1]) || has_nan(two[2]);
                 pow = pow2(max(static_cast<int>((head[3] >> 16) & 0xFFu), 11) - 138);
-                at = fetch(t + 1, have_next, valid);
-                if (have_next) load_sector(head, at, 0);
             }
 #pragma unroll
             for (int m = 0; m < 3; ++m) {
                 if (before) {
-                    ok = __all_sync(0xFFFFFFFFu,
-                                    t < 2 || wait_bar(&v_free[m], t & 1, abort_flag, p.status));
-                    if (!ok) break;
                     uint32_t v[32];
                     tmem_ld32(k_col + 64 * m, v);
+                    if (t > 1) wait_bar(&v_free[m], t & 1, abort_flag, p.status);
                     tmem_wait_ld();
 #pragma unroll
                     for (int w = 0; w < 8; ++w)
-                        *reinterpret_cast<uint4 *>(to_v + 2 * m * kChunk + ((w ^ swz) << 4)) =
-                            make_uint4(v[4 * w], v[4 * w + 1], v[4 * w + 2], v[4 * w + 3]);
+                        store_piece((to_v + 2 * m * kChunk) ^ (16 * w), v + 4 * w);
                     if (odd) make_finite(to_v + 2 * m * kChunk);
                     fence_proxy_async_smem();
-                    tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&v_full[m]);
+                    if (m == 0 && have) {    // QK of block t - 1 has read what is overwritten
+                        wait_bar(qa_done, (t - 1) & 1, abort_flag, p.status);
+                        tc_fence_after();
+                    }
                 }
                 if (have) {
-                    if (m == 0 && before) {   // QK of block t - 1 has read what is overwritten
-                        ok = __all_sync(0xFFFFFFFFu, wait_bar(qa_done, (t - 1) & 1, abort_flag,
-                                                              p.status));
-                        if (!ok) break;
-                        tc_fence_after();
+                    // the 32 bytes of chunk 2 m + h: half (1 - h) of part m + h
+                    uint32_t raw[8];
+                    const uint32_t at = (from + ((m + h) & 1) * 8192) ^ (h ? 0 : 32);
+                    wait_bar(&raw_full[(m + h) & 1], (m + h) >> 1, abort_flag, p.status);
+                    load_piece(raw, at);
+                    load_piece(raw + 4, at ^ 16);
+                    if (m == 2) {
+                        // and those of chunk 6: the second half of part 3
+                        if (h == 0) wait_bar(&raw_full[1], 1, abort_flag, p.status);
+                        load_piece(raw6, (from + 8192) ^ (32 + 16 * h));
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&raw_free[(m + h) & 1]);
+                        if (m == 2 && h == 0) mbar_arrive(&raw_free[1]);
                     }
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         uint32_t v[16];
-                        unpack32(raw[m] + 4 * half, (two[m] >> (16 * half)) & 0xFFFFu, pow, v);
+                        unpack32(raw + 4 * half, (two[m] >> (16 * half)) & 0xFFFFu, pow, v);
                         tmem_st16(k_col + 64 * m + 16 * half, v);
                     }
-                    if (have_next) load_sector(raw[m], at, 32 * (2 * m + h + 1));
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&tm_full[m]);
                 }
             }
-            if (!ok) break;
             odd = odd_next;
             before = have;
-            have = have_next;
         }
     } else {
         // ---------------- softmax + epilogue, 8 warps: TMEM lanes of sub-partition sp (keys,
@@ -656,10 +687,21 @@ __global__ void __launch_bounds__(kT, 1)
         const int hb = 32 * hh;
         const int kl = sp * 32 + lane;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(sp * 32) << 16);
-        Walk walk(p, sStart);
-        Segment x;
+        // (the walk and the segments in shared memory, the half's own: registers are few)
+        SoftWalk &mine = reinterpret_cast<SoftWalk *>(smem + kOffWalk)[hh];
+        if (sp == 0 && lane == 0) mine.walk = Walk(p, sStart);
         int i = 0, g = 0, cur = 0;
-        for (; walk.next(p, x); ++i) {
+        for (;; ++i) {
+            const Segment &x = mine.x[i & 1];
+            if (sp == 0 && lane == 0) {
+                Walk w = mine.walk;
+                Segment next;
+                mine.more[i & 1] = w.next(p, next);
+                mine.x[i & 1] = next;
+                mine.walk = w;
+            }
+            bar_group(hh);
+            if (!mine.more[i & 1]) break;
             uint64_t l[16];   // sums of rows 2 j and 2 j + 1, over this lane's keys
 #pragma unroll
             for (int j = 0; j < 16; ++j) l[j] = 0;
@@ -674,7 +716,7 @@ __global__ void __launch_bounds__(kT, 1)
                 tc_fence_after();
                 const uint32_t s_col = lane_base + kSCol + hb;
                 uint32_t sa[32];
-                const uint32_t valid = sValid[4 * (g & 1) + sp];
+                const uint32_t valid = sValid[4 * (g & (kRing - 1)) + sp];
                 if (live) tmem_ld32(s_col, sa);
                 uint32_t vis = 0xFFFFFFFFu;   // rows hb + j that see key k0 + kl
                 // every row sees every key of the warp, unless ...
@@ -713,9 +755,8 @@ __global__ void __launch_bounds__(kT, 1)
                     uint32_t keys =
                         __ballot_sync(0xFFFFFFFFu, odd && live && (ra > 0 || rb < x.nrows));
                     if (keys) {
-                        mbar_wait(&r_full[g & 1], (g >> 1) & 1, abort_flag, p.status);
-                        uint8_t *tile = (lane & 8 ? smem + kOff7 + (g & 1) * kChunk : s6) +
-                                        sp * 4096 + (lane & 7) * 16;
+                        mbar_wait(r_full, g & 1, abort_flag, p.status);
+                        uint8_t *tile = s6 + (lane >> 3) * kChunk + sp * 4096 + (lane & 7) * 16;
 #pragma unroll 1
                         for (; keys && lane < 16; keys &= keys - 1) {
                             uint4 *at = reinterpret_cast<uint4 *>(tile + (__ffs(keys) - 1) * 128);
@@ -982,13 +1023,14 @@ extern "C" int dsa_paged_q4_attn(const void *q, int32_t heads, int64_t n_new,
     int sms = 0;
     rc = setup(&sms);
     if (rc != DSA_OK) return rc;
-    CUtensorMap tm_q, tm_kv;
+    CUtensorMap tm_q, tm_raw, tm_rope;
     if (!make_tmap_bf16(&tm_q, q, kD, static_cast<uint64_t>(n_new) * heads, kD * 2, 64, p.rows) ||
-        !make_tmap_pages(&tm_kv, pages, p.b, kQ4PageRow))
+        !make_tmap_pages(&tm_raw, pages, p.b, kQ4PageRow, 32) ||
+        !make_tmap_pages(&tm_rope, pages, p.b, kQ4PageRow))
         return DSA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int ctas = std::min(sms, kMaxCtas);
-    rc = launch_overlapped(q4_attn_kernel, ctas, kT, kSmem, s, tm_q, tm_kv, p,
+    rc = launch_overlapped(q4_attn_kernel, ctas, kT, kSmem, s, tm_q, tm_raw, tm_rope, p,
                            static_cast<const uint8_t *>(pages));
     return rc == DSA_OK ? enqueue_paged_join(p, ctas, s) : rc;
 }
