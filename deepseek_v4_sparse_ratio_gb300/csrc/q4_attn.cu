@@ -23,10 +23,9 @@
 // bytes each, a sector and a line for every lane of a load keep the load unit busy for longer than
 // the products take.)
 //
-// Roles (640 threads): warp 0 loads the 4-bit bytes, warp 3 chunk 7; warp 1 issues the products, in
-// the order QK chunks 0-5 (b), three tiles of PV (b - 1), QK chunks 6-7 (b), the last tile of PV
-// (b - 1); warp 2 loads q and turns it; warps 4-11 unpack: thread = key, each half of the warps
-// every other chunk; warps 12-19 softmax and results, 32 rows of 32 keys a warp.
+// Roles (640 threads): warp 0 loads the 4-bit bytes; warp 1 issues QK, warp 3 PV; warp 2 loads q,
+// turns it, and loads chunk 7; warps 4-11 unpack: thread = key, each half of the warps every other
+// chunk; warps 12-19 softmax and results, 32 rows of 32 keys a warp.
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -43,12 +42,14 @@ namespace {
 using namespace paged;
 
 constexpr int kT = 640;
-constexpr int kMmaWarp = 1;
+constexpr int kQkWarp = 1;
 constexpr int kQWarp = 2;
-constexpr int kRopeWarp = 3;
+constexpr int kPvWarp = 3;
 constexpr int kUnpackWarp0 = 4;
 constexpr int kSoftWarp0 = 12;
 constexpr int kRegsLaunch = 96;
+constexpr int kRegsLow = 80;
+constexpr int kRegsSoft = 120;     // 384*80 + 256*120 = 640*96, the launch allocation
 
 constexpr int kRows = 64;          // rows of q in a unit (MMA N)
 constexpr int kRing = 4;           // blocks whose valid keys are kept
@@ -203,8 +204,8 @@ __device__ __forceinline__ void hide32(uint32_t (&s)[32], uint32_t vis) {
         if (!((vis >> j) & 1u)) s[j] = __float_as_uint(-INFINITY);
 }
 
-// s += the negated running maxima; the largest of the 32.
-__device__ __forceinline__ float less_max(uint32_t (&s)[32], const float *minus_m) {
+// The largest of the 32 products less their rows' running maxima (which are negated).
+__device__ __forceinline__ float over_max(const uint32_t (&s)[32], const float *minus_m) {
     const ulonglong2 *m2 = reinterpret_cast<const ulonglong2 *>(minus_m);
     float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -214,10 +215,6 @@ __device__ __forceinline__ float less_max(uint32_t (&s)[32], const float *minus_
         const uint64_t b = add_pair(pair_of(s[4 * j + 2], s[4 * j + 3]), m.y);
         t[j & 1] = max3(t[j & 1], first_of(a), second_of(a));
         t[2 + (j & 1)] = max3(t[2 + (j & 1)], first_of(b), second_of(b));
-        s[4 * j] = __float_as_uint(first_of(a));
-        s[4 * j + 1] = __float_as_uint(second_of(a));
-        s[4 * j + 2] = __float_as_uint(first_of(b));
-        s[4 * j + 3] = __float_as_uint(second_of(b));
     }
     return max3(fmaxf(t[0], t[1]), t[2], t[3]);
 }
@@ -257,8 +254,8 @@ __global__ void __launch_bounds__(kT, 1)
     uint64_t *pv_done = bars + 23;  // P may be written, O rescaled
     uint64_t *o_full = bars + 24;
     uint64_t *o_free = bars + 25;
-    uint64_t *drain = bars + 26;
-    constexpr int kBars = 27;
+    uint64_t *drain = bars + 26;    // [2] one per issuing warp
+    constexpr int kBars = 28;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *sStart = reinterpret_cast<int *>(tmem_holder + 2);    // [5] start of this CTA's run
@@ -284,7 +281,7 @@ __global__ void __launch_bounds__(kT, 1)
         if (bar < v_free || (bar >= k6_full && bar < raw_full)) n = 8;
         if (bar == q_turned) n = 32;
         if (bar == s_free || bar == o_free || bar == p_full) n = 8;
-        if (bar <= drain) mbar_init(bar, n);
+        if (lane < kBars) mbar_init(bar, n);
         if (lane == 31) {
             *abort_flag = 0;
             sStart[4] = 0;
@@ -292,7 +289,7 @@ __global__ void __launch_bounds__(kT, 1)
         }
         fence_barrier_init();
     }
-    if (warp == kMmaWarp) tmem_alloc(tmem_holder, 512);
+    if (warp == kPvWarp) tmem_alloc(tmem_holder, 512);
     if (tid == 32 * kQWarp) {
         prefetch_tmap(&tm_q);
         prefetch_tmap(&tm_raw);
@@ -301,9 +298,15 @@ __global__ void __launch_bounds__(kT, 1)
     wait_before();
     const int cta = static_cast<int>(blockIdx.x);
     find_run<kT>(p, reinterpret_cast<int64_t *>(sV), sStart);
-    const uint32_t tmem = *tmem_holder;
+    // All 512 columns of TMEM begin at 0: known addresses, which the products take without a move.
+    constexpr uint32_t tmem = 0;
+    if (tid == 0 && *tmem_holder != tmem) {
+        *abort_flag = 1;
+        report(p.status, DSA_ERR_CUDA);
+    }
 
     if (warp < kUnpackWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
         if (warp == 0) {
             // ---------------- the 4-bit bytes, 64 of a row at a time. Lane i < np loads page i;
             // a block's table entries are read, and its rows brought to L2, one block ahead.
@@ -382,65 +385,21 @@ __global__ void __launch_bounds__(kT, 1)
                 if (uses1 > 0) drain_wait(&raw_full[1], (uses1 - 1) & 1);
             }
             __syncwarp();
-        } else if (warp == kRopeWarp) {
-            // ---------------- chunk 7 of each block, when PV of the block before has used it
-            const int prows = min(1 << p.b.page_shift, kBlock), np = kBlock / prows;
-            const uint64_t once = policy_evict_first(), keep = policy_evict_normal();
-            PageWalk walk(p, sStart);
-            int row, row_next = 0, t = 0;
-            bool have = walk.have, alone, alone_next = walk.x.alone;
-            int32_t e, e_next = walk.next(p, lane, prows, np, row_next);
-            for (bool more; have; ++t, have = more) {
-                e = e_next;
-                row = row_next;
-                alone = alone_next;
-                alone_next = walk.x.alone;
-                more = walk.have;
-                e_next = walk.next(p, lane, prows, np, row_next);
-                if (!__all_sync(0xFFFFFFFFu, t == 0 || wait_bar(&v_free[3], (t - 1) & 1, abort_flag,
-                                                                p.status)))
-                    break;
-                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, e >= 0);
-                if (lane == 0)
-                    mbar_expect_tx(r_full, static_cast<uint32_t>(__popc(mask)) * prows * 128);
-                __syncwarp();
-                if (e >= 0)
-                    tma_load_3d(smem + kOff7 + lane * prows * 128, &tm_rope, r_full, kQ4Rope / 2,
-                                row, e, alone ? once : keep);
-            }
-            // no copy into this CTA's shared memory may still be in flight at exit
-            if (lane == 0 && t > 0) drain_wait(r_full, (t - 1) & 1);
-            __syncwarp();
-        } else if (warp == kMmaWarp) {
-            // ---------------- the products. PV of a block follows QK of the next one's chunks in
-            // TMEM, and QK of its last two chunks stands between the tiles of PV; where the next
-            // block needs new queries, PV goes first.
+        } else if (warp == kQkWarp) {
+            // ---------------- QK. (It and PV are issued by a warp each, so that neither waits for
+            // what the other one needs.)
             constexpr uint32_t idesc_qk = idesc_bf16(kBlock, kRows, false, false);
-            constexpr uint32_t idesc_pv = idesc_bf16(128, kRows, true, true);
+            const bool turn = p.b.cos_sin && p.turn_q;
             Walk walk(p, sStart);
             Segment x;
-            int i = -1, g = 0;                 // unit and block of QK
-            bool ok = true, pend = false, pend_first = false, pend_last = false;
-            int ends = 0;                      // units whose PV is all issued
-            bool have = walk.next(p, x);
-            const bool turn = p.b.cos_sin && p.turn_q;
-
-            // One pass per block, and one more where PV of the last block has no QK to go with:
-            // before new queries, and at the end. (One copy of each product's code: every byte of
-            // it is fetched anew in every pass.)
-            for (int b = 0; ok && (have || pend);) {
-                const bool fresh = b == 0;
-                const bool qk = have && !(fresh && pend);
-                const bool last = b == x.nb - 1;
-                if (qk) {
-                    if (fresh) {
-                        ++i;
-                        if (!(ok = wait_bar(q_full, i & 1, abort_flag, p.status))) break;
-                    }
-                    // QK, chunks 0-5
+            int i = 0, g = 0;
+            bool ok = true;
+            for (; ok && walk.next(p, x); ++i) {
+                if (!(ok = wait_bar(q_full, i & 1, abort_flag, p.status))) break;
+                for (int b = 0; b < x.nb; ++b, ++g) {
                     if (!(ok = wait_bar(s_free, (g & 1) ^ 1, abort_flag, p.status))) break;
-#pragma unroll 1
-                    for (int m = 0; m < 3; ++m) {
+#pragma unroll
+                    for (int m = 0; m < 3; ++m) {   // chunks 0-5
                         if (!(ok = wait_bar(&tm_full[m], g & 1, abort_flag, p.status))) break;
                         tc_fence_after();
                         if (elect_one()) {
@@ -455,21 +414,50 @@ __global__ void __launch_bounds__(kT, 1)
                         __syncwarp();
                     }
                     if (!ok) break;
+                    // chunk 6 and chunk 7
+                    if (!(ok = wait_bar(k6_full, g & 1, abort_flag, p.status))) break;
+                    if (!(ok = wait_bar(r_full, g & 1, abort_flag, p.status))) break;
+                    if (b == 0 && turn && !(ok = wait_bar(q_turned, i & 1, abort_flag, p.status)))
+                        break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t bd = desc_sw128(smem_u32(sQ) + 6 * 8192, 16, 1024);
+                        const uint64_t a6 = desc_sw128(smem_u32(s6), 16, 1024);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_bf16(tmem + kSCol, a6 + (k / 4) * (kChunk >> 4) + 2 * (k % 4),
+                                     bd + (k / 4) * (8192 >> 4) + 2 * (k % 4), idesc_qk, 1u);
+                        mma_commit(s_full);
+                        if (b == x.nb - 1) mma_commit(q_free);
+                    }
+                    __syncwarp();
                 }
-#pragma unroll 1
-                for (int st = 0; st < 4; ++st) {
-                    if (pend) {
-                        // tile m of PV of block g - 1, dims 128 m ..; the last one first, as its
-                        // chunk 6 is what QK of the next block waits for
-                        const int gb = g - 1, m = (st + 3) & 3;
-                        if (st == 0) {
-                            ok = wait_bar(p_full, gb & 1, abort_flag, p.status);
-                            if (ok && pend_first && ends > 0)
-                                ok = wait_bar(o_free, (ends - 1) & 1, abort_flag, p.status);
-                        } else {
-                            ok = wait_bar(&v_full[m], gb & 1, abort_flag, p.status);
-                        }
-                        if (!ok) break;
+            }
+            if (elect_one()) {
+                mma_commit(&drain[0]);
+                drain_wait(&drain[0], 0);
+            }
+            __syncwarp();
+        } else if (warp == kPvWarp) {
+            // ---------------- PV, tile by tile: the last one first, as its chunk 6 is what QK of
+            // the next block waits for
+            constexpr uint32_t idesc_pv = idesc_bf16(128, kRows, true, true);
+            Walk walk(p, sStart);
+            Segment x;
+            int i = 0, g = 0;
+            bool ok = true;
+            for (; ok && walk.next(p, x); ++i) {
+                for (int b = 0; b < x.nb && ok; ++b, ++g) {
+                    if (!(ok = wait_bar(p_full, g & 1, abort_flag, p.status))) break;
+                    // the results of the unit before must have left O^T
+                    if (b == 0 && i > 0 &&
+                        !(ok = wait_bar(o_free, (i - 1) & 1, abort_flag, p.status)))
+                        break;
+#pragma unroll
+                    for (int st = 0; st < 4; ++st) {
+                        const int m = (st + 3) & 3;   // dims 128 m ..
+                        if (st > 0 && !(ok = wait_bar(&v_full[m], g & 1, abort_flag, p.status)))
+                            break;
                         tc_fence_after();
                         if (elect_one()) {
                             const uint64_t ad = desc_sw128(
@@ -479,103 +467,104 @@ __global__ void __launch_bounds__(kT, 1)
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk)
                                 mma_bf16(tmem + kOCol + 64 * m, ad + ((kk * 2048) >> 4),
-                                         bd + ((kk * 2048) >> 4), idesc_pv,
-                                         kk > 0 || !pend_first);
+                                         bd + ((kk * 2048) >> 4), idesc_pv, kk > 0 || b > 0);
                             mma_commit(&v_free[m]);
                             if (st == 3) {
                                 mma_commit(pv_done);
-                                if (pend_last) mma_commit(o_full);
+                                if (b == x.nb - 1) mma_commit(o_full);
                             }
                         }
                         __syncwarp();
                     }
-                    if (st == 2 && qk) {
-                        // QK, chunk 6 and chunk 7
-                        ok = wait_bar(k6_full, g & 1, abort_flag, p.status) &&
-                             wait_bar(r_full, g & 1, abort_flag, p.status);
-                        if (ok && fresh && turn)
-                            ok = wait_bar(q_turned, i & 1, abort_flag, p.status);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-                            const uint64_t bd = desc_sw128(smem_u32(sQ) + 6 * 8192, 16, 1024);
-                            const uint64_t a6 = desc_sw128(smem_u32(s6), 16, 1024);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                mma_bf16(tmem + kSCol, a6 + (k / 4) * (kChunk >> 4) + 2 * (k % 4),
-                                         bd + (k / 4) * (8192 >> 4) + 2 * (k % 4), idesc_qk, 1u);
-                            mma_commit(s_full);
-                            if (last) mma_commit(q_free);
-                        }
-                        __syncwarp();
-                    }
-                }
-                if (!ok) break;
-                if (pend && pend_last) ++ends;
-                pend = qk;
-                if (qk) {
-                    pend_first = fresh;
-                    pend_last = last;
-                    ++g;
-                    if (++b == x.nb) {
-                        b = 0;
-                        have = walk.next(p, x);
-                    }
                 }
             }
             if (elect_one()) {
-                mma_commit(drain);
-                drain_wait(drain, 0);
+                mma_commit(&drain[1]);
+                drain_wait(&drain[1], 0);
             }
             __syncwarp();
         } else {
-            // ---------------- the queries: loaded when the last unit's products have read theirs,
-            // and turned in place, two rows a thread
+            // ---------------- the queries, loaded when the last unit's products have read theirs and
+            // turned in place, two rows a thread; and chunk 7 of each block, when PV of the block
+            // before has used it
             const bool turn = p.b.cos_sin && p.turn_q;
-            const uint64_t pol_stream = policy_evict_first();
+            const int prows = min(1 << p.b.page_shift, kBlock), np = kBlock / prows;
+            const uint64_t once = policy_evict_first(), keep = policy_evict_normal();
             Walk walk(p, sStart);
             Segment x;
-            int i = 0;
-            for (; walk.next(p, x); ++i) {
-                if (!__all_sync(0xFFFFFFFFu, wait_bar(q_free, (i & 1) ^ 1, abort_flag, p.status)))
+            int i = 0, t = 0;
+            bool ok = true;
+            for (; ok && walk.next(p, x); ++i) {
+                if (!(ok = __all_sync(0xFFFFFFFFu,
+                                      wait_bar(q_free, (i & 1) ^ 1, abort_flag, p.status))))
                     break;
                 if (lane == 0) {
                     mbar_expect_tx(q_full, 65536);
                     for (int c = 0; c < 8; ++c)
                         tma_load_2d(sQ + c * 8192, &tm_q, q_full, c * 64, static_cast<int>(x.row),
-                                    pol_stream);
+                                    once);
                 }
                 __syncwarp();
-                if (!turn) continue;
-                if (!__all_sync(0xFFFFFFFFu, wait_bar(q_full, i & 1, abort_flag, p.status))) {
+                for (int b = 0; b < x.nb; ++b, ++t) {
+                    // (a bad table entry is reported by the other loader)
+                    const int pos = x.block_pos(b) + lane * prows;
+                    int32_t e = -1;
+                    if (lane < np && pos <= x.posl && (pos > x.lo - prows || pos < p.sinks))
+                        e = __ldg(p.b.page_table + int64_t{x.s} * p.b.max_pages +
+                                  (pos >> p.b.page_shift));
+                    const bool there = e >= 0 && e < p.b.n_pages;
+                    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there);
+                    if (!(ok = __all_sync(0xFFFFFFFFu,
+                                          t == 0 || wait_bar(&v_free[3], (t - 1) & 1, abort_flag,
+                                                             p.status))))
+                        break;
+                    if (lane == 0)
+                        mbar_expect_tx(r_full, static_cast<uint32_t>(__popc(mask)) * prows * 128);
+                    __syncwarp();
+                    if (there)
+                        tma_load_3d(smem + kOff7 + lane * prows * 128, &tm_rope, r_full,
+                                    kQ4Rope / 2, pos & ((1 << p.b.page_shift) - 1), e,
+                                    x.alone ? once : keep);
+                    if (b > 0 || !turn) continue;
+                    if (!(ok = __all_sync(0xFFFFFFFFu,
+                                          wait_bar(q_full, i & 1, abort_flag, p.status)))) {
+                        ++t;
+                        break;
+                    }
+#pragma unroll 1
+                    for (int r = lane; r < x.nrows; r += 32) {
+                        uint8_t *row = sQ + 7 * 8192 + r * 128;
+                        const float4 *src = reinterpret_cast<const float4 *>(
+                            p.b.cos_sin + int64_t{row_pos(p, x.posf, r)} * kRope);
+#pragma unroll 4
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 c0 = __ldg(src + 2 * k), c1 = __ldg(src + 2 * k + 1);
+                            uint4 *at = reinterpret_cast<uint4 *>(row + ((k ^ (r & 7)) << 4));
+                            uint4 v = *at;
+                            v.x = turn_pair(v.x, c0.x, c0.y);
+                            v.y = turn_pair(v.y, c0.z, c0.w);
+                            v.z = turn_pair(v.z, c1.x, c1.y);
+                            v.w = turn_pair(v.w, c1.z, c1.w);
+                            *at = v;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(q_turned);
+                }
+                if (!ok) {
                     ++i;
                     break;
                 }
-#pragma unroll 1
-                for (int r = lane; r < x.nrows; r += 32) {
-                    uint8_t *row = sQ + 7 * 8192 + r * 128;
-                    const float4 *src = reinterpret_cast<const float4 *>(
-                        p.b.cos_sin + int64_t{row_pos(p, x.posf, r)} * kRope);
-#pragma unroll 4
-                    for (int k = 0; k < 8; ++k) {
-                        const float4 c0 = __ldg(src + 2 * k), c1 = __ldg(src + 2 * k + 1);
-                        uint4 *at = reinterpret_cast<uint4 *>(row + ((k ^ (r & 7)) << 4));
-                        uint4 v = *at;
-                        v.x = turn_pair(v.x, c0.x, c0.y);
-                        v.y = turn_pair(v.y, c0.z, c0.w);
-                        v.z = turn_pair(v.z, c1.x, c1.y);
-                        v.w = turn_pair(v.w, c1.z, c1.w);
-                        *at = v;
-                    }
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(q_turned);
             }
             // no copy into this CTA's shared memory may still be in flight at exit
-            if (lane == 0 && i > 0) drain_wait(q_full, (i - 1) & 1);
+            if (lane == 0) {
+                if (i > 0) drain_wait(q_full, (i - 1) & 1);
+                if (t > 0) drain_wait(r_full, (t - 1) & 1);
+            }
             __syncwarp();
         }
     } else if (warp < kSoftWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
         // ---------------- unpacking. Step t: chunk 6 of block t - 1, then pair by pair the chunks
         // of block t - 1 from TMEM to shared memory and those of block t into TMEM. (Once the kernel
         // gives up no wait lasts, and the next block does not come.)
@@ -628,17 +617,19 @@ __global__ void __launch_bounds__(kT, 1)
                 odd_next = has_nan(two[0]) || has_nan(two[1]) || has_nan(two[2]);
                 pow = pow2(max(static_cast<int>((head[3] >> 16) & 0xFFu), 11) - 138);
             }
-#pragma unroll
+            // (one copy of the code for the three pairs: fetching it costs more than the loop)
+#pragma unroll 1
             for (int m = 0; m < 3; ++m) {
+                const uint32_t col = k_col + 64 * m;
                 if (before) {
                     uint32_t v[32];
-                    tmem_ld32(k_col + 64 * m, v);
+                    const uint32_t to = to_v + 2 * m * kChunk;
+                    tmem_ld32(col, v);
                     if (t > 1) wait_bar(&v_free[m], t & 1, abort_flag, p.status);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int w = 0; w < 8; ++w)
-                        store_piece((to_v + 2 * m * kChunk) ^ (16 * w), v + 4 * w);
-                    if (odd) make_finite(to_v + 2 * m * kChunk);
+                    for (int w = 0; w < 8; ++w) store_piece(to ^ (16 * w), v + 4 * w);
+                    if (odd) make_finite(to);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&v_full[m]);
@@ -650,8 +641,9 @@ __global__ void __launch_bounds__(kT, 1)
                 if (have) {
                     // the 32 bytes of chunk 2 m + h: half (1 - h) of part m + h
                     uint32_t raw[8];
-                    const uint32_t at = (from + ((m + h) & 1) * 8192) ^ (h ? 0 : 32);
-                    wait_bar(&raw_full[(m + h) & 1], (m + h) >> 1, abort_flag, p.status);
+                    const int part = m + h;
+                    const uint32_t at = (from + (part & 1) * 8192) ^ (h ? 0 : 32);
+                    wait_bar(&raw_full[part & 1], part >> 1, abort_flag, p.status);
                     load_piece(raw, at);
                     load_piece(raw + 4, at ^ 16);
                     if (m == 2) {
@@ -661,15 +653,17 @@ __global__ void __launch_bounds__(kT, 1)
                     }
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(&raw_free[(m + h) & 1]);
+                        mbar_arrive(&raw_free[part & 1]);
                         if (m == 2 && h == 0) mbar_arrive(&raw_free[1]);
                     }
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         uint32_t v[16];
-                        unpack32(raw + 4 * half, (two[m] >> (16 * half)) & 0xFFFFu, pow, v);
-                        tmem_st16(k_col + 64 * m + 16 * half, v);
+                        unpack32(raw + 4 * half, (two[0] >> (16 * half)) & 0xFFFFu, pow, v);
+                        tmem_st16(col + 16 * half, v);
                     }
+                    two[0] = two[1];
+                    two[1] = two[2];
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -680,6 +674,7 @@ __global__ void __launch_bounds__(kT, 1)
             before = have;
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
         // ---------------- softmax + epilogue, 8 warps: TMEM lanes of sub-partition sp (keys,
         // later dims) x rows [32 hh, 32 hh + 32)
         const int sp = warp & 3;
@@ -718,12 +713,15 @@ __global__ void __launch_bounds__(kT, 1)
                 uint32_t sa[32];
                 const uint32_t valid = sValid[4 * (g & (kRing - 1)) + sp];
                 if (live) tmem_ld32(s_col, sa);
-                uint32_t vis = 0xFFFFFFFFu;   // rows hb + j that see key k0 + kl
                 // every row sees every key of the warp, unless ...
                 const bool masked = k0 + 32 * sp + 31 > x.posf ||
                                     (p.window > 0 && k0 <= x.posl - p.window) ||
                                     valid != 0xFFFFFFFFu || !live;
                 tmem_wait_ld();
+                // S may take QK of the next block
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free);
                 if (masked) {
                     // rows [ra, rb) of the unit see the key: their token is not before it and
                     // less than `window` after it, or it is one of the first
@@ -738,7 +736,7 @@ __global__ void __launch_bounds__(kT, 1)
                     const int a = max(0, min(32, ra - hb)), e = max(0, min(32, rb - hb));
                     const uint32_t below_e = e == 32 ? 0xFFFFFFFFu : (1u << e) - 1u;
                     const uint32_t below_a = a == 32 ? 0xFFFFFFFFu : (1u << a) - 1u;
-                    vis = below_e & ~below_a;
+                    const uint32_t vis = below_e & ~below_a;   // rows hb + j that see the key
                     // A row of the cache that holds an infinity or NaN makes its logit non-finite
                     // in every row of q. Where a row of q must not see the key, those elements
                     // become zero in the tile (0 * inf in PV would reach every row); rows that
@@ -770,13 +768,8 @@ __global__ void __launch_bounds__(kT, 1)
                         __syncwarp();
                     }
                 }
-                // how far the products lie above the running maximum: decides the rescale, and
-                // times c is the exponent
-                if (vote_any_group(less_max(sa, sM + cur * 64 + hb) * p.c > kRescale, hh)) {
+                if (vote_any_group(over_max(sa, sM + cur * 64 + hb) * p.c > kRescale, hh)) {
                     // exact block maxima -> new running maximum; sums and O^T rescaled
-                    if (live) tmem_ld32(s_col, sa);
-                    tmem_wait_ld();
-                    if (masked) hide32(sa, vis);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         const float wm = redux_max(__uint_as_float(sa[j]));
@@ -794,7 +787,6 @@ __global__ void __launch_bounds__(kT, 1)
                     }
                     bar_group(hh);
                     cur ^= 1;
-                    less_max(sa, sM + cur * 64 + hb);
                     const uint64_t *alpha = reinterpret_cast<const uint64_t *>(sAlpha + hb);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) l[j] = mul_pair(l[j], alpha[j]);
@@ -816,17 +808,15 @@ __global__ void __launch_bounds__(kT, 1)
                         tmem_wait_st();
                     }
                 }
-                // S may take QK of the next block
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(s_free);
                 // this thread's 32 rows of P^T for key kl. The sums take P as rounded to bf16, the
                 // values that PV multiplies.
                 uint32_t pk[16];
                 const uint64_t c2 = pair_of(p.c);
+                const uint64_t *m2 = reinterpret_cast<const uint64_t *>(sM + cur * 64 + hb);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const uint64_t y = mul_pair(pair_of(sa[2 * j], sa[2 * j + 1]), c2);
+                    const uint64_t y =
+                        mul_pair(add_pair(pair_of(sa[2 * j], sa[2 * j + 1]), m2[j]), c2);
                     const __nv_bfloat162 v =
                         __floats2bfloat162_rn(ex2(first_of(y)), ex2(second_of(y)));
                     pk[j] = *reinterpret_cast<const uint32_t *>(&v);
@@ -943,7 +933,7 @@ __global__ void __launch_bounds__(kT, 1)
         }
     }
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == kPvWarp) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
