@@ -23,9 +23,9 @@
 // bytes each, a sector and a line for every lane of a load keep the load unit busy for longer than
 // the products take.)
 //
-// Roles (640 threads): warp 0 loads the 4-bit bytes; warp 1 issues QK, warp 3 PV; warp 2 loads q,
-// turns it, and loads chunk 7; warps 4-11 unpack: thread = key, each half of the warps every other
-// chunk; warps 12-19 softmax and results, 32 rows of 32 keys a warp.
+// Roles (768 threads): warp 0 loads the 4-bit bytes; warp 1 issues QK, warp 3 PV; warp 2 loads q,
+// turns it, and loads chunk 7; warps 4-15 unpack: thread = key, a third of the warps each pair of
+// chunks 0-5; warps 16-23 softmax and results, 32 rows of 32 keys a warp.
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -41,15 +41,15 @@ namespace {
 
 using namespace paged;
 
-constexpr int kT = 640;
+constexpr int kT = 768;
 constexpr int kQkWarp = 1;
 constexpr int kQWarp = 2;
 constexpr int kPvWarp = 3;
 constexpr int kUnpackWarp0 = 4;
-constexpr int kSoftWarp0 = 12;
-constexpr int kRegsLaunch = 96;
-constexpr int kRegsLow = 80;
-constexpr int kRegsSoft = 120;     // 384*80 + 256*120 = 640*96, the launch allocation
+constexpr int kSoftWarp0 = 16;
+constexpr int kRegsLaunch = 80;
+constexpr int kRegsLow = 64;
+constexpr int kRegsSoft = 112;     // 512*64 + 256*112 = 768*80, the launch allocation
 
 constexpr int kRows = 64;          // rows of q in a unit (MMA N)
 constexpr int kRing = 4;           // blocks whose valid keys are kept
@@ -90,6 +90,17 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
         " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
         : "memory");
 }
 
@@ -168,6 +179,15 @@ __device__ __forceinline__ void load_piece(uint32_t *v, uint32_t at) {
                  : "memory");
 }
 
+// Hands bytes of shared memory that this warp has read back to the copies that fill them. (The fence
+// is needed: an arrival alone is performed while loads are on their way, and without it the next
+// part's bytes were unpacked in the place of this one's.)
+__device__ __forceinline__ void give_back(uint64_t *bar, int lane) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+
 // A chunk's row of a key in shared memory without its infinities and NaN.
 static __device__ __noinline__ void make_finite(uint32_t row) {
 #pragma unroll 1
@@ -241,21 +261,21 @@ __global__ void __launch_bounds__(kT, 1)
     uint64_t *v_full = bars + 3;    // [3] pair of chunks 0-5 in shared memory
     uint64_t *v_free = bars + 6;    // [4] pair of chunks used by PV
     uint64_t *k6_full = bars + 10;  // chunk 6 unpacked
-    uint64_t *raw_free = bars + 11; // [2] 4-bit bytes taken
-    uint64_t *raw_full = bars + 13; // [2] 4-bit bytes landed
-    uint64_t *r_full = bars + 15;   // chunk 7 landed
-    uint64_t *qa_done = bars + 16;  // QK has read the chunks in TMEM
-    uint64_t *q_full = bars + 17;
-    uint64_t *q_free = bars + 18;
-    uint64_t *q_turned = bars + 19;
-    uint64_t *s_full = bars + 20;
-    uint64_t *s_free = bars + 21;
-    uint64_t *p_full = bars + 22;
-    uint64_t *pv_done = bars + 23;  // P may be written, O rescaled
-    uint64_t *o_full = bars + 24;
-    uint64_t *o_free = bars + 25;
-    uint64_t *drain = bars + 26;    // [2] one per issuing warp
-    constexpr int kBars = 28;
+    uint64_t *raw_free = bars + 11; // [4] a part of the 4-bit bytes taken
+    uint64_t *raw_full = bars + 15; // [4] ... landed
+    uint64_t *r_full = bars + 19;   // chunk 7 landed
+    uint64_t *qa_done = bars + 20;  // QK has read the chunks in TMEM
+    uint64_t *q_full = bars + 21;
+    uint64_t *q_free = bars + 22;
+    uint64_t *q_turned = bars + 23;
+    uint64_t *s_full = bars + 24;
+    uint64_t *s_free = bars + 25;
+    uint64_t *p_full = bars + 26;
+    uint64_t *pv_done = bars + 27;  // P may be written, O rescaled
+    uint64_t *o_full = bars + 28;
+    uint64_t *o_free = bars + 29;
+    uint64_t *drain = bars + 30;    // [2] one per issuing warp
+    constexpr int kBars = 32;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + kBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *sStart = reinterpret_cast<int *>(tmem_holder + 2);    // [5] start of this CTA's run
@@ -273,15 +293,17 @@ __global__ void __launch_bounds__(kT, 1)
         return;
     }
     if (warp == 0) {
-        // arrivals a phase takes: 8 unpacking warps on tm_full, v_full, k6_full and raw_free, the
-        // turning warp's threads on q_turned, 8 softmax warps on s_free, p_full and o_free, one on
-        // the others
+        // arrivals a phase takes: the unpacking warps of a pair on tm_full and v_full, of both
+        // halves of chunk 6 on k6_full, those that read a part on raw_free; the turning warp's
+        // threads on q_turned, 8 softmax warps on s_free, p_full and o_free, one on the others
         int n = 1;
         uint64_t *bar = bars + lane;
-        if (bar < v_free || (bar >= k6_full && bar < raw_full)) n = 8;
+        if (bar < v_free) n = 4;
+        if (bar == k6_full || bar == raw_free + 1 || bar == raw_free + 2) n = 8;
+        if (bar == raw_free || bar == raw_free + 3) n = 12;
         if (bar == q_turned) n = 32;
         if (bar == s_free || bar == o_free || bar == p_full) n = 8;
-        if (lane < kBars) mbar_init(bar, n);
+        mbar_init(bar, n);
         if (lane == 31) {
             *abort_flag = 0;
             sStart[4] = 0;
@@ -320,7 +342,7 @@ __global__ void __launch_bounds__(kT, 1)
             // keys [a, b) and those below c of a block are seen by some token
             int a = 0, b = 0, c = 0, a_next = 0, b_next = 0, c_next = 0;
             bool alone = false, alone_next = false;
-            int uses0 = 0, uses1 = 0;   // of either slot, the end's among them
+            int parts = 0;   // loaded so far
             for (int t = -1;; ++t) {
                 have_next = walk.have;
                 if (have_next) {
@@ -340,8 +362,10 @@ __global__ void __launch_bounds__(kT, 1)
                     const uint32_t bytes = static_cast<uint32_t>(__popc(mask)) * prows * 64;
 #pragma unroll 1
                     for (int j = 0; j < 4; ++j) {
-                        ok = __all_sync(0xFFFFFFFFu, wait_bar(&raw_free[j & 1], (j >> 1) ^ 1,
-                                                              abort_flag, p.status));
+                        // (the part before in the slot: 2, 3 of the last block, then 0, 1)
+                        ok = __all_sync(0xFFFFFFFFu,
+                                        wait_bar(&raw_free[j ^ 2], (t & 1) ^ (j < 2), abort_flag,
+                                                 p.status));
                         if (!ok) break;
                         if (j == 0) {
 #pragma unroll
@@ -355,17 +379,16 @@ __global__ void __launch_bounds__(kT, 1)
                             if (lane == 4) sMore[t & (kRing - 1)] = have;
                             __syncwarp();
                         }
-                        uses0 += ~j & 1;
-                        uses1 += j & 1;
                         if (!have) {
                             if (lane == 0) mbar_arrive(&raw_full[0]);
                             break;
                         }
-                        if (lane == 0) mbar_expect_tx(&raw_full[j & 1], bytes);
+                        ++parts;
+                        if (lane == 0) mbar_expect_tx(&raw_full[j], bytes);
                         __syncwarp();
                         if (e >= 0)
                             tma_load_3d(smem + kOffRaw + (j & 1) * 8192 + lane * prows * 64,
-                                        &tm_raw, &raw_full[j & 1], 32 * j, row, e,
+                                        &tm_raw, &raw_full[j], 32 * j, row, e,
                                         alone ? once : keep);
                     }
                     if (!ok || !have) break;
@@ -381,8 +404,8 @@ __global__ void __launch_bounds__(kT, 1)
             // no copy into this CTA's shared memory may still be in flight at exit
             __syncwarp();
             if (lane == 0) {
-                if (uses0 > 0) drain_wait(&raw_full[0], (uses0 - 1) & 1);
-                if (uses1 > 0) drain_wait(&raw_full[1], (uses1 - 1) & 1);
+                for (int l = max(0, parts - 2); l < parts; ++l)
+                    drain_wait(&raw_full[l & 3], (l >> 2) & 1);
             }
             __syncwarp();
         } else if (warp == kQkWarp) {
@@ -398,7 +421,7 @@ __global__ void __launch_bounds__(kT, 1)
                 if (!(ok = wait_bar(q_full, i & 1, abort_flag, p.status))) break;
                 for (int b = 0; b < x.nb; ++b, ++g) {
                     if (!(ok = wait_bar(s_free, (g & 1) ^ 1, abort_flag, p.status))) break;
-#pragma unroll
+#pragma unroll 1
                     for (int m = 0; m < 3; ++m) {   // chunks 0-5
                         if (!(ok = wait_bar(&tm_full[m], g & 1, abort_flag, p.status))) break;
                         tc_fence_after();
@@ -453,7 +476,7 @@ __global__ void __launch_bounds__(kT, 1)
                     if (b == 0 && i > 0 &&
                         !(ok = wait_bar(o_free, (i - 1) & 1, abort_flag, p.status)))
                         break;
-#pragma unroll
+#pragma unroll 1
                     for (int st = 0; st < 4; ++st) {
                         const int m = (st + 3) & 3;   // dims 128 m ..
                         if (st > 0 && !(ok = wait_bar(&v_full[m], g & 1, abort_flag, p.status)))
@@ -565,24 +588,25 @@ __global__ void __launch_bounds__(kT, 1)
         }
     } else if (warp < kSoftWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
-        // ---------------- unpacking. Step t: chunk 6 of block t - 1, then pair by pair the chunks
-        // of block t - 1 from TMEM to shared memory and those of block t into TMEM. (Once the kernel
-        // gives up no wait lasts, and the next block does not come.)
+        // ---------------- unpacking. Step t: chunk 6 of block t - 1 (a half by each of the first two
+        // thirds of the warps), then a third's pair of chunks of block t - 1 from TMEM to shared
+        // memory and that of block t into TMEM. (Once the kernel gives up no wait lasts, and the
+        // next block does not come.)
         const int sp = warp & 3, h = (warp - kUnpackWarp0) >> 2;
         const int key = 32 * sp + lane;
-        const uint32_t k_col = tmem + (static_cast<uint32_t>(sp * 32) << 16) + kKCol + 32 * h;
+        const uint32_t k_col = tmem + (static_cast<uint32_t>(sp * 32) << 16) + kKCol + 64 * h;
         // (piece w of a swizzled row lies at the row's place ^ 16 w)
         const uint32_t row_at = key * 128 + ((key & 7) << 4);
         const uint32_t to6 = (smem_u32(s6) + row_at) ^ (64 * h);
-        const uint32_t to_v = smem_u32(sV) + h * kChunk + row_at;
+        const uint32_t to_v = smem_u32(sV) + 2 * h * kChunk + row_at;
         const uint32_t from = smem_u32(smem) + kOffRaw + key * 64 + (((key >> 1) & 3) << 4);
 
-        uint32_t raw6[4], two[3], two6;      // bytes of chunk 6's half; scales of the chunks' halves
+        uint32_t raw6[4], two6 = 0;          // bytes of chunk 6's half, its scales
         float pow = 0.0f;                    // half of the row's power of two
         bool odd = false;                    // a scale that is NaN, in the block to be copied
         bool have = true, before = false;    // block t is there, block t - 1 is to be copied
         for (int t = 0;; ++t) {
-            if (before) {
+            if (before && h < 2) {
                 // chunk 6 of block t - 1, in the place that PV of block t - 2 has left
                 uint32_t v[16];
                 unpack32(raw6, two6 & 0xFFFFu, pow, v);
@@ -593,10 +617,11 @@ __global__ void __launch_bounds__(kT, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(k6_full);
             }
+            uint32_t two[2] = {};            // scales of the pair's chunks
             bool odd_next = false;
             if (have) {
                 const bool ok =
-                    __all_sync(0xFFFFFFFFu, wait_bar(&raw_full[0], 0, abort_flag, p.status));
+                    __all_sync(0xFFFFFFFFu, wait_bar(&raw_full[0], t & 1, abort_flag, p.status));
                 have = ok && sMore[t & (kRing - 1)];
             }
             if (!have && !before) break;
@@ -605,70 +630,67 @@ __global__ void __launch_bounds__(kT, 1)
                 uint32_t head[8];
                 load_piece(head, from);
                 load_piece(head + 4, from ^ 16);
-                if (h == 1) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&raw_free[0]);
-                }
                 const bool there = (sValid[4 * (t & (kRing - 1)) + sp] >> lane) & 1u;
-#pragma unroll
-                for (int m = 0; m < 3; ++m)   // chunk 2 m + h: bytes 4 m + 2 h of either half
-                    two[m] = there ? __byte_perm(head[m], head[4 + m], h ? 0x7632 : 0x5410) : 0u;
-                two6 = there ? (h ? head[7] : head[3]) : 0u;  // chunk 6, half h: bytes 12 and 13
-                odd_next = has_nan(two[0]) || has_nan(two[1]) || has_nan(two[2]);
+                // chunk c: bytes 2 c and 2 c + 1 of either half; chunk 6's half h: 12 and 13
+                const uint32_t lo = h == 0 ? head[0] : h == 1 ? head[1] : head[2];
+                const uint32_t hi = h == 0 ? head[4] : h == 1 ? head[5] : head[6];
+                two6 = h ? head[7] : head[3];
+                if (there) {
+                    two[0] = __byte_perm(lo, hi, 0x5410);
+                    two[1] = __byte_perm(lo, hi, 0x7632);
+                } else {
+                    two6 = 0;
+                }
+                odd_next = has_nan(two[0]) || has_nan(two[1]);
                 pow = pow2(max(static_cast<int>((head[3] >> 16) & 0xFFu), 11) - 138);
+                if (h > 0) give_back(&raw_free[0], lane);
             }
-            // (one copy of the code for the three pairs: fetching it costs more than the loop)
+            if (before) {
+                if (t > 1) wait_bar(&v_free[h], t & 1, abort_flag, p.status);
 #pragma unroll 1
-            for (int m = 0; m < 3; ++m) {
-                const uint32_t col = k_col + 64 * m;
-                if (before) {
+                for (int c = 0; c < 2; ++c) {
                     uint32_t v[32];
-                    const uint32_t to = to_v + 2 * m * kChunk;
-                    tmem_ld32(col, v);
-                    if (t > 1) wait_bar(&v_free[m], t & 1, abort_flag, p.status);
+                    const uint32_t to = to_v + c * kChunk;
+                    tmem_ld32(k_col + 32 * c, v);
                     tmem_wait_ld();
 #pragma unroll
                     for (int w = 0; w < 8; ++w) store_piece(to ^ (16 * w), v + 4 * w);
                     if (odd) make_finite(to);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&v_full[m]);
-                    if (m == 0 && have) {    // QK of block t - 1 has read what is overwritten
-                        wait_bar(qa_done, (t - 1) & 1, abort_flag, p.status);
-                        tc_fence_after();
-                    }
                 }
-                if (have) {
-                    // the 32 bytes of chunk 2 m + h: half (1 - h) of part m + h
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&v_full[h]);
+                // QK of block t - 1 has read what is overwritten
+                wait_bar(qa_done, (t - 1) & 1, abort_flag, p.status);
+                tc_fence_after();
+            }
+            if (have) {
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    // the 32 bytes of chunk 2 h + c: half (1 - c) of part h + c
                     uint32_t raw[8];
-                    const int part = m + h;
-                    const uint32_t at = (from + (part & 1) * 8192) ^ (h ? 0 : 32);
-                    wait_bar(&raw_full[part & 1], part >> 1, abort_flag, p.status);
+                    const int part = h + c;
+                    const uint32_t at = (from + (part & 1) * 8192) ^ (c ? 0 : 32);
+                    wait_bar(&raw_full[part], t & 1, abort_flag, p.status);
                     load_piece(raw, at);
                     load_piece(raw + 4, at ^ 16);
-                    if (m == 2) {
-                        // and those of chunk 6: the second half of part 3
-                        if (h == 0) wait_bar(&raw_full[1], 1, abort_flag, p.status);
-                        load_piece(raw6, (from + 8192) ^ (32 + 16 * h));
-                    }
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&raw_free[part & 1]);
-                        if (m == 2 && h == 0) mbar_arrive(&raw_free[1]);
-                    }
+                    if (part < 3) give_back(&raw_free[part], lane);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         uint32_t v[16];
                         unpack32(raw + 4 * half, (two[0] >> (16 * half)) & 0xFFFFu, pow, v);
-                        tmem_st16(col + 16 * half, v);
+                        tmem_st16(k_col + 32 * c + 16 * half, v);
                     }
                     two[0] = two[1];
-                    two[1] = two[2];
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&tm_full[m]);
                 }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tm_full[h]);
+                // the bytes of chunk 6: the second half of part 3
+                wait_bar(&raw_full[3], t & 1, abort_flag, p.status);
+                if (h < 2) load_piece(raw6, (from + 8192) ^ (32 + 16 * h));
+                give_back(&raw_free[3], lane);
             }
             odd = odd_next;
             before = have;
