@@ -360,6 +360,16 @@ __global__ void __launch_bounds__(kT, 1)
                     *sBlocks = static_cast<uint32_t>(t) + 1;
                     const uint32_t mask = __ballot_sync(0xFFFFFFFFu, e >= 0);
                     const uint32_t bytes = static_cast<uint32_t>(__popc(mask)) * prows * 64;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int key = 32 * w + lane;
+                        const uint32_t there = __ballot_sync(
+                            0xFFFFFFFFu, ((mask >> (key >> key_shift)) & 1u) && key < b &&
+                                             (key >= a || key < c));
+                        if (lane == w) sValid[4 * (t & (kRing - 1)) + w] = there;
+                    }
+                    if (lane == 4) sMore[t & (kRing - 1)] = have;
+                    __syncwarp();
 #pragma unroll 1
                     for (int j = 0; j < 4; ++j) {
                         // (the part before in the slot: 2, 3 of the last block, then 0, 1)
@@ -367,18 +377,6 @@ __global__ void __launch_bounds__(kT, 1)
                                         wait_bar(&raw_free[j ^ 2], (t & 1) ^ (j < 2), abort_flag,
                                                  p.status));
                         if (!ok) break;
-                        if (j == 0) {
-#pragma unroll
-                            for (int w = 0; w < 4; ++w) {
-                                const int key = 32 * w + lane;
-                                const uint32_t there = __ballot_sync(
-                                    0xFFFFFFFFu, ((mask >> (key >> key_shift)) & 1u) && key < b &&
-                                                     (key >= a || key < c));
-                                if (lane == w) sValid[4 * (t & (kRing - 1)) + w] = there;
-                            }
-                            if (lane == 4) sMore[t & (kRing - 1)] = have;
-                            __syncwarp();
-                        }
                         if (!have) {
                             if (lane == 0) mbar_arrive(&raw_full[0]);
                             break;
@@ -617,7 +615,7 @@ __global__ void __launch_bounds__(kT, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(k6_full);
             }
-            uint32_t two[2] = {};            // scales of the pair's chunks
+            uint32_t two[2] = {}, raw[2][8];  // scales and bytes of the pair's chunks
             bool odd_next = false;
             if (have) {
                 const bool ok =
@@ -644,17 +642,31 @@ __global__ void __launch_bounds__(kT, 1)
                 odd_next = has_nan(two[0]) || has_nan(two[1]);
                 pow = pow2(max(static_cast<int>((head[3] >> 16) & 0xFFu), 11) - 138);
                 if (h > 0) give_back(&raw_free[0], lane);
+                // The pair's bytes: chunk 2 h + c is half (1 - c) of part h + c. (All of them here, so
+                // that the next block's are on their way during the copy and the conversion.)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int part = h + c;
+                    const uint32_t at = (from + (part & 1) * 8192) ^ (c ? 0 : 32);
+                    wait_bar(&raw_full[part], t & 1, abort_flag, p.status);
+                    load_piece(raw[c], at);
+                    load_piece(raw[c] + 4, at ^ 16);
+                    if (part < 3) give_back(&raw_free[part], lane);
+                }
             }
             if (before) {
                 if (t > 1) wait_bar(&v_free[h], t & 1, abort_flag, p.status);
 #pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t v[32];
                     const uint32_t to = to_v + c * kChunk;
-                    tmem_ld32(k_col + 32 * c, v);
-                    tmem_wait_ld();
 #pragma unroll
-                    for (int w = 0; w < 8; ++w) store_piece(to ^ (16 * w), v + 4 * w);
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t v[16];
+                        tmem_ld16(k_col + 32 * c + 16 * k, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) store_piece(to ^ (64 * k + 16 * w), v + 4 * w);
+                    }
                     if (odd) make_finite(to);
                 }
                 fence_proxy_async_smem();
@@ -665,24 +677,14 @@ __global__ void __launch_bounds__(kT, 1)
                 tc_fence_after();
             }
             if (have) {
-#pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                    // the 32 bytes of chunk 2 h + c: half (1 - c) of part h + c
-                    uint32_t raw[8];
-                    const int part = h + c;
-                    const uint32_t at = (from + (part & 1) * 8192) ^ (c ? 0 : 32);
-                    wait_bar(&raw_full[part], t & 1, abort_flag, p.status);
-                    load_piece(raw, at);
-                    load_piece(raw + 4, at ^ 16);
-                    if (part < 3) give_back(&raw_free[part], lane);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         uint32_t v[16];
-                        unpack32(raw + 4 * half, (two[0] >> (16 * half)) & 0xFFFFu, pow, v);
+                        unpack32(raw[c] + 4 * half, (two[c] >> (16 * half)) & 0xFFFFu, pow, v);
                         tmem_st16(k_col + 32 * c + 16 * half, v);
                     }
-                    two[0] = two[1];
-                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
