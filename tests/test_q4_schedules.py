@@ -2,7 +2,7 @@
 test_paged_schedules.py (whose machine and rules it uses): every wait is checked for missed phases
 and for phases it would take for an earlier one, every buffer for whom it is for.
 
-The four warps of a third of the unpackers are two here, as are the four of a half of the softmax.
+The four warps of a half of the unpackers are two here, as are those of a half of the softmax.
 (The wait for o_free is implied by others: PV of a unit's first block waits for the P of warps that
 have stored the unit before.)"""
 import random
@@ -21,23 +21,24 @@ def ahead(name, role):
 
 
 def q4(rng, left_out=None):
-    """q4_attn.cu: raw loader, queries and chunk 7, QK, PV, unpackers in thirds, softmax in halves."""
+    """q4_attn.cu: raw loader, queries and chunk 7, QK, PV, unpackers and softmax in halves."""
     m = Machine(rng, left_out)
     rope = rng.random() < 0.7
     units = [rng.choice([1, 1, 1, 2, 3, 5]) for _ in range(rng.randint(1, 7))]
     blocks = [(i, b) for i, nb in enumerate(units) for b in range(nb)]
     n = len(blocks)
-    tm_full, v_full = [Bar(2) for _ in range(3)], [Bar(2) for _ in range(3)]
+    tm_full, v_full = [Bar(4) for _ in range(3)], [Bar(4) for _ in range(3)]
     v_free = [Bar() for _ in range(4)]
-    raw_free = [Bar(6), Bar(4), Bar(4), Bar(6)]
+    raw_free = [Bar(4) for _ in range(4)]
     raw_full = [Bar() for _ in range(4)]
     k6_full, r_full, qa_done = Bar(4), Bar(), Bar()
     q_full, q_free, q_turned = Bar(), Bar(), Bar()
     s_full, s_free, p_full, pv_done, o_full, o_free = Bar(), Bar(4), Bar(4), Bar(), Bar(), Bar(4)
     group = [Bar(2), Bar(2)]
     raw, valid = [None, None], [None] * RING      # raw: (block, part)
-    tmem = {(h, w): None for h in range(3) for w in range(2)}
+    tmem = {(m_, h, w): None for m_ in range(3) for h in range(2) for w in range(2)}
     V, k6 = dict(tmem), {(h, w): None for h in range(2) for w in range(2)}
+    pair = lambda of, k: [of[k, h, w] for h in range(2) for w in range(2)]  # noqa: E731
     at = dict(q=None, turned=None, S=None, O=None, r=None)
     P = {}
 
@@ -94,7 +95,7 @@ def q4(rng, left_out=None):
                     yield m.wait("tm_full", tm_full[h], g)
 
                     def step(i=i, g=g, h=h):
-                        assert at["q"] == i and [tmem[h, w] for w in range(2)] == [g] * 2
+                        assert at["q"] == i and pair(tmem, h) == [g] * 4
                         at["S"] = None
                         if h == 2:
                             qa_done.arrive()
@@ -131,7 +132,7 @@ def q4(rng, left_out=None):
                         if st == 0:
                             assert list(k6.values()) == [g] * 4 and at["r"] == g
                         else:
-                            assert [V[h, w] for w in range(2)] == [g] * 2
+                            assert pair(V, h) == [g] * 4
                         at["O"] = (i, b, st)
                         v_free[h].arrive()
                         if st == 3:
@@ -144,7 +145,7 @@ def q4(rng, left_out=None):
     def unpack(h, w):
         have, before, t = True, False, 0
         while True:
-            if before and h < 2:
+            if before:
                 if t > 1:
                     yield m.wait("v_free of chunk 6", v_free[3], t - 2)
                 k6[h, w] = t - 1
@@ -157,35 +158,37 @@ def q4(rng, left_out=None):
                 return
             if have:
                 assert raw[0] == (t, 0) and valid[t % RING] == t
-                if h > 0:
+                if h == 1:
                     yield None
                     raw_free[0].arrive()
-            if before:
-                if t > 1:
-                    yield m.wait("v_free", v_free[h], t - 2)
-                assert tmem[h, w] == t - 1
-                V[h, w] = t - 1
-                yield None
-                v_full[h].arrive()
-                yield m.wait("qa_done", qa_done, t - 1)
-            if have:
-                tmem[h, w] = None
-                for c in range(2):
-                    part = h + c
+            for k in range(3):
+                part = k + h
+                if have:
                     yield m.wait("raw_full", raw_full[part], t)
                     assert raw[part & 1] == (t, part)
                     yield None
                     assert raw[part & 1] == (t, part)
                     if part < 3:
                         raw_free[part].arrive()
+                if before:
+                    if t > 1:
+                        yield m.wait("v_free", v_free[k], t - 2)
+                    assert tmem[k, h, w] == t - 1
+                    V[k, h, w] = t - 1
                     yield None
-                tmem[h, w] = t
-                yield None
-                tm_full[h].arrive()
-                yield m.wait("raw_full", raw_full[3], t)
-                assert raw[1] == (t, 3)
-                yield None
-                raw_free[3].arrive()
+                    v_full[k].arrive()
+                    if k == 0 and have:
+                        yield m.wait("qa_done", qa_done, t - 1)
+                if have:
+                    tmem[k, h, w] = None
+                    if k == 2:
+                        yield m.wait("raw_full", raw_full[3], t)
+                        assert raw[1] == (t, 3)
+                        yield None
+                        raw_free[3].arrive()
+                    tmem[k, h, w] = t
+                    yield None
+                    tm_full[k].arrive()
             before = have
             t += 1
 
@@ -215,11 +218,9 @@ def q4(rng, left_out=None):
             o_free.arrive()
 
     m.roles = dict(load=loader(), q=queries(), qk=qk(), pv=pv())
-    for h in range(3):
-        for w in range(2):
-            m.roles["unpack", h, w] = unpack(h, w)
     for half in range(2):
         for w in range(2):
+            m.roles["unpack", half, w] = unpack(half, w)
             P[half, w] = None
             m.roles["soft", half, w] = softmax(half, w)
     m.roles = {k: ahead(k, v) for k, v in m.roles.items()}
