@@ -8,12 +8,16 @@
 #include <math.h>
 
 #include "common.cuh"
-#include "paged.h"
+#include "paged_walk.cuh"
 #include "q4.h"
 
 namespace dsa {
 
 namespace {
+
+using paged::add_pair;
+using paged::fma_pair;
+using paged::pair_of;
 
 constexpr int kQ4Warps = 8;
 constexpr uint32_t kQ4Limit = (124u + 127u) << 23;  // the bits of 2^124
@@ -54,8 +58,39 @@ __device__ __forceinline__ bool find_row(const PagedBatch &b, int64_t r, int lan
     return true;
 }
 
+// x / s rounded to a whole number of -7 .. 7, ties to even, plus 8, from x and 1 / s (0 for 8 or
+// where the group holds what is not finite). x has eight significant bits and s four, so a quotient
+// of 0.4 or more that is no tie is 2^-10.9 or more from one; the product with the rounded 1 / s is
+// 2^-19 off at most. Rounded to a multiple of 2^-11 first (by adding 6,144, whose last bit that is),
+// ties are ties and nothing else is.
+constexpr float kSnap = 6144.0f;
+constexpr float kWhole = 12582912.0f + 8.0f;   // 1.5 2^23 + 8: the last bit is 1
+__device__ __forceinline__ uint32_t whole_plus8(float x, float per, bool finite) {
+    const float t = __fadd_rn(fmaf(x, per, kSnap), -kSnap);
+    const float n = fminf(fmaxf(finite ? t : 0.0f, -7.0f), 7.0f);
+    return __float_as_uint(__fadd_rn(n, kWhole)) & 15u;
+}
+
+// The same for four words of two elements each, without the bounds, in the order of a word of codes.
+// Two elements an instruction; a sum in base 16 of the bits of n + kWhole, which are n + 8 above
+// those of kWhole - 8.
+__device__ __forceinline__ uint32_t eight_plain(const uint32_t *w, float per) {
+    const uint64_t p2 = pair_of(per), snap = pair_of(kSnap), back = pair_of(-kSnap);
+    const uint64_t whole = pair_of(kWhole);
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int k = 3; k >= 0; --k) {
+        const uint64_t x = pair_of(w[k] << 16, w[k] & 0xFFFF0000u);
+        const uint64_t n = add_pair(add_pair(fma_pair(x, p2, snap), back), whole);
+        lo = lo * 16u + static_cast<uint32_t>(n);
+        hi = hi * 16u + static_cast<uint32_t>(n >> 32);
+    }
+    constexpr uint32_t kBits = 0x4B400000u;   // of 1.5 2^23
+    return (lo - kBits * 0x1111u) | (hi - kBits * 0x1111u) << 16;
+}
+
 // Lane l has dims 16 l ..: a group of the 448, or (lanes 28 to 31) a quarter of the rotated ones.
-__global__ void __launch_bounds__(kQ4Warps * 32)
+__global__ void __launch_bounds__(kQ4Warps * 32, 2048 / (kQ4Warps * 32))
     q4_append_kernel(const PagedBatch b, const uint4 *kv, uint8_t *pages, int32_t *status) {
     wait_before();
     const int lane = threadIdx.x & 31;
@@ -71,11 +106,13 @@ __global__ void __launch_bounds__(kQ4Warps * 32)
     if (!row) return;
     uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
     const bool rope = lane >= 28;
-    // magnitudes as the bits of an fp32: whole numbers in the same order, NaN above all
-    uint32_t amax = 0;
+    // the group's largest magnitude (NaN with a NaN among them) as the bits of an fp32: whole numbers
+    // in the same order, NaN above all
+    uint32_t m2 = w[0] & 0x7FFF7FFFu;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        amax = max(amax, max((w[k] << 16) & 0x7FFF0000u, w[k] & 0x7FFF0000u));
+    for (int k = 1; k < 8; ++k)
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(w[k] & 0x7FFF7FFFu));
+    const uint32_t amax = max(m2 << 16, m2 & 0x7FFF0000u);
     const bool finite = amax < kQ4Limit;
     const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, rope || !finite ? 0u : amax);
     const int e = max(static_cast<int>(top >> 23) - 127, kQ4LeastExp);
@@ -86,17 +123,23 @@ __global__ void __launch_bounds__(kQ4Warps * 32)
         finite ? __nv_cvt_float_to_fp8(__uint_as_float(amax) * up / 7.0f, __NV_SATFINITE,
                                        __NV_E4M3)
                : 0x7Fu;
+    const float unit = finite ? e4m3(scale) : 0.0f;
+    const float per = unit > 0.0f ? 1.0f / unit : 0.0f;
+    // Ordinary rows: the power of two goes into 1 / s, and a normal s (off by 2^-4 at most) leaves
+    // no quotient above 7.5.
+    const bool plain = __all_sync(0xFFFFFFFFu, rope || (finite && (scale >= 8 || scale == 0))) &&
+                       e > -50 && e < 70;
     if (!rope) {
-        const float unit = finite ? e4m3(scale) : 0.0f;
         uint32_t code[2] = {0, 0};
+        if (plain) {
+            code[0] = eight_plain(w, up * per);
+            code[1] = eight_plain(w + 4, up * per);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            // (quotients that end in a half are exact: ties go to even numbers)
-            const float x0 = bf16lo(w[k]) * up / unit, x1 = bf16hi(w[k]) * up / unit;
-            const int n0 = unit > 0.0f ? max(-7, min(7, __float2int_rn(x0))) : 0;
-            const int n1 = unit > 0.0f ? max(-7, min(7, __float2int_rn(x1))) : 0;
-            code[k / 4] |= static_cast<uint32_t>(n0 + 8) << (4 * (k % 4));
-            code[k / 4] |= static_cast<uint32_t>(n1 + 8) << (4 * (k % 4) + 16);
+            for (int k = 0; k < 8; ++k) {
+                code[k / 4] |= whole_plus8(bf16lo(w[k]) * up, per, finite) << (4 * (k % 4));
+                code[k / 4] |= whole_plus8(bf16hi(w[k]) * up, per, finite) << (4 * (k % 4) + 16);
+            }
         }
         *reinterpret_cast<uint2 *>(row + 32 + 8 * lane) = make_uint2(code[0], code[1]);
     } else {
