@@ -292,26 +292,6 @@ def _refuse(where: str, name: str, dtype, want: str, device):
                                 f"cuda:{device}")
 
 
-def _angles(where: str, cos_sin, device):
-    """(address, positions) of the table of angles."""
-    if cos_sin is None:
-        return None, 0
-    n_pos = cos_sin.shape[0] if cos_sin.dim() else 0
-    if not (cos_sin.shape == (n_pos, ROPE_DIM // 2, 2) and cos_sin.dtype is _F32
-            and cos_sin.get_device() == device and cos_sin.is_contiguous()):
-        _refuse(where, "cos_sin", _F32, f"*, {ROPE_DIM // 2}, 2", device)
-    return cos_sin.data_ptr(), n_pos
-
-
-def _starts(where: str, new_start, seq_len, n_seqs, device):
-    if not (new_start.shape == (n_seqs + 1,) and new_start.dtype is _I32
-            and new_start.get_device() == device and new_start.is_contiguous()):
-        _refuse(where, "new_start", _I32, n_seqs + 1, device)
-    if not (seq_len.shape == (n_seqs,) and seq_len.dtype is _I32
-            and seq_len.get_device() == device and seq_len.is_contiguous()):
-        _refuse(where, "seq_len", _I32, n_seqs, device)
-
-
 def _paged(where: str, new_start, seq_len, page_table, pages, cos_sin, device, width=DIM,
            dtype=_BF16):
     """The arguments the paged calls share, checked, in the ABI's order. A row of the pages is
@@ -321,7 +301,12 @@ def _paged(where: str, new_start, seq_len, page_table, pages, cos_sin, device, w
             and page_table.is_contiguous()):
         _refuse(where, "page_table", _I32, "*, *", device)
     n_seqs, max_pages = table
-    _starts(where, new_start, seq_len, n_seqs, device)
+    if not (new_start.shape == (n_seqs + 1,) and new_start.dtype is _I32
+            and new_start.get_device() == device and new_start.is_contiguous()):
+        _refuse(where, "new_start", _I32, n_seqs + 1, device)
+    if not (seq_len.shape == (n_seqs,) and seq_len.dtype is _I32
+            and seq_len.get_device() == device and seq_len.is_contiguous()):
+        _refuse(where, "seq_len", _I32, n_seqs, device)
     if not (len(shape) == 3 and shape[2] == width and strides[2] == 1 and strides[1] == width
             and pages.dtype is dtype and pages.get_device() == device):
         raise DsaError(DSA_ERR_ARG, f"{where}: pages has to be a {dtype} tensor "
@@ -330,9 +315,16 @@ def _paged(where: str, new_start, seq_len, page_table, pages, cos_sin, device, w
     if (n_seqs | max_pages | page_size) >> 31:   # ctypes would drop the upper bits
         raise DsaError(DSA_ERR_SHAPE, f"{where}: {n_seqs} sequences of {max_pages} pages of "
                                       f"{page_size} rows are no 32-bit counts")
+    angles, n_pos = None, 0
+    if cos_sin is not None:
+        n_pos = cos_sin.shape[0] if cos_sin.dim() else 0
+        if not (cos_sin.shape == (n_pos, ROPE_DIM // 2, 2) and cos_sin.dtype is _F32
+                and cos_sin.get_device() == device and cos_sin.is_contiguous()):
+            _refuse(where, "cos_sin", _F32, f"*, {ROPE_DIM // 2}, 2", device)
+        angles = cos_sin.data_ptr()
     return (new_start.data_ptr(), seq_len.data_ptr(), n_seqs, page_table.data_ptr(), max_pages,
             pages.data_ptr(), n_pages, strides[0] if n_pages > 1 else page_size * width, page_size,
-            *_angles(where, cos_sin, device))
+            angles, n_pos)
 
 
 def _status(where: str, dev_status, device):
@@ -414,13 +406,24 @@ def dsa_qk_norm_rope(q, kv, new_start, seq_len, q_out, kv_out, cos_sin=None, q_w
                                   and w.is_contiguous()):
             _refuse(where, name, _F32, DIM, dev)
     n_seqs = seq_len.shape[0] if seq_len.dim() else 0
-    _starts(where, new_start, seq_len, n_seqs, dev)
+    if not (seq_len.shape == (n_seqs,) and seq_len.dtype is _I32 and seq_len.get_device() == dev
+            and seq_len.is_contiguous()):
+        _refuse(where, "seq_len", _I32, "*", dev)
+    if not (new_start.shape == (n_seqs + 1,) and new_start.dtype is _I32
+            and new_start.get_device() == dev and new_start.is_contiguous()):
+        _refuse(where, "new_start", _I32, n_seqs + 1, dev)
+    n_pos = 0
+    if cos_sin is not None:
+        n_pos = cos_sin.shape[0] if cos_sin.dim() else 0
+        if not (cos_sin.shape == (n_pos, ROPE_DIM // 2, 2) and cos_sin.dtype is _F32
+                and cos_sin.get_device() == dev and cos_sin.is_contiguous()):
+            _refuse(where, "cos_sin", _F32, f"*, {ROPE_DIM // 2}, 2", dev)
     if (n_seqs | shape[1]) >> 31:   # ctypes would drop the upper bits
         raise DsaError(DSA_ERR_SHAPE, f"{where}: {n_seqs} sequences or {shape[1]} heads are no "
                                       "32-bit counts")
     rc = (_lib or load()).dsa_qk_norm_rope(
         q.data_ptr(), shape[1], kv.data_ptr(), shape[0], new_start.data_ptr(), seq_len.data_ptr(),
-        n_seqs, _p(q_weight), _p(kv_weight), eps, *_angles(where, cos_sin, dev), q_out.data_ptr(),
+        n_seqs, _p(q_weight), _p(kv_weight), eps, _p(cos_sin), n_pos, q_out.data_ptr(),
         kv_out.data_ptr(), _status(where, dev_status, dev), _stream_of(stream, dev))
     _check(rc, where)
 
