@@ -793,11 +793,25 @@ __global__ void __launch_bounds__(kT, 1)
                 }
                 if (vote_any_group(over_max(sa, sM + cur * 64 + hb) * p.c > kRescale, hh)) {
                     // exact block maxima -> new running maximum; sums and O^T rescaled
+                    // (transposed and reduced over the warp's keys as the sums below: lane = row; a
+                    // redux.sync per row takes 4,000 cycles here, with all eight warps at it)
+                    float top[16];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float wm = redux_max(__uint_as_float(sa[j]));
-                        if (lane == j) sRed[sp * 64 + hb + j] = wm;
+                    for (int j = 0; j < 16; ++j) {
+                        const bool up = (lane & 16) != 0;
+                        const float lo = __uint_as_float(sa[j]), hi = __uint_as_float(sa[j + 16]);
+                        top[j] = fmaxf(up ? hi : lo,
+                                       __shfl_xor_sync(0xFFFFFFFFu, up ? lo : hi, 16));
                     }
+#pragma unroll
+                    for (int w = 8; w >= 1; w >>= 1) {
+                        const bool up = (lane & w) != 0;
+#pragma unroll
+                        for (int j = 0; j < w; ++j)
+                            top[j] = fmaxf(up ? top[j + w] : top[j],
+                                           __shfl_xor_sync(0xFFFFFFFFu, up ? top[j] : top[j + w], w));
+                    }
+                    sRed[sp * 64 + hb + lane] = top[0];
                     bar_group(hh);
                     if (sp == 0) {
                         const int r = hb + lane;
