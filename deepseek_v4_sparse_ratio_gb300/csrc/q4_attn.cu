@@ -907,61 +907,69 @@ __global__ void __launch_bounds__(kT, 1)
             bar_group(hh);
             // O^T into registers one d-tile at a time: lane holds dim 128 m + 32 sp + lane of
             // rows hb .. hb + 31, so a warp writes 32 consecutive dims of each row
-            const bool live = mbar_wait(o_full, i & 1, abort_flag, p.status);
-            tc_fence_after();
+            // (8 rows a step: the code stays where it is fetched from, and is fetched once)
             const int rows = min(32, x.nrows - hb);
+            const uint32_t o_col = lane_base + kOCol + hb;
             if (x.whole) {
-                __nv_bfloat16 *orow = p.out + (x.row + hb) * kD + 32 * sp + lane;
+                __nv_bfloat16 *o = p.out + (x.row + hb) * kD + 32 * sp + lane;
+                // turned back by the token's position; a pair is in two adjacent lanes
+                const bool turns = p.b.cos_sin && sp >= 2;
+                const float2 *cs =
+                    reinterpret_cast<const float2 *>(p.b.cos_sin) + ((sp - 2) * 16 + (lane >> 1));
+                // (a unit of one token's heads has one position)
+                int pos = p.tpu == 1 ? x.posf : x.posf + hb / p.rpt;
+                int left = p.tpu == 1 ? 32 : p.rpt - hb % p.rpt;  // rows at pos
+                float2 a = make_float2(1.0f, 0.0f);
+                if (turns) a = __ldg(cs + int64_t{pos <= x.posl ? pos : x.posl} * kRopePairs);
+                const bool live = mbar_wait(o_full, i & 1, abort_flag, p.status);
+                tc_fence_after();
 #pragma unroll 1
-                for (int m = 0; m < 4; ++m) {
-                    uint32_t oa[32];
+                for (int m = 0; m < 16; ++m) {    // dims 128 (m / 4) .., rows 8 (m % 4) ..
+                    uint32_t oa[8];
                     if (!__all_sync(0xFFFFFFFFu, live)) break;
-                    tmem_ld32(lane_base + kOCol + 64 * m + hb, oa);
+                    const int j0 = 8 * (m % 4);
+                    tmem_ld8(o_col + 64 * (m / 4) + j0, oa);
                     tmem_wait_ld();
-                    __nv_bfloat16 *o = orow + 128 * m;
-                    if (p.b.cos_sin && m == 3 && sp >= 2) {
-                        // turned back by the token's position; a pair is in two adjacent lanes
-                        const float2 *cs = reinterpret_cast<const float2 *>(p.b.cos_sin) +
-                                           ((sp - 2) * 16 + (lane >> 1));
-                        // (a unit of one token's heads has one position)
-                        int pos = p.tpu == 1 ? x.posf : x.posf + hb / p.rpt;
-                        int left = p.tpu == 1 ? 32 : p.rpt - hb % p.rpt;  // rows at pos
-                        float2 a = __ldg(cs + int64_t{pos <= x.posl ? pos : x.posl} * kRopePairs);
+                    __nv_bfloat16 *to = o + 128 * (m / 4) + j0 * kD;
+                    const float *inv = sLinv + hb + j0;
+                    if (turns && m >= 12) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float v = __uint_as_float(oa[j]) * sLinv[hb + j];
+                        for (int j = 0; j < 8; ++j) {
+                            const float v = __uint_as_float(oa[j]) * inv[j];
                             const float w = __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-                            if (j < rows) {
+                            if (j0 + j < rows) {
                                 if (left == 0) {
                                     ++pos;
                                     left = p.rpt;
                                     a = __ldg(cs + int64_t{pos} * kRopePairs);
                                 }
                                 --left;
-                                o[j * kD] = __float2bfloat16_rn(v * a.x + (lane & 1 ? -w : w) * a.y);
+                                to[j * kD] = __float2bfloat16_rn(v * a.x + (lane & 1 ? -w : w) * a.y);
                             }
                         }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j < rows)
-                                o[j * kD] =
-                                    __float2bfloat16_rn(__uint_as_float(oa[j]) * sLinv[hb + j]);
+                        for (int j = 0; j < 8; ++j)
+                            if (j0 + j < rows)
+                                to[j * kD] = __float2bfloat16_rn(__uint_as_float(oa[j]) * inv[j]);
                     }
                 }
             } else {
-                float *orow = reinterpret_cast<float *>(p.ws + kWsO) +
-                              (int64_t{slot} * kRows + hb) * kD + 32 * sp + lane;
+                float *o = reinterpret_cast<float *>(p.ws + kWsO) +
+                           (int64_t{slot} * kRows + hb) * kD + 32 * sp + lane;
+                const bool live = mbar_wait(o_full, i & 1, abort_flag, p.status);
+                tc_fence_after();
 #pragma unroll 1
-                for (int m = 0; m < 4; ++m) {
-                    uint32_t oa[32];
+                for (int m = 0; m < 16; ++m) {
+                    uint32_t oa[8];
                     if (!__all_sync(0xFFFFFFFFu, live)) break;
-                    tmem_ld32(lane_base + kOCol + 64 * m + hb, oa);
+                    const int j0 = 8 * (m % 4);
+                    tmem_ld8(o_col + 64 * (m / 4) + j0, oa);
                     tmem_wait_ld();
-                    float *o = orow + 128 * m;
+                    float *to = o + 128 * (m / 4) + j0 * kD;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j < rows) o[j * kD] = __uint_as_float(oa[j]);
+                    for (int j = 0; j < 8; ++j)
+                        if (j0 + j < rows) to[j * kD] = __uint_as_float(oa[j]);
                 }
             }
             tc_fence_before();
