@@ -598,10 +598,9 @@ __global__ void __launch_bounds__(kT, 1)
     } else if (warp < kSoftWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
         // ---------------- unpacking. Step t: chunk 6 of block t - 1 (a half by each half of the
-        // warps), then pair by pair the chunks of block t - 1 from TMEM to shared memory and those of
-        // block t into TMEM; at its end the bytes of block t + 1 come into registers, so that their
-        // slots are free a block ahead. (Once the kernel gives up no wait lasts, and the next block
-        // does not come.)
+        // warps), then pair by pair the bytes of block t into registers, the chunks of block t - 1
+        // from TMEM to shared memory and those of block t into TMEM. (Once the kernel gives up no
+        // wait lasts, and the next block does not come.)
         const int sp = warp & 3, h = (warp - kUnpackWarp0) >> 2;
         const int key = 32 * sp + lane;
         const uint32_t k_col = tmem + (static_cast<uint32_t>(sp * 32) << 16) + kKCol + 32 * h;
@@ -707,24 +706,30 @@ __global__ void __launch_bounds__(kT, 1)
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(sp * 32) << 16);
         // (the walk and the segments in shared memory, the half's own: registers are few)
         SoftWalk &mine = reinterpret_cast<SoftWalk *>(smem + kOffWalk)[hh];
-        if (sp == 0 && lane == 0) mine.walk = Walk(p, sStart);
+        auto step_walk = [&](int at) {
+            Walk w = mine.walk;
+            Segment next;
+            mine.more[at] = w.next(p, next);
+            mine.x[at] = next;
+            mine.walk = w;
+        };
+        if (sp == 0 && lane == 0) {
+            mine.walk = Walk(p, sStart);
+            step_walk(0);
+        }
+        bar_group(hh);
         int i = 0, g = 0, cur = 0;
         for (;; ++i) {
             const Segment &x = mine.x[i & 1];
-            if (sp == 0 && lane == 0) {
-                Walk w = mine.walk;
-                Segment next;
-                mine.more[i & 1] = w.next(p, next);
-                mine.x[i & 1] = next;
-                mine.walk = w;
-            }
-            bar_group(hh);
             if (!mine.more[i & 1]) break;
             uint64_t l[16];   // sums of rows 2 j and 2 j + 1, over this lane's keys
 #pragma unroll
             for (int j = 0; j < 16; ++j) l[j] = 0;
             if (sp == 0) sM[cur * 64 + hb + lane] = -kNoMax;
             bar_group(hh);
+            // (the next segment, while the first products are on their way; in the place of the one
+            // before, which the whole group has left)
+            if (sp == 0 && lane == 0) step_walk((i + 1) & 1);
             for (int b = 0; b < x.nb; ++b, ++g) {
                 const int k0 = x.block_pos(b);
                 const bool live = __all_sync(
