@@ -923,9 +923,7 @@ __global__ void __launch_bounds__(kT, 1)
                     reinterpret_cast<const float2 *>(p.b.cos_sin) + ((sp - 2) * 16 + (lane >> 1));
                 // (a unit of one token's heads has one position)
                 int pos = p.tpu == 1 ? x.posf : x.posf + hb / p.rpt;
-                int left = p.tpu == 1 ? 32 : p.rpt - hb % p.rpt;  // rows at pos
-                float2 a = make_float2(1.0f, 0.0f);
-                if (turns) a = __ldg(cs + int64_t{pos <= x.posl ? pos : x.posl} * kRopePairs);
+                int left = p.tpu == 1 ? kRows : p.rpt - hb % p.rpt;  // rows at pos
                 const bool live = mbar_wait(o_full, i & 1, abort_flag, p.status);
                 tc_fence_after();
 #pragma unroll 1
@@ -938,19 +936,21 @@ __global__ void __launch_bounds__(kT, 1)
                     __nv_bfloat16 *to = o + 128 * (m / 4) + j0 * kD;
                     const float *inv = sLinv + hb + j0;
                     if (turns && m >= 12) {
+                        float2 a[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            a[j] = __ldg(cs + int64_t{min(pos, x.posl)} * kRopePairs);
+                            const bool last = --left == 0;
+                            pos += last;
+                            left = last ? p.rpt : left;
+                        }
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const float v = __uint_as_float(oa[j]) * inv[j];
                             const float w = __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-                            if (j0 + j < rows) {
-                                if (left == 0) {
-                                    ++pos;
-                                    left = p.rpt;
-                                    a = __ldg(cs + int64_t{pos} * kRopePairs);
-                                }
-                                --left;
-                                to[j * kD] = __float2bfloat16_rn(v * a.x + (lane & 1 ? -w : w) * a.y);
-                            }
+                            if (j0 + j < rows)
+                                to[j * kD] =
+                                    __float2bfloat16_rn(v * a[j].x + (lane & 1 ? -w : w) * a[j].y);
                         }
                     } else {
 #pragma unroll
