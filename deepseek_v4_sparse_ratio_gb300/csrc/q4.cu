@@ -3,8 +3,11 @@
 //
 // A row of 512 bf16 becomes 384 bytes (the header has the layout): 448 whole numbers n of -7 .. 7,
 // a scale s in e4m3 for each 16, a power of two 2^E for the row, x ~ n s 2^E; and the 64 rotated
-// dims in bf16. Both calls take one warp per row, as the bf16 append does, and are bound by HBM
-// (1,408 bytes a row), or by the launch up to a few thousand rows.
+// dims in bf16. Both calls take one warp per row, as the bf16 append does (two or four rows a warp,
+// and blocks of 4 or 16 warps, were equal or slower). 56,436 rows take 27 us to write and 21 us to
+// read back from a cold L2, where their 1,408 bytes a row need 11.9: they are bound by the
+// instructions (about 350 a row to write, three issued a cycle; one element an instruction took 33
+// us). 135,011 rows read back: 40 us of 28. Up to a few thousand rows the launch counts.
 #include <math.h>
 
 #include "common.cuh"
@@ -61,8 +64,8 @@ __device__ __forceinline__ bool find_row(const PagedBatch &b, int64_t r, int lan
 // x / s rounded to a whole number of -7 .. 7, ties to even, plus 8, from x and 1 / s (0 for 8 or
 // where the group holds what is not finite). x has eight significant bits and s four, so a quotient
 // of 0.4 or more that is no tie is 2^-10.9 or more from one; the product with the rounded 1 / s is
-// 2^-19 off at most. Rounded to a multiple of 2^-11 first (by adding 6,144, whose last bit that is),
-// ties are ties and nothing else is.
+// 2^-19 off at most. Rounded to a multiple of 2^-11 first (by adding 6,144, whose last bit that
+// is), ties are ties and nothing else is.
 constexpr float kSnap = 6144.0f;
 constexpr float kWhole = 12582912.0f + 8.0f;   // 1.5 2^23 + 8: the last bit is 1
 __device__ __forceinline__ uint32_t whole_plus8(float x, float per, bool finite) {
@@ -71,17 +74,17 @@ __device__ __forceinline__ uint32_t whole_plus8(float x, float per, bool finite)
     return __float_as_uint(__fadd_rn(n, kWhole)) & 15u;
 }
 
-// The same for four words of two elements each, without the bounds, in the order of a word of codes.
+// The same for four words of two elements each, without the bounds, in a code word's order.
 // Two elements an instruction; a sum in base 16 of the bits of n + kWhole, which are n + 8 above
 // those of kWhole - 8.
 __device__ __forceinline__ uint32_t eight_plain(const uint32_t *w, float per) {
-    const uint64_t p2 = pair_of(per), snap = pair_of(kSnap), back = pair_of(-kSnap);
-    const uint64_t whole = pair_of(kWhole);
+    // (the last addition takes kSnap off as well: kWhole - kSnap is whole, nothing rounds twice)
+    const uint64_t p2 = pair_of(per), snap = pair_of(kSnap), whole = pair_of(kWhole - kSnap);
     uint32_t lo = 0, hi = 0;
 #pragma unroll
     for (int k = 3; k >= 0; --k) {
         const uint64_t x = pair_of(w[k] << 16, w[k] & 0xFFFF0000u);
-        const uint64_t n = add_pair(add_pair(fma_pair(x, p2, snap), back), whole);
+        const uint64_t n = add_pair(fma_pair(x, p2, snap), whole);
         lo = lo * 16u + static_cast<uint32_t>(n);
         hi = hi * 16u + static_cast<uint32_t>(n >> 32);
     }
@@ -89,7 +92,7 @@ __device__ __forceinline__ uint32_t eight_plain(const uint32_t *w, float per) {
     return (lo - kBits * 0x1111u) | (hi - kBits * 0x1111u) << 16;
 }
 
-// Lane l has dims 16 l ..: a group of the 448, or (lanes 28 to 31) a quarter of the rotated ones.
+// Lanes 0 to 27 have a group each, dims 16 l .., and every lane a pair of the rotated dims.
 __global__ void __launch_bounds__(kQ4Warps * 32, 2048 / (kQ4Warps * 32))
     q4_append_kernel(const PagedBatch b, const uint4 *kv, uint8_t *pages, int32_t *status) {
     wait_before();
@@ -97,24 +100,30 @@ __global__ void __launch_bounds__(kQ4Warps * 32, 2048 / (kQ4Warps * 32))
     const int64_t r = int64_t{blockIdx.x} * kQ4Warps + (threadIdx.x >> 5);
     report_bad(b, status);
     if (r >= b.n_new) return;
+    const bool group = lane < kQ4Dims / 16;
     const uint4 *src = kv + r * (kD / 8) + 2 * lane;
-    const uint4 v0 = __ldg(src), v1 = __ldg(src + 1);
+    uint4 v0 = {}, v1 = {};
+    if (group) {
+        v0 = __ldg(src);
+        v1 = __ldg(src + 1);
+    }
+    uint32_t pair =
+        __ldg(reinterpret_cast<const uint32_t *>(kv + r * (kD / 8)) + kQ4Dims / 2 + lane);
     int s;
     int32_t p;
     if (!find_row(b, r, lane, s, p)) return;
     uint8_t *row = row_of(b, pages, s, p, lane, status);
     if (!row) return;
-    uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-    const bool rope = lane >= 28;
-    // the group's largest magnitude (NaN with a NaN among them) as the bits of an fp32: whole numbers
-    // in the same order, NaN above all
-    uint32_t m2 = w[0] & 0x7FFF7FFFu;
+    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    // the group's largest magnitude (NaN with a NaN among them) as the bits of an fp32: whole
+    // numbers in the same order, NaN above all
+    uint32_t m2 = w[0];
 #pragma unroll
     for (int k = 1; k < 8; ++k)
-        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(w[k] & 0x7FFF7FFFu));
-    const uint32_t amax = max(m2 << 16, m2 & 0x7FFF0000u);
+        asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(w[k]));
+    const uint32_t amax = max((m2 << 16) & 0x7FFF0000u, m2 & 0x7FFF0000u);
     const bool finite = amax < kQ4Limit;
-    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, rope || !finite ? 0u : amax);
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, finite ? amax : 0u);
     const int e = max(static_cast<int>(top >> 23) - 127, kQ4LeastExp);
     const float up = pow2(10 - e);
     // 0 <= amax 2^-E / 7 < 293; the division's rounding never meets a border of e4m3 (amax has
@@ -127,9 +136,9 @@ __global__ void __launch_bounds__(kQ4Warps * 32, 2048 / (kQ4Warps * 32))
     const float per = unit > 0.0f ? 1.0f / unit : 0.0f;
     // Ordinary rows: the power of two goes into 1 / s, and a normal s (off by 2^-4 at most) leaves
     // no quotient above 7.5.
-    const bool plain = __all_sync(0xFFFFFFFFu, rope || (finite && (scale >= 8 || scale == 0))) &&
-                       e > -50 && e < 70;
-    if (!rope) {
+    const bool plain = __all_sync(0xFFFFFFFFu, finite && (scale >= 8 || scale == 0)) && e > -50 &&
+                       e < 70;
+    if (group) {
         uint32_t code[2] = {0, 0};
         if (plain) {
             code[0] = eight_plain(w, up * per);
@@ -142,29 +151,21 @@ __global__ void __launch_bounds__(kQ4Warps * 32, 2048 / (kQ4Warps * 32))
             }
         }
         *reinterpret_cast<uint2 *>(row + 32 + 8 * lane) = make_uint2(code[0], code[1]);
-    } else {
-        if (b.cos_sin) {
-            const float4 *cs = reinterpret_cast<const float4 *>(b.cos_sin + int64_t{p} * kRope) +
-                               (lane - 28) * 4;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float4 a = __ldg(cs + k);
-                w[2 * k] = turn_pair(w[2 * k], a.x, a.y);
-                w[2 * k + 1] = turn_pair(w[2 * k + 1], a.z, a.w);
-            }
-        }
-        uint4 *to = reinterpret_cast<uint4 *>(row + kQ4Rope) + 2 * (lane - 28);
-        to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        to[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
+    if (b.cos_sin) {
+        const float2 a =
+            __ldg(reinterpret_cast<const float2 *>(b.cos_sin + int64_t{p} * kRope) + lane);
+        pair = turn_pair(pair, a.x, a.y);
+    }
+    reinterpret_cast<uint32_t *>(row + kQ4Rope)[lane] = pair;
     // the first 32 bytes: chunk lane / 4, half (lane / 2) % 2, group lane % 2 of the half
-    const int half = rope ? lane & 1 : (lane >> 1) & 1;
-    const int at = rope ? (lane < 30 ? 14 : 15) : 2 * (lane >> 2) + (lane & 1);
-    row[16 * half + at] = static_cast<uint8_t>(!rope ? scale : lane < 30 ? e + 127 : 0);
+    const int half = group ? (lane >> 1) & 1 : lane & 1;
+    const int at = group ? 2 * (lane >> 2) + (lane & 1) : lane < 30 ? 14 : 15;
+    row[16 * half + at] = static_cast<uint8_t>(group ? scale : lane < 30 ? e + 127 : 0);
 }
 
-// Lane l has dims 8 l .. and 256 + 8 l ..: words l and l + 32 of the codes, or (lanes 24 to 31) an
-// eighth of the rotated dims.
+// Lane l has dims 8 l .. and (lanes 0 to 23) 256 + 8 l ..: words l and l + 32 of the codes; and a
+// pair of the rotated dims.
 __global__ void __launch_bounds__(kQ4Warps * 32)
     q4_read_kernel(const PagedBatch b, uint8_t *pages, uint4 *out, int32_t *status) {
     wait_before();
@@ -177,14 +178,11 @@ __global__ void __launch_bounds__(kQ4Warps * 32)
     if (!find_row(b, r, lane, s, p)) return;
     const uint8_t *row = row_of(b, pages, s, p, lane, status);
     if (!row) return;
-    const bool rope = lane >= 24;
+    const bool more = lane < kQ4Dims / 8 - 32;
     const uint32_t first = __ldg(reinterpret_cast<const uint32_t *>(row + 32) + lane);
     uint32_t second = 0;
-    uint4 v1 = {};
-    if (rope)
-        v1 = __ldg(reinterpret_cast<const uint4 *>(row + kQ4Rope) + lane - 24);
-    else
-        second = __ldg(reinterpret_cast<const uint32_t *>(row + 32) + 32 + lane);
+    if (more) second = __ldg(reinterpret_cast<const uint32_t *>(row + 32) + 32 + lane);
+    uint32_t pair = __ldg(reinterpret_cast<const uint32_t *>(row + kQ4Rope) + lane);
     const uint32_t head = __ldg(row + lane);   // the scales, a byte a lane
     const uint32_t exponent = __shfl_sync(0xFFFFFFFFu, head, 14);
     auto words = [&](uint32_t code, int word) {
@@ -199,21 +197,16 @@ __global__ void __launch_bounds__(kQ4Warps * 32)
                           q4_pair(code, 2, half, off), q4_pair(code, 3, half, off));
     };
     const uint4 v0 = words(first, lane);
-    const uint4 v2 = words(second, lane + 32);
-    if (!rope) {
-        v1 = v2;
-    } else if (b.cos_sin) {
-        const float4 *cs =
-            reinterpret_cast<const float4 *>(b.cos_sin + int64_t{p} * kRope) + (lane - 24) * 2;
-        const float4 a = __ldg(cs), c = __ldg(cs + 1);
-        v1.x = turn_pair(v1.x, a.x, -a.y);
-        v1.y = turn_pair(v1.y, a.z, -a.w);
-        v1.z = turn_pair(v1.z, c.x, -c.y);
-        v1.w = turn_pair(v1.w, c.z, -c.w);
+    const uint4 v1 = words(second, lane + 32);
+    if (b.cos_sin) {
+        const float2 a =
+            __ldg(reinterpret_cast<const float2 *>(b.cos_sin + int64_t{p} * kRope) + lane);
+        pair = turn_pair(pair, a.x, -a.y);
     }
-    uint4 *dst = out + r * (kD / 8) + lane;
-    dst[0] = v0;
-    dst[32] = v1;
+    uint4 *dst = out + r * (kD / 8);
+    dst[lane] = v0;
+    if (more) dst[32 + lane] = v1;
+    reinterpret_cast<uint32_t *>(dst)[kQ4Dims / 2 + lane] = pair;
 }
 
 }  // namespace

@@ -18,10 +18,17 @@
 //   chunks 0-5: TMEM for QK, shared memory for PV;  chunk 6: shared memory for both, unpacked when
 //   PV of the block before has used it (the first tile of PV);  chunk 7, the rotated dims (bf16 in
 //   the pages): TMA into their place as soon as the same tile has left it.
-// The 4-bit bytes come by TMA too, 64 of a row's first 256 at a time (the scales and chunk 0, chunks
-// 1-2, 3-4, 5-6), into two slots in turn. (Loaded by the unpacking threads themselves, a key's
-// bytes each, a sector and a line for every lane of a load keep the load unit busy for longer than
-// the products take.)
+// The 4-bit bytes come by TMA too, 64 of a row's first 256 at a time (the scales and chunk 0,
+// chunks 1-2, 3-4, 5-6), into two slots in turn. (Loaded by the unpacking threads themselves, a
+// key's bytes each, a sector and a line for every lane of a load keep the load unit busy for longer
+// than the products take.)
+// Measured: 2,048 tokens of 64 heads at 16,384 in 4.59 ms (900 TFLOP/s, 0.46 of the peak); a block
+// takes 5,600 cycles there, about 4,000 of them shared memory's, and the eight unpacking warps are
+// busy through it: that chain is what bounds it now (the 128 rows of the bf16 chunk kernel share a
+// block's loads among twice the rows: 3.75 ms). One token at 131,072: 41.2 us, 6,700 cycles a block.
+// Between units lie 18,000 cycles (results out, first block's softmax): 310 us for 7 prompts of up
+// to 1,701 tokens of 16 heads with a window of 512. The code that is run there is kept in short
+// loops: fetching it is most of its time.
 //
 // Roles (640 threads): warp 0 loads the 4-bit bytes; warp 1 issues QK, warp 3 PV; warp 2 loads q,
 // turns it, and loads chunk 7; warps 4-11 unpack: thread = key, each half of the warps every other
@@ -64,7 +71,7 @@ constexpr uint32_t kOffRaw = kOff7 + kChunk;      // [2][128 keys x 64 B] of the
 constexpr uint32_t kOffP = kOffRaw + 16384;       // P^T [128 keys x 64 rows] bf16
 constexpr uint32_t kOffRed = kOffP + 16384;       // [4][64] block maxima | partial sums
 constexpr uint32_t kOffLinv = kOffRed + 1024;     // [64] rescale factors | 1/sum
-constexpr uint32_t kOffM = kOffLinv + 256;        // [2][64] running maximum, negated, double-buffered
+constexpr uint32_t kOffM = kOffLinv + 256;        // [2][64] running maxima, negated, in turn
 constexpr uint32_t kOffWalk = kOffM + 512;        // [2] where the softmax is, by half
 constexpr uint32_t kOffBar = kOffWalk + 2 * 192;
 constexpr uint32_t kSmem = kOffBar + 384;
@@ -179,9 +186,9 @@ __device__ __forceinline__ void load_piece(uint32_t *v, uint32_t at) {
                  : "memory");
 }
 
-// Hands bytes of shared memory that this warp has read back to the copies that fill them. (The fence
-// is needed: an arrival alone is performed while loads are on their way, and without it the next
-// part's bytes were unpacked in the place of this one's.)
+// Hands bytes of shared memory that this warp has read back to the copies that fill them. (The
+// fence is needed: an arrival alone is performed while loads are on their way, and without it the
+// next part's bytes were unpacked in the place of this one's.)
 __device__ __forceinline__ void give_back(uint64_t *bar, int lane) {
     fence_proxy_async_smem();
     __syncwarp();
@@ -653,8 +660,9 @@ __global__ void __launch_bounds__(kT, 1)
                 uint32_t raw[8];
                 const int part = m + h;
                 if (have) {
-                    // the 32 bytes of chunk 2 m + h: half (1 - h) of part m + h (before the copy: the
-                    // next part is on its way the earlier; 5.09 -> 4.70 ms for 2,048 tokens at 16,384)
+                    // the 32 bytes of chunk 2 m + h: half (1 - h) of part m + h (before the copy:
+                    // the next part is on its way the earlier; 5.09 -> 4.70 ms for 2,048 tokens at
+                    // 16,384)
                     const uint32_t at = (from + (part & 1) * 8192) ^ (h ? 0 : 32);
                     wait_bar(&raw_full[part], t & 1, abort_flag, p.status);
                     load_piece(raw, at);
