@@ -3,10 +3,10 @@
 //   y = R(p) (x rsqrt(mean x^2 + eps) w)
 //
 // A row (a head of q, or a KV row) is 512 elements, 16 of a lane: pieces l and l + 32 of 16 bytes,
-// so that the rotated dims are the second pieces of lanes 24..31. A warp takes up to four heads of a
-// token, whose place and angles it looks up once; a token's KV row is a warp's own.
-// Bound by HBM: 4,096 tokens of 64 heads (545 MB) take 78.6 us, 1.04 of the copy rate (the last 50 MB
-// of the output are still in L2 then); one token takes 8 us, the launch's.
+// so that the rotated dims are the second pieces of lanes 24..31. A warp takes up to four heads of
+// a token, whose place and angles it looks up once; a token's KV row is a warp's own.
+// Bound by HBM: 4,096 tokens of 64 heads (545 MB) take 78.6 us, 1.04 of the copy rate (the last
+// 50 MB of the output are still in L2 then); one token takes 8 us, the launch's.
 #include <math.h>
 
 #include "common.cuh"

@@ -25,7 +25,8 @@
 // Measured: 2,048 tokens of 64 heads at 16,384 in 4.59 ms (900 TFLOP/s, 0.46 of the peak); a block
 // takes 5,600 cycles there, about 4,000 of them shared memory's, and the eight unpacking warps are
 // busy through it: that chain is what bounds it now (the 128 rows of the bf16 chunk kernel share a
-// block's loads among twice the rows: 3.75 ms). One token at 131,072: 41.2 us, 6,700 cycles a block.
+// block's loads among twice the rows: 3.75 ms). One token at 131,072: 41.2 us, 6,700 cycles a
+// block.
 // Between units lie 18,000 cycles (results out, first block's softmax): 310 us for 7 prompts of up
 // to 1,701 tokens of 16 heads with a window of 512. The code that is run there is kept in short
 // loops: fetching it is most of its time.
@@ -165,7 +166,7 @@ __device__ __forceinline__ void unpack32(const uint32_t *w, uint32_t two, float 
         for (int k = 0; k < 4; ++k) out[4 * j + k] = q4_pair(w[j], k, half[j / 2], off[j / 2]);
 }
 
-// Whether a word holds an e4m3 NaN (0x7F or 0xFF) in its bytes under `mask`.
+// Whether a byte of a word is an e4m3 NaN (0x7F or 0xFF).
 __device__ __forceinline__ bool has_nan(uint32_t w) {
     const uint32_t x = ~w & 0x7F7F7F7Fu;   // a byte 0 where all seven bits are set
     return ((x - 0x01010101u) & ~x & 0x80808080u) != 0;
@@ -315,7 +316,8 @@ __global__ void __launch_bounds__(kT, 1)
     }
     if (warp == 0) {
         // arrivals a phase takes: 8 unpacking warps on tm_full, v_full, k6_full and raw_free, the
-        // turning warp's threads on q_turned, 8 softmax warps on s_free, p_full and o_free, one on the others
+        // turning warp's threads on q_turned, 8 softmax warps on s_free, p_full and o_free, one on
+        // the others
         int n = 1;
         uint64_t *bar = bars + lane;
         if (bar < v_free || (bar >= k6_full && bar < raw_full)) n = 8;

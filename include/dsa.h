@@ -521,6 +521,8 @@ int dsa_paged_q4_read(const int32_t *new_start, const int32_t *seq_len, int32_t 
  * The other arguments, the workspace, roundings, logits of any size and what rows that are not seen
  * (whatever they hold) or not finite do: as for dsa_paged_attn. A token that sees no row gets
  * zeros. The same call gives the same bits.
+ * Launch shape: one CTA per SM, all keys of the batch cut evenly over them, units of up to 64 rows
+ * of q whatever the batch, and a join of what was cut.
  * Sizes that would allow one SM 2^31 blocks of 128 keys get DSA_ERR_SHAPE.
  * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE, DSA_ERR_SCRATCH, DSA_ERR_CUDA.
  */
