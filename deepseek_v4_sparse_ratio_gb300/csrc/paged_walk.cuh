@@ -96,10 +96,12 @@ struct Params {
     static constexpr bool kSinks = false;
 };
 
-// With first tokens that stay visible beside a window: the keys of a unit whose window begins
-// behind block 0 are block 0 and then the window's blocks.
+// With first tokens that stay visible beside a window. Where a unit's window begins behind block 0,
+// they take the first places of the window's first block if these hold keys before the window, whole
+// pages of them; otherwise block 0 comes before the window's blocks.
 struct SinkParams : Params {
     int32_t sinks;     // 0 without a window; within block 0
+    int32_t sink_keys; // keys of their pages, as far as those lie in block 0
     int32_t turn_q;    // q is to be turned by its positions
     static constexpr bool kSinks = true;
 };
@@ -150,20 +152,20 @@ __device__ __forceinline__ void key_range(const P &p, const PagedSeq &q, int t0,
     hi = q.len - q.n + min(t0 + p.tpu, q.n) - 1;
 }
 
-// Whether block 0 stands before the blocks of a window that begins at lo.
+// The number of a unit's first block, its window beginning at lo: that of lo, or one less where the
+// first tokens need a block of their own.
 template <class P>
-__device__ __forceinline__ bool sink_block(const P &p, int lo) {
+__device__ __forceinline__ int first_block(const P &p, int lo) {
     if constexpr (P::kSinks)
-        return p.sinks > 0 && lo >= kBlock;
-    else
-        return false;
+        if (lo >= kBlock) lo -= p.sink_keys;
+    return lo >> 7;
 }
 
 template <class P>
 __device__ __forceinline__ int group_blocks(const P &p, const PagedSeq &q, int g) {
     int lo, hi;
     key_range(p, q, g * p.tpu, lo, hi);
-    return (hi >> 7) - (lo >> 7) + 1 + sink_block(p, lo);
+    return (hi >> 7) - first_block(p, lo) + 1;
 }
 
 // Places of the first G token groups of a sequence, for each part (G = all of them: the last one
@@ -175,12 +177,14 @@ static __device__ __noinline__ int64_t places_before_many(const P &p, PagedSeq q
     if (G * d > q.n) sum += ((q.len - 1) >> 7) - ((base + G * d - 1) >> 7);
     if (p.window > 0) {
         const int a = base - p.window + 1;  // (a window is shorter than the longest sequence)
-        const int g0 = a >= 0 ? 0 : (-a + d - 1) / d;
-        sum -= floor_sum(G - g0, a + g0 * d, d);
-        if constexpr (P::kSinks) {  // the groups whose windows begin behind block 0
-            const int g1 = a >= kBlock ? 0 : (kBlock - a + d - 1) / d;
-            if (p.sinks > 0) sum += max(0, G - g1);
+        // the first group whose window begins at 0 or later; with first tokens, behind block 0
+        int first = 0, keys = 0;
+        if constexpr (P::kSinks) {
+            first = kBlock;
+            keys = p.sink_keys;
         }
+        const int g0 = a >= first ? 0 : (first - a + d - 1) / d;
+        sum -= floor_sum(G - g0, a + g0 * d - keys, d);
     }
     return sum;
 }
@@ -258,11 +262,16 @@ struct Segment {
     int lo;            // lowest position any of its tokens sees
     bool whole;        // all of the unit's blocks
     bool alone;        // the sequence's only unit: nothing else reads its keys
-    bool jump;         // the first block is block 0, the next one blk + 1
+    int ahead;         // keys at the start of the first block that are positions 0 ..; kBlock:
+                       // it is block 0, and the next one blk + 1
 
-    // The first position of block b.
+    // The position of block b, as of its last keys.
     __device__ __forceinline__ int block_pos(int b) const {
-        return jump && b == 0 ? 0 : (blk + b) * kBlock;
+        return ahead == kBlock && b == 0 ? 0 : (blk + b) * kBlock;
+    }
+    // The position of key k of block b.
+    __device__ __forceinline__ int key_pos(int b, int k) const {
+        return b == 0 && k < ahead ? k : (blk + b) * kBlock + k;
     }
 };
 
@@ -295,8 +304,7 @@ struct Walk {
         const int t0 = at.g * p.tpu, t1 = min(t0 + p.tpu, q.n);
         int hi;
         key_range(p, q, t0, x.lo, hi);
-        const int sink = sink_block(p, x.lo);
-        const int blo = (x.lo >> 7) - sink, nblk = (hi >> 7) - blo + 1;
+        const int blo = first_block(p, x.lo), nblk = (hi >> 7) - blo + 1;
         const int before = max(0, kUnitCost - at.off), off = max(0, at.off - kUnitCost);
         x.nb = min(nblk - off, left - before);
         if (x.nb <= 0) {  // the run ends before the unit's first block
@@ -310,7 +318,9 @@ struct Walk {
         x.nrows = unit_rows(p, t1 - t0, at.part);
         x.part = at.part;
         x.blk = blo + off;
-        x.jump = sink > 0 && off == 0;
+        x.ahead = 0;
+        if constexpr (P::kSinks)
+            if (off == 0 && x.lo >= kBlock) x.ahead = blo < x.lo >> 7 ? kBlock : p.sink_keys;
         x.whole = x.nb == nblk;
         x.alone = p.upt == 1 && q.n <= p.tpu;
         left -= before + x.nb;
@@ -342,7 +352,7 @@ struct PageWalk {
                                             int &row) {
         int32_t e = -1;
         if (have) {
-            const int pos = x.block_pos(b) + page * prows;
+            const int pos = x.key_pos(b, page * prows);
             row = pos & ((1 << p.b.page_shift) - 1);
             bool seen = pos > x.lo - prows;
             if constexpr (P::kSinks) seen |= pos < p.sinks;

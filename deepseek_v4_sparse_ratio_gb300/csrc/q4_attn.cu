@@ -22,12 +22,12 @@
 // chunks 1-2, 3-4, 5-6), into two slots in turn. (Loaded by the unpacking threads themselves, a
 // key's bytes each, a sector and a line for every lane of a load keep the load unit busy for longer
 // than the products take.)
-// Measured: 2,048 tokens of 64 heads at 16,384 in 4.59 ms (900 TFLOP/s, 0.46 of the peak); a block
+// Measured: 2,048 tokens of 64 heads at 16,384 in 4.62 ms (893 TFLOP/s, 0.45 of the peak); a block
 // takes 5,600 cycles there, about 4,000 of them shared memory's, and the eight unpacking warps are
 // busy through it: that chain is what bounds it now (the 128 rows of the bf16 chunk kernel share a
-// block's loads among twice the rows: 3.75 ms). One token at 131,072: 41.2 us, 6,700 cycles a
+// block's loads among twice the rows: 3.75 ms). One token at 131,072: 41.4 us, 6,700 cycles a
 // block.
-// Between units lie 18,000 cycles (results out, first block's softmax): 310 us for 7 prompts of up
+// Between units lie 18,000 cycles (results out, first block's softmax): 287 us for 7 prompts of up
 // to 1,701 tokens of 16 heads with a window of 512. The code that is run there is kept in short
 // loops: fetching it is most of its time.
 //
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kT, 1)
                     const int pos = walk.x.block_pos(walk.b);
                     a_next = walk.x.lo - pos;
                     b_next = walk.x.posl - pos + 1;
-                    c_next = p.sinks - pos;
+                    c_next = walk.b == 0 && walk.x.ahead > 0 ? p.sinks : p.sinks - pos;
                     alone_next = walk.x.alone;
                     e_next = walk.next(p, lane, prows, np, row_next);
                     if (e_next >= 0)
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kT, 1)
                 __syncwarp();
                 for (int b = 0; b < x.nb; ++b, ++t) {
                     // (a bad table entry is reported by the other loader)
-                    const int pos = x.block_pos(b) + lane * prows;
+                    const int pos = x.key_pos(b, lane * prows);
                     int32_t e = -1;
                     if (lane < np && pos <= x.posl && (pos > x.lo - prows || pos < p.sinks))
                         e = __ldg(p.b.page_table + int64_t{x.s} * p.b.max_pages +
@@ -763,10 +763,11 @@ __global__ void __launch_bounds__(kT, 1)
                 if (masked) {
                     // rows [ra, rb) of the unit see the key: their token is not before it and
                     // less than `window` after it, or it is one of the first
-                    const int64_t ahead = int64_t{k0} + kl - x.posf;
+                    const int pos = x.key_pos(b, kl);
+                    const int64_t ahead = int64_t{pos} - x.posf;
                     const int ta = static_cast<int>(max(int64_t{0}, min(ahead, int64_t{64})));
                     const int64_t gone =
-                        p.window > 0 && k0 + kl >= p.sinks ? ahead + p.window : 64;
+                        p.window > 0 && pos >= p.sinks ? ahead + p.window : 64;
                     const int tb = static_cast<int>(max(int64_t{0}, min(gone, int64_t{64})));
                     const int ra = min(64, ta * p.rpt);
                     int rb = min(64, tb * p.rpt);
@@ -1056,6 +1057,8 @@ extern "C" int dsa_paged_q4_attn(const void *q, int32_t heads, int64_t n_new,
     // a window no shorter than any sequence is no window
     p.window = window >= p.b.len_limit ? 0 : window;
     p.sinks = p.window > 0 ? sinks : 0;
+    const int prows = std::min(page_size, kBlock);
+    p.sink_keys = (p.sinks + prows - 1) / prows * prows;
     p.turn_q = !q_turned;
     const int64_t keys =
         p.window > 0 ? std::min(p.b.len_limit, p.window + p.tpu) + kBlock : p.b.len_limit;

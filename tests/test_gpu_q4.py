@@ -792,3 +792,26 @@ def test_the_larger_of_two_kinds_of_rows(dsa, workspace, lens, heads, size, sign
             err = (out[r] - want).abs()
             assert bool((err <= Q.U + 2 * c * 2.0 ** -24).all()), (t, err.max())
             r += 1
+
+
+@pytest.mark.parametrize("page,sinks", [(16, 1), (16, 16), (16, 37), (32, 16), (32, 65), (64, 4),
+                                        (64, 100), (128, 8), (256, 8), (16, 128)])
+@pytest.mark.parametrize("lens,heads,window", [
+    ([(1, 129 + 9 * i) for i in range(45)], 64, 90),      # windows that begin everywhere in a block
+    ([(330, 700), (1, 300)], 16, 130),                    # four tokens a unit
+    ([(150, 420)], 64, 1), ([(140, 600)], 5, 257), ([(90, 500), (3, 260)], 128, 128)])
+def test_first_tokens_in_the_places_before_a_window(dsa, workspace, page, sinks, lens, heads, window):
+    """The first tokens' pages lie in the window's first block where it has room for them, and in a
+    block of their own where it has not."""
+    batch = Q.make(lens, page, seed=page + sinks)
+    # rows that no token sees: NaN
+    pages, table = batch["pages"], batch["page_table"]
+    for s, (n, c) in enumerate(lens):
+        pos = torch.arange(c)
+        gone = pos[(pos >= sinks) & (pos <= c - n - window)]
+        pages[table[s, gone // page].long(), gone % page] = 0xFF
+    q = queries(batch, heads, 21)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = run_attn(batch, q, window, sinks, workspace, status=status)
+    assert status.item() == 0
+    check_attn(out, batch, q, window, sinks)
