@@ -23,10 +23,16 @@ __device__ __forceinline__ float e4m3(uint32_t byte) {
         __half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3)));
 }
 
-// A scale times the row's power of two: s 2^(b - 137), b the row's byte (14 to 250 as written;
-// other memory may hold any, and those below 11 count as 11).
+// E from the row's byte, 14 to 250 as written. Other memory may hold any: those below 11 count as 11,
+// and those above 250 as 250, with which every scale leaves values that are finite (72 u, u = 448
+// 2^113 at most, is 2^127.98).
+__device__ __forceinline__ int q4_exp(uint32_t b) {
+    return min(max(static_cast<int>(b), 11), 250) - 137;
+}
+
+// A scale times the row's power of two: s 2^E.
 __device__ __forceinline__ float q4_unit(uint32_t scale, uint32_t b) {
-    return e4m3(scale) * pow2(max(static_cast<int>(b), 11) - 137);
+    return e4m3(scale) * pow2(q4_exp(b));
 }
 
 // Dims 2 k and 2 k + 1 of a word of eight codes, as two bf16: (n + 8) 2 + 128 = 144 + 2 n has its

@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kT, 1)
                     two[m] = there ? __byte_perm(head[m], head[4 + m], h ? 0x7632 : 0x5410) : 0u;
                 two6 = there ? (h ? head[7] : head[3]) : 0u;  // chunk 6, half h: bytes 12 and 13
                 odd_next = has_nan(two[0]) || has_nan(two[1]) || has_nan(two[2]);
-                pow = pow2(max(static_cast<int>((head[3] >> 16) & 0xFFu), 11) - 138);
+                pow = pow2(q4_exp((head[3] >> 16) & 0xFFu) - 1);
                 if (h == 1) give_back(&raw_free[0], lane);
             }
             // (one copy of the code for the three pairs: fetching it costs more than the loop)
