@@ -23,11 +23,11 @@ __device__ __forceinline__ float e4m3(uint32_t byte) {
         __half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3)));
 }
 
-// E from the row's byte, 14 to 250 as written. Other memory may hold any: those below 11 count as 11,
-// and those above 250 as 250, with which every scale leaves values that are finite (72 u, u = 448
-// 2^113 at most, is 2^127.98).
+// E from the row's byte. 14 to 250 are written; other memory may hold any, and counts as the nearest
+// of these in every reader: below 14, halves of the smallest values would be no bf16, and above 250
+// the values of the largest scales no finite ones (72 u, u = 448 2^113 at most, is 2^127.98).
 __device__ __forceinline__ int q4_exp(uint32_t b) {
-    return min(max(static_cast<int>(b), 11), 250) - 137;
+    return min(max(static_cast<int>(b), 14), 250) - 137;
 }
 
 // A scale times the row's power of two: s 2^E.

@@ -476,8 +476,8 @@ int dsa_qk_norm_rope(const void *q, int32_t heads, const void *kv, int64_t n_new
  *   holds a NaN, an infinity or an element of 2^124 or more has a NaN for its scale and reads back
  *   as NaN; the others of its row are as without it (A is taken over the others).
  *   Bytes 32 j + 16 h .. 32 j + 16 h + 15, h = 0 and 1 the half (32 dims) of a chunk of 64 dims:
- *     j = 0       the half's 14 scales, two a chunk; one byte E + 137 (250 at most: others that a
- *                 page may hold count as 250); one byte 0;
+ *     j = 0       the half's 14 scales, two a chunk; one byte E + 137 (14 to 250; others that a
+ *                 page may hold count as the nearest of these); one byte 0;
  *     j = 1 .. 7  chunk j - 1 in four words of eight dims; dim 2 k of a word is its nibble k and
  *                 dim 2 k + 1 its nibble k + 4, as n + 8;
  *     j = 8 .. 11 the last 64 dims in order, two bytes each.
