@@ -1,5 +1,6 @@
-// What the two kernels of dsa_paged_attn share: the list of units and key blocks that is cut
-// evenly over the CTAs, the workspace in which the parts of a cut unit meet, and small helpers.
+// What the two kernels of dsa_paged_attn and that of dsa_paged_q4_attn share: the list of units and
+// key blocks that is cut evenly over the CTAs, the workspace in which the parts of a cut unit meet,
+// and small helpers.
 //
 // Work. A unit is a few whole tokens of one sequence (or part of one token's heads): rows of q
 // that attend over the same rows of the cache, each up to its own position. Its keys are blocks

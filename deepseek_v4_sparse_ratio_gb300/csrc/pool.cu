@@ -330,8 +330,8 @@ bool make_tmap_bf16(CUtensorMap *map, const void *base, uint64_t inner, uint64_t
                        swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// The pages as [n_pages][page_size][512]; a box is 64 dims of one page, or of 128 rows of a
-// longer one, with the 128-byte swizzle.
+// The pages as [n_pages][page_size][a row's bytes / 2] of 16-bit elements; a box is 64 (or 32) of
+// them by one page, or by 128 rows of a longer one, with the 128-byte (64-byte) swizzle.
 bool make_tmap_pages(CUtensorMap *map, const void *pages, const PagedBatch &b, PageRow row,
                      uint32_t box_inner) {
     const cuuint64_t rows = cuuint64_t{1} << b.page_shift;

@@ -4,10 +4,13 @@
 // A row of 512 bf16 becomes 384 bytes (the header has the layout): 448 whole numbers n of -7 .. 7,
 // a scale s in e4m3 for each 16, a power of two 2^E for the row, x ~ n s 2^E; and the 64 rotated
 // dims in bf16. Both calls take one warp per row, as the bf16 append does (two or four rows a warp,
-// and blocks of 4 or 16 warps, were equal or slower). 56,436 rows take 27 us to write and 21 us to
-// read back from a cold L2, where their 1,408 bytes a row need 11.9: they are bound by the
-// instructions (about 350 a row to write, three issued a cycle; one element an instruction took 33
-// us). 135,011 rows read back: 40 us of 28. Up to a few thousand rows the launch counts.
+// and blocks of 4 or 16 warps, were equal or slower). Measured as a call among others, and as one
+// from a cold L2 with the 2 us of the events around it:
+//   write 56,436 rows   20.0, 25.2 us (their 1,408 bytes a row need 11.9): bound by the instructions,
+//                       about 350 a row, three issued a cycle
+//   read 56,436 rows    14.1, 19.1 us of 11.9
+//   read 135,011 rows   35.2, 37.5 us of 28.4: 0.8 of the copy rate
+// (the first figures have the pages in L2, 22 and 52 MB). Up to a few thousand rows the launch counts.
 #include <math.h>
 
 #include "common.cuh"

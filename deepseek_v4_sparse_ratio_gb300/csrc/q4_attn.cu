@@ -8,7 +8,7 @@
 // the MMA's M:
 //   S^T[key, row]  = K_blk[128 x 512] . Q^T        (M=128, N=64, K=512)
 //   O^T[d, row]   += V_blk^T[512 x 128] . P^T       (4 x (M=128, N=64, K=128))
-// in bf16, which holds what a 4-bit element stands for exactly. What bounds it is shared memory:
+// in bf16, which holds what a 4-bit element stands for exactly. What binds first is shared memory:
 // with both operands there a product of N=64 takes 48 cycles for 32 of the tensor pipe, and the
 // unpacked rows are written on top. So six of the eight 64-dim chunks of K are unpacked into TMEM,
 // where the first product takes them from (32 cycles), and from there into shared memory when the
@@ -22,12 +22,15 @@
 // chunks 1-2, 3-4, 5-6), into two slots in turn. (Loaded by the unpacking threads themselves, a
 // key's bytes each, a sector and a line for every lane of a load keep the load unit busy for longer
 // than the products take.)
-// Measured: 2,048 tokens of 64 heads at 16,384 in 4.62 ms (893 TFLOP/s, 0.45 of the peak); a block
-// takes 5,600 cycles there, about 4,000 of them shared memory's, and the eight unpacking warps are
-// busy through it: that chain is what bounds it now (the 128 rows of the bf16 chunk kernel share a
-// block's loads among twice the rows: 3.75 ms). One token at 131,072: 41.4 us, 6,700 cycles a
-// block.
-// Between units lie 18,000 cycles (results out, first block's softmax): 287 us for 7 prompts of up
+// Measured: 2,048 tokens of 64 heads at 16,384 in 4.63 ms (892 TFLOP/s, 0.45 of the peak); a block
+// takes 5,600 cycles there, and the eight unpacking warps are busy through it: that chain is what
+// bounds it now, before shared memory and the tensor pipe (2,048 cycles). Shared memory's part by
+// bytes, at 128 a cycle: operands of QK 64 + 32 KB and of PV 192 KB, 4-bit bytes in and out 64 KB,
+// unpacked rows in 112 KB, chunk 7 and P 16 KB each, 496 KB or 3,970 cycles. (The 128 rows of the
+// bf16 chunk kernel share a block's loads among twice the rows: 3.71 ms, and 3.65 ms with the
+// context's rows read back first.) One token at 131,072: 41.1 us among other calls, its 50 MB of
+// pages in L2 by then; from a cold L2 6 us more. 6,700 cycles a block.
+// Between units lie 18,000 cycles (results out, first block's softmax): 285 us for 7 prompts of up
 // to 1,701 tokens of 16 heads with a window of 512. The code that is run there is kept in short
 // loops: fetching it is most of its time.
 //

@@ -515,7 +515,8 @@ int dsa_paged_q4_read(const int32_t *new_start, const int32_t *seq_len, int32_t 
  * of position t sees the rows u <= t with u > t - window or u < sinks (window > 0), or all
  * u <= t (window = 0).
  *   sinks: first tokens that stay visible beside a window, 0 to DSA_MAX_SINKS (no meaning
- *   without a window);
+ *   without a window); keys of the cache as the others are, not a learned logit in the softmax's
+ *   sum;
  *   q_turned: 1 where q comes turned by its positions (dsa_qk_norm_rope), 0 where this call turns
  *   it; the output is turned back with cos_sin in either case, and without cos_sin nothing is
  *   turned.
@@ -523,7 +524,12 @@ int dsa_paged_q4_read(const int32_t *new_start, const int32_t *seq_len, int32_t 
  * (whatever they hold) or not finite do: as for dsa_paged_attn. A token that sees no row gets
  * zeros. The same call gives the same bits.
  * Launch shape: one CTA per SM, all keys of the batch cut evenly over them, units of up to 64 rows
- * of q whatever the batch, and a join of what was cut.
+ * of q whatever the batch, and a join of what was cut. For single tokens about as fast as
+ * dsa_paged_attn over bf16 pages (39 and 44 us for one at 131,072 of 64 heads, 72 and 76 us for 64
+ * users), with 3/8 of the memory. For many tokens of a prompt over a whole context dsa_paged_attn is
+ * the faster one, as it has units of 128 rows: 2,048 tokens at 16,384 take 4.63 ms here, 3.65 ms
+ * with the context's rows read back into bf16 pages (dsa_paged_q4_read without cos_sin, all seq_len
+ * rows as new, 11 us) and attended over there.
  * Sizes that would allow one SM 2^31 blocks of 128 keys get DSA_ERR_SHAPE.
  * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE, DSA_ERR_SCRATCH, DSA_ERR_CUDA.
  */
